@@ -76,7 +76,8 @@ enum {
     LORA_FLAG_SLOT_RANGE = 1u << 0,   /* a seq_slot value >= max_loras was seen; those rows got no delta */
     LORA_FLAG_WAIT_TIMEOUT = 1u << 1, /* an in-kernel wait gave up; that call's output is not valid */
     LORA_FLAG_BAD_OFFSETS = 1u << 2,  /* expert_offsets not non-decreasing within [0, T]; rows outside skipped */
-    LORA_FLAG_TOKEN_RANGE = 1u << 3,  /* lora_embed_apply: a token outside [0, vocab); its row is zero */
+    LORA_FLAG_TOKEN_RANGE = 1u << 3,  /* lora_embed_apply: a token outside [0, vocab); its row is zero.
+                                         lora_logprobs: a token >= V; treated as none */
     LORA_FLAG_EXPERT_RANGE = 1u << 4  /* lora_moe_gather_apply: an expert index outside [0, E); that slot-row adds nothing */
 };
 
@@ -524,6 +525,83 @@ lora_status lora_moe_gather_apply(const void *x, int64_t x_stride, const void *c
                                   const int32_t *seq_slot, const lora_route *rts, const float *combine,
                                   int top_k, void *y, int64_t y_stride, void *ws, size_t ws_bytes,
                                   lora_stream_t stream);
+
+/*
+ * ------------------------------------------------------------------------
+ * What a server answers with: log probabilities of given tokens, entropy, the
+ * best alternatives, and their gradient (no counterpart on the pages).
+ * ------------------------------------------------------------------------
+ */
+
+/* Element types of the calls that take one. */
+enum {
+    LORA_DTYPE_BF16 = 0,
+    LORA_DTYPE_F32 = 1
+};
+
+/* Largest top_k of lora_logprobs. */
+#define LORA_MAX_TOP 32
+
+/* Workspace of lora_logprobs: the status words. */
+size_t lora_logprobs_workspace_bytes(int M, int V, int top_k);
+
+/*
+ * Row i of logits, x, with t = inv_temperature, m = max x:
+ *   stats[i]    = { m, log sum_v e^((x_v - m) t) }
+ *   logprob[i]  = (x_k - m) t - stats[i][1],  k = tokens[i]
+ *   entropy[i]  = - sum_v p_v log p_v
+ *   top_ids[i][0..top_k), top_logprobs[i][0..top_k): the top_k elements of the
+ *                 row in descending order, of equal ones the lower index first
+ *                 (-0 equals +0), and their log probabilities
+ *
+ *   logits   device, M rows of V elements of `dtype` (LORA_DTYPE_*), row i at
+ *            logits + i*stride (elements; any stride >= V, any row alignment)
+ *   tokens   device [M] int32, or NULL (then logprob must be NULL); a negative
+ *            token asks for nothing: its logprob is 0. One >= V counts as
+ *            negative and sets LORA_FLAG_TOKEN_RANGE
+ *   logprob, entropy   device [M] f32, each or NULL
+ *   stats    device [M][2] f32 or NULL; lora_logprobs_grad reads it
+ *   top_ids, top_logprobs   device [M][top_k], both non-NULL when top_k > 0
+ *   ws       device workspace of lora_logprobs_workspace_bytes bytes, for the
+ *            status word
+ * Sums are fp32. A masked element (-infinity) has probability 0, adds nothing
+ * to the entropy and is no alternative: places without one hold id -1 and
+ * -infinity. A row with nothing but -infinity has entropy 0, log probabilities
+ * of -infinity and stats { -infinity, 0 }. A row that holds a NaN or +infinity
+ * has no distribution: its floats are NaN and its ids -1. The type's lowest
+ * value is an ordinary element: a row of it alone is uniform.
+ * Results are the same on every run. M = 0 is a no-op. Enqueued on `stream`
+ * only (no allocation, no synchronisation; graph-safe).
+ * Errors: NULL logits or ws, M < 0, V < 1, stride < V, an unknown dtype, an
+ * inv_temperature that is not positive and finite, top_k outside [0,
+ * min(V, LORA_MAX_TOP)], NULL top arrays with top_k > 0, logprob without
+ * tokens, logits not aligned to their type, ws too small or not 256-byte
+ * aligned.
+ */
+lora_status lora_logprobs(const void *logits, int dtype, int64_t stride, int M, int V, const int32_t *tokens,
+                          float inv_temperature, int top_k, float *logprob, float *entropy, float *stats,
+                          int32_t *top_ids, float *top_logprobs, void *ws, size_t ws_bytes, lora_stream_t stream);
+
+/*
+ * The gradient of sum_i grad_logprob[i] * logprob[i] + grad_entropy[i] *
+ * entropy[i] with respect to the logits:
+ *   dlogits[i][v] = t (g (1[v = k] - p_v) - h p_v (log p_v + entropy[i])),
+ *   g = grad_logprob[i] (0 for a token outside [0, V)), h = grad_entropy[i].
+ *   stats    [M][2] of lora_logprobs on the same logits and inv_temperature
+ *   entropy  [M] of that call; NULL allowed when grad_entropy is NULL
+ *   grad_logprob, grad_entropy   device [M] f32, each or NULL (0); grad_logprob
+ *            needs tokens
+ *   dlogits  device, M rows of V elements of `dtype`, row i at dlogits +
+ *            i*d_stride; may be logits itself with the same stride
+ * A row with nothing but -infinity gets zeros, a masked element 0, a row whose
+ * stats are NaN gets NaN. fp32 arithmetic, rounded once.
+ * Errors: as lora_logprobs; NULL stats or dlogits; neither gradient given;
+ * d_stride < V.
+ */
+lora_status lora_logprobs_grad(const void *logits, int dtype, int64_t stride, int M, int V, const int32_t *tokens,
+                               float inv_temperature, const float *stats, const float *entropy,
+                               const float *grad_logprob, const float *grad_entropy, void *dlogits,
+                               int64_t d_stride, lora_stream_t stream);
 
 /* Read the status word (LORA_FLAG_* bits) of the most recent call that used
  * workspace `ws`. Synchronises `stream` (diagnostic, not a hot-path call).

@@ -47,6 +47,10 @@ LORA_STATIC_WS_BYTES = 8 << 20
 LORA_COMP_STRIDE = 256
 
 
+LORA_DTYPE_BF16 = 0
+LORA_DTYPE_F32 = 1
+LORA_MAX_TOP = 32
+
 LORA_PLAN_SIMT = 1
 LORA_PLAN_TC = 2
 LORA_PLAN_ONE_LAUNCH = 3
@@ -139,6 +143,9 @@ _SIGNATURES = {
     "lora_embed_pool_pack": (_i, [_rtp, _i, _vp, _vp, _i, _f, _i, _f, _vp]),
     "lora_embed_workspace_bytes": (_sz, [_i, _rtp]),
     "lora_embed_apply": (_i, [_vp, _vp, _i, _i, _i, _vp, _rtp, _vp, _i64, _vp, _sz, _vp]),
+    "lora_logprobs_workspace_bytes": (_sz, [_i, _i, _i]),
+    "lora_logprobs": (_i, [_vp, _i, _i64, _i, _i, _vp, _f, _i, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "lora_logprobs_grad": (_i, [_vp, _i, _i64, _i, _i, _vp, _f, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
     "lora_status_get": (_i, [_vp, ctypes.POINTER(ctypes.c_uint32), _vp]),
     "lora_test_wait_hook": (None, [ctypes.c_uint64, _i]),
     "lora_proj_plan": (_i, [_i, _rtp, _i, _i, ctypes.POINTER(lora_plan_info)]),
@@ -364,6 +371,28 @@ def lora_moe_gather_apply(x, x_stride: int, W_e, indices, E: int, T: int, K: int
     _check(lib().lora_moe_gather_apply(_ptr(x), x_stride, wp, _ptr(indices), E, T, K, N, _ptr(seq_slot), arr,
                                        _ptr(combine), top_k, _ptr(y), y_stride, _ptr(ws), ws_bytes,
                                        _stream(stream)))
+
+
+def lora_logprobs_workspace_bytes(M: int, V: int, top_k: int) -> int:
+    return int(lib().lora_logprobs_workspace_bytes(M, V, top_k))
+
+
+def lora_logprobs(logits, dtype: int, stride: int, M: int, V: int, tokens, inv_temperature: float, top_k: int,
+                  logprob, entropy, stats, top_ids, top_logprobs, ws, ws_bytes: int, stream=None) -> None:
+    """Log probability of tokens[i], entropy, softmax statistics and the top_k
+    best elements of each row of logits (any output may be None)."""
+    _check(lib().lora_logprobs(_ptr(logits), dtype, stride, M, V, _ptr(tokens), inv_temperature, top_k,
+                               _ptr(logprob), _ptr(entropy), _ptr(stats), _ptr(top_ids), _ptr(top_logprobs),
+                               _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def lora_logprobs_grad(logits, dtype: int, stride: int, M: int, V: int, tokens, inv_temperature: float, stats,
+                       entropy, grad_logprob, grad_entropy, dlogits, d_stride: int, stream=None) -> None:
+    """The gradient of the log probabilities and entropies of lora_logprobs
+    with respect to the logits (either incoming gradient may be None)."""
+    _check(lib().lora_logprobs_grad(_ptr(logits), dtype, stride, M, V, _ptr(tokens), inv_temperature, _ptr(stats),
+                                    _ptr(entropy), _ptr(grad_logprob), _ptr(grad_entropy), _ptr(dlogits), d_stride,
+                                    _stream(stream)))
 
 
 def lora_status_get(ws, stream=None) -> int:

@@ -12,6 +12,7 @@
 #include <cudaTypedefs.h>
 
 #include "lora_internal.cuh"
+#include "lora_logprob.cuh"
 
 using namespace rd;
 
@@ -1386,6 +1387,136 @@ lora_status lora_moe_gather_apply(const void *x, int64_t x_stride, const void *c
     if (s != LORA_OK)
         return s;
     e = launch_gather_combine(g, di.num_sms, st);
+    if (e != cudaSuccess)
+        return cuda_fail(e, who);
+    return ok();
+}
+
+} // extern "C"
+
+namespace {
+
+// Rows of logits as lora_logprobs and lora_logprobs_grad take them.
+lora_status check_logits(const char *who, const void *logits, int dtype, int64_t stride, int M, int V, float inv_t)
+{
+    if (dtype != LORA_DTYPE_BF16 && dtype != LORA_DTYPE_F32)
+        return fail(LORA_ERR_RANGE, "%s: dtype %d is not one of LORA_DTYPE_*", who, dtype);
+    if (M < 0 || V < 1)
+        return fail(LORA_ERR_SHAPE, "%s: need M %d >= 0 and V %d >= 1", who, M, V);
+    if (stride < V)
+        return fail(LORA_ERR_SHAPE, "%s: stride %lld must be >= V %d", who, (long long)stride, V);
+    if (!(inv_t > 0.0f) || !std::isfinite(inv_t))
+        return fail(LORA_ERR_RANGE, "%s: inv_temperature %g must be positive and finite", who, (double)inv_t);
+    if (V > (1 << 30) || (int64_t)M * (V / 4096 + 8) > 0x7fffffff)
+        return fail(LORA_ERR_UNSUPPORTED, "%s: M %d rows of V %d elements are more than one launch takes", who, M, V);
+    if (M > 0 && logits == nullptr)
+        return fail(LORA_ERR_NULL, "%s: logits is NULL", who);
+    if (reinterpret_cast<uintptr_t>(logits) % (dtype == LORA_DTYPE_F32 ? 4 : 2) != 0)
+        return fail(LORA_ERR_ALIGN, "%s: logits must be aligned to their type", who);
+    return LORA_OK;
+}
+
+} // namespace
+
+extern "C" {
+
+size_t lora_logprobs_workspace_bytes(int M, int V, int top_k)
+{
+    (void)M;
+    (void)V;
+    (void)top_k;
+    return 256;
+}
+
+lora_status lora_logprobs(const void *logits, int dtype, int64_t stride, int M, int V, const int32_t *tokens,
+                          float inv_temperature, int top_k, float *logprob, float *entropy, float *stats,
+                          int32_t *top_ids, float *top_logprobs, void *ws, size_t ws_bytes, lora_stream_t stream)
+{
+    const char *who = "lora_logprobs";
+    lora_status s = check_logits(who, logits, dtype, stride, M, V, inv_temperature);
+    if (s != LORA_OK)
+        return s;
+    if (top_k < 0 || top_k > LORA_MAX_TOP || top_k > V)
+        return fail(LORA_ERR_RANGE, "%s: top_k %d must be in [0, %d] for V %d", who, top_k,
+                    V < LORA_MAX_TOP ? V : LORA_MAX_TOP, V);
+    if (M == 0)
+        return ok();
+    if (top_k > 0 && (top_ids == nullptr || top_logprobs == nullptr))
+        return fail(LORA_ERR_NULL, "%s: top_ids and top_logprobs must be non-NULL for top_k %d", who, top_k);
+    if (logprob != nullptr && tokens == nullptr)
+        return fail(LORA_ERR_NULL, "%s: logprob needs tokens", who);
+    if (ws == nullptr)
+        return fail(LORA_ERR_NULL, "%s: workspace is NULL", who);
+    if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+        return fail(LORA_ERR_ALIGN, "%s: workspace must be 256-byte aligned", who);
+    const size_t need = lora_logprobs_workspace_bytes(M, V, top_k);
+    if (ws_bytes < need)
+        return fail(LORA_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", who, ws_bytes, need);
+    DevInfo di;
+    if (!device_info(di))
+        return fail(LORA_ERR_CUDA, "%s: no CUDA device", who);
+    LogprobParams p;
+    memset(&p, 0, sizeof p);
+    p.logits = logits;
+    p.stride = stride;
+    p.M = M;
+    p.V = V;
+    p.tokens = tokens;
+    p.inv_t = inv_temperature;
+    p.top_k = top_k;
+    p.logprob = logprob;
+    p.entropy = entropy;
+    p.stats = stats;
+    p.top_ids = top_ids;
+    p.top_logprobs = top_logprobs;
+    p.status = static_cast<uint32_t *>(ws);
+    cudaError_t e = launch_logprob(p, dtype, di.num_sms, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return cuda_fail(e, who);
+    return ok();
+}
+
+lora_status lora_logprobs_grad(const void *logits, int dtype, int64_t stride, int M, int V, const int32_t *tokens,
+                               float inv_temperature, const float *stats, const float *entropy,
+                               const float *grad_logprob, const float *grad_entropy, void *dlogits,
+                               int64_t d_stride, lora_stream_t stream)
+{
+    const char *who = "lora_logprobs_grad";
+    lora_status s = check_logits(who, logits, dtype, stride, M, V, inv_temperature);
+    if (s != LORA_OK)
+        return s;
+    if (d_stride < V)
+        return fail(LORA_ERR_SHAPE, "%s: d_stride %lld must be >= V %d", who, (long long)d_stride, V);
+    if (M == 0)
+        return ok();
+    if (stats == nullptr || dlogits == nullptr)
+        return fail(LORA_ERR_NULL, "%s: stats and dlogits must be non-NULL", who);
+    if (grad_logprob == nullptr && grad_entropy == nullptr)
+        return fail(LORA_ERR_NULL, "%s: neither grad_logprob nor grad_entropy is given", who);
+    if (grad_logprob != nullptr && tokens == nullptr)
+        return fail(LORA_ERR_NULL, "%s: grad_logprob needs tokens", who);
+    if (grad_entropy != nullptr && entropy == nullptr)
+        return fail(LORA_ERR_NULL, "%s: grad_entropy needs entropy", who);
+    if (reinterpret_cast<uintptr_t>(dlogits) % (dtype == LORA_DTYPE_F32 ? 4 : 2) != 0)
+        return fail(LORA_ERR_ALIGN, "%s: dlogits must be aligned to its type", who);
+    if (dlogits == logits && d_stride != stride)
+        return fail(LORA_ERR_SHAPE, "%s: dlogits over logits needs the same stride (%lld, %lld)", who,
+                    (long long)d_stride, (long long)stride);
+    LogprobGradParams p;
+    memset(&p, 0, sizeof p);
+    p.logits = logits;
+    p.stride = stride;
+    p.M = M;
+    p.V = V;
+    p.tokens = tokens;
+    p.inv_t = inv_temperature;
+    p.stats = stats;
+    p.entropy = entropy;
+    p.g_logprob = grad_logprob;
+    p.g_entropy = grad_entropy;
+    p.dlogits = dlogits;
+    p.d_stride = d_stride;
+    cudaError_t e = launch_logprob_grad(p, dtype, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return cuda_fail(e, who);
     return ok();
