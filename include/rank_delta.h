@@ -526,18 +526,87 @@ lora_status lora_moe_gather_apply(const void *x, int64_t x_stride, const void *c
                                   int top_k, void *y, int64_t y_stride, void *ws, size_t ws_bytes,
                                   lora_stream_t stream);
 
+/* Element types of the calls that take one. */
+enum {
+    LORA_DTYPE_BF16 = 0,
+    LORA_DTYPE_F32 = 1
+};
+
+/*
+ * ------------------------------------------------------------------------
+ * A base weight in microscaled 4-bit floating point, adapters in bf16 on top
+ * (no counterpart on the pages).
+ * ------------------------------------------------------------------------
+ *
+ * A matrix [rows][K], K a multiple of LORA_MX4_BLOCK, is held as
+ *   codes   [rows][K / 2] bytes, 16-byte aligned: two 4-bit codes a byte, the
+ *           even k in the low half. A code is sign, two exponent bits, one
+ *           mantissa bit: +-0, 0.5, 1, 1.5, 2, 3, 4, 6
+ *   scales  [rows][K / 32] bytes b: the 32 values of a block are
+ *           code * 2^(b - 127); b = 255 makes the block NaN
+ */
+#define LORA_MX4_BLOCK 32
+
+/* Bytes of the codes and of the scales (0 for sizes that do not fit the form). */
+size_t lora_mx4_code_bytes(int64_t rows, int K);
+size_t lora_mx4_scale_bytes(int64_t rows, int K);
+
+/*
+ * Quantise w: b = max(0, floor(log2 max |w|) - 2 + 127) over the block (0 for a
+ * block of zeros, 255 with codes 0 for one that holds a NaN or an infinity),
+ * and each w / 2^(b - 127) to the nearest code, ties to the even one, beyond 6
+ * to 6.
+ *   w   device, rows of K elements of `dtype` (LORA_DTYPE_*), row i at
+ *       w + i*w_stride (elements; any stride >= K, aligned to its type)
+ * Enqueued on `stream` only. rows = 0 is a no-op. Errors: an unknown dtype,
+ * rows < 0, K < 32 or not a multiple of 32, w_stride < K, NULL pointers, codes
+ * not 16-byte aligned, w not aligned to its type.
+ */
+lora_status lora_mx4_quantize(const void *w, int dtype, int64_t w_stride, int64_t rows, int K, uint8_t *codes,
+                              uint8_t *scales, lora_stream_t stream);
+
+/* The values back: w[i][k] = code * 2^(b - 127), rounded to `dtype` (exact for
+ * both types except where 2^(b - 127) takes the value out of their range).
+ * Arguments and errors as lora_mx4_quantize. */
+lora_status lora_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int K, void *w, int dtype,
+                                int64_t w_stride, lora_stream_t stream);
+
+/* Path of lora_mx4_proj_apply_ex (lora_mx4_proj_apply uses LORA_MX4_PATH_AUTO). */
+enum {
+    LORA_MX4_PATH_AUTO = 0,   /* by row count */
+    LORA_MX4_PATH_STREAM = 1, /* codes to the tensor cores' registers: few rows */
+    LORA_MX4_PATH_EXPAND = 2  /* the weight widened to bf16 in the workspace, then lora_proj_apply: many rows */
+};
+
+/* Workspace of lora_mx4_proj_apply for M rows on route `rt`: the routing sort,
+ * h, the status word, and for many rows the weight in bf16 (2 n_out n_in
+ * bytes). 0 if rt is NULL, not initialised or not a projection route. */
+size_t lora_mx4_proj_workspace_bytes(int M, const lora_route *rt);
+size_t lora_mx4_proj_workspace_bytes_ex(int M, const lora_route *rt, int path);
+
+/*
+ * y[i, :] = dq(W) x_i + s * B_s (A_s x_i), s = seq_slot[i]: lora_proj_apply with
+ * the base [N][K] as codes and scales. The codes are widened to bf16 exactly;
+ * x, the adapters and y are bf16, accumulation is fp32, y is rounded once.
+ * Every row rule, the status word (lora_status_get(ws)) and the errors are
+ * those of lora_proj_apply; besides, K must be a multiple of 32, and codes and
+ * scales non-NULL, codes 16-byte aligned. y rows may have any stride >= N.
+ */
+lora_status lora_mx4_proj_apply(const void *x, int64_t x_stride, const uint8_t *codes, const uint8_t *scales, int M,
+                                int K, int N, const int32_t *seq_slot, const lora_route *rt, void *y,
+                                int64_t y_stride, void *ws, size_t ws_bytes, lora_stream_t stream);
+/* The same on an explicit path (LORA_MX4_PATH_*); paths agree within the
+ * fp32 accumulation-order tolerance, not bit for bit. */
+lora_status lora_mx4_proj_apply_ex(const void *x, int64_t x_stride, const uint8_t *codes, const uint8_t *scales, int M,
+                                   int K, int N, const int32_t *seq_slot, const lora_route *rt, void *y,
+                                   int64_t y_stride, void *ws, size_t ws_bytes, int path, lora_stream_t stream);
+
 /*
  * ------------------------------------------------------------------------
  * What a server answers with: log probabilities of given tokens, entropy, the
  * best alternatives, and their gradient (no counterpart on the pages).
  * ------------------------------------------------------------------------
  */
-
-/* Element types of the calls that take one. */
-enum {
-    LORA_DTYPE_BF16 = 0,
-    LORA_DTYPE_F32 = 1
-};
 
 /* Largest top_k of lora_logprobs. */
 #define LORA_MAX_TOP 32

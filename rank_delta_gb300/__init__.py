@@ -50,6 +50,11 @@ LORA_COMP_STRIDE = 256
 LORA_DTYPE_BF16 = 0
 LORA_DTYPE_F32 = 1
 LORA_MAX_TOP = 32
+LORA_MX4_BLOCK = 32
+
+LORA_MX4_PATH_AUTO = 0
+LORA_MX4_PATH_STREAM = 1
+LORA_MX4_PATH_EXPAND = 2
 
 LORA_PLAN_SIMT = 1
 LORA_PLAN_TC = 2
@@ -143,6 +148,14 @@ _SIGNATURES = {
     "lora_embed_pool_pack": (_i, [_rtp, _i, _vp, _vp, _i, _f, _i, _f, _vp]),
     "lora_embed_workspace_bytes": (_sz, [_i, _rtp]),
     "lora_embed_apply": (_i, [_vp, _vp, _i, _i, _i, _vp, _rtp, _vp, _i64, _vp, _sz, _vp]),
+    "lora_mx4_code_bytes": (_sz, [_i64, _i]),
+    "lora_mx4_scale_bytes": (_sz, [_i64, _i]),
+    "lora_mx4_quantize": (_i, [_vp, _i, _i64, _i64, _i, _vp, _vp, _vp]),
+    "lora_mx4_dequantize": (_i, [_vp, _vp, _i64, _i, _vp, _i, _i64, _vp]),
+    "lora_mx4_proj_workspace_bytes": (_sz, [_i, _rtp]),
+    "lora_mx4_proj_workspace_bytes_ex": (_sz, [_i, _rtp, _i]),
+    "lora_mx4_proj_apply": (_i, [_vp, _i64, _vp, _vp, _i, _i, _i, _vp, _rtp, _vp, _i64, _vp, _sz, _vp]),
+    "lora_mx4_proj_apply_ex": (_i, [_vp, _i64, _vp, _vp, _i, _i, _i, _vp, _rtp, _vp, _i64, _vp, _sz, _i, _vp]),
     "lora_logprobs_workspace_bytes": (_sz, [_i, _i, _i]),
     "lora_logprobs": (_i, [_vp, _i, _i64, _i, _i, _vp, _f, _i, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "lora_logprobs_grad": (_i, [_vp, _i, _i64, _i, _i, _vp, _f, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
@@ -371,6 +384,42 @@ def lora_moe_gather_apply(x, x_stride: int, W_e, indices, E: int, T: int, K: int
     _check(lib().lora_moe_gather_apply(_ptr(x), x_stride, wp, _ptr(indices), E, T, K, N, _ptr(seq_slot), arr,
                                        _ptr(combine), top_k, _ptr(y), y_stride, _ptr(ws), ws_bytes,
                                        _stream(stream)))
+
+
+def lora_mx4_code_bytes(rows: int, K: int) -> int:
+    return int(lib().lora_mx4_code_bytes(rows, K))
+
+
+def lora_mx4_scale_bytes(rows: int, K: int) -> int:
+    return int(lib().lora_mx4_scale_bytes(rows, K))
+
+
+def lora_mx4_quantize(w, dtype: int, w_stride: int, rows: int, K: int, codes, scales, stream=None) -> None:
+    """w [rows][K] to 4-bit codes [rows][K/2] and scale bytes [rows][K/32]."""
+    _check(lib().lora_mx4_quantize(_ptr(w), dtype, w_stride, rows, K, _ptr(codes), _ptr(scales), _stream(stream)))
+
+
+def lora_mx4_dequantize(codes, scales, rows: int, K: int, w, dtype: int, w_stride: int, stream=None) -> None:
+    _check(lib().lora_mx4_dequantize(_ptr(codes), _ptr(scales), rows, K, _ptr(w), dtype, w_stride, _stream(stream)))
+
+
+def lora_mx4_proj_workspace_bytes(M: int, rt: lora_route, path: int = LORA_MX4_PATH_AUTO) -> int:
+    if path == LORA_MX4_PATH_AUTO:
+        return int(lib().lora_mx4_proj_workspace_bytes(M, ctypes.byref(rt)))
+    return int(lib().lora_mx4_proj_workspace_bytes_ex(M, ctypes.byref(rt), path))
+
+
+def lora_mx4_proj_apply(x, x_stride: int, codes, scales, M: int, K: int, N: int, seq_slot, rt: lora_route, y,
+                        y_stride: int, ws, ws_bytes: int, stream=None, path: int = LORA_MX4_PATH_AUTO) -> None:
+    """lora_proj_apply with the base [N][K] as 4-bit codes and scales."""
+    if path == LORA_MX4_PATH_AUTO:
+        code = lib().lora_mx4_proj_apply(_ptr(x), x_stride, _ptr(codes), _ptr(scales), M, K, N, _ptr(seq_slot),
+                                         ctypes.byref(rt), _ptr(y), y_stride, _ptr(ws), ws_bytes, _stream(stream))
+    else:
+        code = lib().lora_mx4_proj_apply_ex(_ptr(x), x_stride, _ptr(codes), _ptr(scales), M, K, N, _ptr(seq_slot),
+                                            ctypes.byref(rt), _ptr(y), y_stride, _ptr(ws), ws_bytes, path,
+                                            _stream(stream))
+    _check(code)
 
 
 def lora_logprobs_workspace_bytes(M: int, V: int, top_k: int) -> int:

@@ -13,6 +13,7 @@
 
 #include "lora_internal.cuh"
 #include "lora_logprob.cuh"
+#include "lora_mx4.cuh"
 
 using namespace rd;
 
@@ -21,6 +22,7 @@ namespace {
 constexpr uint64_t ROUTE_MAGIC = 0x6c6f72615f727431ull; // "lora_rt1"
 constexpr int MAX_LORAS = MAX_BUCKETS - 1;
 constexpr int MAX_RANK = 256;
+constexpr int MX4_STREAM_MAX_ROWS = 64; // LORA_MX4_PATH_AUTO: at most this many rows read the codes directly
 constexpr int SIMT_MAX_ROWS = 16; // LORA_PATH_AUTO: at most this many rows per segment -> GEMV
 
 thread_local std::string g_err;
@@ -1388,6 +1390,197 @@ lora_status lora_moe_gather_apply(const void *x, int64_t x_stride, const void *c
         return s;
     e = launch_gather_combine(g, di.num_sms, st);
     if (e != cudaSuccess)
+        return cuda_fail(e, who);
+    return ok();
+}
+
+} // extern "C"
+
+namespace {
+
+lora_status check_mx4(const char *who, const void *w, int dtype, int64_t w_stride, int64_t rows, int K, const void *codes,
+                      const void *scales)
+{
+    if (dtype != LORA_DTYPE_BF16 && dtype != LORA_DTYPE_F32)
+        return fail(LORA_ERR_RANGE, "%s: dtype %d is not one of LORA_DTYPE_*", who, dtype);
+    if (rows < 0 || K < LORA_MX4_BLOCK || K % LORA_MX4_BLOCK != 0)
+        return fail(LORA_ERR_SHAPE, "%s: need rows %lld >= 0 and K %d a positive multiple of %d", who, (long long)rows, K,
+                    LORA_MX4_BLOCK);
+    if (w_stride < K)
+        return fail(LORA_ERR_SHAPE, "%s: w_stride %lld must be >= K %d", who, (long long)w_stride, K);
+    if (rows > 0 && (w == nullptr || codes == nullptr || scales == nullptr))
+        return fail(LORA_ERR_NULL, "%s: w, codes and scales must be non-NULL", who);
+    if (!aligned16(codes))
+        return fail(LORA_ERR_ALIGN, "%s: codes must be 16-byte aligned", who);
+    if (reinterpret_cast<uintptr_t>(w) % (dtype == LORA_DTYPE_F32 ? 4 : 2) != 0)
+        return fail(LORA_ERR_ALIGN, "%s: w must be aligned to its type", who);
+    return LORA_OK;
+}
+
+// The path a call of M rows takes.
+int mx4_path(int M, int path)
+{
+    if (path != LORA_MX4_PATH_AUTO)
+        return path;
+    return M <= MX4_STREAM_MAX_ROWS ? LORA_MX4_PATH_STREAM : LORA_MX4_PATH_EXPAND;
+}
+
+} // namespace
+
+extern "C" {
+
+size_t lora_mx4_code_bytes(int64_t rows, int K)
+{
+    return rows > 0 && K > 0 && K % LORA_MX4_BLOCK == 0 ? (size_t)rows * (size_t)(K / 2) : 0;
+}
+
+size_t lora_mx4_scale_bytes(int64_t rows, int K)
+{
+    return rows > 0 && K > 0 && K % LORA_MX4_BLOCK == 0 ? (size_t)rows * (size_t)(K / LORA_MX4_BLOCK) : 0;
+}
+
+lora_status lora_mx4_quantize(const void *w, int dtype, int64_t w_stride, int64_t rows, int K, uint8_t *codes,
+                              uint8_t *scales, lora_stream_t stream)
+{
+    const char *who = "lora_mx4_quantize";
+    lora_status s = check_mx4(who, w, dtype, w_stride, rows, K, codes, scales);
+    if (s != LORA_OK)
+        return s;
+    if (rows == 0)
+        return ok();
+    DevInfo di;
+    if (!device_info(di))
+        return fail(LORA_ERR_CUDA, "%s: no CUDA device", who);
+    const Mx4QuantParams p{w, w_stride, rows, K, codes, scales};
+    cudaError_t e = launch_mx4_quantize(p, dtype, di.num_sms, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return cuda_fail(e, who);
+    return ok();
+}
+
+lora_status lora_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int K, void *w, int dtype,
+                                int64_t w_stride, lora_stream_t stream)
+{
+    const char *who = "lora_mx4_dequantize";
+    lora_status s = check_mx4(who, w, dtype, w_stride, rows, K, codes, scales);
+    if (s != LORA_OK)
+        return s;
+    if (rows == 0)
+        return ok();
+    DevInfo di;
+    if (!device_info(di))
+        return fail(LORA_ERR_CUDA, "%s: no CUDA device", who);
+    const Mx4DequantParams p{codes, scales, rows, K, w, w_stride};
+    cudaError_t e = launch_mx4_dequantize(p, dtype, di.num_sms, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return cuda_fail(e, who);
+    return ok();
+}
+
+size_t lora_mx4_proj_workspace_bytes_ex(int M, const lora_route *rt, int path)
+{
+    if (rt == nullptr || rt->magic != ROUTE_MAGIC || rt->kind != LORA_ROUTE_PROJ || M < 0)
+        return 0;
+    if (mx4_path(M, path) == LORA_MX4_PATH_EXPAND) // the projection's, then the weight in bf16
+        return align256(lora_proj_workspace_bytes(M, rt)) + align256((size_t)rt->n_out * (size_t)rt->n_in * 2);
+    return ws_layout(M, rt->max_loras + 1, rt->max_rank, shrink_kparts(rt->n_in)).total;
+}
+
+size_t lora_mx4_proj_workspace_bytes(int M, const lora_route *rt)
+{
+    return lora_mx4_proj_workspace_bytes_ex(M, rt, LORA_MX4_PATH_AUTO);
+}
+
+lora_status lora_mx4_proj_apply(const void *x, int64_t x_stride, const uint8_t *codes, const uint8_t *scales, int M,
+                                int K, int N, const int32_t *seq_slot, const lora_route *rt, void *y,
+                                int64_t y_stride, void *ws, size_t ws_bytes, lora_stream_t stream)
+{
+    return lora_mx4_proj_apply_ex(x, x_stride, codes, scales, M, K, N, seq_slot, rt, y, y_stride, ws, ws_bytes,
+                                  LORA_MX4_PATH_AUTO, stream);
+}
+
+lora_status lora_mx4_proj_apply_ex(const void *x, int64_t x_stride, const uint8_t *codes, const uint8_t *scales, int M,
+                                   int K, int N, const int32_t *seq_slot, const lora_route *rt, void *y,
+                                   int64_t y_stride, void *ws, size_t ws_bytes, int path, lora_stream_t stream)
+{
+    const char *who = "lora_mx4_proj_apply";
+    lora_status s = check_route_kind(rt, LORA_ROUTE_PROJ, who);
+    if (s != LORA_OK)
+        return s;
+    if (M < 0)
+        return fail(LORA_ERR_SHAPE, "%s: M %d is negative", who, M);
+    if (path < LORA_MX4_PATH_AUTO || path > LORA_MX4_PATH_EXPAND)
+        return fail(LORA_ERR_RANGE, "%s: path %d is not one of LORA_MX4_PATH_*", who, path);
+    if (K != rt->n_in || N != rt->n_out)
+        return fail(LORA_ERR_SHAPE, "%s: x is [M %d][K %d] and W [N %d][K %d], but the route is [n_out %d x n_in %d]", who,
+                    M, K, N, K, rt->n_out, rt->n_in);
+    if (K % LORA_MX4_BLOCK != 0)
+        return fail(LORA_ERR_SHAPE, "%s: K %d must be a multiple of %d", who, K, LORA_MX4_BLOCK);
+    if (M == 0)
+        return ok();
+    if (codes == nullptr || scales == nullptr)
+        return fail(LORA_ERR_NULL, "%s: codes and scales must be non-NULL", who);
+    if (!aligned16(codes))
+        return fail(LORA_ERR_ALIGN, "%s: codes must be 16-byte aligned", who);
+    if ((s = check_io(who, x, x_stride, M, K, N, seq_slot, y, y_stride)) != LORA_OK)
+        return s;
+    path = mx4_path(M, path);
+    const size_t need = lora_mx4_proj_workspace_bytes_ex(M, rt, path);
+    if (ws == nullptr)
+        return fail(LORA_ERR_NULL, "%s: workspace is NULL", who);
+    if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+        return fail(LORA_ERR_ALIGN, "%s: workspace must be 256-byte aligned", who);
+    if (ws_bytes < need)
+        return fail(LORA_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu (%d rows, [%d x %d], max_rank %d)", who,
+                    ws_bytes, need, M, N, K, rt->max_rank);
+    DevInfo di;
+    if (!device_info(di))
+        return fail(LORA_ERR_CUDA, "%s: no CUDA device", who);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (path == LORA_MX4_PATH_EXPAND) {
+        const size_t proj = align256(lora_proj_workspace_bytes(M, rt));
+        uint8_t *W = static_cast<uint8_t *>(ws) + proj;
+        const Mx4DequantParams q{codes, scales, N, K, W, K};
+        if ((e = launch_mx4_dequantize(q, LORA_DTYPE_BF16, di.num_sms, st)) != cudaSuccess)
+            return cuda_fail(e, who);
+        return proj_apply(x, x_stride, W, M, K, N, seq_slot, rt, y, y_stride, ws, proj, LORA_PATH_AUTO, stream);
+    }
+    Params p; // routing and shrink, as the CUDA-core path of lora_proj_apply runs them
+    memset(&p, 0, sizeof p);
+    p.x = static_cast<const uint16_t *>(x);
+    p.x_stride = x_stride;
+    p.seq_slot = seq_slot;
+    p.E = 1;
+    p.rows = M;
+    p.K = K;
+    p.N = N;
+    p.L = rt->max_loras;
+    p.R = rt->max_rank;
+    p.tab[0] = tables_of(*rt);
+    p.kp = shrink_kparts(K);
+    if ((s = carve_ws(ws, ws_bytes, M, p.L + 1, p.R, p.kp, 0, 0, p.ws, who)) != LORA_OK)
+        return s;
+    if ((e = launch_prep(p, st)) != cudaSuccess || (e = launch_shrink(p, di.num_sms, st)) != cudaSuccess)
+        return cuda_fail(e, who);
+    Mx4ProjParams q;
+    memset(&q, 0, sizeof q);
+    q.x = p.x;
+    q.x_stride = x_stride;
+    q.codes = codes;
+    q.scales = scales;
+    q.M = M;
+    q.K = K;
+    q.N = N;
+    q.L = p.L;
+    q.R = p.R;
+    q.seq_slot = seq_slot;
+    q.tab = p.tab[0];
+    q.h = p.ws.h;
+    q.kp = p.kp;
+    q.y = static_cast<uint16_t *>(y);
+    q.y_stride = y_stride;
+    if ((e = launch_mx4_stream(q, di.num_sms, st)) != cudaSuccess)
         return cuda_fail(e, who);
     return ok();
 }

@@ -1,0 +1,85 @@
+// Microscaled 4-bit matrices (lora_mx4.cu): what the host ABI hands to the
+// kernels, and the conversions they share.
+//
+// A value is an E2M1 code (sign, two exponent bits, one mantissa bit: 0, 0.5,
+// 1, 1.5, 2, 3, 4, 6) times the power of two 2^(byte - 127) that 32
+// consecutive values of a row share. Byte 255 makes its block NaN.
+#pragma once
+#include "lora_internal.cuh"
+
+namespace rd {
+
+struct Mx4QuantParams {
+    const void *w; // rows of K, row stride in elements
+    int64_t w_stride;
+    int64_t rows;
+    int K;
+    uint8_t *codes;  // [rows][K / 2]
+    uint8_t *scales; // [rows][K / 32]
+};
+
+struct Mx4DequantParams {
+    const uint8_t *codes, *scales;
+    int64_t rows;
+    int K;
+    void *w;
+    int64_t w_stride;
+};
+
+struct Mx4ProjParams {
+    const uint16_t *x;
+    int64_t x_stride;
+    const uint8_t *codes, *scales;
+    int M, K, N, L, R;
+    const int32_t *seq_slot;
+    Tables tab;
+    const float *h; // [kp][M][R] of the shrink
+    int kp;
+    uint16_t *y;
+    int64_t y_stride;
+};
+
+cudaError_t launch_mx4_quantize(const Mx4QuantParams &p, int dtype, int num_sms, cudaStream_t st);
+cudaError_t launch_mx4_dequantize(const Mx4DequantParams &p, int dtype, int num_sms, cudaStream_t st);
+cudaError_t launch_mx4_stream(const Mx4ProjParams &p, int num_sms, cudaStream_t st);
+
+// The bf16 factors that turn an E2M1 value held with its exponent field as in
+// fp16 (that is, value * 2^-112) into value * 2^(byte - 127). The second is 1
+// unless the first would leave bf16's range (byte > 142).
+__device__ __forceinline__ void mx4_factors(uint32_t byte, uint32_t &f1, uint32_t &f2)
+{
+    const uint32_t e = byte + 112u;
+    const uint32_t a = e < 254u ? e : 254u;
+    f1 = a << 7;
+    f2 = (127u + e - a) << 7;
+    if (byte == 255u)
+        f1 = 0x7FC0u;
+    f1 |= f1 << 16;
+    f2 |= f2 << 16;
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Eight codes (the lowest four bits first) as bf16 pairs, unscaled: each value
+// times 2^-112 (fp16's five exponent bits moved under bf16's eight).
+__device__ __forceinline__ void mx4_unpack8(uint32_t w, uint32_t (&o)[4])
+{
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+        : "r"(w));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        o[i] = ((o[i] >> 3) & 0x0FFF0FFFu) | (o[i] & 0x80008000u);
+}
+
+} // namespace rd

@@ -67,3 +67,64 @@ def test_logprobs_grad_refusals():
     expect(rd.LORA_ERR_ALIGN, call(d=8194))
     expect(rd.LORA_ERR_RANGE, call(inv_t=0.0))
     call(M=0)()
+
+
+def test_mx4_sizes_and_refusals():
+    assert rd.lora_mx4_code_bytes(10, 64) == 320 and rd.lora_mx4_scale_bytes(10, 64) == 20
+    assert rd.lora_mx4_code_bytes(10, 65) == 0 and rd.lora_mx4_scale_bytes(0, 64) == 0
+    assert rd.lora_mx4_code_bytes(1 << 32, 64) == 32 << 32
+    good = dict(w=4096, dtype=rd.LORA_DTYPE_BF16, stride=64, rows=4, K=64, codes=512, scales=77)
+
+    def quant(**kw):
+        a = dict(good, **kw)
+        return lambda: rd.lora_mx4_quantize(a["w"], a["dtype"], a["stride"], a["rows"], a["K"], a["codes"], a["scales"])
+
+    def back(**kw):
+        a = dict(good, **kw)
+        return lambda: rd.lora_mx4_dequantize(a["codes"], a["scales"], a["rows"], a["K"], a["w"], a["dtype"], a["stride"])
+
+    for call in (quant, back):
+        expect(rd.LORA_ERR_RANGE, call(dtype=3), contains=("dtype 3",))
+        expect(rd.LORA_ERR_SHAPE, call(rows=-1))
+        for K in (0, 16, 40):
+            expect(rd.LORA_ERR_SHAPE, call(K=K), contains=(f"K {K}", "32"))
+        expect(rd.LORA_ERR_SHAPE, call(stride=63), contains=("w_stride 63",))
+        for name in ("w", "codes", "scales"):
+            expect(rd.LORA_ERR_NULL, call(**{name: 0}))
+        expect(rd.LORA_ERR_ALIGN, call(codes=520))
+        expect(rd.LORA_ERR_ALIGN, call(w=4097))
+        expect(rd.LORA_ERR_ALIGN, call(w=4098, dtype=rd.LORA_DTYPE_F32))
+        call(rows=0, w=0, codes=0, scales=0)()
+
+
+def test_mx4_projection_refusals():
+    from tests.test_abi_cpu import fake_route
+    rt = fake_route(L=4, R=8, K=256, N=256)
+    need = rd.lora_mx4_proj_workspace_bytes(8, rt)
+    assert need > 0
+    many = rd.lora_mx4_proj_workspace_bytes(8, rt, rd.LORA_MX4_PATH_EXPAND)
+    assert many >= rd.lora_proj_workspace_bytes(8, rt) + 256 * 256 * 2
+    assert rd.lora_mx4_proj_workspace_bytes(8, fake_route(kind=rd.LORA_ROUTE_EMBED)) == 0
+    good = dict(x=4096, xs=256, codes=8192, scales=513, M=8, K=256, N=256, slots=4096, rt=rt, y=4096, ys=256, ws=1 << 20,
+                n=need, path=0)
+
+    def call(**kw):
+        a = dict(good, **kw)
+        return lambda: rd.lora_mx4_proj_apply(a["x"], a["xs"], a["codes"], a["scales"], a["M"], a["K"], a["N"], a["slots"],
+                                              a["rt"], a["y"], a["ys"], a["ws"], a["n"], None, a["path"])
+
+    expect(rd.LORA_ERR_NOT_INIT, call(rt=rd.lora_route()))
+    expect(rd.LORA_ERR_UNSUPPORTED, call(rt=fake_route(kind=rd.LORA_ROUTE_EMBED)))
+    expect(rd.LORA_ERR_SHAPE, call(M=-1))
+    expect(rd.LORA_ERR_RANGE, call(path=9), contains=("path 9",))
+    expect(rd.LORA_ERR_SHAPE, call(K=512), contains=("K 512", "n_in 256"))
+    expect(rd.LORA_ERR_SHAPE, call(rt=fake_route(K=264), K=264, xs=264), contains=("K 264", "32"))
+    for name in ("codes", "scales", "x", "slots", "y", "ws"):
+        expect(rd.LORA_ERR_NULL, call(**{name: 0}))
+    expect(rd.LORA_ERR_ALIGN, call(codes=8200))
+    expect(rd.LORA_ERR_ALIGN, call(x=4098))
+    expect(rd.LORA_ERR_ALIGN, call(xs=260))
+    expect(rd.LORA_ERR_SHAPE, call(ys=255))
+    expect(rd.LORA_ERR_ALIGN, call(ws=(1 << 20) + 16))
+    expect(rd.LORA_ERR_WORKSPACE, call(n=need - 1), contains=(str(need), str(need - 1)))
+    call(M=0, x=0, codes=0, ws=0, n=0)()
