@@ -7,17 +7,19 @@
 //
 // logprob_kernel reads a row once: every thread keeps a running maximum with
 // S and sum e^d d relative to it and rescales both when a group of its
-// elements raises the maximum (rare after the first group). Differences are
-// taken before the scaling by t (a row of the type's lowest values is a
-// uniform row, and nothing overflows but what is masked), sums are fp32, e^d
-// is the hardware's 2^x (about 2^-22 relative).
+// elements raises the maximum (rare after the first group). Sums are fp32, e^d
+// is the hardware's 2^x (about 2^-22 relative). While one group is summed the
+// next one, or the next row's first, is on its way: the kernel is bound by HBM
+// as long as its loads never stop.
 //
 // The best alternatives cost the pass nothing but the maximum it needs anyway:
 // of the threads' own best elements the k-th largest is a lower bound of the
-// row's k-th best, so only the (exactly k) threads whose best reaches it can
+// row's k-th best, so only the (at most k) threads whose best reaches it can
 // hold any of the k, and their shares, V / threads elements each, are read
 // again from L2. Elements are compared by (value, lowest index first) packed
-// into 64 bits, which orders them totally; -0 equals +0.
+// into 64 bits, which orders them totally; -0 equals +0. Sorted lists of the
+// warps are merged by counting: a key's place is its place in its own list
+// plus, by binary search, how many of each other list precede it.
 //
 // A row is split over a cluster of up to 8 CTAs when there are too few rows to
 // fill the SMs; the parts are joined through distributed shared memory in
@@ -110,6 +112,17 @@ template <> struct Vec<uint16_t> {
         return make_uint4(pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7]));
     }
     static __device__ __forceinline__ uint16_t narrow(float v) { return f32_to_bf16_bits(v); }
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
+    {
+        uint32_t r;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ float largest(const uint4 &q)
+    {
+        const uint32_t m = max2(max2(q.x, q.y), max2(q.z, q.w));
+        return max_nan(bf_lo(m), bf_hi(m));
+    }
 };
 template <> struct Vec<float> {
     static constexpr int E = 4;
@@ -124,6 +137,11 @@ template <> struct Vec<float> {
         return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
     }
     static __device__ __forceinline__ float narrow(float v) { return v; }
+    static __device__ __forceinline__ float largest(const uint4 &q)
+    {
+        return max_nan(max_nan(__uint_as_float(q.x), __uint_as_float(q.y)),
+                       max_nan(__uint_as_float(q.z), __uint_as_float(q.w)));
+    }
 };
 
 // Elements of a row's first 16-byte vector that lie before the row.
@@ -132,19 +150,30 @@ template <typename T> __device__ __forceinline__ int row_lead(const T *row)
     return (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
 }
 
-// Vector c of a row (elements [c E - lead, c E - lead + E)); elements outside
-// the row are -infinity and not read.
-template <typename T> __device__ __forceinline__ void load_vec(const T *row, int V, int lead, int c, float (&f)[Vec<T>::E])
+// Vector c of a row (elements [c E - lead, c E - lead + E)), read past L1;
+// elements outside the row are -infinity and not read.
+template <typename T> __device__ __forceinline__ uint4 load_vec(const T *row, int V, int lead, int c)
 {
     constexpr int E = Vec<T>::E;
     const int i0 = c * E - lead;
     if (i0 >= 0 && i0 + E <= V) {
-        Vec<T>::unpack(__ldg(reinterpret_cast<const uint4 *>(row + i0)), f);
-    } else {
-#pragma unroll
-        for (int q = 0; q < E; ++q)
-            f[q] = i0 + q >= 0 && i0 + q < V ? Vec<T>::widen(row[i0 + q]) : neg_inf();
+        uint4 q;
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                     : "l"(row + i0));
+        return q;
     }
+    float f[E];
+#pragma unroll
+    for (int q = 0; q < E; ++q)
+        f[q] = i0 + q >= 0 && i0 + q < V ? Vec<T>::widen(row[i0 + q]) : neg_inf();
+    return Vec<T>::pack(f); // exact: the values came from T
+}
+
+template <typename T> __device__ __forceinline__ uint4 empty_vec()
+{
+    const uint32_t w = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+    return make_uint4(w, w, w, w);
 }
 
 // (value, index) as one number: larger value first, then the lower index. 0
@@ -162,14 +191,6 @@ __device__ __forceinline__ float key_value(unsigned long long c)
 }
 __device__ __forceinline__ int key_index(unsigned long long c) { return (int)(0xFFFFFFFFu - (uint32_t)c); }
 
-__device__ __forceinline__ unsigned long long warp_max_key(unsigned long long c)
-{
-    const uint32_t hi = (uint32_t)(c >> 32);
-    const uint32_t mh = __reduce_max_sync(0xffffffffu, hi);
-    const uint32_t ml = __reduce_max_sync(0xffffffffu, hi == mh ? (uint32_t)c : 0u);
-    return (unsigned long long)mh << 32 | ml;
-}
-
 // The lanes' keys in descending order.
 __device__ __forceinline__ unsigned long long warp_sort_desc(unsigned long long c, int lane)
 {
@@ -184,68 +205,210 @@ __device__ __forceinline__ unsigned long long warp_sort_desc(unsigned long long 
     return c;
 }
 
-// The running statistics of part of a row: maximum, sum of 2^a and sum of
-// 2^a a with a = (x - maximum) t log2 e.
+// Statistics of part of a row: maximum, sum of 2^a and sum of 2^a a with
+// a = (x - maximum) t log2 e.
 struct Stat {
     float m, s, u;
 };
 
-__device__ __forceinline__ Stat join(Stat a, Stat b, float c)
+// Factor and shift of a part with maximum m in a whole with maximum top.
+__device__ __forceinline__ void rescale(Stat &st, float top, float c)
 {
-    Stat r;
-    r.m = max_nan(a.m, b.m);
-    const float mm = r.m == neg_inf() ? 0.0f : r.m;
+    const float mm = top == neg_inf() ? 0.0f : top;
     // a part without elements (m = -inf) holds s = u = 0
-    const float da = a.m == neg_inf() ? 0.0f : max_nan((a.m - mm) * c, -1000.0f);
-    const float db = b.m == neg_inf() ? 0.0f : max_nan((b.m - mm) * c, -1000.0f);
-    const float fa = exp2_fast(da), fb = exp2_fast(db);
-    r.s = fa * a.s + fb * b.s;
-    r.u = fa * (a.u + da * a.s) + fb * (b.u + db * b.s);
-    return r;
+    const float d = st.m == neg_inf() ? 0.0f : max_nan((st.m - mm) * c, -1000.0f);
+    const float f = exp2_fast(d);
+    st.u = f * (st.u + d * st.s);
+    st.s *= f;
+    st.m = top;
 }
 
-struct LpShared {
-    Stat warp[LP_WARPS];
-    Stat cta;
-    unsigned long long lists[LP_WARPS][32];
-    unsigned long long fin[32]; // the CTA's best, descending
-    unsigned long long bound;
-    int picked[LP_THREADS];
-    int npicked;
-};
-
-// The k best of n <= 32 descending lists of 32 (0 = no element), by one warp:
-// lane l holds the head of list l. out(i, key) is called by every lane.
-template <typename At, typename Out>
-__device__ __forceinline__ void merge_lists(int n, int k, int lane, At at, Out out)
+__device__ __forceinline__ Stat join(Stat a, Stat b, float c)
 {
-    int pos = 0;
-    unsigned long long head = lane < n ? at(lane, 0) : 0ull;
-    for (int i = 0; i < k; ++i) {
-        const unsigned long long best = warp_max_key(head);
-        out(i, best);
-        if (best != 0ull && head == best) {
-            ++pos;
-            head = pos < 32 ? at(lane, pos) : 0ull;
+    const float top = max_nan(a.m, b.m);
+    rescale(a, top, c);
+    rescale(b, top, c);
+    return Stat{top, a.s + b.s, a.u + b.u};
+}
+
+__device__ __forceinline__ Stat warp_join(Stat st, float c)
+{
+    float top = st.m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+    rescale(st, top, c);
+    st.s = warp_sum(st.s);
+    st.u = warp_sum(st.u);
+    return st;
+}
+
+// What a thread has summed of its elements. For bf16 the difference to the
+// maximum and the scaling are one fused operation, a = x c - ref with ref =
+// fl(m c), and masked elements are raised, two at a time, to a value whose
+// power of two is 0 (so that 0 times their a is 0): that holds while m c is
+// small enough for ref's rounding to be put right afterwards to first order
+// and the raised value lies far enough below m. Other rows (and fp32, which
+// has half the elements a byte) take the difference first and clamp a.
+template <typename T> struct Sums {
+    float m, ref, c;
+    bool fused;
+    uint32_t low; // the raised value, twice
+    f2 s, u;
+
+    __device__ __forceinline__ void clear(float c_)
+    {
+        m = neg_inf();
+        ref = 0.0f;
+        c = c_;
+        fused = false;
+        low = 0u;
+        s = u = make_f2(0.0f, 0.0f);
+    }
+    // ref - m c, what the sums' origin is off by
+    __device__ __forceinline__ float origin() const { return fused ? fmaf(-m, c, ref) : 0.0f; }
+
+    __device__ __forceinline__ void raise(float top)
+    {
+        const float old = origin(), from = m;
+        m = top;
+        ref = m * c;
+        if (sizeof(T) == 2) {
+            const uint32_t b = f32_to_bf16_bits(m - 400.0f / c);
+            const float raised = __uint_as_float(b << 16);
+            low = b | b << 16;
+            fused = fabsf(ref) <= 4096.0f && (raised - m) * c <= -150.0f && raised > neg_inf();
+        }
+        if (from != neg_inf()) {
+            const float d = max_nan((from - m) * c + (old - origin()), -1000.0f);
+            const float w = exp2_fast(d);
+            const f2 d2 = make_f2(d, d), w2 = make_f2(w, w);
+            u = mul_f2(w2, fma_f2(d2, s, u));
+            s = mul_f2(w2, s);
         }
     }
+    __device__ __forceinline__ void add_pair(f2 a2)
+    {
+        float a0, a1;
+        split_f2(a2, a0, a1);
+        const f2 e2 = make_f2(exp2_fast(a0), exp2_fast(a1));
+        s = add_f2(s, e2);
+        u = fma_f2(e2, a2, u);
+    }
+    template <int N> __device__ __forceinline__ void add(const uint4 (&v)[N])
+    {
+        constexpr int E = Vec<T>::E;
+        if (sizeof(T) == 2 && fused) {
+            const f2 c2 = make_f2(c, c), r2 = make_f2(-ref, -ref);
+#pragma unroll
+            for (int q = 0; q < N; ++q) {
+                const uint32_t w[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t x;
+                    asm("max.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(w[i]), "r"(low));
+                    add_pair(fma_f2(make_f2(bf_lo(x), bf_hi(x)), c2, r2));
+                }
+            }
+        } else {
+            const float nm = m == neg_inf() ? 0.0f : -m;
+            const f2 c2 = make_f2(c, c), nm2 = make_f2(nm, nm);
+#pragma unroll
+            for (int q = 0; q < N; ++q) {
+                float f[E];
+                Vec<T>::unpack(v[q], f);
+#pragma unroll
+                for (int e = 0; e < E; e += 2) {
+                    float a0, a1;
+                    split_f2(mul_f2(add_f2(make_f2(f[e], f[e + 1]), nm2), c2), a0, a1);
+                    add_pair(make_f2(max_nan(a0, -1000.0f), max_nan(a1, -1000.0f)));
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ Stat stat() const
+    {
+        float a, b;
+        Stat st;
+        st.m = m;
+        split_f2(s, a, b);
+        st.s = a + b;
+        split_f2(u, a, b);
+        st.u = a + b;
+        const float d = origin(); // at most 2^-13: 2^d is 1 + d ln 2
+        st.u += d * st.s;
+        st.u = fmaf(d * LN2, st.u, st.u);
+        st.s = fmaf(d * LN2, st.s, st.s);
+        return st;
+    }
+};
+
+using Key = unsigned long long;
+
+struct LpShared {
+    Stat warp[2][LP_WARPS]; // by row parity: a warp may be a row ahead
+    Stat cta;
+    Key lists[LP_WARPS][32];  // descending
+    Key found[LP_WARPS][32];
+    Key fin[32], last[32];    // the CTA's best, the row's
+    Key bound;
+    int picked[32];
+};
+
+// How many of a descending list of 32 come before `k`.
+__device__ __forceinline__ int count_before(const Key *list, Key k)
+{
+    int n = 0;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1)
+        if (list[n + s - 1] > k)
+            n += s;
+    return n + (list[n] > k ? 1 : 0);
+}
+
+// The place of key [own][at] among all lists.
+__device__ __forceinline__ int place(const Key (*lists)[32], int own, int at, Key k)
+{
+    int n = at;
+#pragma unroll
+    for (int l = 0; l < LP_WARPS; ++l)
+        if (l != own)
+            n += count_before(lists[l], k);
+    return n;
 }
 
 } // namespace
 
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(LP_THREADS) logprob_kernel(LogprobParams p, int parts)
+__global__ void __launch_bounds__(LP_THREADS, 4) logprob_kernel(LogprobParams p, int parts)
 {
-    constexpr int E = Vec<T>::E;
+    constexpr int E = Vec<T>::E, GROUP = LP_UNROLL * LP_THREADS;
     __shared__ LpShared sm;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int row = blockIdx.x / parts, part = blockIdx.x % parts;
-    const T *x = static_cast<const T *>(p.logits) + (int64_t)row * p.stride;
-    const int lead = row_lead(x);
-    const int nvec = (int)(((int64_t)lead + p.V + E - 1) / E);
-    const int per = (nvec + parts - 1) / parts;
-    const int vb = part * per, ve = min(nvec, vb + per);
+    const int part = blockIdx.x % parts, row_step = gridDim.x / parts;
     const float c = p.inv_t * LOG2E;
+
+    // a row and the vectors [vb, ve) of it that this CTA takes
+    int row = blockIdx.x / parts;
+    const T *x;
+    int lead, vb, ve;
+    auto enter = [&](int r) {
+        x = static_cast<const T *>(p.logits) + (int64_t)r * p.stride;
+        lead = row_lead(x);
+        const int nvec = (int)(((int64_t)lead + p.V + E - 1) / E), per = (nvec + parts - 1) / parts;
+        vb = min(nvec, part * per);
+        ve = min(nvec, vb + per);
+    };
+    uint4 next[LP_UNROLL];
+    auto fetch = [&](int v0) {
+#pragma unroll
+        for (int q = 0; q < LP_UNROLL; ++q) {
+            const int v = v0 + q * LP_THREADS;
+            next[q] = v < ve ? load_vec(x, p.V, lead, v) : empty_vec<T>();
+        }
+    };
+    enter(row);
+    fetch(vb + tid);
 
     if (blockIdx.x == 0) { // the call's status: any token past the vocabulary
         int bad = 0;
@@ -257,214 +420,191 @@ __global__ void __launch_bounds__(LP_THREADS) logprob_kernel(LogprobParams p, in
             status_begin(p.status, bad ? (uint32_t)LORA_FLAG_TOKEN_RANGE : 0u);
     }
 
-    // ---- the pass
-    float m = neg_inf();
-    int best_vec = -1; // first vector of the group that set the maximum
-    f2 s2 = make_f2(0.0f, 0.0f), u2 = s2;
-    const f2 c2 = make_f2(c, c);
-    for (int v0 = vb + tid; v0 < ve; v0 += LP_UNROLL * LP_THREADS) {
-        float f[LP_UNROLL][E];
+    for (int parity = 0; row < p.M; parity ^= 1) {
+        // ---- the pass
+        const T *const rx = x;
+        const int rlead = lead, rvb = vb, rve = ve, rrow = row;
+        Sums<T> sums;
+        sums.clear(c);
+        int best_vec = -1; // the vector that holds the thread's maximum
+        for (int g0 = rvb; g0 < rve; g0 += GROUP) {
+            uint4 cur[LP_UNROLL];
 #pragma unroll
-        for (int q = 0; q < LP_UNROLL; ++q) {
-            const int v = v0 + q * LP_THREADS;
-            if (v < ve) {
-                load_vec(x, p.V, lead, v, f[q]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    f[q][e] = neg_inf();
+            for (int q = 0; q < LP_UNROLL; ++q)
+                cur[q] = next[q];
+            if (g0 + GROUP < rve) {
+                fetch(g0 + GROUP + tid);
+            } else if ((row += row_step) < p.M) {
+                enter(row);
+                fetch(vb + tid);
             }
-        }
-        float gm = neg_inf();
+            float vm[LP_UNROLL], gm;
 #pragma unroll
-        for (int q = 0; q < LP_UNROLL; ++q) {
-            float vm = f[q][0];
-#pragma unroll
-            for (int e = 1; e < E; ++e)
-                vm = max_nan(vm, f[q][e]);
-            gm = max_nan(gm, vm);
-        }
-        if (!(gm <= m)) {
-            if (m != neg_inf()) { // rescale what has been summed
-                const float d = max_nan((m - gm) * c, -1000.0f);
-                const float w = exp2_fast(d);
-                const f2 d2 = make_f2(d, d), w2 = make_f2(w, w);
-                u2 = mul_f2(w2, fma_f2(d2, s2, u2));
-                s2 = mul_f2(w2, s2);
+            for (int q = 0; q < LP_UNROLL; ++q) {
+                vm[q] = Vec<T>::largest(cur[q]);
+                gm = q == 0 ? vm[0] : max_nan(gm, vm[q]);
             }
-            m = gm;
-            best_vec = v0;
-        }
-        const float nm = m == neg_inf() ? 0.0f : -m;
-        const f2 nm2 = make_f2(nm, nm);
+            if (!(gm <= sums.m)) {
+                sums.raise(gm);
+                if (TOP) {
 #pragma unroll
-        for (int q = 0; q < LP_UNROLL; ++q)
-#pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                float a0, a1;
-                split_f2(mul_f2(add_f2(make_f2(f[q][e], f[q][e + 1]), nm2), c2), a0, a1);
-                // masked elements add nothing: 2^-1000 is 0, and so is its product
-                const f2 a2 = make_f2(max_nan(a0, -1000.0f), max_nan(a1, -1000.0f));
-                split_f2(a2, a0, a1);
-                const f2 e2 = make_f2(exp2_fast(a0), exp2_fast(a1));
-                s2 = add_f2(s2, e2);
-                u2 = fma_f2(e2, a2, u2);
+                    for (int q = LP_UNROLL - 1; q >= 0; --q)
+                        if (vm[q] == gm)
+                            best_vec = g0 + tid + q * LP_THREADS;
+                }
             }
-    }
-    Stat st;
-    float h0, h1;
-    st.m = m;
-    split_f2(s2, h0, h1);
-    st.s = h0 + h1;
-    split_f2(u2, h0, h1);
-    st.u = h0 + h1;
+            sums.add(cur);
+        }
+        if (row == rrow && (row += row_step) < p.M) { // a part without vectors
+            enter(row);
+            fetch(vb + tid);
+        }
 
-    // ---- this thread's best element, the warp's in order
-    if (TOP) {
-        unsigned long long mine = 0ull;
-        if (m > neg_inf()) {
-            for (int q = LP_UNROLL - 1; q >= 0; --q) { // the lowest index is found last
-                const int v = best_vec + q * LP_THREADS;
-                if (v < ve) {
-                    float f[E];
-                    load_vec(x, p.V, lead, v, f);
+        // ---- the warps' statistics and best elements
+        const Stat ws = warp_join(sums.stat(), c);
+        if (lane == 0)
+            sm.warp[parity][warp] = ws;
+        Key sorted = 0ull;
+        if (TOP) {
+            if (best_vec >= 0 && sums.m > neg_inf()) {
+                float f[E];
+                Vec<T>::unpack(load_vec(rx, p.V, rlead, best_vec), f);
 #pragma unroll
-                    for (int e = E - 1; e >= 0; --e)
-                        if (f[e] == m)
-                            mine = order_key(m, v * E - lead + e);
-                }
+                for (int e = E - 1; e >= 0; --e) // the lowest index last
+                    if (f[e] == sums.m)
+                        sorted = order_key(f[e], best_vec * E - rlead + e);
+            }
+            sorted = warp_sort_desc(sorted, lane);
+            sm.lists[warp][lane] = sorted;
+            if (tid < 32) {
+                sm.picked[tid] = -1;
+                sm.fin[tid] = 0ull;
+                if (tid == 0)
+                    sm.bound = 1ull; // fewer than k threads hold any element: every element counts
             }
         }
-        sm.lists[warp][lane] = warp_sort_desc(mine, lane);
-        if (tid == 0)
-            sm.npicked = 0;
         __syncthreads();
-        if (warp == 0) {
-            unsigned long long kth = 0ull;
-            merge_lists(LP_WARPS, p.top_k, lane, [&](int l, int i) { return sm.lists[l][i]; },
-                        [&](int, unsigned long long k) { kth = k; });
-            if (lane == 0)
-                sm.bound = kth != 0ull ? kth : 1ull; // fewer than k threads hold any: every element counts
-        }
-        __syncthreads();
-        const unsigned long long bound = sm.bound;
-        if (mine >= bound)
-            sm.picked[atomicAdd(&sm.npicked, 1)] = tid; // any order: what comes of it is ordered by key
-        __syncthreads();
-        // ---- the picked threads' shares again, a warp each
-        unsigned long long list = 0ull, floor = bound; // lane i: the i-th best so far
-        for (int i = warp; i < sm.npicked; i += LP_WARPS) {
-            const int first = vb + sm.picked[i];
-            for (int w0 = first; w0 < ve; w0 += 32 * LP_THREADS) {
-                const int v = w0 + lane * LP_THREADS;
-                float f[E];
-                if (v < ve) {
-                    load_vec(x, p.V, lead, v, f);
-                } else {
+        if (TOP) {
+            const int at = sorted != 0ull && lane < p.top_k ? place(sm.lists, warp, lane, sorted) : 32;
+            if (p.top_k == 1) { // the best of the bests needs no second look
+                if (at == 0)
+                    sm.fin[0] = sorted;
+            } else {
+                if (at < p.top_k) // the thread whose best it is
+                    sm.picked[at] = ((key_index(sorted) + rlead) / E - rvb) % LP_THREADS;
+                if (at == p.top_k - 1)
+                    sm.bound = sorted;
+                __syncthreads();
+                // ---- the picked threads' shares again, a warp each
+                Key list = 0ull, floor = sm.bound; // lane i: the i-th best so far
+                for (int i = warp; i < p.top_k && sm.picked[i] >= 0; i += LP_WARPS) {
+                    for (int w0 = rvb + sm.picked[i]; w0 < rve; w0 += 32 * LP_THREADS) {
+                        const int v = w0 + lane * LP_THREADS;
+                        const uint4 raw = v < rve ? load_vec(rx, p.V, rlead, v) : empty_vec<T>();
+                        float f[E];
+                        Vec<T>::unpack(raw, f);
+                        // whether any lane has a candidate at all (by value; ties are settled below)
+                        if (!__any_sync(0xffffffffu, order_key(Vec<T>::largest(raw), 0) >= floor))
+                            continue;
 #pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        f[e] = neg_inf();
-                }
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const unsigned long long k = f[e] > neg_inf() ? order_key(f[e], v * E - lead + e) : 0ull;
-                    uint32_t who = __ballot_sync(0xffffffffu, k >= floor);
-                    while (who != 0u) {
-                        const int src = __ffs(who) - 1;
-                        who &= who - 1;
-                        const unsigned long long n = __shfl_sync(0xffffffffu, k, src);
-                        if (n >= floor) { // uniform; the floor may have risen since the vote
-                            const int at = __popc(__ballot_sync(0xffffffffu, list > n));
-                            const unsigned long long up = __shfl_up_sync(0xffffffffu, list, 1);
-                            list = lane < at ? list : (lane == at ? n : up);
-                            const unsigned long long kth = __shfl_sync(0xffffffffu, list, p.top_k - 1);
-                            floor = kth > floor ? kth : floor;
+                        for (int e = 0; e < E; ++e) {
+                            const Key k = f[e] > neg_inf() ? order_key(f[e], v * E - rlead + e) : 0ull;
+                            uint32_t who = __ballot_sync(0xffffffffu, k >= floor);
+                            while (who != 0u) {
+                                const int src = __ffs(who) - 1;
+                                who &= who - 1;
+                                const Key n = __shfl_sync(0xffffffffu, k, src);
+                                if (n >= floor) { // uniform; the floor may have risen since the vote
+                                    const int to = __popc(__ballot_sync(0xffffffffu, list > n));
+                                    const Key up = __shfl_up_sync(0xffffffffu, list, 1);
+                                    list = lane < to ? list : (lane == to ? n : up);
+                                    const Key kth = __shfl_sync(0xffffffffu, list, p.top_k - 1);
+                                    floor = kth > floor ? kth : floor;
+                                }
+                            }
                         }
                     }
                 }
-            }
-        }
-        sm.lists[warp][lane] = list;
-    }
-
-    // ---- join: lanes, warps, then the cluster's parts
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        Stat b;
-        b.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-        b.s = __shfl_xor_sync(0xffffffffu, st.s, o);
-        b.u = __shfl_xor_sync(0xffffffffu, st.u, o);
-        st = lane & o ? join(b, st, c) : join(st, b, c); // the same order in both lanes
-    }
-    if (lane == 0)
-        sm.warp[warp] = st;
-    __syncthreads();
-    if (warp == 0) {
-        st = sm.warp[0];
-        for (int w = 1; w < LP_WARPS; ++w)
-            st = join(st, sm.warp[w], c);
-        if (lane == 0)
-            sm.cta = st;
-        if (TOP && parts > 1)
-            merge_lists(LP_WARPS, p.top_k, lane, [&](int l, int i) { return sm.lists[l][i]; },
-                        [&](int i, unsigned long long k) {
-                            if (lane == 0)
-                                sm.fin[i] = k;
-                        });
-        if (TOP && parts > 1 && lane >= p.top_k)
-            sm.fin[lane] = 0ull;
-    }
-    if (parts > 1) {
-        cg::cluster_group cl = cg::this_cluster();
-        cl.sync();
-        if (part == 0 && warp == 0)
-            for (int r = 1; r < parts; ++r)
-                st = join(st, cl.map_shared_rank(&sm, r)->cta, c);
-    }
-    if (part == 0 && warp == 0) {
-        const bool empty = st.m == neg_inf();
-        const float logsum = empty ? 0.0f : logf(st.s); // NaN when the row holds a NaN or +infinity
-        const bool none = !(logsum == logsum);
-        if (lane == 0) {
-            if (p.stats != nullptr) {
-                p.stats[2 * (int64_t)row] = none ? quiet_nan() : st.m;
-                p.stats[2 * (int64_t)row + 1] = logsum;
-            }
-            if (p.entropy != nullptr)
-                p.entropy[row] = empty ? 0.0f : logsum - LN2 * (st.u / st.s);
-            if (p.logprob != nullptr) {
-                const int t = p.tokens[row];
-                float lp = 0.0f;
-                if (t >= 0 && t < p.V)
-                    lp = empty ? neg_inf() : (Vec<T>::widen(x[t]) - st.m) * p.inv_t - logsum;
-                p.logprob[row] = lp;
-            }
-        }
-        if (TOP) {
-            auto put = [&](int i, unsigned long long k) {
-                if (lane == 0) {
-                    const float lp = k != 0ull ? (key_value(k) - st.m) * p.inv_t - logsum : neg_inf();
-                    const bool some = k != 0ull && lp > neg_inf();
-                    p.top_logprobs[(int64_t)row * p.top_k + i] = none ? quiet_nan() : lp;
-                    p.top_ids[(int64_t)row * p.top_k + i] = some ? key_index(k) : -1;
+                sm.found[warp][lane] = list;
+                __syncthreads();
+                if (list != 0ull && lane < p.top_k) {
+                    const int to = place(sm.found, warp, lane, list);
+                    if (to < p.top_k)
+                        sm.fin[to] = list;
                 }
-            };
-            if (parts > 1) {
-                cg::cluster_group cl = cg::this_cluster();
-                merge_lists(parts, p.top_k, lane,
-                            [&](int l, int i) { return cl.map_shared_rank(&sm, l)->fin[i]; }, put);
-            } else {
-                merge_lists(LP_WARPS, p.top_k, lane, [&](int l, int i) { return sm.lists[l][i]; }, put);
+            }
+            __syncthreads();
+        }
+
+        // ---- join: warps, then the cluster's parts
+        Stat st;
+        if (warp == 0) {
+            st = sm.warp[parity][0];
+            for (int w = 1; w < LP_WARPS; ++w)
+                st = join(st, sm.warp[parity][w], c);
+        }
+        const Key *fin = sm.fin;
+        if (parts > 1) {
+            cg::cluster_group cl = cg::this_cluster();
+            if (tid == 0)
+                sm.cta = st;
+            cl.sync();
+            if (part == 0) {
+                if (warp == 0)
+                    for (int r = 1; r < parts; ++r)
+                        st = join(st, cl.map_shared_rank(&sm, r)->cta, c);
+                if (TOP) {
+                    const Key k = warp < parts ? cl.map_shared_rank(&sm, warp)->fin[lane] : 0ull;
+                    sm.lists[warp][lane] = k;
+                    if (tid < 32)
+                        sm.last[tid] = 0ull;
+                    __syncthreads();
+                    const int at = k != 0ull ? place(sm.lists, warp, lane, k) : 32;
+                    if (at < p.top_k)
+                        sm.last[at] = k;
+                    __syncthreads();
+                    fin = sm.last;
+                }
             }
         }
+        if (part == 0 && warp == 0) {
+            const bool empty = st.m == neg_inf();
+            const float logsum = empty ? 0.0f : logf(st.s); // NaN when the row holds a NaN or +infinity
+            const bool none = !(logsum == logsum);
+            if (lane == 0) {
+                if (p.stats != nullptr) {
+                    p.stats[2 * (int64_t)rrow] = none ? quiet_nan() : st.m;
+                    p.stats[2 * (int64_t)rrow + 1] = logsum;
+                }
+                if (p.entropy != nullptr)
+                    p.entropy[rrow] = empty ? 0.0f : logsum - LN2 * (st.u / st.s);
+                if (p.logprob != nullptr) {
+                    const int t = p.tokens[rrow];
+                    float lp = 0.0f;
+                    if (t >= 0 && t < p.V)
+                        lp = empty ? neg_inf() : (Vec<T>::widen(rx[t]) - st.m) * p.inv_t - logsum;
+                    p.logprob[rrow] = lp;
+                }
+            }
+            if (TOP && lane < p.top_k) {
+                const Key k = fin[lane];
+                const float lp = k != 0ull ? (key_value(k) - st.m) * p.inv_t - logsum : neg_inf();
+                p.top_logprobs[(int64_t)rrow * p.top_k + lane] = none ? quiet_nan() : lp;
+                p.top_ids[(int64_t)rrow * p.top_k + lane] = lp > neg_inf() ? key_index(k) : -1;
+            }
+        }
+        if (parts > 1)
+            cg::this_cluster().sync(); // the parts' shared memory is read until here
     }
-    if (parts > 1)
-        cg::this_cluster().sync(); // the parts' shared memory is read until here
 }
 
-// A CTA takes LP_UNROLL * LP_THREADS vectors of one row of dlogits.
-template <typename T>
-__global__ void __launch_bounds__(LP_THREADS) logprob_grad_kernel(LogprobGradParams p, int segs)
+// A CTA takes LP_UNROLL * LP_THREADS vectors of one row of dlogits. With
+// a = log2 p and one factor for each row, an element is
+//   dx = 2^a (q + r a),  q = -t (g + g_H H),  r = -t g_H ln 2,
+// and the token's own gets t g on top. a = x c - (m c + log S log2 e), the
+// latter held as two fp32 numbers so that p is as good as fp32 allows.
+template <typename T, bool BONUS>
+__global__ void __launch_bounds__(LP_THREADS, 6) logprob_grad_kernel(LogprobGradParams p, int segs)
 {
     constexpr int E = Vec<T>::E;
     const int row = blockIdx.x / segs, seg = blockIdx.x % segs;
@@ -472,48 +612,87 @@ __global__ void __launch_bounds__(LP_THREADS) logprob_grad_kernel(LogprobGradPar
     T *dx = static_cast<T *>(p.dlogits) + (int64_t)row * p.d_stride;
     const int lead = row_lead(dx);
     const bool same = row_lead(x) == lead; // both rows split into the same vectors
-    const float m = p.stats[2 * (int64_t)row], logsum = p.stats[2 * (int64_t)row + 1];
-    int t = p.tokens != nullptr ? p.tokens[row] : -1;
-    const float g = t >= 0 && t < p.V && p.g_logprob != nullptr ? p.g_logprob[row] : 0.0f;
-    const float gh = p.g_entropy != nullptr ? p.g_entropy[row] : 0.0f;
-    const float H = p.g_entropy != nullptr ? p.entropy[row] : 0.0f;
-    const bool empty = m == neg_inf();
     const int nvec = (int)(((int64_t)lead + p.V + E - 1) / E);
     const int v0 = seg * (LP_UNROLL * LP_THREADS) + threadIdx.x;
-    float f[LP_UNROLL][E];
+    uint4 raw[LP_UNROLL];
 #pragma unroll
     for (int q = 0; q < LP_UNROLL; ++q) {
         const int v = v0 + q * LP_THREADS, i0 = v * E - lead;
         if (v < nvec) {
-            if (same && i0 >= 0 && i0 + E <= p.V) {
-                Vec<T>::unpack(*reinterpret_cast<const uint4 *>(x + i0), f[q]);
+            if (same && i0 >= 0 && i0 + E <= p.V) { // not through the read-only path: dlogits may be logits
+                asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(raw[q].x), "=r"(raw[q].y), "=r"(raw[q].z), "=r"(raw[q].w)
+                             : "l"(x + i0)
+                             : "memory");
             } else {
+                float f[E];
 #pragma unroll
                 for (int e = 0; e < E; ++e)
-                    f[q][e] = i0 + e >= 0 && i0 + e < p.V ? Vec<T>::widen(x[i0 + e]) : neg_inf();
+                    f[e] = i0 + e >= 0 && i0 + e < p.V ? Vec<T>::widen(x[i0 + e]) : neg_inf();
+                raw[q] = Vec<T>::pack(f);
             }
         }
     }
+    const float m = p.stats[2 * (int64_t)row], logsum = p.stats[2 * (int64_t)row + 1];
+    int t = p.tokens != nullptr ? p.tokens[row] : -1;
+    t = t < p.V ? t : -1;
+    const float g = t >= 0 && p.g_logprob != nullptr ? p.g_logprob[row] : 0.0f;
+    const float gh = BONUS ? p.g_entropy[row] : 0.0f;
+    const float H = BONUS ? p.entropy[row] : 0.0f;
+    const bool empty = m == neg_inf();
+    const float c = p.inv_t * LOG2E;
+    const float qf = -p.inv_t * (g + gh * H), rf = -p.inv_t * gh * LN2, own = p.inv_t * g;
+    // m c + logsum log2 e in two parts; rows of huge values take the difference first
+    const float mc = m * c, ml = fmaf(m, c, -mc), ls = logsum * LOG2E;
+    const float hi = mc + ls, part = hi - mc, lo = ((mc - (hi - part)) + (ls - part)) + ml;
+    const bool huge = !(fabsf(mc) <= 65536.0f);
+    const f2 c2 = make_f2(c, c), hi2 = make_f2(-hi, -hi), lo2 = make_f2(-lo, -lo), q2 = make_f2(qf, qf), r2 = make_f2(rf, rf);
+    const f2 nm2 = make_f2(-m, -m), ls2 = make_f2(-ls, -ls);
 #pragma unroll
     for (int q = 0; q < LP_UNROLL; ++q) {
         const int v = v0 + q * LP_THREADS, i0 = v * E - lead;
         if (v >= nvec)
             break;
+        float f[E];
+        Vec<T>::unpack(raw[q], f);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float lp = (f[q][e] - m) * p.inv_t - logsum;
-            const float pr = exp2_fast(lp * LOG2E);
-            float d = g * ((i0 + e == t ? 1.0f : 0.0f) - pr);
-            d -= pr != 0.0f ? gh * pr * (lp + H) : 0.0f; // 0 log 0 is 0
-            f[q][e] = empty ? 0.0f : d * p.inv_t;
+        for (int e = 0; e < E; e += 2) {
+            const f2 x2 = make_f2(f[e], f[e + 1]);
+            f2 a2;
+            if (huge)
+                a2 = add_f2(mul_f2(add_f2(x2, nm2), c2), ls2);
+            else
+                a2 = add_f2(fma_f2(x2, c2, hi2), lo2);
+            float a0, a1;
+            split_f2(a2, a0, a1);
+            f2 d2;
+            if (BONUS) { // 0 log 0 is 0
+                a0 = max_nan(a0, -1000.0f);
+                a1 = max_nan(a1, -1000.0f);
+                d2 = fma_f2(make_f2(a0, a1), r2, q2);
+            } else {
+                d2 = q2;
+            }
+            d2 = mul_f2(make_f2(exp2_fast(a0), exp2_fast(a1)), d2);
+            split_f2(d2, f[e], f[e + 1]);
+        }
+        if (t >= i0 && t < i0 + E) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                f[e] += i0 + e == t ? own : 0.0f;
+        }
+        if (empty) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                f[e] = 0.0f;
         }
         if (i0 >= 0 && i0 + E <= p.V) {
-            *reinterpret_cast<uint4 *>(dx + i0) = Vec<T>::pack(f[q]);
+            *reinterpret_cast<uint4 *>(dx + i0) = Vec<T>::pack(f);
         } else {
 #pragma unroll
             for (int e = 0; e < E; ++e)
                 if (i0 + e >= 0 && i0 + e < p.V)
-                    dx[i0 + e] = Vec<T>::narrow(f[q][e]);
+                    dx[i0 + e] = Vec<T>::narrow(f[e]);
         }
     }
 }
@@ -530,7 +709,8 @@ template <typename T> cudaError_t launch_lp(const LogprobParams &p, int num_sms,
     attr.val.clusterDim.x = (unsigned)parts;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.M * parts));
+    // whole rows: as many CTAs as stay resident, each with several rows one after another
+    cfg.gridDim = dim3((unsigned)(parts > 1 || p.M < 4 * num_sms ? p.M * parts : 4 * num_sms));
     cfg.blockDim = dim3(LP_THREADS);
     cfg.stream = st;
     cfg.attrs = &attr;
@@ -549,7 +729,10 @@ template <typename T> cudaError_t launch_grad(const LogprobGradParams &p, cudaSt
     // one vector more than V fills, for rows that start inside one
     const int64_t nvec = ((int64_t)p.V + Vec<T>::E - 1) / Vec<T>::E + 1;
     const int segs = (int)((nvec + LP_UNROLL * LP_THREADS - 1) / (LP_UNROLL * LP_THREADS));
-    logprob_grad_kernel<T><<<(unsigned)(p.M * segs), LP_THREADS, 0, st>>>(p, segs);
+    if (p.g_entropy != nullptr)
+        logprob_grad_kernel<T, true><<<(unsigned)(p.M * segs), LP_THREADS, 0, st>>>(p, segs);
+    else
+        logprob_grad_kernel<T, false><<<(unsigned)(p.M * segs), LP_THREADS, 0, st>>>(p, segs);
     return cudaGetLastError();
 }
 
