@@ -21,7 +21,7 @@ SOURCES = ["lora_api.cu", "lora_prep.cu", "lora_simt.cu", "lora_tc.cu", "lora_em
 HEADERS = ["lora_internal.cuh", "lora_logprob.cuh", "lora_mx4.cuh", "ptx.cuh", "shrink.cuh", "shrink_tc.cuh", "vec.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "nvcc")
-FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
+FLAGS = os.environ.get("XF", "").split() + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr"]
 
 

@@ -5,28 +5,30 @@
 //   S = sum e^{d_v},  log p_v = d_v - log S,  H = log S - (sum e^{d_v} d_v) / S,
 //   dx_v = t [ g (1[v = token] - p_v) - g_H p_v (log p_v + H) ].
 //
-// logprob_kernel reads a row once: every thread keeps a running maximum with
-// S and sum e^d d relative to it and rescales both when a group of its
-// elements raises the maximum (rare after the first group). Sums are fp32, e^d
-// is the hardware's 2^x (about 2^-22 relative). While one group is summed the
-// next one, or the next row's first, is on its way: the kernel is bound by HBM
-// as long as its loads never stop.
+// A row is read once: every thread keeps its maximum, and S and sum e^d d
+// relative to a reference that trails the maximum by at most 2^8 (so both are
+// rescaled rarely). Sums are fp32, e^d is the hardware's 2^x (about 2^-22
+// relative). While one group of vectors is summed the next one, or the next
+// row's first, is on its way.
 //
 // The best alternatives cost the pass nothing but the maximum it needs anyway:
 // of the threads' own best elements the k-th largest is a lower bound of the
 // row's k-th best, so only the (at most k) threads whose best reaches it can
 // hold any of the k, and their shares, V / threads elements each, are read
 // again from L2. Elements are compared by (value, lowest index first) packed
-// into 64 bits, which orders them totally; -0 equals +0. Sorted lists of the
-// warps are merged by counting: a key's place is its place in its own list
-// plus, by binary search, how many of each other list precede it.
+// into 64 bits, which orders them totally; -0 equals +0. What reaches the
+// bound, k elements and a few, is then put in order.
 //
-// A row is split over a cluster of up to 8 CTAs when there are too few rows to
-// fill the SMs; the parts are joined through distributed shared memory in
-// part order, so results do not depend on timing.
+// logprob_rows_kernel   many rows: a CTA takes whole rows, one after another;
+//     eight warps read, a ninth finishes the row before while they are in the
+//     next one, so neither the joins nor the alternatives stop the loads.
+// logprob_split_kernel  few rows: a row is spread over a cluster of up to 8
+//     CTAs, all warps finish it together, and the parts are joined through
+//     distributed shared memory. Nothing depends on timing in either.
 #include <cooperative_groups.h>
 
 #include "lora_logprob.cuh"
+#include "ptx.cuh"
 #include "vec.cuh"
 
 namespace rd {
@@ -35,8 +37,17 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int LP_THREADS = 256;
+constexpr int LP_THREADS = 256;     // gradient, and rows spread over a cluster
 constexpr int LP_WARPS = LP_THREADS / 32;
+#ifndef RT_
+#define RT_ 256
+#endif
+#ifndef RC_
+#define RC_ 3
+#endif
+constexpr int ROW_READERS = RT_;    // whole rows: reading threads of a CTA (and one warp that finishes)
+constexpr int ROW_THREADS = ROW_READERS + 32;
+constexpr int ROW_CTAS = RC_;         // resident a SM
 constexpr int LP_UNROLL = 4;        // 16-byte vectors of a thread in flight
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
@@ -191,6 +202,14 @@ __device__ __forceinline__ float key_value(unsigned long long c)
 }
 __device__ __forceinline__ int key_index(unsigned long long c) { return (int)(0xFFFFFFFFu - (uint32_t)c); }
 
+__device__ __forceinline__ unsigned long long warp_max_key(unsigned long long c)
+{
+    const uint32_t hi = (uint32_t)(c >> 32);
+    const uint32_t mh = __reduce_max_sync(0xffffffffu, hi);
+    const uint32_t ml = __reduce_max_sync(0xffffffffu, hi == mh ? (uint32_t)c : 0u);
+    return (unsigned long long)mh << 32 | ml;
+}
+
 // The lanes' keys in descending order.
 __device__ __forceinline__ unsigned long long warp_sort_desc(unsigned long long c, int lane)
 {
@@ -223,83 +242,91 @@ __device__ __forceinline__ void rescale(Stat &st, float top, float c)
     st.m = top;
 }
 
-__device__ __forceinline__ Stat join(Stat a, Stat b, float c)
+__device__ __forceinline__ float warp_max_nan(float v)
 {
-    const float top = max_nan(a.m, b.m);
-    rescale(a, top, c);
-    rescale(b, top, c);
-    return Stat{top, a.s + b.s, a.u + b.u};
-}
-
-__device__ __forceinline__ Stat warp_join(Stat st, float c)
-{
-    float top = st.m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
-        top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-    rescale(st, top, c);
+        v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// The lanes' parts as one whose maximum is that of the lanes' m.
+__device__ __forceinline__ Stat warp_join(Stat st, float m, float c)
+{
+    rescale(st, warp_max_nan(m), c);
     st.s = warp_sum(st.s);
     st.u = warp_sum(st.u);
     return st;
 }
 
-// What a thread has summed of its elements. For bf16 the difference to the
-// maximum and the scaling are one fused operation, a = x c - ref with ref =
-// fl(m c), and masked elements are raised, two at a time, to a value whose
-// power of two is 0 (so that 0 times their a is 0): that holds while m c is
-// small enough for ref's rounding to be put right afterwards to first order
-// and the raised value lies far enough below m. Other rows (and fp32, which
-// has half the elements a byte) take the difference first and clamp a.
-template <typename T> struct Sums {
-    float m, ref, c;
-    bool fused;
-    uint32_t low; // the raised value, twice
-    f2 s, u;
+// What a thread has summed of its elements, relative to a reference `at` that
+// is one of them and trails the maximum `m` by at most 2^SLACK. For bf16 the
+// difference to the reference and the scaling are one fused operation,
+// a = x c - ref with ref = fl(at c), and masked elements are raised, two at a
+// time, to a value whose power of two is 0 (so that 0 times their a is 0):
+// that holds while at c is small enough for ref's rounding to be put right
+// afterwards to first order and the raised value lies far enough below. Other
+// rows (and fp32, which has half the elements a byte) take the difference
+// first and clamp a.
+constexpr float SLACK = 8.0f;
 
-    __device__ __forceinline__ void clear(float c_)
+template <typename T> struct Sums {
+    float m, at, limit, ref, c, drop, slack;
+    bool fused;
+    uint32_t low;         // the raised value, twice
+    float s0, s1, u0, u1; // two sums each: shorter chains
+
+    __device__ __forceinline__ void scale(float c_)
     {
-        m = neg_inf();
-        ref = 0.0f;
         c = c_;
+        drop = 400.0f / c_;
+        slack = SLACK / c_;
+    }
+    __device__ __forceinline__ void clear()
+    {
+        m = at = limit = neg_inf();
+        ref = 0.0f;
         fused = false;
         low = 0u;
-        s = u = make_f2(0.0f, 0.0f);
+        s0 = s1 = u0 = u1 = 0.0f;
     }
-    // ref - m c, what the sums' origin is off by
-    __device__ __forceinline__ float origin() const { return fused ? fmaf(-m, c, ref) : 0.0f; }
+    // ref - at c, what the sums' origin is off by
+    __device__ __forceinline__ float origin() const { return fused ? fmaf(-at, c, ref) : 0.0f; }
 
+    // a new reference
     __device__ __forceinline__ void raise(float top)
     {
-        const float old = origin(), from = m;
-        m = top;
-        ref = m * c;
+        const float old = origin(), from = at;
+        at = top;
+        ref = at * c;
+        limit = at + slack;
         if (sizeof(T) == 2) {
-            const uint32_t b = f32_to_bf16_bits(m - 400.0f / c);
+            const uint32_t b = f32_to_bf16_bits(at - drop);
             const float raised = __uint_as_float(b << 16);
             low = b | b << 16;
-            fused = fabsf(ref) <= 4096.0f && (raised - m) * c <= -150.0f && raised > neg_inf();
+            fused = fabsf(ref) <= 4096.0f && (raised - at) * c <= -150.0f && raised > neg_inf();
         }
         if (from != neg_inf()) {
-            const float d = max_nan((from - m) * c + (old - origin()), -1000.0f);
+            const float d = max_nan((from - at) * c + (old - origin()), -1000.0f);
             const float w = exp2_fast(d);
-            const f2 d2 = make_f2(d, d), w2 = make_f2(w, w);
-            u = mul_f2(w2, fma_f2(d2, s, u));
-            s = mul_f2(w2, s);
+            u0 = w * fmaf(d, s0, u0);
+            u1 = w * fmaf(d, s1, u1);
+            s0 *= w;
+            s1 *= w;
         }
     }
-    __device__ __forceinline__ void add_pair(f2 a2)
+    __device__ __forceinline__ void add_pair(float a0, float a1)
     {
-        float a0, a1;
-        split_f2(a2, a0, a1);
-        const f2 e2 = make_f2(exp2_fast(a0), exp2_fast(a1));
-        s = add_f2(s, e2);
-        u = fma_f2(e2, a2, u);
+        const float e0 = exp2_fast(a0), e1 = exp2_fast(a1);
+        s0 += e0;
+        s1 += e1;
+        u0 = fmaf(e0, a0, u0);
+        u1 = fmaf(e1, a1, u1);
     }
     template <int N> __device__ __forceinline__ void add(const uint4 (&v)[N])
     {
         constexpr int E = Vec<T>::E;
         if (sizeof(T) == 2 && fused) {
-            const f2 c2 = make_f2(c, c), r2 = make_f2(-ref, -ref);
 #pragma unroll
             for (int q = 0; q < N; ++q) {
                 const uint32_t w[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
@@ -307,34 +334,24 @@ template <typename T> struct Sums {
                 for (int i = 0; i < 4; ++i) {
                     uint32_t x;
                     asm("max.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(w[i]), "r"(low));
-                    add_pair(fma_f2(make_f2(bf_lo(x), bf_hi(x)), c2, r2));
+                    add_pair(fmaf(bf_lo(x), c, -ref), fmaf(bf_hi(x), c, -ref));
                 }
             }
         } else {
-            const float nm = m == neg_inf() ? 0.0f : -m;
-            const f2 c2 = make_f2(c, c), nm2 = make_f2(nm, nm);
+            const float aa = at == neg_inf() ? 0.0f : at;
 #pragma unroll
             for (int q = 0; q < N; ++q) {
                 float f[E];
                 Vec<T>::unpack(v[q], f);
 #pragma unroll
-                for (int e = 0; e < E; e += 2) {
-                    float a0, a1;
-                    split_f2(mul_f2(add_f2(make_f2(f[e], f[e + 1]), nm2), c2), a0, a1);
-                    add_pair(make_f2(max_nan(a0, -1000.0f), max_nan(a1, -1000.0f)));
-                }
+                for (int e = 0; e < E; e += 2)
+                    add_pair(max_nan((f[e] - aa) * c, -1000.0f), max_nan((f[e + 1] - aa) * c, -1000.0f));
             }
         }
     }
-    __device__ __forceinline__ Stat stat() const
+    __device__ __forceinline__ Stat stat() const // relative to `at`
     {
-        float a, b;
-        Stat st;
-        st.m = m;
-        split_f2(s, a, b);
-        st.s = a + b;
-        split_f2(u, a, b);
-        st.u = a + b;
+        Stat st{at, s0 + s1, u0 + u1};
         const float d = origin(); // at most 2^-13: 2^d is 1 + d ln 2
         st.u += d * st.s;
         st.u = fmaf(d * LN2, st.u, st.u);
@@ -344,16 +361,7 @@ template <typename T> struct Sums {
 };
 
 using Key = unsigned long long;
-
-struct LpShared {
-    Stat warp[2][LP_WARPS]; // by row parity: a warp may be a row ahead
-    Stat cta;
-    Key lists[LP_WARPS][32];  // descending
-    Key found[LP_WARPS][32];
-    Key fin[32], last[32];    // the CTA's best, the row's
-    Key bound;
-    int picked[32];
-};
+constexpr int FEW = 8; // up to so many alternatives are taken one by one, more are sorted
 
 // How many of a descending list of 32 come before `k`.
 __device__ __forceinline__ int count_before(const Key *list, Key k)
@@ -377,225 +385,489 @@ __device__ __forceinline__ int place(const Key (*lists)[32], int own, int at, Ke
     return n;
 }
 
-} // namespace
-
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(LP_THREADS, 4) logprob_kernel(LogprobParams p, int parts)
+// The k largest of the lanes' keys in descending order, lane by lane: for few
+// by taking the largest k times, else by sorting.
+__device__ __forceinline__ Key warp_top(Key c, int k, int lane)
 {
-    constexpr int E = Vec<T>::E, GROUP = LP_UNROLL * LP_THREADS;
-    __shared__ LpShared sm;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int part = blockIdx.x % parts, row_step = gridDim.x / parts;
-    const float c = p.inv_t * LOG2E;
-
-    // a row and the vectors [vb, ve) of it that this CTA takes
-    int row = blockIdx.x / parts;
-    const T *x;
-    int lead, vb, ve;
-    auto enter = [&](int r) {
-        x = static_cast<const T *>(p.logits) + (int64_t)r * p.stride;
-        lead = row_lead(x);
-        const int nvec = (int)(((int64_t)lead + p.V + E - 1) / E), per = (nvec + parts - 1) / parts;
-        vb = min(nvec, part * per);
-        ve = min(nvec, vb + per);
-    };
-    uint4 next[LP_UNROLL];
-    auto fetch = [&](int v0) {
-#pragma unroll
-        for (int q = 0; q < LP_UNROLL; ++q) {
-            const int v = v0 + q * LP_THREADS;
-            next[q] = v < ve ? load_vec(x, p.V, lead, v) : empty_vec<T>();
-        }
-    };
-    enter(row);
-    fetch(vb + tid);
-
-    if (blockIdx.x == 0) { // the call's status: any token past the vocabulary
-        int bad = 0;
-        if (p.tokens != nullptr)
-            for (int i = tid; i < p.M; i += LP_THREADS)
-                bad |= p.tokens[i] >= p.V;
-        bad = __syncthreads_or(bad);
-        if (tid == 0)
-            status_begin(p.status, bad ? (uint32_t)LORA_FLAG_TOKEN_RANGE : 0u);
+    if (k > FEW)
+        return warp_sort_desc(c, lane);
+    Key mine = 0ull;
+    for (int i = 0; i < k; ++i) {
+        const Key best = warp_max_key(c);
+        mine = lane == i ? best : mine;
+        c = c == best ? 0ull : c; // keys are unique, or 0
     }
+    return mine;
+}
 
-    for (int parity = 0; row < p.M; parity ^= 1) {
-        // ---- the pass
-        const T *const rx = x;
-        const int rlead = lead, rvb = vb, rve = ve, rrow = row;
-        Sums<T> sums;
-        sums.clear(c);
-        int best_vec = -1; // the vector that holds the thread's maximum
-        for (int g0 = rvb; g0 < rve; g0 += GROUP) {
+// The 32 largest of two descending lists.
+__device__ __forceinline__ Key merge_desc(Key a, Key b, int lane)
+{
+    const Key r = __shfl_sync(0xffffffffu, b, 31 - lane);
+    Key c = a > r ? a : r; // the 32 largest, rising then falling
+#pragma unroll
+    for (int j = 16; j > 0; j >>= 1) {
+        const Key o = __shfl_xor_sync(0xffffffffu, c, j);
+        c = ((lane & j) == 0) == (o > c) ? o : c;
+    }
+    return c;
+}
+
+// One row as a CTA sees it: its vectors [vb, ve).
+template <typename T> struct Part {
+    const T *x;
+    int V, lead, vb, ve;
+};
+
+// The elements that reach `bound` in the shares of `npicked` of THREADS
+// threads, the k best in descending order (of those this warp takes: vectors
+// i0, i0 + step, ... of them, 32 at a time). Lane l's `who` is the l-th picked
+// thread.
+template <int THREADS, typename T>
+__device__ __forceinline__ Key gather_top(const Part<T> &r, int who, int npicked, int i0, int step, Key bound, int k,
+                                          Key *held, int lane)
+{
+    constexpr int E = Vec<T>::E, AHEAD = 5;
+    const int share = (r.ve - r.vb + THREADS - 1) / THREADS, items = npicked * share;
+    Key list = 0ull, floor = bound;
+    int n = 0;
+    for (; i0 < items; i0 += AHEAD * step) {
+        uint4 raw[AHEAD];
+        int at[AHEAD];
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+            const int i = i0 + a * step + lane, pick = min(i / share, 31);
+            const int v = r.vb + __shfl_sync(0xffffffffu, who, pick) + (i - pick * share) * THREADS;
+            at[a] = v * E - r.lead;
+            raw[a] = i < items && v < r.ve ? load_vec(r.x, r.V, r.lead, v) : empty_vec<T>();
+        }
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+            float f[E];
+            Vec<T>::unpack(raw[a], f);
+            const float least = floor == 1ull ? neg_inf() : key_value(floor);
+            uint32_t mine = 0u; // this lane's elements that may reach the floor
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                mine |= f[e] >= least && f[e] > neg_inf() ? 1u << e : 0u;
+            while (__any_sync(0xffffffffu, mine != 0u)) { // one of each lane at a time
+                const int e = __ffs(mine) - 1;
+                float x = f[0];
+#pragma unroll
+                for (int j = 1; j < E; ++j)
+                    x = e == j ? f[j] : x;
+                const Key key = order_key(x, at[a] + e);
+                const bool in = mine != 0u && key >= floor;
+                mine &= mine - 1u;
+                const uint32_t all = __ballot_sync(0xffffffffu, in);
+                if (in)
+                    held[n + __popc(all & ((1u << lane) - 1u))] = key;
+                n += __popc(all);
+                if (n >= 32) {
+                    __syncwarp();
+                    const Key c = held[lane], rest = held[32 + lane];
+                    __syncwarp();
+                    held[lane] = rest;
+                    __syncwarp();
+                    n -= 32;
+                    list = merge_desc(list, warp_sort_desc(c, lane), lane);
+                    const Key kth = __shfl_sync(0xffffffffu, list, k - 1);
+                    floor = kth > floor ? kth : floor;
+                }
+            }
+        }
+    }
+    __syncwarp();
+    const Key rest = lane < n ? held[lane] : 0ull;
+    __syncwarp(); // held is written again for the next row
+    if (!__any_sync(0xffffffffu, list != 0ull))
+        return warp_top(rest, k, lane);
+    return merge_desc(list, warp_sort_desc(rest, lane), lane);
+}
+
+// The key that every element has to reach: the last element of the vector of
+// the k-th best thread (its vector may hold the value more than once), or any
+// element where fewer than k threads hold one.
+template <typename T> __device__ __forceinline__ Key bound_of(Key kth, int lead)
+{
+    return kth != 0ull ? order_key(key_value(kth), key_index(kth) * Vec<T>::E - lead + Vec<T>::E - 1) : 1ull;
+}
+
+// One thread's pass over its share of a row's vectors [vb, ve), with the next
+// group always on its way.
+template <typename T, int THREADS> struct Reader {
+    static constexpr int E = Vec<T>::E, GROUP = LP_UNROLL * THREADS;
+    const LogprobParams &p;
+    int tid;
+    Part<T> r;
+    int safe_from, safe_to; // vectors that lie in the row entirely
+    uint4 next[LP_UNROLL];
+
+    __device__ __forceinline__ void fetch(int g0)
+    {
+        if (g0 >= safe_from && g0 + GROUP <= min(safe_to, r.ve)) {
+            const uint4 *v = reinterpret_cast<const uint4 *>(r.x - r.lead) + (g0 + tid);
+#pragma unroll
+            for (int q = 0; q < LP_UNROLL; ++q)
+                asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(next[q].x), "=r"(next[q].y), "=r"(next[q].z), "=r"(next[q].w)
+                             : "l"(v + q * THREADS));
+        } else {
+#pragma unroll
+            for (int q = 0; q < LP_UNROLL; ++q) {
+                const int v = g0 + tid + q * THREADS;
+                next[q] = v < r.ve ? load_vec(r.x, r.V, r.lead, v) : empty_vec<T>();
+            }
+        }
+    }
+    // row `row`, part `part` of `parts`; its first group is asked for
+    __device__ __forceinline__ void enter(int row, int part, int parts)
+    {
+        r.x = static_cast<const T *>(p.logits) + (int64_t)row * p.stride;
+        r.V = p.V;
+        r.lead = row_lead(r.x);
+        const int nvec = (int)(((int64_t)r.lead + p.V + E - 1) / E), per = (nvec + parts - 1) / parts;
+        r.vb = min(nvec, part * per);
+        r.ve = min(nvec, r.vb + per);
+        safe_from = r.lead > 0 ? 1 : 0;
+        safe_to = (int)(((int64_t)r.lead + p.V) / E);
+        if (r.vb < r.ve)
+            fetch(r.vb);
+    }
+    // the row entered; then(), called while its last group is summed, may enter another
+    template <bool TOP, typename Then>
+    __device__ __forceinline__ void read(Sums<T> &sums, int &best_vec, Then then)
+    {
+        const int vb = r.vb, ve = r.ve;
+        best_vec = -1;
+        for (int g0 = vb; g0 < ve; g0 += GROUP) {
             uint4 cur[LP_UNROLL];
 #pragma unroll
             for (int q = 0; q < LP_UNROLL; ++q)
                 cur[q] = next[q];
-            if (g0 + GROUP < rve) {
-                fetch(g0 + GROUP + tid);
-            } else if ((row += row_step) < p.M) {
-                enter(row);
-                fetch(vb + tid);
-            }
+            if (g0 + GROUP < ve)
+                fetch(g0 + GROUP);
+            else
+                then();
             float vm[LP_UNROLL], gm;
 #pragma unroll
             for (int q = 0; q < LP_UNROLL; ++q) {
                 vm[q] = Vec<T>::largest(cur[q]);
                 gm = q == 0 ? vm[0] : max_nan(gm, vm[q]);
             }
-            if (!(gm <= sums.m)) {
+            if (!(gm <= sums.limit))
                 sums.raise(gm);
-                if (TOP) {
+            const bool up = !(gm <= sums.m);
+            sums.m = up ? gm : sums.m;
+            if (TOP) {
+                int q = LP_UNROLL - 1;
 #pragma unroll
-                    for (int q = LP_UNROLL - 1; q >= 0; --q)
-                        if (vm[q] == gm)
-                            best_vec = g0 + tid + q * LP_THREADS;
-                }
+                for (int j = LP_UNROLL - 2; j >= 0; --j)
+                    q = vm[j] == gm ? j : q;
+                best_vec = up ? g0 + tid + q * THREADS : best_vec;
             }
             sums.add(cur);
         }
-        if (row == rrow && (row += row_step) < p.M) { // a part without vectors
-            enter(row);
-            fetch(vb + tid);
-        }
+        if (vb >= ve)
+            then();
+    }
+};
 
-        // ---- the warps' statistics and best elements
-        const Stat ws = warp_join(sums.stat(), c);
-        if (lane == 0)
-            sm.warp[parity][warp] = ws;
-        Key sorted = 0ull;
-        if (TOP) {
-            if (best_vec >= 0 && sums.m > neg_inf()) {
-                float f[E];
-                Vec<T>::unpack(load_vec(rx, p.V, rlead, best_vec), f);
-#pragma unroll
-                for (int e = E - 1; e >= 0; --e) // the lowest index last
-                    if (f[e] == sums.m)
-                        sorted = order_key(f[e], best_vec * E - rlead + e);
+// The row's results, by one warp: lane i holds the i-th best element.
+template <typename T, bool TOP>
+__device__ __forceinline__ void write_row(const LogprobParams &p, int row, int token, float given, const Stat &st,
+                                          Key top, int lane)
+{
+    const bool empty = st.m == neg_inf();
+    const float logsum = empty ? 0.0f : logf(st.s); // NaN when the row holds a NaN or +infinity
+    const bool none = !(logsum == logsum);
+    if (lane == 0) {
+        if (p.stats != nullptr) {
+            p.stats[2 * (int64_t)row] = none ? quiet_nan() : st.m;
+            p.stats[2 * (int64_t)row + 1] = logsum;
+        }
+        if (p.entropy != nullptr)
+            p.entropy[row] = empty ? 0.0f : logsum - LN2 * (st.u / st.s);
+        if (p.logprob != nullptr) {
+            float lp = 0.0f;
+            if (token >= 0 && token < p.V)
+                lp = empty ? neg_inf() : (given - st.m) * p.inv_t - logsum;
+            p.logprob[row] = lp;
+        }
+    }
+    if (TOP && lane < p.top_k) {
+        const float lp = top != 0ull ? (key_value(top) - st.m) * p.inv_t - logsum : neg_inf();
+        p.top_logprobs[(int64_t)row * p.top_k + lane] = none ? quiet_nan() : lp;
+        p.top_ids[(int64_t)row * p.top_k + lane] = lp > neg_inf() ? key_index(top) : -1;
+    }
+}
+
+// The call's status, by `threads` threads of one CTA: any token past the vocabulary.
+__device__ __forceinline__ void open_status(const LogprobParams &p, int tid, int threads)
+{
+    int bad = 0;
+    if (p.tokens != nullptr)
+        for (int i = tid; i < p.M; i += threads)
+            bad |= p.tokens[i] >= p.V;
+    bad = __syncthreads_or(bad);
+    if (tid == 0)
+        status_begin(p.status, bad ? (uint32_t)LORA_FLAG_TOKEN_RANGE : 0u);
+}
+
+constexpr int BAR_FULL = 1, BAR_FREE = 3; // named barriers, two of each
+
+// What the reading threads leave of a row: maximum, reference and the sums
+// relative to it; and (maximum, vector that holds it), which differ between
+// threads since the vectors are their own.
+template <bool TOP> struct Left {
+    float4 sums[ROW_READERS];
+    Key best[TOP ? ROW_READERS : 1];
+};
+
+} // namespace
+
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(ROW_THREADS, ROW_CTAS) logprob_rows_kernel(LogprobParams p)
+{
+    constexpr int PER = ROW_READERS / 32; // threads a lane of the last warp answers for
+    __shared__ Left<TOP> left[2];
+    __shared__ Key held[TOP ? 64 : 1];
+    const int tid = threadIdx.x, lane = tid & 31, step = gridDim.x;
+    const float c = p.inv_t * LOG2E;
+    if (blockIdx.x == 0)
+        open_status(p, tid, ROW_THREADS);
+    if (tid < ROW_READERS) {
+        Reader<T, ROW_READERS> reader{p, tid};
+        reader.enter(blockIdx.x, 0, 1);
+        Sums<T> sums;
+        sums.scale(c);
+        for (int row = blockIdx.x, turn = 0; row < p.M; row += step, ++turn) {
+            int best_vec;
+            sums.clear();
+            reader.template read<TOP>(sums, best_vec, [&] {
+                if (row + step < p.M)
+                    reader.enter(row + step, 0, 1);
+            });
+            const Stat st = sums.stat();
+            Left<TOP> &l = left[turn & 1];
+            if (turn >= 2) // the row before last has been finished
+                named_bar_sync(BAR_FREE + (turn & 1), ROW_THREADS);
+            l.sums[tid] = make_float4(sums.m, st.m, st.s, st.u);
+            if (TOP) {
+                Key best = best_vec >= 0 && sums.m > neg_inf() ? order_key(sums.m, best_vec) : 0ull;
+                if (p.top_k > FEW)
+                    best = warp_sort_desc(best, tid & 31); // a warp's share of what would keep the last warp too long
+                l.best[tid] = best;
             }
-            sorted = warp_sort_desc(sorted, lane);
-            sm.lists[warp][lane] = sorted;
-            if (tid < 32) {
-                sm.picked[tid] = -1;
-                sm.fin[tid] = 0ull;
-                if (tid == 0)
-                    sm.bound = 1ull; // fewer than k threads hold any element: every element counts
+            named_bar_arrive(BAR_FULL + (turn & 1), ROW_THREADS);
+        }
+        return;
+    }
+    for (int row = blockIdx.x, turn = 0; row < p.M; row += step, ++turn) {
+        Left<TOP> &l = left[turn & 1];
+        Part<T> r;
+        r.x = static_cast<const T *>(p.logits) + (int64_t)row * p.stride;
+        r.V = p.V;
+        r.lead = row_lead(r.x);
+        r.vb = 0;
+        r.ve = (int)(((int64_t)r.lead + p.V + Vec<T>::E - 1) / Vec<T>::E);
+        // what the results need besides, on its way before the wait
+        const int token = p.logprob != nullptr ? p.tokens[row] : -1;
+        const float given = token >= 0 && token < p.V ? Vec<T>::widen(r.x[token]) : 0.0f;
+        named_bar_sync(BAR_FULL + (turn & 1), ROW_THREADS);
+        float4 q[PER];
+        Key key[TOP ? PER : 1], best = 0ull;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            q[i] = l.sums[i * 32 + lane];
+            if (TOP)
+                key[i] = l.best[i * 32 + lane];
+        }
+        if (row + 2 * (int64_t)step < p.M)
+            named_bar_arrive(BAR_FREE + (turn & 1), ROW_THREADS);
+        Key top = 0ull;
+        if (TOP) { // the k best threads, lane by lane
+            if (p.top_k <= FEW) {
+                for (int i = 0; i < p.top_k; ++i) {
+                    Key mine = key[0];
+#pragma unroll
+                    for (int j = 1; j < PER; ++j)
+                        mine = key[j] > mine ? key[j] : mine;
+                    const Key one = warp_max_key(mine);
+                    best = lane == i ? one : best;
+#pragma unroll
+                    for (int j = 0; j < PER; ++j)
+                        key[j] = key[j] == one ? 0ull : key[j];
+                }
+            } else {
+#pragma unroll
+                for (int w = 1; w < PER; w *= 2)
+#pragma unroll
+                    for (int j = 0; j + w < PER; j += 2 * w)
+                        key[j] = merge_desc(key[j], key[j + w], lane);
+                best = lane < p.top_k ? key[0] : 0ull;
+            }
+            const int npicked = __popc(__ballot_sync(0xffffffffu, best != 0ull));
+            const Key bound = bound_of<T>(__shfl_sync(0xffffffffu, best, p.top_k - 1), r.lead);
+            const int who = best != 0ull ? key_index(best) % ROW_READERS : 0;
+            top = gather_top<ROW_READERS>(r, who, npicked, 0, 32, bound, p.top_k, held, lane);
+        }
+        float m = q[0].x;
+#pragma unroll
+        for (int i = 1; i < PER; ++i)
+            m = max_nan(m, q[i].x);
+        m = warp_max_nan(m);
+        Stat st{m, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            Stat one{q[i].y, q[i].z, q[i].w};
+            rescale(one, m, c);
+            st.s += one.s;
+            st.u += one.u;
+        }
+        st.s = warp_sum(st.s);
+        st.u = warp_sum(st.u);
+        write_row<T, TOP>(p, row, token, given, st, top, lane);
+    }
+}
+
+namespace {
+
+constexpr int CAND = 256; // elements that reach the bound, gathered by the whole CTA
+
+template <bool TOP> struct SplitShared {
+    Stat warp[LP_WARPS], cta;
+    Key lists[TOP ? LP_WARPS : 1][32]; // the warps' best (value, vector), descending
+    Key found[TOP ? CAND : 1];
+    Key fin[32], last[32]; // the CTA's best, the row's
+    Key held[TOP ? LP_WARPS : 1][64];
+    Key bound;
+    int picked[32];
+    int nfound;
+};
+
+} // namespace
+
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(LP_THREADS, 4) logprob_split_kernel(LogprobParams p, int parts)
+{
+    constexpr int E = Vec<T>::E;
+    __shared__ SplitShared<TOP> sm;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int part = blockIdx.x % parts, row = blockIdx.x / parts;
+    const float c = p.inv_t * LOG2E;
+    Reader<T, LP_THREADS> reader{p, tid};
+    reader.enter(row, part, parts);
+    const Part<T> r = reader.r;
+    if (blockIdx.x == 0)
+        open_status(p, tid, LP_THREADS);
+    if (TOP && tid < 32) {
+        sm.picked[tid] = -1;
+        sm.fin[tid] = sm.last[tid] = 0ull;
+        if (tid == 0) {
+            sm.bound = 1ull; // with fewer than k threads that hold any element, every element counts
+            sm.nfound = 0;
+        }
+    }
+    const int token = p.logprob != nullptr ? p.tokens[row] : -1;
+    const float given = token >= 0 && token < p.V ? Vec<T>::widen(r.x[token]) : 0.0f;
+    Sums<T> sums;
+    int best_vec;
+    sums.scale(c);
+    sums.clear();
+    reader.template read<TOP>(sums, best_vec, [] {});
+    const Stat ws = warp_join(sums.stat(), sums.m, c);
+    if (lane == 0)
+        sm.warp[warp] = ws;
+    Key best = 0ull;
+    if (TOP) {
+        best = warp_top(best_vec >= 0 && sums.m > neg_inf() ? order_key(sums.m, best_vec) : 0ull, p.top_k, lane);
+        sm.lists[warp][lane] = best;
+    }
+    __syncthreads();
+    if (TOP) {
+        const int at = best != 0ull && lane < p.top_k ? place(sm.lists, warp, lane, best) : 32;
+        if (at < p.top_k) // the thread whose best it is
+            sm.picked[at] = (key_index(best) - r.vb) % LP_THREADS;
+        if (at == p.top_k - 1)
+            sm.bound = bound_of<T>(best, r.lead);
+        __syncthreads();
+        const Key bound = sm.bound;
+        const int share = (r.ve - r.vb + LP_THREADS - 1) / LP_THREADS;
+        const int who = sm.picked[lane], npicked = __popc(__ballot_sync(0xffffffffu, who >= 0));
+        for (int i = tid; i < npicked * share; i += LP_THREADS) {
+            const int pick = i / share, v = r.vb + sm.picked[pick] + (i - pick * share) * LP_THREADS;
+            if (v >= r.ve)
+                continue;
+            const uint4 raw = load_vec(r.x, r.V, r.lead, v);
+            if (order_key(Vec<T>::largest(raw), 0) < bound) // all below it by value
+                continue;
+            float f[E];
+            Vec<T>::unpack(raw, f);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const Key k = f[e] > neg_inf() ? order_key(f[e], v * E - r.lead + e) : 0ull;
+                if (k >= bound) {
+                    const int n = atomicAdd(&sm.nfound, 1); // in any order: they are put in order below
+                    if (n < CAND)
+                        sm.found[n] = k;
+                }
             }
         }
         __syncthreads();
-        if (TOP) {
-            const int at = sorted != 0ull && lane < p.top_k ? place(sm.lists, warp, lane, sorted) : 32;
-            if (p.top_k == 1) { // the best of the bests needs no second look
-                if (at == 0)
-                    sm.fin[0] = sorted;
-            } else {
-                if (at < p.top_k) // the thread whose best it is
-                    sm.picked[at] = ((key_index(sorted) + rlead) / E - rvb) % LP_THREADS;
-                if (at == p.top_k - 1)
-                    sm.bound = sorted;
-                __syncthreads();
-                // ---- the picked threads' shares again, a warp each
-                Key list = 0ull, floor = sm.bound; // lane i: the i-th best so far
-                for (int i = warp; i < p.top_k && sm.picked[i] >= 0; i += LP_WARPS) {
-                    for (int w0 = rvb + sm.picked[i]; w0 < rve; w0 += 32 * LP_THREADS) {
-                        const int v = w0 + lane * LP_THREADS;
-                        const uint4 raw = v < rve ? load_vec(rx, p.V, rlead, v) : empty_vec<T>();
-                        float f[E];
-                        Vec<T>::unpack(raw, f);
-                        // whether any lane has a candidate at all (by value; ties are settled below)
-                        if (!__any_sync(0xffffffffu, order_key(Vec<T>::largest(raw), 0) >= floor))
-                            continue;
-#pragma unroll
-                        for (int e = 0; e < E; ++e) {
-                            const Key k = f[e] > neg_inf() ? order_key(f[e], v * E - rlead + e) : 0ull;
-                            uint32_t who = __ballot_sync(0xffffffffu, k >= floor);
-                            while (who != 0u) {
-                                const int src = __ffs(who) - 1;
-                                who &= who - 1;
-                                const Key n = __shfl_sync(0xffffffffu, k, src);
-                                if (n >= floor) { // uniform; the floor may have risen since the vote
-                                    const int to = __popc(__ballot_sync(0xffffffffu, list > n));
-                                    const Key up = __shfl_up_sync(0xffffffffu, list, 1);
-                                    list = lane < to ? list : (lane == to ? n : up);
-                                    const Key kth = __shfl_sync(0xffffffffu, list, p.top_k - 1);
-                                    floor = kth > floor ? kth : floor;
-                                }
-                            }
-                        }
-                    }
-                }
-                sm.found[warp][lane] = list;
-                __syncthreads();
-                if (list != 0ull && lane < p.top_k) {
-                    const int to = place(sm.found, warp, lane, list);
-                    if (to < p.top_k)
-                        sm.fin[to] = list;
-                }
+        const int nfound = sm.nfound;
+        if (nfound <= CAND) { // a key's place is how many precede it
+            if (tid < nfound) {
+                const Key k = sm.found[tid];
+                int to = 0;
+                for (int i = 0; i < nfound; ++i)
+                    to += sm.found[i] > k;
+                if (to < p.top_k)
+                    sm.fin[to] = k;
             }
+        } else { // a share holds much of the best: sorted lists instead
+            const Key list = gather_top<LP_THREADS>(r, max(who, 0), npicked, warp * 32, LP_THREADS, bound, p.top_k, sm.held[warp],
+                                                     lane);
+            sm.lists[warp][lane] = list;
             __syncthreads();
+            const int to = list != 0ull && lane < p.top_k ? place(sm.lists, warp, lane, list) : 32;
+            if (to < p.top_k)
+                sm.fin[to] = list;
         }
-
-        // ---- join: warps, then the cluster's parts
-        Stat st;
-        if (warp == 0) {
-            st = sm.warp[parity][0];
-            for (int w = 1; w < LP_WARPS; ++w)
-                st = join(st, sm.warp[parity][w], c);
-        }
-        const Key *fin = sm.fin;
-        if (parts > 1) {
-            cg::cluster_group cl = cg::this_cluster();
-            if (tid == 0)
-                sm.cta = st;
-            cl.sync();
-            if (part == 0) {
-                if (warp == 0)
-                    for (int r = 1; r < parts; ++r)
-                        st = join(st, cl.map_shared_rank(&sm, r)->cta, c);
-                if (TOP) {
-                    const Key k = warp < parts ? cl.map_shared_rank(&sm, warp)->fin[lane] : 0ull;
-                    sm.lists[warp][lane] = k;
-                    if (tid < 32)
-                        sm.last[tid] = 0ull;
-                    __syncthreads();
-                    const int at = k != 0ull ? place(sm.lists, warp, lane, k) : 32;
-                    if (at < p.top_k)
-                        sm.last[at] = k;
-                    __syncthreads();
-                    fin = sm.last;
-                }
-            }
-        }
-        if (part == 0 && warp == 0) {
-            const bool empty = st.m == neg_inf();
-            const float logsum = empty ? 0.0f : logf(st.s); // NaN when the row holds a NaN or +infinity
-            const bool none = !(logsum == logsum);
-            if (lane == 0) {
-                if (p.stats != nullptr) {
-                    p.stats[2 * (int64_t)rrow] = none ? quiet_nan() : st.m;
-                    p.stats[2 * (int64_t)rrow + 1] = logsum;
-                }
-                if (p.entropy != nullptr)
-                    p.entropy[rrow] = empty ? 0.0f : logsum - LN2 * (st.u / st.s);
-                if (p.logprob != nullptr) {
-                    const int t = p.tokens[rrow];
-                    float lp = 0.0f;
-                    if (t >= 0 && t < p.V)
-                        lp = empty ? neg_inf() : (Vec<T>::widen(rx[t]) - st.m) * p.inv_t - logsum;
-                    p.logprob[rrow] = lp;
-                }
-            }
-            if (TOP && lane < p.top_k) {
-                const Key k = fin[lane];
-                const float lp = k != 0ull ? (key_value(k) - st.m) * p.inv_t - logsum : neg_inf();
-                p.top_logprobs[(int64_t)rrow * p.top_k + lane] = none ? quiet_nan() : lp;
-                p.top_ids[(int64_t)rrow * p.top_k + lane] = lp > neg_inf() ? key_index(k) : -1;
-            }
-        }
-        if (parts > 1)
-            cg::this_cluster().sync(); // the parts' shared memory is read until here
+        __syncthreads();
     }
+
+    // ---- join: warps, then the cluster's parts
+    Stat st{neg_inf(), 0.0f, 0.0f};
+    if (warp == 0) {
+        if (lane < LP_WARPS)
+            st = sm.warp[lane];
+        st = warp_join(st, st.m, c);
+        if (lane == 0)
+            sm.cta = st;
+    }
+    Key top = 0ull;
+    cg::cluster_group cl = cg::this_cluster();
+    cl.sync();
+    if (part == 0) {
+        if (warp == 0) {
+            st = lane < parts ? cl.map_shared_rank(&sm, lane)->cta : Stat{neg_inf(), 0.0f, 0.0f};
+            st = warp_join(st, st.m, c);
+        }
+        if (TOP) {
+            const Key k = warp < parts && lane < p.top_k ? cl.map_shared_rank(&sm, warp)->fin[lane] : 0ull;
+            sm.lists[warp][lane] = k;
+            __syncthreads();
+            const int at = k != 0ull ? place(sm.lists, warp, lane, k) : 32;
+            if (at < p.top_k)
+                sm.last[at] = k;
+            __syncthreads();
+            top = sm.last[lane];
+        }
+        if (warp == 0)
+            write_row<T, TOP>(p, row, token, given, st, top, lane);
+    }
+    cl.sync(); // the parts' shared memory is read until here
 }
 
 // A CTA takes LP_UNROLL * LP_THREADS vectors of one row of dlogits. With
@@ -704,19 +976,26 @@ template <typename T> cudaError_t launch_lp(const LogprobParams &p, int num_sms,
     int parts = 1;
     while (parts < 8 && (int64_t)p.M * parts < 2 * num_sms && nvec >= 2 * parts * LP_THREADS)
         parts *= 2;
+    if (parts == 1) { // as many CTAs as stay resident, each with rows one after another
+        const int grid = p.M < ROW_CTAS * num_sms ? p.M : ROW_CTAS * num_sms;
+        if (p.top_k > 0)
+            logprob_rows_kernel<T, true><<<grid, ROW_THREADS, 0, st>>>(p);
+        else
+            logprob_rows_kernel<T, false><<<grid, ROW_THREADS, 0, st>>>(p);
+        return cudaGetLastError();
+    }
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = (unsigned)parts;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    // whole rows: as many CTAs as stay resident, each with several rows one after another
-    cfg.gridDim = dim3((unsigned)(parts > 1 || p.M < 4 * num_sms ? p.M * parts : 4 * num_sms));
+    cfg.gridDim = dim3((unsigned)(p.M * parts));
     cfg.blockDim = dim3(LP_THREADS);
     cfg.stream = st;
     cfg.attrs = &attr;
-    cfg.numAttrs = parts > 1 ? 1 : 0;
-    return p.top_k > 0 ? cudaLaunchKernelEx(&cfg, logprob_kernel<T, true>, p, parts)
-                       : cudaLaunchKernelEx(&cfg, logprob_kernel<T, false>, p, parts);
+    cfg.numAttrs = 1;
+    return p.top_k > 0 ? cudaLaunchKernelEx(&cfg, logprob_split_kernel<T, true>, p, parts)
+                       : cudaLaunchKernelEx(&cfg, logprob_split_kernel<T, false>, p, parts);
 }
 
 cudaError_t launch_logprob(const LogprobParams &p, int dtype, int num_sms, cudaStream_t st)
