@@ -575,7 +575,8 @@ lora_status lora_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int
 enum {
     LORA_MX4_PATH_AUTO = 0,   /* by row count */
     LORA_MX4_PATH_STREAM = 1, /* codes to the tensor cores' registers: few rows */
-    LORA_MX4_PATH_EXPAND = 2  /* the weight widened to bf16 in the workspace, then lora_proj_apply: many rows */
+    LORA_MX4_PATH_EXPAND = 2, /* the weight widened to bf16 in the workspace, then lora_proj_apply */
+    LORA_MX4_PATH_TILES = 3   /* codes widened into the shared-memory operand tiles of tcgen05 */
 };
 
 /* Workspace of lora_mx4_proj_apply for M rows on route `rt`: the routing sort,

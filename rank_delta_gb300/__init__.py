@@ -55,6 +55,7 @@ LORA_MX4_BLOCK = 32
 LORA_MX4_PATH_AUTO = 0
 LORA_MX4_PATH_STREAM = 1
 LORA_MX4_PATH_EXPAND = 2
+LORA_MX4_PATH_TILES = 3
 
 LORA_PLAN_SIMT = 1
 LORA_PLAN_TC = 2

@@ -1483,7 +1483,7 @@ size_t lora_mx4_proj_workspace_bytes_ex(int M, const lora_route *rt, int path)
         return 0;
     if (mx4_path(M, path) == LORA_MX4_PATH_EXPAND) // the projection's, then the weight in bf16
         return align256(lora_proj_workspace_bytes(M, rt)) + align256((size_t)rt->n_out * (size_t)rt->n_in * 2);
-    return ws_layout(M, rt->max_loras + 1, rt->max_rank, shrink_kparts(rt->n_in)).total;
+    return align256(256 + sizeof(float) * (size_t)M * (size_t)rt->max_rank); // status, h
 }
 
 size_t lora_mx4_proj_workspace_bytes(int M, const lora_route *rt)
@@ -1509,7 +1509,7 @@ lora_status lora_mx4_proj_apply_ex(const void *x, int64_t x_stride, const uint8_
         return s;
     if (M < 0)
         return fail(LORA_ERR_SHAPE, "%s: M %d is negative", who, M);
-    if (path < LORA_MX4_PATH_AUTO || path > LORA_MX4_PATH_EXPAND)
+    if (path < LORA_MX4_PATH_AUTO || path > LORA_MX4_PATH_TILES)
         return fail(LORA_ERR_RANGE, "%s: path %d is not one of LORA_MX4_PATH_*", who, path);
     if (K != rt->n_in || N != rt->n_out)
         return fail(LORA_ERR_SHAPE, "%s: x is [M %d][K %d] and W [N %d][K %d], but the route is [n_out %d x n_in %d]", who,
@@ -1546,41 +1546,35 @@ lora_status lora_mx4_proj_apply_ex(const void *x, int64_t x_stride, const uint8_
             return cuda_fail(e, who);
         return proj_apply(x, x_stride, W, M, K, N, seq_slot, rt, y, y_stride, ws, proj, LORA_PATH_AUTO, stream);
     }
-    Params p; // routing and shrink, as the CUDA-core path of lora_proj_apply runs them
-    memset(&p, 0, sizeof p);
-    p.x = static_cast<const uint16_t *>(x);
-    p.x_stride = x_stride;
-    p.seq_slot = seq_slot;
-    p.E = 1;
-    p.rows = M;
-    p.K = K;
-    p.N = N;
-    p.L = rt->max_loras;
-    p.R = rt->max_rank;
-    p.tab[0] = tables_of(*rt);
-    p.kp = shrink_kparts(K);
-    if ((s = carve_ws(ws, ws_bytes, M, p.L + 1, p.R, p.kp, 0, 0, p.ws, who)) != LORA_OK)
-        return s;
-    if ((e = launch_prep(p, st)) != cudaSuccess || (e = launch_shrink(p, di.num_sms, st)) != cudaSuccess)
-        return cuda_fail(e, who);
     Mx4ProjParams q;
     memset(&q, 0, sizeof q);
-    q.x = p.x;
+    q.x = static_cast<const uint16_t *>(x);
     q.x_stride = x_stride;
     q.codes = codes;
     q.scales = scales;
     q.M = M;
     q.K = K;
     q.N = N;
-    q.L = p.L;
-    q.R = p.R;
+    q.L = rt->max_loras;
+    q.R = rt->max_rank;
     q.seq_slot = seq_slot;
-    q.tab = p.tab[0];
-    q.h = p.ws.h;
-    q.kp = p.kp;
+    q.tab = tables_of(*rt);
+    q.status = static_cast<uint32_t *>(ws);
+    q.h = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + 256);
     q.y = static_cast<uint16_t *>(y);
     q.y_stride = y_stride;
-    if ((e = launch_mx4_stream(q, di.num_sms, st)) != cudaSuccess)
+    if ((e = launch_mx4_shrink(q, st)) != cudaSuccess)
+        return cuda_fail(e, who);
+    if (path == LORA_MX4_PATH_TILES) {
+        const Mx4TcPlan plan = plan_mx4_tc(q, di.num_sms);
+        CUtensorMap xmap;
+        if (!make_map(&xmap, x, (uint64_t)K, (uint64_t)M, (uint64_t)x_stride, 64, (uint32_t)plan.tn))
+            return fail(LORA_ERR_CUDA, "%s: encoding the x tensor map failed", who);
+        e = launch_mx4_tc(q, plan, xmap, st);
+    } else {
+        e = launch_mx4_stream(q, di.num_sms, st);
+    }
+    if (e != cudaSuccess)
         return cuda_fail(e, who);
     return ok();
 }

@@ -7,6 +7,10 @@
 //            so the largest code is 4 or 6; codes are rounded to nearest even
 //            and saturate. One pass: bound by HBM.
 // dequantize the reverse, one 16-byte store a thread and step.
+// shrink     h = A_s x_i for the rows of each slot, on the tensor cores straight
+//            from memory: 16 rank rows by up to 16 of the slot's rows a CTA and
+//            pass. The projection kernels start behind it at once and wait for
+//            h only where they need it.
 // stream     the product for few rows. The weight's 16-row fragments go from
 //            memory to the tensor cores' registers: a thread copies 16 bytes
 //            (one block of 32 codes) of two weight rows, 128 k of the tile's 16
@@ -234,6 +238,161 @@ cudaError_t launch_mx4_dequantize(const Mx4DequantParams &p, int dtype, int num_
     return cudaGetLastError();
 }
 
+// ------------------------------------------------------------------ shrink
+namespace {
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+constexpr int SH_WARPS = 16;     // they share K
+constexpr int SH_THREADS = SH_WARPS * 32;
+constexpr int SH_ROWS = 64;     // rows a CTA looks through for its slot
+constexpr int SH_TILE = 16;     // rows a pass
+
+__device__ __forceinline__ void grid_dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+} // namespace
+
+// Grid: 16-rank groups, by the u-th distinct slot of a 64-row chunk, by
+// chunks. Each thread multiplies 8 consecutive k of two rank rows
+// and two batch rows at a time: which k a fragment's slots mean is free as
+// long as both operands agree.
+__global__ void __launch_bounds__(SH_THREADS) mx4_shrink_kernel(Mx4ProjParams p)
+{
+    __shared__ uint32_t present[MAX_BUCKETS / 32];
+    __shared__ int slot_s, count_s, rows_s[SH_ROWS];
+    __shared__ float red[SH_WARPS][16][SH_TILE + 1];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int r0 = blockIdx.x * 16, u = blockIdx.y, c0 = blockIdx.z * SH_ROWS;
+    // Launched early behind whatever the stream ran before; nothing is read
+    // until that is complete, and only then may the projection kernel start.
+    grid_dependency_wait();
+    grid_dependents_launch();
+    if (blockIdx.x == 0 && u == 0 && c0 == 0) { // the call's status
+        int bad = 0;
+        for (int i = tid; i < p.M; i += SH_THREADS)
+            bad |= p.seq_slot[i] >= p.L;
+        bad = __syncthreads_or(bad);
+        if (tid == 0)
+            status_begin(p.status, bad ? (uint32_t)LORA_FLAG_SLOT_RANGE : 0u);
+    }
+    // the u-th distinct slot among the chunk's rows, and its rows in order
+    for (int i = tid; i < (p.L + 31) / 32; i += SH_THREADS)
+        present[i] = 0u;
+    int mine = -1;
+    if (tid < SH_ROWS && c0 + tid < p.M)
+        mine = p.seq_slot[c0 + tid];
+    if (mine >= p.L)
+        mine = -1;
+    __syncthreads();
+    if (mine >= 0)
+        atomicOr(&present[mine >> 5], 1u << (mine & 31));
+    if (tid == 0)
+        slot_s = -1;
+    __syncthreads();
+    if (warp == 0) {
+        const uint32_t w = lane < (p.L + 31) / 32 ? present[lane] : 0u;
+        int incl = __popc(w);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += v;
+        }
+        const int before = incl - __popc(w);
+        if (u >= before && u < incl) {
+            uint32_t rest = w;
+            for (int i = before; i < u; ++i)
+                rest &= rest - 1;
+            slot_s = lane * 32 + __ffs(rest) - 1;
+        }
+    }
+    __syncthreads();
+    const int slot = slot_s;
+    if (slot < 0)
+        return;
+    const SlotInfo si = slot_info(p.tab, slot, p.L);
+    if (!si.on || r0 >= si.rank)
+        return;
+    if (warp == 0) {
+        const int s1 = lane + 32;
+        const int a = c0 + lane < p.M ? p.seq_slot[c0 + lane] : -1, b = c0 + s1 < p.M ? p.seq_slot[c0 + s1] : -1;
+        const uint32_t ma = __ballot_sync(0xffffffffu, a == slot), mb = __ballot_sync(0xffffffffu, b == slot);
+        const uint32_t below = (1u << lane) - 1u;
+        if (a == slot)
+            rows_s[__popc(ma & below)] = c0 + lane;
+        if (b == slot)
+            rows_s[__popc(ma) + __popc(mb & below)] = c0 + s1;
+        if (lane == 0)
+            count_s = __popc(ma) + __popc(mb);
+    }
+    __syncthreads();
+    const int count = count_s, nb = p.K / 32;
+    const int b0 = (int)((int64_t)nb * warp / SH_WARPS), b1 = (int)((int64_t)nb * (warp + 1) / SH_WARPS); // this warp's blocks of 32 k
+    // rank rows past the rank read the last one; what comes of them is dropped
+    const uint16_t *ra = si.a + (size_t)min(r0 + g, si.rank - 1) * p.K + t * 8;
+    const uint16_t *rb = si.a + (size_t)min(r0 + g + 8, si.rank - 1) * p.K + t * 8;
+    for (int i0 = 0; i0 < count; i0 += SH_TILE) {
+        const uint16_t *xa = p.x + (int64_t)rows_s[min(i0 + g, count - 1)] * p.x_stride + t * 8;
+        const uint16_t *xb = p.x + (int64_t)rows_s[min(i0 + g + 8, count - 1)] * p.x_stride + t * 8;
+        const bool two = count - i0 > 8;
+        float acc[2][4] = {};
+#pragma unroll 4
+        for (int b = b0; b < b1; ++b) {
+            const uint4 va = ld_nc_16(ra + b * 32), vb = ld_nc_16(rb + b * 32), wa = ld_nc_16(xa + b * 32);
+            mma_16816(acc[0], va.x, vb.x, va.y, vb.y, wa.x, wa.y);
+            mma_16816(acc[0], va.z, vb.z, va.w, vb.w, wa.z, wa.w);
+            if (two) {
+                const uint4 wb = ld_nc_16(xb + b * 32);
+                mma_16816(acc[1], va.x, vb.x, va.y, vb.y, wb.x, wb.y);
+                mma_16816(acc[1], va.z, vb.z, va.w, vb.w, wb.z, wb.w);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            red[warp][g][n * 8 + 2 * t] = acc[n][0];
+            red[warp][g][n * 8 + 2 * t + 1] = acc[n][1];
+            red[warp][g + 8][n * 8 + 2 * t] = acc[n][2];
+            red[warp][g + 8][n * 8 + 2 * t + 1] = acc[n][3];
+        }
+        __syncthreads();
+        for (int i = tid; i < 16 * SH_TILE; i += SH_THREADS) {
+            const int q = i & 15, row = i >> 4;
+            if (i0 + row < count && r0 + q < p.R) {
+                float v = 0.0f;
+#pragma unroll
+                for (int w = 0; w < SH_WARPS; ++w)
+                    v += red[w][q][row];
+                const float f = si.scale * __ldg(p.tab.comp_table + (size_t)slot * LORA_COMP_STRIDE + r0 + q);
+                p.h[(size_t)rows_s[i0 + row] * p.R + r0 + q] = r0 + q < si.rank ? f * v : 0.0f;
+            }
+        }
+        __syncthreads();
+    }
+}
+
+cudaError_t launch_mx4_shrink(const Mx4ProjParams &p, cudaStream_t st)
+{
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    const int distinct = p.M < p.L ? p.M : p.L;
+    cfg.gridDim = dim3((unsigned)((p.R + 15) / 16), (unsigned)(distinct < SH_ROWS ? distinct : SH_ROWS),
+                       (unsigned)((p.M + SH_ROWS - 1) / SH_ROWS));
+    cfg.blockDim = dim3(SH_THREADS);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, mx4_shrink_kernel, p);
+}
+
 // ------------------------------------------------------------------ stream
 namespace {
 
@@ -242,6 +401,7 @@ constexpr int ST_FEATURES = 128;
 constexpr int ST_DEPTH = 6;               // 128-wide k chunks of codes in flight
 constexpr uint32_t ST_RING = ST_DEPTH * 2 * ST_THREADS * 16;
 constexpr uint32_t ST_X_BYTES = 96 * 1024; // x of a pass over part of K, at most
+constexpr int ST_TILE = ST_FEATURES + 4;  // floats of a token's row of the partial tile
 
 // Bytes of a token's x row over `chunks` chunks: every 64-byte block is
 // followed by 16 spare bytes, and rows lie 4 (mod 8) 16-byte units apart, so
@@ -253,22 +413,13 @@ __host__ __device__ inline uint32_t st_x_stride(int chunks)
     return u * 16u;
 }
 
-// Chunks of K a pass may stage for nt tokens tiles of 8.
+// Chunks of K a pass may stage for nt token tiles of 8.
 inline int st_pass_chunks(int nt)
 {
     int c = 1;
     while (c < 64 && (uint32_t)(nt * 8) * st_x_stride(c + 1) <= ST_X_BYTES)
         ++c;
     return c;
-}
-
-__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                          uint32_t b1)
-{
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%0, %1, %2, %3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint4 lds_16(uint32_t addr)
@@ -278,6 +429,67 @@ __device__ __forceinline__ uint4 lds_16(uint32_t addr)
     return v;
 }
 
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// Scale bytes of 128 weight rows, blocks [b0, b0 + n) of each (zero past K), to
+// sc[row][n padded to 4]; W bytes an access, which the caller has checked for
+// alignment. Eight accesses of a thread are in flight at a time.
+template <typename W>
+__device__ __forceinline__ void stage_scales(const uint8_t *scales, int nblk, int N, int f0, int b0, int n, uint8_t *sc,
+                                             int scs, int tid)
+{
+    constexpr int B = sizeof(W);
+    const int each = (n + B - 1) / B, total = ST_FEATURES * each;
+    for (int i0 = tid; i0 < total; i0 += 8 * ST_THREADS) {
+        W v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int i = i0 + u * ST_THREADS, r = i / each, b = (i - r * each) * B;
+            v[u] = W{};
+            if (i < total && b0 + b < nblk)
+                v[u] = __ldg(reinterpret_cast<const W *>(scales + (size_t)min(f0 + r, N - 1) * nblk + b0 + b));
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int i = i0 + u * ST_THREADS, r = i / each, b = (i - r * each) * B;
+            if (i < total)
+                *reinterpret_cast<W *>(sc + r * scs + b) = v[u];
+        }
+    }
+}
+
+// Two blocks' worth of a row pair's codes in registers -> bf16, times their scales.
+struct Widen {
+    uint32_t fa1, fa2, fb1, fb2;
+    bool twice;
+    __device__ __forceinline__ Widen(uint32_t sa, uint32_t sb)
+    {
+        mx4_factors(sa, fa1, fa2);
+        mx4_factors(sb, fb1, fb2);
+        twice = sa > 142u || sb > 142u;
+    }
+    __device__ __forceinline__ void operator()(uint32_t a, uint32_t b, uint32_t (&u)[4], uint32_t (&v)[4]) const
+    {
+        mx4_unpack8(a, u);
+        mx4_unpack8(b, v);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            u[q] = mul_bf16x2(u[q], fa1);
+            v[q] = mul_bf16x2(v[q], fb1);
+        }
+        if (twice) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                u[q] = mul_bf16x2(u[q], fa2);
+                v[q] = mul_bf16x2(v[q], fb2);
+            }
+        }
+    }
+};
+
 } // namespace
 
 // Grid: (feature tiles of 128) x kparts, by token tiles of 8 NT; the kparts
@@ -285,17 +497,19 @@ __device__ __forceinline__ uint4 lds_16(uint32_t addr)
 template <int NT>
 __global__ void __launch_bounds__(ST_THREADS) mx4_stream_kernel(Mx4ProjParams p, int kparts, int pass_chunks)
 {
+    constexpr int TOK = NT * 8;
     extern __shared__ __align__(128) uint8_t st_smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    const int part = blockIdx.x % kparts, f0 = (blockIdx.x / kparts) * ST_FEATURES, t0 = blockIdx.y * (NT * 8);
+    const int part = blockIdx.x % kparts, f0 = (blockIdx.x / kparts) * ST_FEATURES, t0 = blockIdx.y * TOK;
     const int nblk = p.K / 32, nch = (nblk + 3) / 4, per = (nch + kparts - 1) / kparts;
     const int cb = min(nch, part * per), ce = min(nch, cb + per);
+    const int fs = ST_FEATURES / kparts, fb = part * fs; // the features this CTA finishes
     const uint32_t xstr = st_x_stride(pass_chunks);
     const uint32_t smem = smem_u32(st_smem);
     const uint32_t ring = smem + tid * 16;
     const uint32_t xs = smem + ST_RING;
-    uint8_t *sc = st_smem + ST_RING + (uint32_t)(NT * 8) * xstr; // [128][4 pass_chunks] scale bytes
-    const int scs = 4 * pass_chunks;
+    uint8_t *sc = st_smem + ST_RING + (uint32_t)TOK * xstr; // [128][4 pass_chunks] scale bytes
+    const int scs = (4 * pass_chunks + 15) & ~15;
 
     // this thread's two weight rows (rows past N repeat the last; their sums are dropped)
     const int fa = f0 + warp * 16 + g;
@@ -310,37 +524,37 @@ __global__ void __launch_bounds__(ST_THREADS) mx4_stream_kernel(Mx4ProjParams p,
 
     auto fetch = [&](int c, int slot) { // codes of chunk c, zeros past K
         const uint32_t have = c * 4 + t < nblk ? 16u : 0u;
-        const size_t o = (size_t)c * 64;
         const uint32_t d = ring + (uint32_t)slot * (2 * ST_THREADS * 16);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(have ? wa + o : p.codes), "r"(have) : "memory");
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d + ST_THREADS * 16), "l"(have ? wb + o : p.codes), "r"(have) : "memory");
+        cp16(d, have ? wa + (size_t)c * 64 : p.codes, have);
+        cp16(d + ST_THREADS * 16, have ? wb + (size_t)c * 64 : p.codes, have);
     };
 
     for (int c0 = cb; c0 < ce; c0 += pass_chunks) {
         const int nc = min(pass_chunks, ce - c0);
-        // x of the pass (zeros past K and M), then the first chunks of codes
-        for (int i = tid; i < NT * 8 * nc * 16; i += ST_THREADS) {
-            const int tok = i / (nc * 16), q = i - tok * (nc * 16); // 16-byte piece q of the row
-            const int k = c0 * 128 + q * 8;
-            const bool have = t0 + tok < p.M && k < p.K;
-            const uint16_t *src = have ? p.x + (int64_t)(t0 + tok) * p.x_stride + k : p.x;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                             xs + (uint32_t)tok * xstr + (uint32_t)((q >> 2) * 80 + (q & 3) * 16)),
-                         "l"(src), "r"(have ? 16u : 0u)
-                         : "memory");
-        }
-        cp_async_commit();
+        // the first chunks of codes, a group a chunk, also where there is none; x of
+        // the pass (zeros past K and M) goes with the first
 #pragma unroll
-        for (int d = 0; d < ST_DEPTH - 1; ++d) { // a group a chunk, also where there is none
+        for (int d = 0; d < ST_DEPTH - 1; ++d) {
             if (d < nc)
                 fetch(c0 + d, d);
+            if (d == 0) {
+                for (int i = tid; i < TOK * nc * 16; i += ST_THREADS) {
+                    const int tok = i / (nc * 16), q = i - tok * (nc * 16); // 16-byte piece q of the row
+                    const int k = c0 * 128 + q * 8;
+                    const bool have = t0 + tok < p.M && k < p.K;
+                    cp16(xs + (uint32_t)tok * xstr + (uint32_t)((q >> 2) * 80 + (q & 3) * 16),
+                         have ? p.x + (int64_t)(t0 + tok) * p.x_stride + k : p.x, have ? 16u : 0u);
+                }
+            }
             cp_async_commit();
         }
-        for (int i = tid; i < ST_FEATURES * nc * 4; i += ST_THREADS) {
-            const int r = i / (nc * 4), b = i - r * (nc * 4);
-            sc[r * scs + b] = c0 * 4 + b < nblk ? p.scales[(size_t)min(f0 + r, p.N - 1) * nblk + c0 * 4 + b] : (uint8_t)0;
-        }
-        cp_async_wait_group<ST_DEPTH - 1>();
+        if (nblk % 16 == 0 && nc % 4 == 0 && c0 % 4 == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 15u) == 0)
+            stage_scales<uint4>(p.scales, nblk, p.N, f0, c0 * 4, nc * 4, sc, scs, tid);
+        else if (nblk % 4 == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 3u) == 0)
+            stage_scales<uint32_t>(p.scales, nblk, p.N, f0, c0 * 4, nc * 4, sc, scs, tid);
+        else
+            stage_scales<uint8_t>(p.scales, nblk, p.N, f0, c0 * 4, nc * 4, sc, scs, tid);
+        cp_async_wait_group<ST_DEPTH - 2>();
         __syncthreads();
         for (int i = 0, slot = 0; i < nc; ++i) {
             cp_async_wait_group<ST_DEPTH - 2>();
@@ -351,29 +565,12 @@ __global__ void __launch_bounds__(ST_THREADS) mx4_stream_kernel(Mx4ProjParams p,
                 fetch(c0 + ahead, slot == 0 ? ST_DEPTH - 1 : slot - 1);
             cp_async_commit();
             slot = slot + 1 == ST_DEPTH ? 0 : slot + 1;
-            uint32_t fa1, fa2, fb1, fb2;
-            const uint32_t sa = sc[(warp * 16 + g) * scs + i * 4 + t], sb = sc[(warp * 16 + g + 8) * scs + i * 4 + t];
-            mx4_factors(sa, fa1, fa2);
-            mx4_factors(sb, fb1, fb2);
-            const bool twice = sa > 142u || sb > 142u;
+            const Widen widen(sc[(warp * 16 + g) * scs + i * 4 + t], sc[(warp * 16 + g + 8) * scs + i * 4 + t]);
             const uint32_t xa = xs + (uint32_t)g * xstr + (uint32_t)(i * 4 + t) * 80;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 uint32_t u[4], v[4];
-                mx4_unpack8(j == 0 ? a.x : j == 1 ? a.y : j == 2 ? a.z : a.w, u);
-                mx4_unpack8(j == 0 ? b.x : j == 1 ? b.y : j == 2 ? b.z : b.w, v);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    u[q] = mul_bf16x2(u[q], fa1);
-                    v[q] = mul_bf16x2(v[q], fb1);
-                }
-                if (twice) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        u[q] = mul_bf16x2(u[q], fa2);
-                        v[q] = mul_bf16x2(v[q], fb2);
-                    }
-                }
+                widen(j == 0 ? a.x : j == 1 ? a.y : j == 2 ? a.z : a.w, j == 0 ? b.x : j == 1 ? b.y : j == 2 ? b.z : b.w, u, v);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     const uint4 xb = lds_16(xa + (uint32_t)(n * 8) * xstr + (uint32_t)j * 16);
@@ -387,63 +584,88 @@ __global__ void __launch_bounds__(ST_THREADS) mx4_stream_kernel(Mx4ProjParams p,
     cp_async_wait_all();
     __syncthreads();
 
-    // ---- partial tile to shared memory: [token][128 + 4]
+    // ---- partial tile, [token][128 + 4]; then s comp h of the tile's rows, [token][R], and the delta, [token][fs]
     float *tile = reinterpret_cast<float *>(st_smem);
-    constexpr int TS = ST_FEATURES + 4;
+    float *hs = tile + TOK * ST_TILE;
+    float *delta = hs + TOK * p.R;
+    __shared__ const uint16_t *brow_s[TOK]; // B of a row's slot, nullptr: no delta
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int f = warp * 16 + g, tok = n * 8 + 2 * t;
-        tile[tok * TS + f] = acc[n][0];
-        tile[(tok + 1) * TS + f] = acc[n][1];
-        tile[tok * TS + f + 8] = acc[n][2];
-        tile[(tok + 1) * TS + f + 8] = acc[n][3];
+        tile[tok * ST_TILE + f] = acc[n][0];
+        tile[(tok + 1) * ST_TILE + f] = acc[n][1];
+        tile[tok * ST_TILE + f + 8] = acc[n][2];
+        tile[(tok + 1) * ST_TILE + f + 8] = acc[n][3];
     }
     if (kparts > 1)
-        cg::this_cluster().sync();
-    else
-        __syncthreads();
-    // ---- sum over the K parts (part order), the row's adapter, one rounding
-    const int fs = ST_FEATURES / kparts;
-    for (int tok = warp; tok < NT * 8; tok += ST_THREADS / 32) {
-        const int row = t0 + tok;
-        if (row >= p.M)
-            break;
-        const int slot = p.seq_slot[row];
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    grid_dependency_wait(); // h is complete
+    const int rows = min(TOK, p.M - t0);
+#pragma unroll 4
+    for (int i = tid; i < rows * p.R; i += ST_THREADS) {
+        const int tok = i / p.R, r = i - tok * p.R, slot = p.seq_slot[t0 + tok];
         const SlotInfo si = slot_info(p.tab, slot, p.L);
-        const float *cr = p.tab.comp_table + (size_t)(si.on ? slot : 0) * LORA_COMP_STRIDE;
-        for (int q = lane; q < fs; q += 32) {
-            const int f = part * fs + q;
-            if (f0 + f >= p.N)
-                break;
-            float v = 0.0f;
-            if (kparts > 1) {
-                cg::cluster_group cl = cg::this_cluster();
-                for (int r = 0; r < kparts; ++r)
-                    v += cl.map_shared_rank(tile, r)[tok * TS + f];
-            } else {
-                v = tile[tok * TS + f];
-            }
-            if (si.on) {
-                const uint16_t *brow = si.b + (size_t)(f0 + f) * p.R;
-                float d = 0.0f;
-                for (int k = 0; k < si.rank; k += 8) {
-                    float4 h0 = make_float4(0, 0, 0, 0), h1 = h0;
-                    for (int u = 0; u < p.kp; ++u) {
-                        const float4 *hp = reinterpret_cast<const float4 *>(p.h + ((size_t)u * p.M + row) * p.R + k);
-                        const float4 a = hp[0], b = hp[1];
-                        h0.x += a.x; h0.y += a.y; h0.z += a.z; h0.w += a.w;
-                        h1.x += b.x; h1.y += b.y; h1.z += b.z; h1.w += b.w;
-                    }
-                    const float4 c0 = __ldg(reinterpret_cast<const float4 *>(cr + k));
-                    const float4 c1 = __ldg(reinterpret_cast<const float4 *>(cr + k + 4));
-                    h0.x *= c0.x; h0.y *= c0.y; h0.z *= c0.z; h0.w *= c0.w;
-                    h1.x *= c1.x; h1.y *= c1.y; h1.z *= c1.z; h1.w *= c1.w;
-                    d = dot8_bf_f32(d, ld_nc_16(brow + k), h0, h1);
-                }
-                v += si.scale * d;
-            }
-            p.y[(int64_t)row * p.y_stride + f0 + f] = f32_to_bf16_bits(v);
+        if (r == 0)
+            brow_s[tok] = si.on ? si.b : nullptr;
+        float v = 0.0f;
+        if (si.on && r < si.rank)
+            v = __ldcg(p.h + (size_t)(t0 + tok) * p.R + r);
+        hs[i] = v;
+    }
+    __syncthreads();
+    // a B row is `pieces` 16-byte pieces, a lane each: one row, or several
+    const int pieces = p.R / 8;
+    int lanes = 1;
+    while (lanes < pieces)
+        lanes *= 2;
+    const int sub = lane & (lanes - 1), each = 32 / lanes;
+    constexpr int AT_ONCE = 8;
+    for (int i0 = warp * each; i0 < rows * fs; i0 += (ST_THREADS / 32) * each * AT_ONCE) {
+        uint4 b[AT_ONCE];
+        int tok[AT_ONCE];
+#pragma unroll
+        for (int a = 0; a < AT_ONCE; ++a) {
+            const int i = i0 + a * (ST_THREADS / 32) * each + lane / lanes, f = i % fs;
+            tok[a] = i / fs;
+            const uint16_t *base = i < rows * fs && f0 + fb + f < p.N && sub < pieces ? brow_s[tok[a]] : nullptr;
+            b[a] = make_uint4(0, 0, 0, 0);
+            tok[a] = base != nullptr ? tok[a] : -1;
+            if (base != nullptr)
+                b[a] = ld_nc_16(base + (size_t)(f0 + fb + f) * p.R + sub * 8);
         }
+#pragma unroll
+        for (int a = 0; a < AT_ONCE; ++a) {
+            const int i = i0 + a * (ST_THREADS / 32) * each + lane / lanes;
+            float d = 0.0f;
+            if (tok[a] >= 0) {
+                const float4 *hp = reinterpret_cast<const float4 *>(hs + tok[a] * p.R + sub * 8);
+                d = dot8_bf_f32(0.0f, b[a], hp[0], hp[1]);
+            }
+            for (int o = lanes / 2; o > 0; o >>= 1)
+                d += __shfl_xor_sync(0xffffffffu, d, o);
+            if (i < rows * fs && sub == 0)
+                delta[i] = d;
+        }
+    }
+    __syncthreads();
+    if (kparts > 1)
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    // ---- sum over the K parts (part order), the row's adapter, one rounding
+    for (int i = tid; i < rows * fs; i += ST_THREADS) {
+        const int tok = i / fs, f = i - tok * fs;
+        if (f0 + fb + f >= p.N)
+            continue;
+        float v = 0.0f;
+        if (kparts > 1) {
+            cg::cluster_group cl = cg::this_cluster();
+            for (int r = 0; r < kparts; ++r)
+                v += cl.map_shared_rank(tile, r)[tok * ST_TILE + fb + f];
+        } else {
+            v = tile[tok * ST_TILE + f];
+        }
+        if (brow_s[tok] != nullptr) // else the base product to the bit
+            v += delta[i];
+        p.y[(int64_t)(t0 + tok) * p.y_stride + f0 + fb + f] = f32_to_bf16_bits(v);
     }
     if (kparts > 1)
         cg::this_cluster().sync(); // the parts' tiles are read until here
@@ -459,24 +681,26 @@ template <int NT> cudaError_t launch_st(const Mx4ProjParams &p, int num_sms, cud
     int pass = st_pass_chunks(NT);
     const int per = (nch + kparts - 1) / kparts;
     pass = pass < per ? pass : per;
-    uint32_t smem = ST_RING + (uint32_t)(NT * 8) * st_x_stride(pass) + ST_FEATURES * 4 * (uint32_t)pass;
-    const uint32_t tile = (uint32_t)(NT * 8) * (ST_FEATURES + 4) * 4;
-    smem = smem > tile ? smem : tile;
+    uint32_t smem = ST_RING + (uint32_t)(NT * 8) * st_x_stride(pass) + ST_FEATURES * ((4 * (uint32_t)pass + 15) & ~15u);
+    const uint32_t end = (uint32_t)(NT * 8) * (ST_TILE + p.R + ST_FEATURES / kparts) * 4;
+    smem = smem > end ? smem : end;
     static std::atomic<uint64_t> raised{0};
     cudaError_t e = raise_smem_limit(raised, mx4_stream_kernel<NT>, 224 * 1024);
     if (e != cudaSuccess)
         return e;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)kparts;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)kparts;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * kparts), (unsigned)ttiles);
     cfg.blockDim = dim3(ST_THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, mx4_stream_kernel<NT>, p, kparts, pass);
 }
 

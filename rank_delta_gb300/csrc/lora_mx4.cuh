@@ -33,15 +33,23 @@ struct Mx4ProjParams {
     int M, K, N, L, R;
     const int32_t *seq_slot;
     Tables tab;
-    const float *h; // [kp][M][R] of the shrink
-    int kp;
+    float *h; // [M][R]: s comp (A_s x_i) of every adapted row
     uint16_t *y;
     int64_t y_stride;
+    uint32_t *status;
 };
 
 cudaError_t launch_mx4_quantize(const Mx4QuantParams &p, int dtype, int num_sms, cudaStream_t st);
 cudaError_t launch_mx4_dequantize(const Mx4DequantParams &p, int dtype, int num_sms, cudaStream_t st);
+cudaError_t launch_mx4_shrink(const Mx4ProjParams &p, cudaStream_t st);
 cudaError_t launch_mx4_stream(const Mx4ProjParams &p, int num_sms, cudaStream_t st);
+// The tiles of a tensor-core launch: rows of a token tile (the host encodes x
+// in boxes of 64 k by that many rows) and K parts.
+struct Mx4TcPlan {
+    int tn, kparts;
+};
+Mx4TcPlan plan_mx4_tc(const Mx4ProjParams &p, int num_sms);
+cudaError_t launch_mx4_tc(const Mx4ProjParams &p, const Mx4TcPlan &plan, const CUtensorMap &xmap, cudaStream_t st);
 
 // The bf16 factors that turn an E2M1 value held with its exponent field as in
 // fp16 (that is, value * 2^-112) into value * 2^(byte - 127). The second is 1

@@ -1,0 +1,484 @@
+// The projection with a microscaled 4-bit base on the 5th-generation tensor
+// cores: y[i, :] = dq(W) x_i + s B_s (A_s x_i) for batches of more than a few
+// rows.
+//
+// A CTA takes 128 features by one tile of up to 256 rows and a part of K.
+// Eight warps copy the codes of their weight rows into rings of their own
+// (cp.async, 64 bytes of a row at a time), widen them to bf16 exactly and
+// store them as the swizzled K-major operand of tcgen05.mma; x comes by TMA
+// in the same layout; one thread issues the products into TMEM. The weight is
+// widened once for all rows of the tile, so from some 100 rows on the tensor
+// cores are the bound and below it the codes' way from HBM.
+//
+// The adapters are more K: s h of the tile's rows (rounded to bf16, as y
+// itself is; the sums stay fp32) against the B rows of each slot in the tile,
+// a row's columns zero for every slot but its own, into an accumulator of
+// their own, which is added to the rows that have an adapter: the others keep
+// the base product to the bit.
+//
+// With few feature tiles K is split over a cluster of CTAs, whose partial
+// tiles are summed in part order through distributed shared memory.
+#include <cooperative_groups.h>
+
+#include "lora_mx4.cuh"
+#include "ptx.cuh"
+#include "vec.cuh"
+
+namespace rd {
+
+namespace cg = cooperative_groups;
+
+namespace {
+
+constexpr int BM = 128;             // features of a tile: the UMMA M
+constexpr int MAX_STAGES = 4;       // of 64 k: the A tile (16 KB) and tn rows of x
+constexpr int DEPTH = 4;            // steps of 256 k of codes in flight
+constexpr uint32_t A_BYTES = BM * 128;
+constexpr int WIDEN_WARPS = 8;      // also the epilogue
+constexpr int TC_THREADS = (WIDEN_WARPS + 3) * 32;
+constexpr uint32_t RING_BYTES = WIDEN_WARPS * 2048; // codes of 128 rows x 256 k
+constexpr uint32_t SRING_BYTES = WIDEN_WARPS * 32 * 4;
+constexpr int MAX_TN = 256;
+constexpr int TILE_STRIDE = BM + 4; // floats of a row of the partial tile
+
+struct TcShared {
+    uint64_t x_full[MAX_STAGES], a_full[MAX_STAGES], empty[MAX_STAGES], routed, done;
+    uint32_t tmem;
+    int bad;                          // a wait gave up
+    int nseg;
+    uint32_t present[MAX_BUCKETS / 32];
+    int16_t tok_slot[MAX_TN];         // the row's slot, -1: no delta
+    int16_t slot_id[MAX_TN];          // distinct slots of the tile, ascending
+    int seg_start[MAX_TN + 1];        // their first 16-rank segment
+    int nslot;
+    const uint16_t *slot_b[MAX_TN];
+};
+
+__device__ __forceinline__ void cp4(uint32_t dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ uint4 lds_16(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ void sts_16(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_4(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+// Byte offset of 16-byte piece c (0..7) of row r in a swizzled 128-byte-row tile.
+__device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ void wait_or_note(uint64_t *bar, uint32_t parity, int *bad)
+{
+    if (!*reinterpret_cast<volatile int *>(bad) && !mbar_wait(bar, parity))
+        *reinterpret_cast<volatile int *>(bad) = 1;
+}
+
+// One block: 32 codes and their scale byte -> four 16-byte pieces of bf16.
+__device__ __forceinline__ void widen_store(uint4 codes, uint32_t byte, uint32_t tile, int row, int piece)
+{
+    uint32_t f1, f2;
+    mx4_factors(byte, f1, f2);
+    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t o[4];
+        mx4_unpack8(w[j], o);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            o[q] = mul_bf16x2(o[q], f1);
+        if (byte > 142u) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                o[q] = mul_bf16x2(o[q], f2);
+        }
+        sts_16(tile + sw128(row, piece + j), make_uint4(o[0], o[1], o[2], o[3]));
+    }
+}
+
+// The tile's rows and slots, by one warp: each row's slot, the distinct slots
+// in ascending order with their B and their 16-rank segments.
+__device__ __forceinline__ void route_tile(const Mx4ProjParams &p, TcShared &sh, int t0, int tn, int lane)
+{
+    sh.present[lane] = 0u;
+    __syncwarp();
+    for (int i = lane; i < tn; i += 32) {
+        int slot = -1;
+        if (t0 + i < p.M) {
+            const int s = p.seq_slot[t0 + i];
+            if (slot_info(p.tab, s, p.L).on) {
+                slot = s;
+                atomicOr(&sh.present[s >> 5], 1u << (s & 31));
+            }
+        }
+        sh.tok_slot[i] = (int16_t)slot;
+    }
+    __syncwarp();
+    const uint32_t w = sh.present[lane];
+    int segs = 0;
+    for (uint32_t b = w; b != 0u; b &= b - 1)
+        segs += (p.tab.rank_table[lane * 32 + __ffs(b) - 1] + 15) / 16;
+    int slots_before = __popc(w), segs_before = segs;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, slots_before, o), b = __shfl_up_sync(0xffffffffu, segs_before, o);
+        if (lane >= o) {
+            slots_before += a;
+            segs_before += b;
+        }
+    }
+    if (lane == 31) {
+        sh.nslot = slots_before;
+        sh.nseg = segs_before;
+        sh.seg_start[slots_before] = segs_before;
+    }
+    slots_before -= __popc(w);
+    segs_before -= segs;
+    for (uint32_t b = w; b != 0u; b &= b - 1) {
+        const int s = lane * 32 + __ffs(b) - 1;
+        sh.slot_id[slots_before] = (int16_t)s;
+        sh.slot_b[slots_before] = p.tab.b_table[s];
+        sh.seg_start[slots_before] = segs_before;
+        segs_before += (p.tab.rank_table[s] + 15) / 16;
+        ++slots_before;
+    }
+    __syncwarp();
+}
+
+} // namespace
+
+template <int STAGES>
+__global__ void __launch_bounds__(TC_THREADS, 1)
+    mx4_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ Mx4ProjParams p, int tn, int kparts)
+{
+    extern __shared__ uint8_t tc_smem_raw[];
+    __shared__ TcShared sh;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t raw = smem_u32(tc_smem_raw), base = (raw + 1023u) & ~1023u;
+    uint8_t *const smem = tc_smem_raw + (base - raw);
+    const uint32_t x_bytes = (uint32_t)tn * 128u;
+    const uint32_t a_at = base, x_at = base + STAGES * A_BYTES, ring = x_at + STAGES * x_bytes,
+                   sring = ring + DEPTH * RING_BYTES;
+    const int part = blockIdx.x % kparts, f0 = (blockIdx.x / kparts) * BM, t0 = blockIdx.y * tn;
+    const int nblk = p.K / 32, nss = (nblk + 7) / 8; // blocks of 32 k, steps of 256 k
+    const int ss0 = (int)((int64_t)nss * part / kparts), ss1 = (int)((int64_t)nss * (part + 1) / kparts);
+    const int nbase = (ss1 - ss0) * 4; // stages of 64 k
+    uint32_t cols = 32;
+    while ((int)cols < 2 * tn)
+        cols *= 2;
+
+    if (tid == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&sh.x_full[s], 1);
+            mbar_init(&sh.a_full[s], 128);
+            mbar_init(&sh.empty[s], 1);
+        }
+        mbar_init(&sh.routed, 1);
+        mbar_init(&sh.done, 1);
+        sh.bad = 0;
+        fence_barrier_init();
+    }
+    if (warp == WIDEN_WARPS + 1)
+        tmem_alloc(&sh.tmem, cols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+
+    if (warp < WIDEN_WARPS) {
+        // ---- widen: half of the warps take the first 128 k of each 256, half the others
+        const int group = warp >> 2, row = (warp & 3) * 32 + lane;
+        const int rowi = min(f0 + row, p.N - 1); // rows past N repeat the last; their sums are dropped
+        const uint8_t *src[4];
+        uint32_t dst[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { // four lanes bring 64 bytes of a row
+            const int r = i * 8 + (lane >> 2), pc = lane & 3;
+            src[i] = p.codes + (size_t)min(f0 + (warp & 3) * 32 + r, p.N - 1) * (p.K / 2) + pc * 16;
+            dst[i] = ring + (uint32_t)(warp * 2048 + r * 64 + ((pc ^ ((r >> 1) & 3)) << 4));
+        }
+        const bool word_scales = nblk % 4 == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 3u) == 0;
+        const uint8_t *srow = p.scales + (size_t)rowi * nblk;
+        auto fetch = [&](int ss, int slot) {
+            const int b0 = ss * 8 + group * 4;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool have = b0 + (lane & 3) < nblk;
+                cp16(dst[i] + (uint32_t)slot * RING_BYTES, have ? src[i] + (size_t)b0 * 16 : p.codes, have ? 16u : 0u);
+            }
+            if (word_scales) {
+                const bool have = b0 < nblk;
+                cp4(sring + (uint32_t)slot * SRING_BYTES + tid * 4, have ? srow + b0 : p.scales, have ? 4u : 0u);
+            }
+        };
+        auto byte_scales = [&](int ss) { // rows that do not start on a word
+            const int b0 = ss * 8 + group * 4;
+            uint32_t v = 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v |= b0 + i < nblk ? (uint32_t)__ldg(srow + b0 + i) << (8 * i) : 0u;
+            return v;
+        };
+#pragma unroll
+        for (int d = 0; d < DEPTH - 1; ++d) {
+            if (ss0 + d < ss1)
+                fetch(ss0 + d, d);
+            cp_async_commit();
+        }
+        uint32_t sc_next = word_scales ? 0u : byte_scales(ss0);
+        const uint32_t read_at = ring + (uint32_t)(warp * 2048 + lane * 64);
+        const int swz = (lane >> 1) & 3;
+        for (int ss = ss0, slot = 0; ss < ss1; ++ss) {
+            cp_async_wait_group<DEPTH - 2>();
+            __syncwarp(); // the other lanes' copies too, and their reads of the slot filled next
+            uint4 c[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                c[b] = lds_16(read_at + (uint32_t)slot * RING_BYTES + (uint32_t)((b ^ swz) << 4));
+            uint32_t sc = sc_next;
+            if (word_scales)
+                sc = lds_4(sring + (uint32_t)slot * SRING_BYTES + tid * 4);
+            else if (ss + 1 < ss1)
+                sc_next = byte_scales(ss + 1);
+            if (ss + DEPTH - 1 < ss1)
+                fetch(ss + DEPTH - 1, slot == 0 ? DEPTH - 1 : slot - 1);
+            cp_async_commit();
+            slot = slot + 1 == DEPTH ? 0 : slot + 1;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int n = (ss - ss0) * 4 + group * 2 + h, s = n % STAGES, use = n / STAGES;
+                if (use > 0)
+                    wait_or_note(&sh.empty[s], (uint32_t)(use - 1) & 1u, &sh.bad);
+                const uint32_t tile = a_at + (uint32_t)s * A_BYTES;
+                widen_store(c[2 * h], (sc >> (16 * h)) & 255u, tile, row, 0);
+                widen_store(c[2 * h + 1], (sc >> (16 * h + 8)) & 255u, tile, row, 4);
+                fence_proxy_async_smem();
+                mbar_arrive(&sh.a_full[s]);
+            }
+        }
+        cp_async_wait_all();
+
+        // ---- the adapters' operands: four 16-rank segments a stage
+        wait_or_note(&sh.routed, 0, &sh.bad);
+        const int q0 = sh.nseg * part / kparts, q1 = sh.nseg * (part + 1) / kparts;
+        const int ndelta = __any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&sh.bad) != 0) ? 0 : (q1 - q0 + 3) / 4;
+        const int rows = min(tn, p.M - t0);
+        if (ndelta > 0)
+            grid_dependency_wait(); // h is complete
+        for (int d = group; d < ndelta; d += 2) {
+            const int n = nbase + d, s = n % STAGES, use = n / STAGES;
+            if (use > 0)
+                wait_or_note(&sh.empty[s], (uint32_t)(use - 1) & 1u, &sh.bad);
+            const uint32_t at = a_at + (uint32_t)s * A_BYTES, xt = x_at + (uint32_t)s * x_bytes;
+            const int nk = min(4, q1 - q0 - 4 * d);
+            for (int j = 0; j < nk; ++j) {
+                const int q = q0 + 4 * d + j;
+                int lo = 0, hi = sh.nslot; // the slot of segment q
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (sh.seg_start[mid] <= q)
+                        lo = mid;
+                    else
+                        hi = mid;
+                }
+                const int r = (q - sh.seg_start[lo]) * 16, slot = sh.slot_id[lo];
+                const uint16_t *b = sh.slot_b[lo] + (size_t)rowi * p.R + r;
+                cp16(at + sw128(row, 2 * j), b, 16u);
+                cp16(at + sw128(row, 2 * j + 1), r + 8 < p.R ? b + 8 : b, r + 8 < p.R ? 16u : 0u);
+                for (int tok = row; tok < tn; tok += 128) {
+                    uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+                    if (tok < rows && sh.tok_slot[tok] == slot) {
+                        const float4 *h = reinterpret_cast<const float4 *>(p.h + (size_t)(t0 + tok) * p.R + r);
+                        const float4 h0 = __ldcg(h), h1 = __ldcg(h + 1);
+                        v0 = make_uint4(pack2(h0.x, h0.y), pack2(h0.z, h0.w), pack2(h1.x, h1.y), pack2(h1.z, h1.w));
+                        if (r + 8 < p.R) {
+                            const float4 h2 = __ldcg(h + 2), h3 = __ldcg(h + 3);
+                            v1 = make_uint4(pack2(h2.x, h2.y), pack2(h2.z, h2.w), pack2(h3.x, h3.y), pack2(h3.z, h3.w));
+                        }
+                    }
+                    sts_16(xt + sw128(tok, 2 * j), v0);
+                    sts_16(xt + sw128(tok, 2 * j + 1), v1);
+                }
+            }
+            cp_async_wait_all();
+            fence_proxy_async_smem();
+            mbar_arrive(&sh.a_full[s]);
+        }
+
+        // ---- the accumulators
+        wait_or_note(&sh.done, 0, &sh.bad);
+        __syncwarp();
+        tc_fence_after();
+        float *tile = reinterpret_cast<float *>(smem); // every product has read its operands
+        const int f = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        for (int c = group; c < tn / 16; c += 2) {
+            float v[16];
+            tmem_ld16(tmem + lanes + (uint32_t)(c * 16), v);
+            if (ndelta > 0) {
+                float d[16];
+                tmem_ld16(tmem + lanes + (uint32_t)(tn + c * 16), d);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (sh.tok_slot[c * 16 + i] >= 0)
+                        v[i] += d[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int tok = c * 16 + i;
+                if (kparts > 1)
+                    tile[tok * TILE_STRIDE + f] = v[i];
+                else if (tok < rows && f0 + f < p.N)
+                    p.y[(int64_t)(t0 + tok) * p.y_stride + f0 + f] = f32_to_bf16_bits(v[i]);
+            }
+        }
+    } else if (warp == WIDEN_WARPS) {
+        // ---- x
+        if (lane == 0) {
+            prefetch_tmap(&xmap);
+            for (int n = 0; n < nbase; ++n) {
+                const int s = n % STAGES, use = n / STAGES;
+                if (use > 0)
+                    wait_or_note(&sh.empty[s], (uint32_t)(use - 1) & 1u, &sh.bad);
+                mbar_arrive_expect_tx(&sh.x_full[s], x_bytes);
+                tma_load_2d(smem + STAGES * A_BYTES + (uint32_t)s * x_bytes, &xmap, (ss0 * 4 + n) * 64, t0, &sh.x_full[s]);
+            }
+        }
+        __syncwarp();
+    } else if (warp == WIDEN_WARPS + 1) {
+        // ---- products
+        if (lane == 0) {
+            const uint32_t idesc = idesc_bf16_f32(BM, (uint32_t)tn);
+            for (int n = 0; n < nbase; ++n) {
+                const int s = n % STAGES;
+                const uint32_t parity = (uint32_t)(n / STAGES) & 1u;
+                wait_or_note(&sh.x_full[s], parity, &sh.bad);
+                wait_or_note(&sh.a_full[s], parity, &sh.bad);
+                tc_fence_after();
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    umma_bf16(tmem, sw128_kmajor_desc(a_at + (uint32_t)s * A_BYTES + j * 32),
+                              sw128_kmajor_desc(x_at + (uint32_t)s * x_bytes + j * 32), idesc, (n | j) != 0 ? 1u : 0u);
+                umma_commit(&sh.empty[s]);
+            }
+            wait_or_note(&sh.routed, 0, &sh.bad);
+            const int q0 = sh.nseg * part / kparts, q1 = sh.nseg * (part + 1) / kparts;
+            for (int d = 0; 4 * d < q1 - q0 && !*reinterpret_cast<volatile int *>(&sh.bad); ++d) {
+                const int n = nbase + d, s = n % STAGES, nk = min(4, q1 - q0 - 4 * d);
+                wait_or_note(&sh.a_full[s], (uint32_t)(n / STAGES) & 1u, &sh.bad);
+                tc_fence_after();
+                for (int j = 0; j < nk; ++j)
+                    umma_bf16(tmem + (uint32_t)tn, sw128_kmajor_desc(a_at + (uint32_t)s * A_BYTES + j * 32),
+                              sw128_kmajor_desc(x_at + (uint32_t)s * x_bytes + j * 32), idesc, (d | j) != 0 ? 1u : 0u);
+                umma_commit(&sh.empty[s]);
+            }
+            umma_commit(&sh.done);
+        }
+        __syncwarp();
+    } else {
+        route_tile(p, sh, t0, tn, lane);
+        if (lane == 0)
+            mbar_arrive(&sh.routed);
+        __syncwarp();
+    }
+
+    // ---- the K parts' sum, in part order, and one rounding
+    if (kparts > 1) {
+        cg::cluster_group cl = cg::this_cluster();
+        cl.sync();
+        const float *tile = reinterpret_cast<const float *>(smem);
+        const int b0 = BM * part / kparts, fs = BM * (part + 1) / kparts - b0, rows = min(tn, p.M - t0);
+        if (warp < WIDEN_WARPS) {
+            for (int i = tid; i < rows * fs; i += WIDEN_WARPS * 32) {
+                const int tok = i / fs, f = b0 + i - tok * fs;
+                if (f0 + f >= p.N)
+                    continue;
+                float v = 0.0f;
+                for (int r = 0; r < kparts; ++r)
+                    v += cl.map_shared_rank(tile, r)[tok * TILE_STRIDE + f];
+                p.y[(int64_t)(t0 + tok) * p.y_stride + f0 + f] = f32_to_bf16_bits(v);
+            }
+        }
+        cl.sync(); // the parts' tiles are read until here
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == WIDEN_WARPS + 1)
+        tmem_dealloc(tmem, cols);
+    if (tid == 0 && sh.bad) {
+        grid_dependency_wait(); // the call's status is open
+        atomicOr(p.status, (uint32_t)LORA_FLAG_WAIT_TIMEOUT);
+    }
+}
+
+namespace {
+
+uint32_t tc_smem(int tn, int stages)
+{
+    return 1024u + (uint32_t)stages * (A_BYTES + (uint32_t)tn * 128u) + DEPTH * (RING_BYTES + SRING_BYTES);
+}
+
+template <int STAGES>
+cudaError_t launch(const Mx4ProjParams &p, const Mx4TcPlan &plan, const CUtensorMap &xmap, cudaStream_t st)
+{
+    static std::atomic<uint64_t> raised{0};
+    cudaError_t e = raise_smem_limit(raised, mx4_tc_kernel<STAGES>, 222 * 1024);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)plan.kparts;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((p.N + BM - 1) / BM * plan.kparts), (unsigned)((p.M + plan.tn - 1) / plan.tn));
+    cfg.blockDim = dim3(TC_THREADS);
+    cfg.dynamicSmemBytes = tc_smem(plan.tn, STAGES);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, mx4_tc_kernel<STAGES>, xmap, p, plan.tn, plan.kparts);
+}
+
+} // namespace
+
+Mx4TcPlan plan_mx4_tc(const Mx4ProjParams &p, int num_sms)
+{
+    Mx4TcPlan plan;
+    const int tiles = (p.M + MAX_TN - 1) / MAX_TN, each = (p.M + tiles - 1) / tiles;
+    plan.tn = (each + 15) / 16 * 16;
+    const int ctas = (p.N + BM - 1) / BM * tiles, nss = (p.K / 32 + 7) / 8;
+    plan.kparts = 1;
+    while (plan.kparts < 8 && ctas * plan.kparts * 2 <= num_sms && nss >= 2 * plan.kparts)
+        plan.kparts *= 2;
+    return plan;
+}
+
+cudaError_t launch_mx4_tc(const Mx4ProjParams &p, const Mx4TcPlan &plan, const CUtensorMap &xmap, cudaStream_t st)
+{
+    return plan.tn <= 128 ? launch<4>(p, plan, xmap, st) : launch<3>(p, plan, xmap, st); // what fits in 227 KB
+}
+
+} // namespace rd

@@ -19,7 +19,7 @@ from rank_delta_gb300 import torch_helpers as th
 pytestmark = pytest.mark.gpu
 
 GRID = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
-PATHS = [rd.LORA_MX4_PATH_STREAM, rd.LORA_MX4_PATH_EXPAND]
+PATHS = [rd.LORA_MX4_PATH_STREAM, rd.LORA_MX4_PATH_EXPAND, rd.LORA_MX4_PATH_TILES]
 
 
 @pytest.fixture(scope="module", autouse=True)
