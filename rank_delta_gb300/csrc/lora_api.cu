@@ -180,6 +180,23 @@ bool make_map_plain(CUtensorMap *m, const void *base, uint64_t inner, uint64_t r
     return r == CUDA_SUCCESS;
 }
 
+// Packed bytes [rows][inner], boxes of box_inner bytes x box_rows rows.
+bool make_map_bytes(CUtensorMap *m, const void *base, uint64_t inner, uint64_t rows, uint32_t box_inner,
+                    uint32_t box_rows, bool swizzle128)
+{
+    auto fn = encode_fn();
+    if (!fn)
+        return false;
+    cuuint64_t dims[2] = {inner, rows};
+    cuuint64_t strides[1] = {inner};
+    cuuint32_t box[2] = {box_inner, box_rows};
+    cuuint32_t es[2] = {1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 // 3D view [K/64 chunks][rows][64] of a K-major bf16 matrix (K a multiple of
 // 64): one box of box_chunks x box_rows x 64 brings several 64-wide K slices
 // of the same rows in one copy, each slice laid out as a 2D 128-byte-swizzled
@@ -1567,10 +1584,14 @@ lora_status lora_mx4_proj_apply_ex(const void *x, int64_t x_stride, const uint8_
         return cuda_fail(e, who);
     if (path == LORA_MX4_PATH_TILES) {
         const Mx4TcPlan plan = plan_mx4_tc(q, di.num_sms);
-        CUtensorMap xmap;
-        if (!make_map(&xmap, x, (uint64_t)K, (uint64_t)M, (uint64_t)x_stride, 64, (uint32_t)plan.tn))
-            return fail(LORA_ERR_CUDA, "%s: encoding the x tensor map failed", who);
-        e = launch_mx4_tc(q, plan, xmap, st);
+        Mx4TcMaps maps;
+        memset(&maps, 0, sizeof maps);
+        if (!make_map(&maps.x, x, (uint64_t)K, (uint64_t)M, (uint64_t)x_stride, 64, (uint32_t)plan.tn) ||
+            !make_map_bytes(&maps.codes, codes, (uint64_t)(K / 2), (uint64_t)N, 128, 128, true))
+            return fail(LORA_ERR_CUDA, "%s: encoding the tensor maps failed", who);
+        maps.scales_ok = K % 512 == 0 && aligned16(scales) &&
+                         make_map_bytes(&maps.scales, scales, (uint64_t)(K / 32), (uint64_t)N, 16, 128, false);
+        e = launch_mx4_tc(q, plan, maps, st);
     } else {
         e = launch_mx4_stream(q, di.num_sms, st);
     }

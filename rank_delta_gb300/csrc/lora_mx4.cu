@@ -469,7 +469,7 @@ struct Widen {
     {
         mx4_factors(sa, fa1, fa2);
         mx4_factors(sb, fb1, fb2);
-        twice = sa > 142u || sb > 142u;
+        twice = __any_sync(0xffffffffu, sa > MX4_ONE_FACTOR || sb > MX4_ONE_FACTOR);
     }
     __device__ __forceinline__ void operator()(uint32_t a, uint32_t b, uint32_t (&u)[4], uint32_t (&v)[4]) const
     {

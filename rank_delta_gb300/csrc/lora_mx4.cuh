@@ -49,14 +49,21 @@ struct Mx4TcPlan {
     int tn, kparts;
 };
 Mx4TcPlan plan_mx4_tc(const Mx4ProjParams &p, int num_sms);
-cudaError_t launch_mx4_tc(const Mx4ProjParams &p, const Mx4TcPlan &plan, const CUtensorMap &xmap, cudaStream_t st);
+struct Mx4TcMaps {
+    CUtensorMap x;      // boxes of 64 k x tn rows, 128-byte swizzle
+    CUtensorMap codes;  // bytes [N][K / 2], boxes of 128 bytes x 128 rows, 128-byte swizzle
+    CUtensorMap scales; // bytes [N][K / 32], boxes of 16 bytes x 128 rows, when rows lie 16 bytes apart
+    int scales_ok;      // 1: encoded
+};
+cudaError_t launch_mx4_tc(const Mx4ProjParams &p, const Mx4TcPlan &plan, const Mx4TcMaps &maps, cudaStream_t st);
 
-// The bf16 factors that turn an E2M1 value held with its exponent field as in
-// fp16 (that is, value * 2^-112) into value * 2^(byte - 127). The second is 1
-// unless the first would leave bf16's range (byte > 142).
+// The bf16 factors that turn value * 2^-126 (what mx4_unpack8 gives) into value
+// * 2^(byte - 127). The second is 1 unless the first would leave bf16's range
+// (byte > MX4_ONE_FACTOR).
+constexpr uint32_t MX4_ONE_FACTOR = 128;
 __device__ __forceinline__ void mx4_factors(uint32_t byte, uint32_t &f1, uint32_t &f2)
 {
-    const uint32_t e = byte + 112u;
+    const uint32_t e = byte + 126u;
     const uint32_t a = e < 254u ? e : 254u;
     f1 = a << 7;
     f2 = (127u + e - a) << 7;
@@ -73,21 +80,29 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
     return r;
 }
 
-// Eight codes (the lowest four bits first) as bf16 pairs, unscaled: each value
-// times 2^-112 (fp16's five exponent bits moved under bf16's eight).
+template <uint32_t SELECT> __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "n"(SELECT));
+    return r;
+}
+
+// Eight codes (the lowest four bits first) as bf16 pairs in order, each value
+// times 2^-126: a code's three magnitude bits become the two lowest exponent
+// bits and the highest fraction bit (0.5 is a subnormal), its sign bit 15. The
+// even and the odd codes are set apart, a pair's two are put at the bottom of
+// the halves of a word (byte selectors 8.. replicate a sign bit, here zeros),
+// and one product by 2^12 + 2^6 brings both to both places.
 __device__ __forceinline__ void mx4_unpack8(uint32_t w, uint32_t (&o)[4])
 {
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
-        : "r"(w));
+    const uint32_t even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
+    o[0] = prmt<0x8480>(even, odd);
+    o[1] = prmt<0x8581>(even, odd);
+    o[2] = prmt<0x8682>(even, odd);
+    o[3] = prmt<0x8783>(even, odd);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        o[i] = ((o[i] >> 3) & 0x0FFF0FFFu) | (o[i] & 0x80008000u);
+        o[i] = (o[i] * 0x1040u) & 0x81C081C0u;
 }
 
 } // namespace rd

@@ -3,10 +3,9 @@
 // rows.
 //
 // A CTA takes 128 features by one tile of up to 256 rows and a part of K.
-// Eight warps copy the codes of their weight rows into rings of their own
-// (cp.async, 64 bytes of a row at a time), widen them to bf16 exactly and
-// store them as the swizzled K-major operand of tcgen05.mma; x comes by TMA
-// in the same layout; one thread issues the products into TMEM. The weight is
+// The codes come by TMA, 256 k of 128 rows a box; sixteen warps widen them to
+// bf16 exactly and store them as the swizzled K-major operand of tcgen05.mma; x
+// comes by TMA in the same layout; one thread issues the products into TMEM. The weight is
 // widened once for all rows of the tile, so from some 100 rows on the tensor
 // cores are the bound and below it the codes' way from HBM.
 //
@@ -31,18 +30,22 @@ namespace cg = cooperative_groups;
 namespace {
 
 constexpr int BM = 128;             // features of a tile: the UMMA M
-constexpr int MAX_STAGES = 4;       // of 64 k: the A tile (16 KB) and tn rows of x
-constexpr int DEPTH = 4;            // steps of 256 k of codes in flight
+constexpr int MAX_STAGES = 6;       // of 64 k: the A tile (16 KB) and tn rows of x
+constexpr int DEPTH = 3;            // steps of codes in flight: 256 k of 128 rows, and 16 scale bytes a row
+constexpr uint32_t CODE_BYTES = BM * 128, SCALE_BYTES = BM * 16;
+// Groups of four warps (128 rows) that widen, stage n by group n mod groups,
+// and drain the accumulators. Not more than there are stages: a group that
+// waits for its stage's slot has been told, by the wait for its stage before,
+// that the slot's use before the last is through; were that still open, the
+// parity of the last use would not tell the two apart.
+constexpr int groups_of(int stages) { return stages < 4 ? stages : 4; }
+constexpr int threads_of(int stages) { return (groups_of(stages) * 4 + 4) * 32; }
 constexpr uint32_t A_BYTES = BM * 128;
-constexpr int WIDEN_WARPS = 8;      // also the epilogue
-constexpr int TC_THREADS = (WIDEN_WARPS + 3) * 32;
-constexpr uint32_t RING_BYTES = WIDEN_WARPS * 2048; // codes of 128 rows x 256 k
-constexpr uint32_t SRING_BYTES = WIDEN_WARPS * 32 * 4;
 constexpr int MAX_TN = 256;
 constexpr int TILE_STRIDE = BM + 4; // floats of a row of the partial tile
 
 struct TcShared {
-    uint64_t x_full[MAX_STAGES], a_full[MAX_STAGES], empty[MAX_STAGES], routed, done;
+    uint64_t x_full[MAX_STAGES], a_full[MAX_STAGES], empty[MAX_STAGES], c_full[DEPTH], c_free[DEPTH], routed, done;
     uint32_t tmem;
     int bad;                          // a wait gave up
     int nseg;
@@ -54,10 +57,6 @@ struct TcShared {
     const uint16_t *slot_b[MAX_TN];
 };
 
-__device__ __forceinline__ void cp4(uint32_t dst, const void *src, uint32_t bytes)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, uint32_t bytes)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -72,10 +71,10 @@ __device__ __forceinline__ void sts_16(uint32_t addr, uint4 v)
 {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-__device__ __forceinline__ uint32_t lds_4(uint32_t addr)
+__device__ __forceinline__ uint32_t lds_2(uint32_t addr)
 {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
     return v;
 }
 // Byte offset of 16-byte piece c (0..7) of row r in a swizzled 128-byte-row tile.
@@ -88,31 +87,49 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     return r;
 }
 
+// Wait for a phase, at most WAIT_NS; the clock is read only every 256 polls
+// from the first on (a read of it takes longer than a stage).
 __device__ __forceinline__ void wait_or_note(uint64_t *bar, uint32_t parity, int *bad)
 {
-    if (!*reinterpret_cast<volatile int *>(bad) && !mbar_wait(bar, parity))
-        *reinterpret_cast<volatile int *>(bad) = 1;
+    const uint32_t a = smem_u32(bar);
+    uint64_t t0 = 0;
+    for (uint32_t i = 1; !mbar_try_wait(a, parity); ++i) {
+        if ((i & 255u) != 0)
+            continue;
+        const uint64_t t = globaltimer_ns();
+        t0 = t0 == 0 ? t : t0;
+        if (t - t0 > WAIT_NS || *reinterpret_cast<volatile int *>(bad) != 0) {
+            *reinterpret_cast<volatile int *>(bad) = 1;
+            return;
+        }
+    }
 }
 
-// One block: 32 codes and their scale byte -> four 16-byte pieces of bf16.
-__device__ __forceinline__ void widen_store(uint4 codes, uint32_t byte, uint32_t tile, int row, int piece)
+// Two blocks of a row, 32 codes each, and their scale bytes -> the row's 128
+// bytes of bf16.
+__device__ __forceinline__ void widen_store(const uint4 (&codes)[2], uint32_t s0, uint32_t s1, uint32_t tile, int row)
 {
-    uint32_t f1, f2;
-    mx4_factors(byte, f1, f2);
-    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+    uint32_t f1[2], f2[2];
+    mx4_factors(s0, f1[0], f2[0]);
+    mx4_factors(s1, f1[1], f2[1]);
+    const bool twice = __any_sync(0xffffffffu, s0 > MX4_ONE_FACTOR || s1 > MX4_ONE_FACTOR);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        uint32_t o[4];
-        mx4_unpack8(w[j], o);
+    for (int b = 0; b < 2; ++b) {
+        const uint32_t w[4] = {codes[b].x, codes[b].y, codes[b].z, codes[b].w};
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            o[q] = mul_bf16x2(o[q], f1);
-        if (byte > 142u) {
+        for (int j = 0; j < 4; ++j) {
+            uint32_t o[4];
+            mx4_unpack8(w[j], o);
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                o[q] = mul_bf16x2(o[q], f2);
+                o[q] = mul_bf16x2(o[q], f1[b]);
+            if (twice) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    o[q] = mul_bf16x2(o[q], f2[b]);
+            }
+            sts_16(tile + sw128(row, b * 4 + j), make_uint4(o[0], o[1], o[2], o[3]));
         }
-        sts_16(tile + sw128(row, piece + j), make_uint4(o[0], o[1], o[2], o[3]));
     }
 }
 
@@ -168,21 +185,22 @@ __device__ __forceinline__ void route_tile(const Mx4ProjParams &p, TcShared &sh,
 } // namespace
 
 template <int STAGES>
-__global__ void __launch_bounds__(TC_THREADS, 1)
-    mx4_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ Mx4ProjParams p, int tn, int kparts)
+__global__ void __launch_bounds__(threads_of(STAGES), 1)
+    mx4_tc_kernel(const __grid_constant__ Mx4TcMaps maps, const __grid_constant__ Mx4ProjParams p, int tn, int kparts)
 {
+    constexpr int GROUPS = groups_of(STAGES), WIDEN_WARPS = GROUPS * 4;
     extern __shared__ uint8_t tc_smem_raw[];
     __shared__ TcShared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t raw = smem_u32(tc_smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *const smem = tc_smem_raw + (base - raw);
     const uint32_t x_bytes = (uint32_t)tn * 128u;
-    const uint32_t a_at = base, x_at = base + STAGES * A_BYTES, ring = x_at + STAGES * x_bytes,
-                   sring = ring + DEPTH * RING_BYTES;
+    const uint32_t a_at = base, x_at = base + STAGES * A_BYTES, codes_at = x_at + STAGES * x_bytes,
+                   scales_at = codes_at + DEPTH * CODE_BYTES;
     const int part = blockIdx.x % kparts, f0 = (blockIdx.x / kparts) * BM, t0 = blockIdx.y * tn;
-    const int nblk = p.K / 32, nss = (nblk + 7) / 8; // blocks of 32 k, steps of 256 k
-    const int ss0 = (int)((int64_t)nss * part / kparts), ss1 = (int)((int64_t)nss * (part + 1) / kparts);
-    const int nbase = (ss1 - ss0) * 4; // stages of 64 k
+    const int nblk = p.K / 32, nst = (nblk + 1) / 2, nsteps = (nst + 3) / 4; // blocks of 32 k, stages of 64, steps of 256
+    const int j0 = (int)((int64_t)nsteps * part / kparts), j1 = (int)((int64_t)nsteps * (part + 1) / kparts);
+    const int n0 = 4 * j0, nbase = min(nst, 4 * j1) - n0;
     uint32_t cols = 32;
     while ((int)cols < 2 * tn)
         cols *= 2;
@@ -192,6 +210,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             mbar_init(&sh.x_full[s], 1);
             mbar_init(&sh.a_full[s], 128);
             mbar_init(&sh.empty[s], 1);
+        }
+        for (int d = 0; d < DEPTH; ++d) {
+            mbar_init(&sh.c_full[d], 1);
+            mbar_init(&sh.c_free[d], 16); // four warps for each of the step's four stages
         }
         mbar_init(&sh.routed, 1);
         mbar_init(&sh.done, 1);
@@ -206,77 +228,36 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     const uint32_t tmem = sh.tmem;
 
     if (warp < WIDEN_WARPS) {
-        // ---- widen: half of the warps take the first 128 k of each 256, half the others
+        // ---- widen: every GROUPS-th stage of 64 k
         const int group = warp >> 2, row = (warp & 3) * 32 + lane;
         const int rowi = min(f0 + row, p.N - 1); // rows past N repeat the last; their sums are dropped
-        const uint8_t *src[4];
-        uint32_t dst[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) { // four lanes bring 64 bytes of a row
-            const int r = i * 8 + (lane >> 2), pc = lane & 3;
-            src[i] = p.codes + (size_t)min(f0 + (warp & 3) * 32 + r, p.N - 1) * (p.K / 2) + pc * 16;
-            dst[i] = ring + (uint32_t)(warp * 2048 + r * 64 + ((pc ^ ((r >> 1) & 3)) << 4));
-        }
-        const bool word_scales = nblk % 4 == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 3u) == 0;
         const uint8_t *srow = p.scales + (size_t)rowi * nblk;
-        auto fetch = [&](int ss, int slot) {
-            const int b0 = ss * 8 + group * 4;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bool have = b0 + (lane & 3) < nblk;
-                cp16(dst[i] + (uint32_t)slot * RING_BYTES, have ? src[i] + (size_t)b0 * 16 : p.codes, have ? 16u : 0u);
-            }
-            if (word_scales) {
-                const bool have = b0 < nblk;
-                cp4(sring + (uint32_t)slot * SRING_BYTES + tid * 4, have ? srow + b0 : p.scales, have ? 4u : 0u);
-            }
+        auto byte_scales = [&](int n) { // rows of scales that TMA cannot take
+            const int b0 = (n0 + n) * 2;
+            return (uint32_t)__ldg(srow + b0) | (b0 + 1 < nblk ? (uint32_t)__ldg(srow + b0 + 1) << 8 : 0u);
         };
-        auto byte_scales = [&](int ss) { // rows that do not start on a word
-            const int b0 = ss * 8 + group * 4;
-            uint32_t v = 0u;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v |= b0 + i < nblk ? (uint32_t)__ldg(srow + b0 + i) << (8 * i) : 0u;
-            return v;
-        };
-#pragma unroll
-        for (int d = 0; d < DEPTH - 1; ++d) {
-            if (ss0 + d < ss1)
-                fetch(ss0 + d, d);
-            cp_async_commit();
-        }
-        uint32_t sc_next = word_scales ? 0u : byte_scales(ss0);
-        const uint32_t read_at = ring + (uint32_t)(warp * 2048 + lane * 64);
-        const int swz = (lane >> 1) & 3;
-        for (int ss = ss0, slot = 0; ss < ss1; ++ss) {
-            cp_async_wait_group<DEPTH - 2>();
-            __syncwarp(); // the other lanes' copies too, and their reads of the slot filled next
-            uint4 c[4];
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-                c[b] = lds_16(read_at + (uint32_t)slot * RING_BYTES + (uint32_t)((b ^ swz) << 4));
+        uint32_t sc_next = !maps.scales_ok && group < nbase ? byte_scales(group) : 0u;
+        for (int n = group; n < nbase; n += GROUPS) {
+            const int j = n >> 2, cs = j % DEPTH, quarter = n & 3;
+            wait_or_note(&sh.c_full[cs], (uint32_t)(j / DEPTH) & 1u, &sh.bad);
+            const uint32_t at = codes_at + (uint32_t)cs * CODE_BYTES;
+            const uint4 c[2] = {lds_16(at + sw128(row, quarter * 2)), lds_16(at + sw128(row, quarter * 2 + 1))};
             uint32_t sc = sc_next;
-            if (word_scales)
-                sc = lds_4(sring + (uint32_t)slot * SRING_BYTES + tid * 4);
-            else if (ss + 1 < ss1)
-                sc_next = byte_scales(ss + 1);
-            if (ss + DEPTH - 1 < ss1)
-                fetch(ss + DEPTH - 1, slot == 0 ? DEPTH - 1 : slot - 1);
-            cp_async_commit();
-            slot = slot + 1 == DEPTH ? 0 : slot + 1;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int n = (ss - ss0) * 4 + group * 2 + h, s = n % STAGES, use = n / STAGES;
-                if (use > 0)
-                    wait_or_note(&sh.empty[s], (uint32_t)(use - 1) & 1u, &sh.bad);
-                const uint32_t tile = a_at + (uint32_t)s * A_BYTES;
-                widen_store(c[2 * h], (sc >> (16 * h)) & 255u, tile, row, 0);
-                widen_store(c[2 * h + 1], (sc >> (16 * h + 8)) & 255u, tile, row, 4);
-                fence_proxy_async_smem();
-                mbar_arrive(&sh.a_full[s]);
-            }
+            if (maps.scales_ok)
+                sc = lds_2(scales_at + (uint32_t)cs * SCALE_BYTES + row * 16 + ((n0 + n) * 2 & 15));
+            else if (n + GROUPS < nbase)
+                sc_next = byte_scales(n + GROUPS);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.c_free[cs]);
+            const int s = n % STAGES, use = n / STAGES;
+            if (use > 0)
+                wait_or_note(&sh.empty[s], (uint32_t)(use - 1) & 1u, &sh.bad);
+            __syncwarp();
+            widen_store(c, sc & 255u, (sc >> 8) & 255u, a_at + (uint32_t)s * A_BYTES, row);
+            fence_proxy_async_smem();
+            mbar_arrive(&sh.a_full[s]);
         }
-        cp_async_wait_all();
 
         // ---- the adapters' operands: four 16-rank segments a stage
         wait_or_note(&sh.routed, 0, &sh.bad);
@@ -285,7 +266,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         const int rows = min(tn, p.M - t0);
         if (ndelta > 0)
             grid_dependency_wait(); // h is complete
-        for (int d = group; d < ndelta; d += 2) {
+        for (int d = (group + GROUPS - nbase % GROUPS) % GROUPS; d < ndelta; d += GROUPS) {
             const int n = nbase + d, s = n % STAGES, use = n / STAGES;
             if (use > 0)
                 wait_or_note(&sh.empty[s], (uint32_t)(use - 1) & 1u, &sh.bad);
@@ -332,7 +313,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         float *tile = reinterpret_cast<float *>(smem); // every product has read its operands
         const int f = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        for (int c = group; c < tn / 16; c += 2) {
+        for (int c = group; c < tn / 16; c += GROUPS) {
             float v[16];
             tmem_ld16(tmem + lanes + (uint32_t)(c * 16), v);
             if (ndelta > 0) {
@@ -355,13 +336,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     } else if (warp == WIDEN_WARPS) {
         // ---- x
         if (lane == 0) {
-            prefetch_tmap(&xmap);
+            prefetch_tmap(&maps.x);
             for (int n = 0; n < nbase; ++n) {
                 const int s = n % STAGES, use = n / STAGES;
                 if (use > 0)
                     wait_or_note(&sh.empty[s], (uint32_t)(use - 1) & 1u, &sh.bad);
                 mbar_arrive_expect_tx(&sh.x_full[s], x_bytes);
-                tma_load_2d(smem + STAGES * A_BYTES + (uint32_t)s * x_bytes, &xmap, (ss0 * 4 + n) * 64, t0, &sh.x_full[s]);
+                tma_load_2d(smem + STAGES * A_BYTES + (uint32_t)s * x_bytes, &maps.x, (n0 + n) * 64, t0, &sh.x_full[s]);
             }
         }
         __syncwarp();
@@ -393,6 +374,22 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 umma_commit(&sh.empty[s]);
             }
             umma_commit(&sh.done);
+        }
+        __syncwarp();
+    } else if (warp == WIDEN_WARPS + 2) {
+        // ---- codes and scales
+        if (lane == 0) {
+            for (int j = 0; 4 * j < nbase; ++j) {
+                const int cs = j % DEPTH, use = j / DEPTH;
+                if (use > 0)
+                    wait_or_note(&sh.c_free[cs], (uint32_t)(use - 1) & 1u, &sh.bad);
+                mbar_arrive_expect_tx(&sh.c_full[cs], CODE_BYTES + (maps.scales_ok ? SCALE_BYTES : 0u));
+                uint8_t *at = smem + STAGES * (A_BYTES + x_bytes);
+                tma_load_2d(at + (uint32_t)cs * CODE_BYTES, &maps.codes, (j0 + j) * 128, f0, &sh.c_full[cs]);
+                if (maps.scales_ok) // the 16 bytes that hold the step's eight
+                    tma_load_2d(at + DEPTH * CODE_BYTES + (uint32_t)cs * SCALE_BYTES, &maps.scales, ((j0 + j) * 8) & ~15, f0,
+                                &sh.c_full[cs]);
+            }
         }
         __syncwarp();
     } else {
@@ -436,11 +433,11 @@ namespace {
 
 uint32_t tc_smem(int tn, int stages)
 {
-    return 1024u + (uint32_t)stages * (A_BYTES + (uint32_t)tn * 128u) + DEPTH * (RING_BYTES + SRING_BYTES);
+    return 1024u + (uint32_t)stages * (A_BYTES + (uint32_t)tn * 128u) + DEPTH * (CODE_BYTES + SCALE_BYTES);
 }
 
 template <int STAGES>
-cudaError_t launch(const Mx4ProjParams &p, const Mx4TcPlan &plan, const CUtensorMap &xmap, cudaStream_t st)
+cudaError_t launch(const Mx4ProjParams &p, const Mx4TcPlan &plan, const Mx4TcMaps &maps, cudaStream_t st)
 {
     static std::atomic<uint64_t> raised{0};
     cudaError_t e = raise_smem_limit(raised, mx4_tc_kernel<STAGES>, 222 * 1024);
@@ -454,12 +451,12 @@ cudaError_t launch(const Mx4ProjParams &p, const Mx4TcPlan &plan, const CUtensor
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((p.N + BM - 1) / BM * plan.kparts), (unsigned)((p.M + plan.tn - 1) / plan.tn));
-    cfg.blockDim = dim3(TC_THREADS);
+    cfg.blockDim = dim3((unsigned)threads_of(STAGES));
     cfg.dynamicSmemBytes = tc_smem(plan.tn, STAGES);
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, mx4_tc_kernel<STAGES>, xmap, p, plan.tn, plan.kparts);
+    return cudaLaunchKernelEx(&cfg, mx4_tc_kernel<STAGES>, maps, p, plan.tn, plan.kparts);
 }
 
 } // namespace
@@ -469,16 +466,19 @@ Mx4TcPlan plan_mx4_tc(const Mx4ProjParams &p, int num_sms)
     Mx4TcPlan plan;
     const int tiles = (p.M + MAX_TN - 1) / MAX_TN, each = (p.M + tiles - 1) / tiles;
     plan.tn = (each + 15) / 16 * 16;
-    const int ctas = (p.N + BM - 1) / BM * tiles, nss = (p.K / 32 + 7) / 8;
+    const int ctas = (p.N + BM - 1) / BM * tiles, nst = (p.K / 32 + 1) / 2;
     plan.kparts = 1;
-    while (plan.kparts < 8 && ctas * plan.kparts * 2 <= num_sms && nss >= 2 * plan.kparts)
+    while (plan.kparts < 8 && ctas * plan.kparts * 2 <= num_sms && nst >= 8 * plan.kparts)
         plan.kparts *= 2;
     return plan;
 }
 
-cudaError_t launch_mx4_tc(const Mx4ProjParams &p, const Mx4TcPlan &plan, const CUtensorMap &xmap, cudaStream_t st)
+cudaError_t launch_mx4_tc(const Mx4ProjParams &p, const Mx4TcPlan &plan, const Mx4TcMaps &maps, cudaStream_t st)
 {
-    return plan.tn <= 128 ? launch<4>(p, plan, xmap, st) : launch<3>(p, plan, xmap, st); // what fits in 227 KB
+    // as many stages as fit in 227 KB
+    if (plan.tn <= 64)
+        return launch<6>(p, plan, maps, st);
+    return plan.tn <= 128 ? launch<4>(p, plan, maps, st) : launch<3>(p, plan, maps, st);
 }
 
 } // namespace rd
