@@ -30,22 +30,33 @@ namespace cg = cooperative_groups;
 namespace {
 
 constexpr int BM = 128;             // features of a tile: the UMMA M
-constexpr int MAX_STAGES = 6;       // of 64 k: the A tile (16 KB) and tn rows of x
-constexpr int DEPTH = 3;            // steps of codes in flight: 256 k of 128 rows, and 16 scale bytes a row
+// Three rings between TMA, the widening warps and the products. A stage is SUB
+// sub-tiles of 64 k: AS slots of widened weights (16 KB a sub-tile), XS slots of
+// tn rows of x (tn 128 bytes), CS steps of codes (256 k of 128 rows, and 16 scale
+// bytes a row). Groups of four warps (128 rows) widen, sub-tile m by group m mod
+// GROUPS, and drain the accumulators.
+//
+// The thread that issues the products spends some 100 cycles on each wait and
+// more on a commit, which is longer than the products of 64 k take for up to
+// about 128 rows: there a stage has two sub-tiles.
+template <int SUB_, int AS_, int XS_, int CS_> struct Rings {
+    static constexpr int SUB = SUB_, AS = AS_, XS = XS_, CS = CS_;
+    static constexpr int GROUPS = SUB == 1 && AS < 4 ? AS : 4, WARPS = GROUPS * 4, THREADS = (WARPS + 4) * 32;
+    // A group that waits for its stage's slot has been told, by the wait for its
+    // stage before (GROUPS / SUB stages earlier), that the slot's use before the
+    // last is through; were that still open, the parity of the last use would
+    // not tell the two apart.
+    static_assert(AS >= GROUPS / SUB && XS >= AS, "parity of a slot's last use");
+};
+constexpr int MAX_RING = 16;
 constexpr uint32_t CODE_BYTES = BM * 128, SCALE_BYTES = BM * 16;
-// Groups of four warps (128 rows) that widen, stage n by group n mod groups,
-// and drain the accumulators. Not more than there are stages: a group that
-// waits for its stage's slot has been told, by the wait for its stage before,
-// that the slot's use before the last is through; were that still open, the
-// parity of the last use would not tell the two apart.
-constexpr int groups_of(int stages) { return stages < 4 ? stages : 4; }
-constexpr int threads_of(int stages) { return (groups_of(stages) * 4 + 4) * 32; }
 constexpr uint32_t A_BYTES = BM * 128;
 constexpr int MAX_TN = 256;
 constexpr int TILE_STRIDE = BM + 4; // floats of a row of the partial tile
 
 struct TcShared {
-    uint64_t x_full[MAX_STAGES], a_full[MAX_STAGES], empty[MAX_STAGES], c_full[DEPTH], c_free[DEPTH], routed, done;
+    uint64_t x_full[MAX_RING], x_free[MAX_RING], a_full[MAX_RING], a_free[MAX_RING], c_full[MAX_RING], c_free[MAX_RING];
+    uint64_t routed, done;
     uint32_t tmem;
     int bad;                          // a wait gave up
     int nseg;
@@ -105,9 +116,30 @@ __device__ __forceinline__ void wait_or_note(uint64_t *bar, uint32_t parity, int
     }
 }
 
+// umma_bf16 and umma_commit by the lanes with lead != 0.
+__device__ __forceinline__ void umma_bf16_by(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p, q;\n\t"
+                 "setp.ne.b32 q, %5, 0;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+                 : "memory");
+}
+__device__ __forceinline__ void umma_commit_by(uint32_t lead, uint64_t *bar)
+{
+    asm volatile("{\n\t.reg .pred q;\n\t"
+                 "setp.ne.b32 q, %1, 0;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+                 "r"(lead)
+                 : "memory");
+}
+
 // Two blocks of a row, 32 codes each, and their scale bytes -> the row's 128
-// bytes of bf16.
-__device__ __forceinline__ void widen_store(const uint4 (&codes)[2], uint32_t s0, uint32_t s1, uint32_t tile, int row)
+// bytes of bf16. row_at is where its piece 0 lies: the swizzle's exclusive or
+// with the row goes into the address once.
+__device__ __forceinline__ void widen_store(const uint4 (&codes)[2], uint32_t s0, uint32_t s1, uint32_t row_at)
 {
     uint32_t f1[2], f2[2];
     mx4_factors(s0, f1[0], f2[0]);
@@ -128,7 +160,7 @@ __device__ __forceinline__ void widen_store(const uint4 (&codes)[2], uint32_t s0
                 for (int q = 0; q < 4; ++q)
                     o[q] = mul_bf16x2(o[q], f2[b]);
             }
-            sts_16(tile + sw128(row, b * 4 + j), make_uint4(o[0], o[1], o[2], o[3]));
+            sts_16(row_at ^ (uint32_t)((b * 4 + j) << 4), make_uint4(o[0], o[1], o[2], o[3]));
         }
     }
 }
@@ -184,36 +216,40 @@ __device__ __forceinline__ void route_tile(const Mx4ProjParams &p, TcShared &sh,
 
 } // namespace
 
-template <int STAGES>
-__global__ void __launch_bounds__(threads_of(STAGES), 1)
+template <typename RINGS>
+__global__ void __launch_bounds__(RINGS::THREADS, 1)
     mx4_tc_kernel(const __grid_constant__ Mx4TcMaps maps, const __grid_constant__ Mx4ProjParams p, int tn, int kparts)
 {
-    constexpr int GROUPS = groups_of(STAGES), WIDEN_WARPS = GROUPS * 4;
+    constexpr int SUB = RINGS::SUB, AS = RINGS::AS, XS = RINGS::XS, CS = RINGS::CS, GROUPS = RINGS::GROUPS, WIDEN_WARPS = RINGS::WARPS;
     extern __shared__ uint8_t tc_smem_raw[];
     __shared__ TcShared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t raw = smem_u32(tc_smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *const smem = tc_smem_raw + (base - raw);
     const uint32_t x_bytes = (uint32_t)tn * 128u;
-    const uint32_t a_at = base, x_at = base + STAGES * A_BYTES, codes_at = x_at + STAGES * x_bytes,
-                   scales_at = codes_at + DEPTH * CODE_BYTES;
+    const uint32_t a_at = base, x_at = base + AS * SUB * A_BYTES, codes_at = x_at + XS * SUB * x_bytes,
+                   scales_at = codes_at + CS * CODE_BYTES;
     const int part = blockIdx.x % kparts, f0 = (blockIdx.x / kparts) * BM, t0 = blockIdx.y * tn;
-    const int nblk = p.K / 32, nst = (nblk + 1) / 2, nsteps = (nst + 3) / 4; // blocks of 32 k, stages of 64, steps of 256
+    const int nblk = p.K / 32, nst = (nblk + 1) / 2, nsteps = (nst + 3) / 4; // blocks of 32 k, sub-tiles of 64, steps of 256
     const int j0 = (int)((int64_t)nsteps * part / kparts), j1 = (int)((int64_t)nsteps * (part + 1) / kparts);
-    const int n0 = 4 * j0, nbase = min(nst, 4 * j1) - n0;
+    // sub-tiles of the part, whole stages (past K both operands are zeros)
+    const int m0 = 4 * j0, mbase = (min(nst, 4 * j1) - m0 + SUB - 1) / SUB * SUB, nbase = mbase / SUB;
     uint32_t cols = 32;
     while ((int)cols < 2 * tn)
         cols *= 2;
 
     if (tid == 0) {
-        for (int s = 0; s < STAGES; ++s) {
+        for (int s = 0; s < XS; ++s) {
             mbar_init(&sh.x_full[s], 1);
-            mbar_init(&sh.a_full[s], 128);
-            mbar_init(&sh.empty[s], 1);
+            mbar_init(&sh.x_free[s], 1);
         }
-        for (int d = 0; d < DEPTH; ++d) {
-            mbar_init(&sh.c_full[d], 1);
-            mbar_init(&sh.c_free[d], 16); // four warps for each of the step's four stages
+        for (int s = 0; s < AS; ++s) {
+            mbar_init(&sh.a_full[s], 4 * SUB); // the groups' warps
+            mbar_init(&sh.a_free[s], 1);
+        }
+        for (int s = 0; s < CS; ++s) {
+            mbar_init(&sh.c_full[s], 1);
+            mbar_init(&sh.c_free[s], 16); // four warps for each of the step's four stages
         }
         mbar_init(&sh.routed, 1);
         mbar_init(&sh.done, 1);
@@ -228,49 +264,55 @@ __global__ void __launch_bounds__(threads_of(STAGES), 1)
     const uint32_t tmem = sh.tmem;
 
     if (warp < WIDEN_WARPS) {
-        // ---- widen: every GROUPS-th stage of 64 k
+        // ---- widen: every GROUPS-th sub-tile
         const int group = warp >> 2, row = (warp & 3) * 32 + lane;
         const int rowi = min(f0 + row, p.N - 1); // rows past N repeat the last; their sums are dropped
         const uint8_t *srow = p.scales + (size_t)rowi * nblk;
-        auto byte_scales = [&](int n) { // rows of scales that TMA cannot take
-            const int b0 = (n0 + n) * 2;
-            return (uint32_t)__ldg(srow + b0) | (b0 + 1 < nblk ? (uint32_t)__ldg(srow + b0 + 1) << 8 : 0u);
+        auto byte_scales = [&](int m) { // rows of scales that TMA cannot take
+            const int b0 = (m0 + m) * 2;
+            return (b0 < nblk ? (uint32_t)__ldg(srow + b0) : 0u) | (b0 + 1 < nblk ? (uint32_t)__ldg(srow + b0 + 1) << 8 : 0u);
         };
-        uint32_t sc_next = !maps.scales_ok && group < nbase ? byte_scales(group) : 0u;
-        for (int n = group; n < nbase; n += GROUPS) {
-            const int j = n >> 2, cs = j % DEPTH, quarter = n & 3;
-            wait_or_note(&sh.c_full[cs], (uint32_t)(j / DEPTH) & 1u, &sh.bad);
+        uint32_t sc_next = !maps.scales_ok && group < mbase ? byte_scales(group) : 0u;
+        const uint32_t own = sw128(row, 0);
+        for (int m = group; m < mbase; m += GROUPS) {
+            const int j = m >> 2, cs = j % CS, quarter = m & 3;
+            wait_or_note(&sh.c_full[cs], (uint32_t)(j / CS) & 1u, &sh.bad);
             const uint32_t at = codes_at + (uint32_t)cs * CODE_BYTES;
-            const uint4 c[2] = {lds_16(at + sw128(row, quarter * 2)), lds_16(at + sw128(row, quarter * 2 + 1))};
+            const uint4 c[2] = {lds_16((at + own) ^ (uint32_t)(quarter << 5)), lds_16((at + own) ^ (uint32_t)(quarter << 5 | 16))};
             uint32_t sc = sc_next;
             if (maps.scales_ok)
-                sc = lds_2(scales_at + (uint32_t)cs * SCALE_BYTES + row * 16 + ((n0 + n) * 2 & 15));
-            else if (n + GROUPS < nbase)
-                sc_next = byte_scales(n + GROUPS);
+                sc = lds_2(scales_at + (uint32_t)cs * SCALE_BYTES + row * 16 + ((m0 + m) * 2 & 15));
+            else if (m + GROUPS < mbase)
+                sc_next = byte_scales(m + GROUPS);
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&sh.c_free[cs]);
-            const int s = n % STAGES, use = n / STAGES;
+            const int n = m / SUB, s = n % AS, use = n / AS;
             if (use > 0)
-                wait_or_note(&sh.empty[s], (uint32_t)(use - 1) & 1u, &sh.bad);
+                wait_or_note(&sh.a_free[s], (uint32_t)(use - 1) & 1u, &sh.bad);
             __syncwarp();
-            widen_store(c, sc & 255u, (sc >> 8) & 255u, a_at + (uint32_t)s * A_BYTES, row);
+            widen_store(c, sc & 255u, (sc >> 8) & 255u, a_at + (uint32_t)(s * SUB + m % SUB) * A_BYTES + own);
             fence_proxy_async_smem();
-            mbar_arrive(&sh.a_full[s]);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.a_full[s]);
         }
 
-        // ---- the adapters' operands: four 16-rank segments a stage
+        // ---- the adapters' operands: four 16-rank segments a sub-tile
         wait_or_note(&sh.routed, 0, &sh.bad);
         const int q0 = sh.nseg * part / kparts, q1 = sh.nseg * (part + 1) / kparts;
-        const int ndelta = __any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&sh.bad) != 0) ? 0 : (q1 - q0 + 3) / 4;
+        const int ndelta = __any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&sh.bad) != 0) ? 0 : (q1 - q0 + 4 * SUB - 1) / (4 * SUB) * SUB;
         const int rows = min(tn, p.M - t0);
         if (ndelta > 0)
             grid_dependency_wait(); // h is complete
-        for (int d = (group + GROUPS - nbase % GROUPS) % GROUPS; d < ndelta; d += GROUPS) {
-            const int n = nbase + d, s = n % STAGES, use = n / STAGES;
+        for (int d = (group + GROUPS - mbase % GROUPS) % GROUPS; d < ndelta; d += GROUPS) {
+            const int n = nbase + d / SUB, s = n % AS, use = n / AS, xslot = n % XS, xuse = n / XS;
             if (use > 0)
-                wait_or_note(&sh.empty[s], (uint32_t)(use - 1) & 1u, &sh.bad);
-            const uint32_t at = a_at + (uint32_t)s * A_BYTES, xt = x_at + (uint32_t)s * x_bytes;
+                wait_or_note(&sh.a_free[s], (uint32_t)(use - 1) & 1u, &sh.bad);
+            if (xuse > 0)
+                wait_or_note(&sh.x_free[xslot], (uint32_t)(xuse - 1) & 1u, &sh.bad);
+            const uint32_t at = a_at + (uint32_t)(s * SUB + d % SUB) * A_BYTES,
+                           xt = x_at + (uint32_t)(xslot * SUB + d % SUB) * x_bytes;
             const int nk = min(4, q1 - q0 - 4 * d);
             for (int j = 0; j < nk; ++j) {
                 const int q = q0 + 4 * d + j;
@@ -303,7 +345,9 @@ __global__ void __launch_bounds__(threads_of(STAGES), 1)
             }
             cp_async_wait_all();
             fence_proxy_async_smem();
-            mbar_arrive(&sh.a_full[s]);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.a_full[s]);
         }
 
         // ---- the accumulators
@@ -338,56 +382,74 @@ __global__ void __launch_bounds__(threads_of(STAGES), 1)
         if (lane == 0) {
             prefetch_tmap(&maps.x);
             for (int n = 0; n < nbase; ++n) {
-                const int s = n % STAGES, use = n / STAGES;
+                const int s = n % XS, use = n / XS;
                 if (use > 0)
-                    wait_or_note(&sh.empty[s], (uint32_t)(use - 1) & 1u, &sh.bad);
-                mbar_arrive_expect_tx(&sh.x_full[s], x_bytes);
-                tma_load_2d(smem + STAGES * A_BYTES + (uint32_t)s * x_bytes, &maps.x, (n0 + n) * 64, t0, &sh.x_full[s]);
+                    wait_or_note(&sh.x_free[s], (uint32_t)(use - 1) & 1u, &sh.bad);
+                mbar_arrive_expect_tx(&sh.x_full[s], SUB * x_bytes);
+                for (int h = 0; h < SUB; ++h)
+                    tma_load_2d(smem + AS * SUB * A_BYTES + (uint32_t)(s * SUB + h) * x_bytes, &maps.x, (m0 + n * SUB + h) * 64,
+                                t0, &sh.x_full[s]);
             }
         }
         __syncwarp();
     } else if (warp == WIDEN_WARPS + 1) {
-        // ---- products
-        if (lane == 0) {
-            const uint32_t idesc = idesc_bf16_f32(BM, (uint32_t)tn);
-            for (int n = 0; n < nbase; ++n) {
-                const int s = n % STAGES;
-                const uint32_t parity = (uint32_t)(n / STAGES) & 1u;
-                wait_or_note(&sh.x_full[s], parity, &sh.bad);
-                wait_or_note(&sh.a_full[s], parity, &sh.bad);
-                tc_fence_after();
+        // ---- products: the whole warp goes along, so that what the instructions
+        // take is known to be the same in all lanes; lane 0 issues
+        const uint32_t lead = lane == 0 ? 1u : 0u, idesc = idesc_bf16_f32(BM, (uint32_t)tn);
+        const uint64_t adesc = sw128_kmajor_desc(a_at), xdesc = sw128_kmajor_desc(x_at);
+        auto stage = [&](uint32_t d_tmem, int s, int xslot, int steps, bool first) {
+            const uint64_t ad = adesc + (uint64_t)(uint32_t)(s * SUB) * (A_BYTES >> 4);
+            const uint64_t xd = xdesc + (uint64_t)((uint32_t)(xslot * SUB) * (x_bytes >> 4));
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    umma_bf16(tmem, sw128_kmajor_desc(a_at + (uint32_t)s * A_BYTES + j * 32),
-                              sw128_kmajor_desc(x_at + (uint32_t)s * x_bytes + j * 32), idesc, (n | j) != 0 ? 1u : 0u);
-                umma_commit(&sh.empty[s]);
+            for (int j = 0; j < 4 * SUB; ++j)
+                if (j < steps)
+                    umma_bf16_by(lead, d_tmem, ad + (uint64_t)((j >> 2) * (A_BYTES >> 4) + (j & 3) * 2),
+                                 xd + (uint64_t)((uint32_t)(j >> 2) * (x_bytes >> 4) + (uint32_t)(j & 3) * 2u), idesc,
+                                 first && j == 0 ? 0u : 1u);
+            umma_commit_by(lead, &sh.a_free[s]);
+            umma_commit_by(lead, &sh.x_free[xslot]);
+        };
+        int s = 0, xslot = 0;
+        uint32_t a_parity = 0, x_parity = 0;
+        auto advance = [&] {
+            if (++s == AS) {
+                s = 0;
+                a_parity ^= 1u;
             }
-            wait_or_note(&sh.routed, 0, &sh.bad);
-            const int q0 = sh.nseg * part / kparts, q1 = sh.nseg * (part + 1) / kparts;
-            for (int d = 0; 4 * d < q1 - q0 && !*reinterpret_cast<volatile int *>(&sh.bad); ++d) {
-                const int n = nbase + d, s = n % STAGES, nk = min(4, q1 - q0 - 4 * d);
-                wait_or_note(&sh.a_full[s], (uint32_t)(n / STAGES) & 1u, &sh.bad);
-                tc_fence_after();
-                for (int j = 0; j < nk; ++j)
-                    umma_bf16(tmem + (uint32_t)tn, sw128_kmajor_desc(a_at + (uint32_t)s * A_BYTES + j * 32),
-                              sw128_kmajor_desc(x_at + (uint32_t)s * x_bytes + j * 32), idesc, (d | j) != 0 ? 1u : 0u);
-                umma_commit(&sh.empty[s]);
+            if (++xslot == XS) {
+                xslot = 0;
+                x_parity ^= 1u;
             }
-            umma_commit(&sh.done);
+        };
+        for (int n = 0; n < nbase; ++n) {
+            wait_or_note(&sh.x_full[xslot], x_parity, &sh.bad);
+            wait_or_note(&sh.a_full[s], a_parity, &sh.bad);
+            tc_fence_after();
+            stage(tmem, s, xslot, 4 * SUB, n == 0);
+            advance();
         }
+        wait_or_note(&sh.routed, 0, &sh.bad);
+        const int q0 = sh.nseg * part / kparts, q1 = sh.nseg * (part + 1) / kparts;
+        for (int q = q0; q < q1 && !__any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&sh.bad) != 0); q += 4 * SUB) {
+            wait_or_note(&sh.a_full[s], a_parity, &sh.bad);
+            tc_fence_after();
+            stage(tmem + (uint32_t)tn, s, xslot, q1 - q, q == q0);
+            advance();
+        }
+        umma_commit_by(lead, &sh.done);
         __syncwarp();
     } else if (warp == WIDEN_WARPS + 2) {
         // ---- codes and scales
         if (lane == 0) {
-            for (int j = 0; 4 * j < nbase; ++j) {
-                const int cs = j % DEPTH, use = j / DEPTH;
+            for (int j = 0; 4 * j < mbase; ++j) {
+                const int cs = j % CS, use = j / CS;
                 if (use > 0)
                     wait_or_note(&sh.c_free[cs], (uint32_t)(use - 1) & 1u, &sh.bad);
                 mbar_arrive_expect_tx(&sh.c_full[cs], CODE_BYTES + (maps.scales_ok ? SCALE_BYTES : 0u));
-                uint8_t *at = smem + STAGES * (A_BYTES + x_bytes);
+                uint8_t *at = smem + AS * SUB * A_BYTES + XS * SUB * x_bytes;
                 tma_load_2d(at + (uint32_t)cs * CODE_BYTES, &maps.codes, (j0 + j) * 128, f0, &sh.c_full[cs]);
                 if (maps.scales_ok) // the 16 bytes that hold the step's eight
-                    tma_load_2d(at + DEPTH * CODE_BYTES + (uint32_t)cs * SCALE_BYTES, &maps.scales, ((j0 + j) * 8) & ~15, f0,
+                    tma_load_2d(at + CS * CODE_BYTES + (uint32_t)cs * SCALE_BYTES, &maps.scales, ((j0 + j) * 8) & ~15, f0,
                                 &sh.c_full[cs]);
             }
         }
@@ -431,16 +493,11 @@ __global__ void __launch_bounds__(threads_of(STAGES), 1)
 
 namespace {
 
-uint32_t tc_smem(int tn, int stages)
-{
-    return 1024u + (uint32_t)stages * (A_BYTES + (uint32_t)tn * 128u) + DEPTH * (CODE_BYTES + SCALE_BYTES);
-}
-
-template <int STAGES>
+template <typename RINGS>
 cudaError_t launch(const Mx4ProjParams &p, const Mx4TcPlan &plan, const Mx4TcMaps &maps, cudaStream_t st)
 {
     static std::atomic<uint64_t> raised{0};
-    cudaError_t e = raise_smem_limit(raised, mx4_tc_kernel<STAGES>, 222 * 1024);
+    cudaError_t e = raise_smem_limit(raised, mx4_tc_kernel<RINGS>, 222 * 1024);
     if (e != cudaSuccess)
         return e;
     cudaLaunchAttribute attr[2];
@@ -451,12 +508,13 @@ cudaError_t launch(const Mx4ProjParams &p, const Mx4TcPlan &plan, const Mx4TcMap
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((p.N + BM - 1) / BM * plan.kparts), (unsigned)((p.M + plan.tn - 1) / plan.tn));
-    cfg.blockDim = dim3((unsigned)threads_of(STAGES));
-    cfg.dynamicSmemBytes = tc_smem(plan.tn, STAGES);
+    cfg.blockDim = dim3((unsigned)RINGS::THREADS);
+    cfg.dynamicSmemBytes = 1024u + RINGS::SUB * (RINGS::AS * A_BYTES + RINGS::XS * (uint32_t)plan.tn * 128u) +
+                           RINGS::CS * (CODE_BYTES + SCALE_BYTES);
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, mx4_tc_kernel<STAGES>, maps, p, plan.tn, plan.kparts);
+    return cudaLaunchKernelEx(&cfg, mx4_tc_kernel<RINGS>, maps, p, plan.tn, plan.kparts);
 }
 
 } // namespace
@@ -475,10 +533,9 @@ Mx4TcPlan plan_mx4_tc(const Mx4ProjParams &p, int num_sms)
 
 cudaError_t launch_mx4_tc(const Mx4ProjParams &p, const Mx4TcPlan &plan, const Mx4TcMaps &maps, cudaStream_t st)
 {
-    // as many stages as fit in 227 KB
     if (plan.tn <= 64)
-        return launch<6>(p, plan, maps, st);
-    return plan.tn <= 128 ? launch<4>(p, plan, maps, st) : launch<3>(p, plan, maps, st);
+        return launch<Rings<2, 3, 4, 3>>(p, plan, maps, st); // what fits in 227 KB
+    return plan.tn <= 128 ? launch<Rings<2, 2, 3, 3>>(p, plan, maps, st) : launch<Rings<1, 3, 4, 2>>(p, plan, maps, st);
 }
 
 } // namespace rd
