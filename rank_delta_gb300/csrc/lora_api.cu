@@ -1500,7 +1500,9 @@ size_t lora_mx4_proj_workspace_bytes_ex(int M, const lora_route *rt, int path)
         return 0;
     if (mx4_path(M, path) == LORA_MX4_PATH_EXPAND) // the projection's, then the weight in bf16
         return align256(lora_proj_workspace_bytes(M, rt)) + align256((size_t)rt->n_out * (size_t)rt->n_in * 2);
-    return align256(256 + sizeof(float) * (size_t)M * (size_t)rt->max_rank); // status, h
+    // status, h in fp32, h in bf16
+    return align256(256 + sizeof(float) * (size_t)M * (size_t)rt->max_rank) +
+           align256(sizeof(uint16_t) * (size_t)M * (size_t)rt->max_rank);
 }
 
 size_t lora_mx4_proj_workspace_bytes(int M, const lora_route *rt)
@@ -1578,6 +1580,7 @@ lora_status lora_mx4_proj_apply_ex(const void *x, int64_t x_stride, const uint8_
     q.tab = tables_of(*rt);
     q.status = static_cast<uint32_t *>(ws);
     q.h = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + 256);
+    q.hs = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(ws) + align256(256 + sizeof(float) * (size_t)M * (size_t)q.R));
     q.y = static_cast<uint16_t *>(y);
     q.y_stride = y_stride;
     if ((e = launch_mx4_shrink(q, st)) != cudaSuccess)

@@ -252,28 +252,69 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
 
 constexpr int SH_WARPS = 16;     // they share K
 constexpr int SH_THREADS = SH_WARPS * 32;
-constexpr int SH_ROWS = 64;     // rows a CTA looks through for its slot
-constexpr int SH_TILE = 16;     // rows a pass
+constexpr int SH_ROWS = 64;      // rows a CTA looks through for its slot
+constexpr int SH_PAIR = 16;      // rows whose sums are joined at a time
 
 __device__ __forceinline__ void grid_dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// NT * 8 rows of the slot (from i0; past the last they repeat it) against 16
+// rank rows over the warp's blocks of 32 k, `AHEAD` blocks' loads in flight.
+template <int NT, int AHEAD>
+__device__ __forceinline__ void shrink_tile(const Mx4ProjParams &p, const uint16_t *ra, const uint16_t *rb, const int *rows,
+                                            int count, int i0, int b0, int b1, int g, int t, float (&acc)[NT][4])
+{
+    const uint16_t *x[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        x[n] = p.x + (int64_t)rows[min(i0 + n * 8 + g, count - 1)] * p.x_stride + t * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            acc[n][i] = 0.0f;
+    }
+    for (int b = b0; b < b1; b += AHEAD) {
+        uint4 va[AHEAD], vb[AHEAD], vx[AHEAD][NT];
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+            const bool have = b + a < b1;
+            const uint4 z = make_uint4(0, 0, 0, 0);
+            va[a] = have ? ld_nc_16(ra + (b + a) * 32) : z;
+            vb[a] = have ? ld_nc_16(rb + (b + a) * 32) : z;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                vx[a][n] = have ? ld_nc_16(x[n] + (b + a) * 32) : z;
+        }
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                mma_16816(acc[n], va[a].x, vb[a].x, va[a].y, vb[a].y, vx[a][n].x, vx[a][n].y);
+                mma_16816(acc[n], va[a].z, vb[a].z, va[a].w, vb[a].w, vx[a][n].z, vx[a][n].w);
+            }
+    }
+}
+
 } // namespace
 
-// Grid: 16-rank groups, by the u-th distinct slot of a 64-row chunk, by
-// chunks. Each thread multiplies 8 consecutive k of two rank rows
-// and two batch rows at a time: which k a fragment's slots mean is free as
-// long as both operands agree.
+// Grid: 16-rank groups, by slots (or, for more than SH_ROWS of them, the u-th
+// distinct slot of the chunk), by 64-row chunks. Each thread multiplies 8
+// consecutive k of two rank rows and of the slot's rows at a time: which k a
+// fragment's slots mean is free as long as both operands agree.
 __global__ void __launch_bounds__(SH_THREADS) mx4_shrink_kernel(Mx4ProjParams p)
 {
     __shared__ uint32_t present[MAX_BUCKETS / 32];
     __shared__ int slot_s, count_s, rows_s[SH_ROWS];
-    __shared__ float red[SH_WARPS][16][SH_TILE + 1];
+    __shared__ float red[SH_WARPS][16][SH_PAIR + 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int r0 = blockIdx.x * 16, u = blockIdx.y, c0 = blockIdx.z * SH_ROWS;
     // Launched early behind whatever the stream ran before; nothing is read
     // until that is complete, and only then may the projection kernel start.
     grid_dependency_wait();
     grid_dependents_launch();
+    const int mine = tid < SH_ROWS && c0 + tid < p.M ? p.seq_slot[c0 + tid] : -1;
+    SlotInfo si;
+    int slot = u;
+    if (p.L <= SH_ROWS)
+        si = slot_info(p.tab, slot, p.L); // on its way with the rows' slots
     if (blockIdx.x == 0 && u == 0 && c0 == 0) { // the call's status
         int bad = 0;
         for (int i = tid; i < p.M; i += SH_THREADS)
@@ -282,98 +323,102 @@ __global__ void __launch_bounds__(SH_THREADS) mx4_shrink_kernel(Mx4ProjParams p)
         if (tid == 0)
             status_begin(p.status, bad ? (uint32_t)LORA_FLAG_SLOT_RANGE : 0u);
     }
-    // the u-th distinct slot among the chunk's rows, and its rows in order
-    for (int i = tid; i < (p.L + 31) / 32; i += SH_THREADS)
-        present[i] = 0u;
-    int mine = -1;
-    if (tid < SH_ROWS && c0 + tid < p.M)
-        mine = p.seq_slot[c0 + tid];
-    if (mine >= p.L)
-        mine = -1;
-    __syncthreads();
-    if (mine >= 0)
-        atomicOr(&present[mine >> 5], 1u << (mine & 31));
-    if (tid == 0)
-        slot_s = -1;
-    __syncthreads();
-    if (warp == 0) {
-        const uint32_t w = lane < (p.L + 31) / 32 ? present[lane] : 0u;
-        int incl = __popc(w);
+    if (p.L > SH_ROWS) { // the u-th distinct slot among the chunk's rows
+        present[lane] = 0u;
+        if (tid == 0)
+            slot_s = -1;
+        __syncthreads();
+        if (mine >= 0 && mine < p.L)
+            atomicOr(&present[mine >> 5], 1u << (mine & 31));
+        __syncthreads();
+        if (warp == 0) {
+            const uint32_t w = present[lane];
+            int incl = __popc(w);
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o)
-                incl += v;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o)
+                    incl += v;
+            }
+            const int before = incl - __popc(w);
+            if (u >= before && u < incl) {
+                uint32_t rest = w;
+                for (int i = before; i < u; ++i)
+                    rest &= rest - 1;
+                slot_s = lane * 32 + __ffs(rest) - 1;
+            }
         }
-        const int before = incl - __popc(w);
-        if (u >= before && u < incl) {
-            uint32_t rest = w;
-            for (int i = before; i < u; ++i)
-                rest &= rest - 1;
-            slot_s = lane * 32 + __ffs(rest) - 1;
-        }
+        __syncthreads();
+        slot = slot_s;
+        if (slot < 0)
+            return;
+        si = slot_info(p.tab, slot, p.L);
     }
-    __syncthreads();
-    const int slot = slot_s;
-    if (slot < 0)
-        return;
-    const SlotInfo si = slot_info(p.tab, slot, p.L);
     if (!si.on || r0 >= si.rank)
         return;
-    if (warp == 0) {
-        const int s1 = lane + 32;
-        const int a = c0 + lane < p.M ? p.seq_slot[c0 + lane] : -1, b = c0 + s1 < p.M ? p.seq_slot[c0 + s1] : -1;
-        const uint32_t ma = __ballot_sync(0xffffffffu, a == slot), mb = __ballot_sync(0xffffffffu, b == slot);
-        const uint32_t below = (1u << lane) - 1u;
-        if (a == slot)
-            rows_s[__popc(ma & below)] = c0 + lane;
-        if (b == slot)
-            rows_s[__popc(ma) + __popc(mb & below)] = c0 + s1;
+    if (tid < SH_ROWS) { // the slot's rows, in order
+        const uint32_t m = __ballot_sync(0xffffffffu, mine == slot);
         if (lane == 0)
-            count_s = __popc(ma) + __popc(mb);
+            present[warp] = m;
     }
     __syncthreads();
-    const int count = count_s, nb = p.K / 32;
+    if (tid < SH_ROWS && mine == slot)
+        rows_s[(warp == 1 ? __popc(present[0]) : 0) + __popc(present[warp] & ((1u << lane) - 1u))] = c0 + tid;
+    const int count = __popc(present[0]) + __popc(present[1]);
+    __syncthreads();
+    if (count == 0)
+        return;
+    const int nb = p.K / 32;
     const int b0 = (int)((int64_t)nb * warp / SH_WARPS), b1 = (int)((int64_t)nb * (warp + 1) / SH_WARPS); // this warp's blocks of 32 k
     // rank rows past the rank read the last one; what comes of them is dropped
     const uint16_t *ra = si.a + (size_t)min(r0 + g, si.rank - 1) * p.K + t * 8;
     const uint16_t *rb = si.a + (size_t)min(r0 + g + 8, si.rank - 1) * p.K + t * 8;
-    for (int i0 = 0; i0 < count; i0 += SH_TILE) {
-        const uint16_t *xa = p.x + (int64_t)rows_s[min(i0 + g, count - 1)] * p.x_stride + t * 8;
-        const uint16_t *xb = p.x + (int64_t)rows_s[min(i0 + g + 8, count - 1)] * p.x_stride + t * 8;
-        const bool two = count - i0 > 8;
-        float acc[2][4] = {};
-#pragma unroll 4
-        for (int b = b0; b < b1; ++b) {
-            const uint4 va = ld_nc_16(ra + b * 32), vb = ld_nc_16(rb + b * 32), wa = ld_nc_16(xa + b * 32);
-            mma_16816(acc[0], va.x, vb.x, va.y, vb.y, wa.x, wa.y);
-            mma_16816(acc[0], va.z, vb.z, va.w, vb.w, wa.z, wa.w);
-            if (two) {
-                const uint4 wb = ld_nc_16(xb + b * 32);
-                mma_16816(acc[1], va.x, vb.x, va.y, vb.y, wb.x, wb.y);
-                mma_16816(acc[1], va.z, vb.z, va.w, vb.w, wb.z, wb.w);
-            }
-        }
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            red[warp][g][n * 8 + 2 * t] = acc[n][0];
-            red[warp][g][n * 8 + 2 * t + 1] = acc[n][1];
-            red[warp][g + 8][n * 8 + 2 * t] = acc[n][2];
-            red[warp][g + 8][n * 8 + 2 * t + 1] = acc[n][3];
-        }
+    const float *comp = p.tab.comp_table + (size_t)slot * LORA_COMP_STRIDE;
+
+    // the warps' sums of two tiles of 8 rows, in warp order, to h
+    auto join = [&](int i0, const float (&a)[4], const float (&b)[4]) {
+        red[warp][g][2 * t] = a[0];
+        red[warp][g][2 * t + 1] = a[1];
+        red[warp][g + 8][2 * t] = a[2];
+        red[warp][g + 8][2 * t + 1] = a[3];
+        red[warp][g][8 + 2 * t] = b[0];
+        red[warp][g][8 + 2 * t + 1] = b[1];
+        red[warp][g + 8][8 + 2 * t] = b[2];
+        red[warp][g + 8][8 + 2 * t + 1] = b[3];
         __syncthreads();
-        for (int i = tid; i < 16 * SH_TILE; i += SH_THREADS) {
+        for (int i = tid; i < 16 * SH_PAIR; i += SH_THREADS) {
             const int q = i & 15, row = i >> 4;
             if (i0 + row < count && r0 + q < p.R) {
                 float v = 0.0f;
 #pragma unroll
                 for (int w = 0; w < SH_WARPS; ++w)
                     v += red[w][q][row];
-                const float f = si.scale * __ldg(p.tab.comp_table + (size_t)slot * LORA_COMP_STRIDE + r0 + q);
-                p.h[(size_t)rows_s[i0 + row] * p.R + r0 + q] = r0 + q < si.rank ? f * v : 0.0f;
+                v = r0 + q < si.rank ? si.scale * __ldg(comp + r0 + q) * v : 0.0f;
+                const size_t at = (size_t)rows_s[i0 + row] * p.R + r0 + q;
+                p.h[at] = v;
+                p.hs[at] = f32_to_bf16_bits(v);
             }
         }
         __syncthreads();
+    };
+    const float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (count <= 8) {
+        float acc[1][4];
+        shrink_tile<1, 8>(p, ra, rb, rows_s, count, 0, b0, b1, g, t, acc);
+        join(0, acc[0], none);
+        return;
+    }
+    int i0 = 0;
+    for (; count - i0 > 16; i0 += 32) {
+        float acc[4][4];
+        shrink_tile<4, 4>(p, ra, rb, rows_s, count, i0, b0, b1, g, t, acc);
+        join(i0, acc[0], acc[1]);
+        join(i0 + 16, acc[2], acc[3]);
+    }
+    if (i0 < count) {
+        float acc[2][4];
+        shrink_tile<2, 6>(p, ra, rb, rows_s, count, i0, b0, b1, g, t, acc);
+        join(i0, acc[0], acc[1]);
     }
 }
 
@@ -383,8 +428,8 @@ cudaError_t launch_mx4_shrink(const Mx4ProjParams &p, cudaStream_t st)
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    const int distinct = p.M < p.L ? p.M : p.L;
-    cfg.gridDim = dim3((unsigned)((p.R + 15) / 16), (unsigned)(distinct < SH_ROWS ? distinct : SH_ROWS),
+    const int distinct = p.M < SH_ROWS ? p.M : SH_ROWS; // at most, in a chunk
+    cfg.gridDim = dim3((unsigned)((p.R + 15) / 16), (unsigned)(p.L <= SH_ROWS ? p.L : distinct),
                        (unsigned)((p.M + SH_ROWS - 1) / SH_ROWS));
     cfg.blockDim = dim3(SH_THREADS);
     cfg.stream = st;

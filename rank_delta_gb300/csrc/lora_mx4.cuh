@@ -33,7 +33,8 @@ struct Mx4ProjParams {
     int M, K, N, L, R;
     const int32_t *seq_slot;
     Tables tab;
-    float *h; // [M][R]: s comp (A_s x_i) of every adapted row
+    float *h;      // [M][R]: s comp (A_s x_i) of every adapted row
+    uint16_t *hs;  // the same rounded to bf16
     uint16_t *y;
     int64_t y_stride;
     uint32_t *status;

@@ -52,11 +52,10 @@ constexpr int MAX_RING = 16;
 constexpr uint32_t CODE_BYTES = BM * 128, SCALE_BYTES = BM * 16;
 constexpr uint32_t A_BYTES = BM * 128;
 constexpr int MAX_TN = 256;
-constexpr int TILE_STRIDE = BM + 4; // floats of a row of the partial tile
 
 struct TcShared {
     uint64_t x_full[MAX_RING], x_free[MAX_RING], a_full[MAX_RING], a_free[MAX_RING], c_full[MAX_RING], c_free[MAX_RING];
-    uint64_t routed, done;
+    uint64_t d_full[MAX_RING], routed, done;
     uint32_t tmem;
     int bad;                          // a wait gave up
     int nseg;
@@ -246,6 +245,7 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         for (int s = 0; s < AS; ++s) {
             mbar_init(&sh.a_full[s], 4 * SUB); // the groups' warps
             mbar_init(&sh.a_free[s], 1);
+            mbar_init(&sh.d_full[s], WIDEN_WARPS * 32);
         }
         for (int s = 0; s < CS; ++s) {
             mbar_init(&sh.c_full[s], 1);
@@ -298,85 +298,44 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
                 mbar_arrive(&sh.a_full[s]);
         }
 
-        // ---- the adapters' operands: four 16-rank segments a sub-tile
+        // ---- the adapters' operands: 4 SUB segments of 16 ranks a stage, every
+        // GROUPS-th by this group
         wait_or_note(&sh.routed, 0, &sh.bad);
         const int q0 = sh.nseg * part / kparts, q1 = sh.nseg * (part + 1) / kparts;
-        const int ndelta = __any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&sh.bad) != 0) ? 0 : (q1 - q0 + 4 * SUB - 1) / (4 * SUB) * SUB;
+        const int ndelta = __any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&sh.bad) != 0)
+                               ? 0
+                               : (q1 - q0 + 4 * SUB - 1) / (4 * SUB);
         const int rows = min(tn, p.M - t0);
         if (ndelta > 0)
             grid_dependency_wait(); // h is complete
-        for (int d = (group + GROUPS - mbase % GROUPS) % GROUPS; d < ndelta; d += GROUPS) {
-            const int n = nbase + d / SUB, s = n % AS, use = n / AS, xslot = n % XS, xuse = n / XS;
+        int q = q0 + group, lo = 0; // this group's next segment, and the slot it belongs to
+        for (int d = 0; d < ndelta; ++d) {
+            const int n = nbase + d, s = n % AS, use = n / AS, xslot = n % XS, xuse = n / XS;
             if (use > 0)
                 wait_or_note(&sh.a_free[s], (uint32_t)(use - 1) & 1u, &sh.bad);
             if (xuse > 0)
                 wait_or_note(&sh.x_free[xslot], (uint32_t)(xuse - 1) & 1u, &sh.bad);
-            const uint32_t at = a_at + (uint32_t)(s * SUB + d % SUB) * A_BYTES,
-                           xt = x_at + (uint32_t)(xslot * SUB + d % SUB) * x_bytes;
-            const int nk = min(4, q1 - q0 - 4 * d);
-            for (int j = 0; j < nk; ++j) {
-                const int q = q0 + 4 * d + j;
-                int lo = 0, hi = sh.nslot; // the slot of segment q
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (sh.seg_start[mid] <= q)
-                        lo = mid;
-                    else
-                        hi = mid;
-                }
+            for (; q < min(q1, q0 + 4 * SUB * (d + 1)); q += GROUPS) {
+                const int j = q - q0 - 4 * SUB * d;
+                while (lo + 1 < sh.nslot && sh.seg_start[lo + 1] <= q)
+                    ++lo;
                 const int r = (q - sh.seg_start[lo]) * 16, slot = sh.slot_id[lo];
+                const uint32_t two = r + 8 < p.R ? 16u : 0u, at = a_at + (uint32_t)(s * SUB + (j >> 2)) * A_BYTES,
+                               xt = x_at + (uint32_t)(xslot * SUB + (j >> 2)) * x_bytes;
                 const uint16_t *b = sh.slot_b[lo] + (size_t)rowi * p.R + r;
-                cp16(at + sw128(row, 2 * j), b, 16u);
-                cp16(at + sw128(row, 2 * j + 1), r + 8 < p.R ? b + 8 : b, r + 8 < p.R ? 16u : 0u);
-                for (int tok = row; tok < tn; tok += 128) {
-                    uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
-                    if (tok < rows && sh.tok_slot[tok] == slot) {
-                        const float4 *h = reinterpret_cast<const float4 *>(p.h + (size_t)(t0 + tok) * p.R + r);
-                        const float4 h0 = __ldcg(h), h1 = __ldcg(h + 1);
-                        v0 = make_uint4(pack2(h0.x, h0.y), pack2(h0.z, h0.w), pack2(h1.x, h1.y), pack2(h1.z, h1.w));
-                        if (r + 8 < p.R) {
-                            const float4 h2 = __ldcg(h + 2), h3 = __ldcg(h + 3);
-                            v1 = make_uint4(pack2(h2.x, h2.y), pack2(h2.z, h2.w), pack2(h3.x, h3.y), pack2(h3.z, h3.w));
-                        }
-                    }
-                    sts_16(xt + sw128(tok, 2 * j), v0);
-                    sts_16(xt + sw128(tok, 2 * j + 1), v1);
+                cp16(at + sw128(row, 2 * (j & 3)), b, 16u);
+                cp16(at + sw128(row, 2 * (j & 3) + 1), two ? b + 8 : b, two);
+                for (int tok = row; tok < tn; tok += 128) { // zeros for the other slots' rows
+                    const bool mine = sh.tok_slot[tok] == slot;
+                    const uint16_t *h = p.hs + (size_t)(t0 + (mine ? tok : 0)) * p.R + r;
+                    cp16(xt + sw128(tok, 2 * (j & 3)), h, mine ? 16u : 0u);
+                    cp16(xt + sw128(tok, 2 * (j & 3) + 1), two ? h + 8 : h, mine ? two : 0u);
                 }
             }
-            cp_async_wait_all();
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&sh.a_full[s]);
+            cp_async_mbar_arrive_noinc(&sh.d_full[s]); // when this thread's copies have landed
         }
-
-        // ---- the accumulators
         wait_or_note(&sh.done, 0, &sh.bad);
         __syncwarp();
-        tc_fence_after();
-        float *tile = reinterpret_cast<float *>(smem); // every product has read its operands
-        const int f = (warp & 3) * 32 + lane;
-        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        for (int c = group; c < tn / 16; c += GROUPS) {
-            float v[16];
-            tmem_ld16(tmem + lanes + (uint32_t)(c * 16), v);
-            if (ndelta > 0) {
-                float d[16];
-                tmem_ld16(tmem + lanes + (uint32_t)(tn + c * 16), d);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (sh.tok_slot[c * 16 + i] >= 0)
-                        v[i] += d[i];
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int tok = c * 16 + i;
-                if (kparts > 1)
-                    tile[tok * TILE_STRIDE + f] = v[i];
-                else if (tok < rows && f0 + f < p.N)
-                    p.y[(int64_t)(t0 + tok) * p.y_stride + f0 + f] = f32_to_bf16_bits(v[i]);
-            }
-        }
     } else if (warp == WIDEN_WARPS) {
         // ---- x
         if (lane == 0) {
@@ -431,7 +390,8 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         wait_or_note(&sh.routed, 0, &sh.bad);
         const int q0 = sh.nseg * part / kparts, q1 = sh.nseg * (part + 1) / kparts;
         for (int q = q0; q < q1 && !__any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&sh.bad) != 0); q += 4 * SUB) {
-            wait_or_note(&sh.a_full[s], a_parity, &sh.bad);
+            wait_or_note(&sh.d_full[s], (uint32_t)((q - q0) / (4 * SUB) / AS) & 1u, &sh.bad);
+            fence_proxy_async_smem(); // cp.async (generic proxy) wrote both operands
             tc_fence_after();
             stage(tmem + (uint32_t)tn, s, xslot, q1 - q, q == q0);
             advance();
@@ -461,24 +421,68 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         __syncwarp();
     }
 
-    // ---- the K parts' sum, in part order, and one rounding
-    if (kparts > 1) {
-        cg::cluster_group cl = cg::this_cluster();
-        cl.sync();
-        const float *tile = reinterpret_cast<const float *>(smem);
-        const int b0 = BM * part / kparts, fs = BM * (part + 1) / kparts - b0, rows = min(tn, p.M - t0);
-        if (warp < WIDEN_WARPS) {
-            for (int i = tid; i < rows * fs; i += WIDEN_WARPS * 32) {
-                const int tok = i / fs, f = b0 + i - tok * fs;
-                if (f0 + f >= p.N)
-                    continue;
-                float v = 0.0f;
-                for (int r = 0; r < kparts; ++r)
-                    v += cl.map_shared_rank(tile, r)[tok * TILE_STRIDE + f];
-                p.y[(int64_t)(t0 + tok) * p.y_stride + f0 + f] = f32_to_bf16_bits(v);
+    // ---- the accumulators: each part finishes 128 / kparts features, and gets
+    // them from every part in its shared memory, [part][row][features + 4]
+    cg::cluster_group cl = cg::this_cluster();
+    if (kparts > 1)
+        cl.sync(); // every part's products have read their operands
+    else
+        __syncthreads();
+    const int fs = BM / kparts, stride = fs + 4, rows = min(tn, p.M - t0);
+    float *const tile = reinterpret_cast<float *>(smem);
+    if (warp < WIDEN_WARPS) {
+        tc_fence_after();
+        const bool adapted = sh.nseg * (part + 1) / kparts > sh.nseg * part / kparts;
+        const int f = (warp & 3) * 32 + lane, owner = f / fs;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        float *const to = (kparts > 1 ? cl.map_shared_rank(tile, owner) : tile) + (size_t)part * tn * stride + (f - owner * fs);
+        for (int c = warp >> 2; c < tn / 16; c += GROUPS) {
+            uint32_t v[16], d[16];
+            tmem_ld16_nowait(tmem + lanes + (uint32_t)(c * 16), v);
+            if (adapted)
+                tmem_ld16_nowait(tmem + lanes + (uint32_t)(tn + c * 16), d);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float o = __uint_as_float(v[i]);
+                if (adapted && sh.tok_slot[c * 16 + i] >= 0)
+                    o += __uint_as_float(d[i]);
+                to[(c * 16 + i) * stride] = o;
             }
         }
-        cl.sync(); // the parts' tiles are read until here
+    }
+    if (kparts > 1)
+        cl.sync();
+    else
+        __syncthreads();
+    // ---- the parts' sum, in part order, and one rounding; 8 features of a row at a time
+    {
+        const int eights = fs / 8, b0 = part * fs;
+        const bool vec = (reinterpret_cast<uintptr_t>(p.y) & 15u) == 0 && p.y_stride % 8 == 0;
+        for (int i = tid; i < rows * eights; i += RINGS::THREADS) {
+            const int tok = i / eights, f = (i - tok * eights) * 8, feature = f0 + b0 + f;
+            if (feature >= p.N)
+                continue;
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[k] = 0.0f;
+            for (int r = 0; r < kparts; ++r) {
+                const float4 *src = reinterpret_cast<const float4 *>(tile + ((size_t)r * tn + tok) * stride + f);
+                const float4 a = src[0], b = src[1];
+                v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+                v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+            }
+            uint16_t *y = p.y + (int64_t)(t0 + tok) * p.y_stride + feature;
+            if (vec && feature + 8 <= p.N) {
+                *reinterpret_cast<uint4 *>(y) = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (feature + k < p.N)
+                        y[k] = f32_to_bf16_bits(v[k]);
+            }
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -497,7 +501,7 @@ template <typename RINGS>
 cudaError_t launch(const Mx4ProjParams &p, const Mx4TcPlan &plan, const Mx4TcMaps &maps, cudaStream_t st)
 {
     static std::atomic<uint64_t> raised{0};
-    cudaError_t e = raise_smem_limit(raised, mx4_tc_kernel<RINGS>, 222 * 1024);
+    cudaError_t e = raise_smem_limit(raised, mx4_tc_kernel<RINGS>, 217 * 1024);
     if (e != cudaSuccess)
         return e;
     cudaLaunchAttribute attr[2];
