@@ -194,17 +194,19 @@ def exported_symbols():
 def _ptr(v) -> int:
     if v is None:
         return 0
-    if hasattr(v, "data_ptr"):
-        return int(v.data_ptr())
-    return int(v)
+    try:
+        return v.data_ptr()
+    except AttributeError:
+        return int(v)
 
 
 def _stream(s) -> int:
     if s is None:
         return 0
-    if hasattr(s, "cuda_stream"):
-        return int(s.cuda_stream)
-    return int(s)
+    try:
+        return s.cuda_stream
+    except AttributeError:
+        return int(s)
 
 
 def _check(code: int) -> None:

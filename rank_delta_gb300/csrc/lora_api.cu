@@ -1425,6 +1425,8 @@ lora_status check_mx4(const char *who, const void *w, int dtype, int64_t w_strid
                     LORA_MX4_BLOCK);
     if (w_stride < K)
         return fail(LORA_ERR_SHAPE, "%s: w_stride %lld must be >= K %d", who, (long long)w_stride, K);
+    if (rows > ((int64_t)1 << 40) / K)
+        return fail(LORA_ERR_UNSUPPORTED, "%s: %lld rows of K %d are more than one launch takes", who, (long long)rows, K);
     if (rows > 0 && (w == nullptr || codes == nullptr || scales == nullptr))
         return fail(LORA_ERR_NULL, "%s: w, codes and scales must be non-NULL", who);
     if (!aligned16(codes))
@@ -1465,11 +1467,8 @@ lora_status lora_mx4_quantize(const void *w, int dtype, int64_t w_stride, int64_
         return s;
     if (rows == 0)
         return ok();
-    DevInfo di;
-    if (!device_info(di))
-        return fail(LORA_ERR_CUDA, "%s: no CUDA device", who);
     const Mx4QuantParams p{w, w_stride, rows, K, codes, scales};
-    cudaError_t e = launch_mx4_quantize(p, dtype, di.num_sms, reinterpret_cast<cudaStream_t>(stream));
+    cudaError_t e = launch_mx4_quantize(p, dtype, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return cuda_fail(e, who);
     return ok();
@@ -1484,11 +1483,8 @@ lora_status lora_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int
         return s;
     if (rows == 0)
         return ok();
-    DevInfo di;
-    if (!device_info(di))
-        return fail(LORA_ERR_CUDA, "%s: no CUDA device", who);
     const Mx4DequantParams p{codes, scales, rows, K, w, w_stride};
-    cudaError_t e = launch_mx4_dequantize(p, dtype, di.num_sms, reinterpret_cast<cudaStream_t>(stream));
+    cudaError_t e = launch_mx4_dequantize(p, dtype, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return cuda_fail(e, who);
     return ok();
@@ -1561,7 +1557,7 @@ lora_status lora_mx4_proj_apply_ex(const void *x, int64_t x_stride, const uint8_
         const size_t proj = align256(lora_proj_workspace_bytes(M, rt));
         uint8_t *W = static_cast<uint8_t *>(ws) + proj;
         const Mx4DequantParams q{codes, scales, N, K, W, K};
-        if ((e = launch_mx4_dequantize(q, LORA_DTYPE_BF16, di.num_sms, st)) != cudaSuccess)
+        if ((e = launch_mx4_dequantize(q, LORA_DTYPE_BF16, st)) != cudaSuccess)
             return cuda_fail(e, who);
         return proj_apply(x, x_stride, W, M, K, N, seq_slot, rt, y, y_stride, ws, proj, LORA_PATH_AUTO, stream);
     }

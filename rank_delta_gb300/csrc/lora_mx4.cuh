@@ -40,8 +40,8 @@ struct Mx4ProjParams {
     uint32_t *status;
 };
 
-cudaError_t launch_mx4_quantize(const Mx4QuantParams &p, int dtype, int num_sms, cudaStream_t st);
-cudaError_t launch_mx4_dequantize(const Mx4DequantParams &p, int dtype, int num_sms, cudaStream_t st);
+cudaError_t launch_mx4_quantize(const Mx4QuantParams &p, int dtype, cudaStream_t st);
+cudaError_t launch_mx4_dequantize(const Mx4DequantParams &p, int dtype, cudaStream_t st);
 cudaError_t launch_mx4_shrink(const Mx4ProjParams &p, cudaStream_t st);
 cudaError_t launch_mx4_stream(const Mx4ProjParams &p, int num_sms, cudaStream_t st);
 // The tiles of a tensor-core launch: rows of a token tile (the host encodes x

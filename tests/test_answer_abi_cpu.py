@@ -94,6 +94,7 @@ def test_mx4_sizes_and_refusals():
         expect(rd.LORA_ERR_ALIGN, call(codes=520))
         expect(rd.LORA_ERR_ALIGN, call(w=4097))
         expect(rd.LORA_ERR_ALIGN, call(w=4098, dtype=rd.LORA_DTYPE_F32))
+        expect(rd.LORA_ERR_UNSUPPORTED, call(rows=1 << 60), contains=("K 64",))
         call(rows=0, w=0, codes=0, scales=0)()
 
 
