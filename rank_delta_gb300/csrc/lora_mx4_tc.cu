@@ -61,6 +61,7 @@ struct TcShared {
     int nseg;
     uint32_t present[MAX_BUCKETS / 32];
     int16_t tok_slot[MAX_TN];         // the row's slot, -1: no delta
+    uint32_t adapted[MAX_TN / 32];    // bit of a row: it has a delta
     int16_t slot_id[MAX_TN];          // distinct slots of the tile, ascending
     int seg_start[MAX_TN + 1];        // their first 16-rank segment
     int nslot;
@@ -170,9 +171,10 @@ __device__ __forceinline__ void route_tile(const Mx4ProjParams &p, TcShared &sh,
 {
     sh.present[lane] = 0u;
     __syncwarp();
-    for (int i = lane; i < tn; i += 32) {
+    for (int i0 = 0; i0 < tn; i0 += 32) {
+        const int i = i0 + lane;
         int slot = -1;
-        if (t0 + i < p.M) {
+        if (i < tn && t0 + i < p.M) {
             const int s = p.seq_slot[t0 + i];
             if (slot_info(p.tab, s, p.L).on) {
                 slot = s;
@@ -180,6 +182,10 @@ __device__ __forceinline__ void route_tile(const Mx4ProjParams &p, TcShared &sh,
             }
         }
         sh.tok_slot[i] = (int16_t)slot;
+        __syncwarp();
+        const uint32_t on = __ballot_sync(0xffffffffu, slot >= 0);
+        if (lane == 0)
+            sh.adapted[i0 >> 5] = on;
     }
     __syncwarp();
     const uint32_t w = sh.present[lane];
@@ -381,8 +387,12 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
             }
         };
         for (int n = 0; n < nbase; ++n) {
-            wait_or_note(&sh.x_full[xslot], x_parity, &sh.bad);
-            wait_or_note(&sh.a_full[s], a_parity, &sh.bad);
+            // both polls on their way at once
+            const bool x_in = mbar_try_wait(smem_u32(&sh.x_full[xslot]), x_parity), a_in = mbar_try_wait(smem_u32(&sh.a_full[s]), a_parity);
+            if (!x_in)
+                wait_or_note(&sh.x_full[xslot], x_parity, &sh.bad);
+            if (!a_in)
+                wait_or_note(&sh.a_full[s], a_parity, &sh.bad);
             tc_fence_after();
             stage(tmem, s, xslot, 4 * SUB, n == 0);
             advance();
@@ -441,11 +451,12 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
             tmem_ld16_nowait(tmem + lanes + (uint32_t)(c * 16), v);
             if (adapted)
                 tmem_ld16_nowait(tmem + lanes + (uint32_t)(tn + c * 16), d);
+            const uint32_t on = adapted ? sh.adapted[c >> 1] >> ((c & 1) * 16) : 0u;
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 float o = __uint_as_float(v[i]);
-                if (adapted && sh.tok_slot[c * 16 + i] >= 0)
+                if (on >> i & 1u)
                     o += __uint_as_float(d[i]);
                 to[(c * 16 + i) * stride] = o;
             }
@@ -457,19 +468,19 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         __syncthreads();
     // ---- the parts' sum, in part order, and one rounding; 8 features of a row at a time
     {
-        const int eights = fs / 8, b0 = part * fs;
+        const int eights = fs / 8, log_eights = 31 - __clz(eights), b0 = part * fs;
         const bool vec = (reinterpret_cast<uintptr_t>(p.y) & 15u) == 0 && p.y_stride % 8 == 0;
+#pragma unroll 4
         for (int i = tid; i < rows * eights; i += RINGS::THREADS) {
-            const int tok = i / eights, f = (i - tok * eights) * 8, feature = f0 + b0 + f;
-            if (feature >= p.N)
-                continue;
+            const int tok = i >> log_eights, f = (i & (eights - 1)) * 8, feature = f0 + b0 + f;
             float v[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                v[k] = 0.0f;
-            for (int r = 0; r < kparts; ++r) {
-                const float4 *src = reinterpret_cast<const float4 *>(tile + ((size_t)r * tn + tok) * stride + f);
-                const float4 a = src[0], b = src[1];
+            const float4 *src = reinterpret_cast<const float4 *>(tile + tok * stride + f);
+            const float4 first = src[0], second = src[1];
+            v[0] = first.x; v[1] = first.y; v[2] = first.z; v[3] = first.w;
+            v[4] = second.x; v[5] = second.y; v[6] = second.z; v[7] = second.w;
+            for (int r = 1; r < kparts; ++r) {
+                const float4 *more = src + r * (tn * stride / 4);
+                const float4 a = more[0], b = more[1];
                 v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
                 v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
             }
