@@ -573,17 +573,15 @@ lora_status lora_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int
 
 /* Path of lora_mx4_proj_apply_ex (lora_mx4_proj_apply uses LORA_MX4_PATH_AUTO). */
 enum {
-    LORA_MX4_PATH_AUTO = 0,   /* by row count */
-    LORA_MX4_PATH_STREAM = 1, /* codes to the tensor cores' registers: few rows */
-    LORA_MX4_PATH_EXPAND = 2, /* the weight widened to bf16 in the workspace, then lora_proj_apply */
-    LORA_MX4_PATH_TILES = 3   /* codes widened into the shared-memory operand tiles of tcgen05 */
+    LORA_MX4_PATH_AUTO = 0,  /* LORA_MX4_PATH_ROWS where it is possible */
+    LORA_MX4_PATH_ROWS = 1,  /* up to 8 rows and n_in 8192: codes widened into the tensor cores' registers (other
+                                calls take LORA_MX4_PATH_TILES) */
+    LORA_MX4_PATH_TILES = 2  /* codes widened into the shared-memory operand tiles of tcgen05 */
 };
 
-/* Workspace of lora_mx4_proj_apply for M rows on route `rt`: the routing sort,
- * h, the status word, and for many rows the weight in bf16 (2 n_out n_in
- * bytes). 0 if rt is NULL, not initialised or not a projection route. */
+/* Workspace of lora_mx4_proj_apply for M rows on route `rt`: the status word
+ * and h. 0 if rt is NULL, not initialised or not a projection route. */
 size_t lora_mx4_proj_workspace_bytes(int M, const lora_route *rt);
-size_t lora_mx4_proj_workspace_bytes_ex(int M, const lora_route *rt, int path);
 
 /*
  * y[i, :] = dq(W) x_i + s * B_s (A_s x_i), s = seq_slot[i]: lora_proj_apply with

@@ -53,9 +53,8 @@ LORA_MAX_TOP = 32
 LORA_MX4_BLOCK = 32
 
 LORA_MX4_PATH_AUTO = 0
-LORA_MX4_PATH_STREAM = 1
-LORA_MX4_PATH_EXPAND = 2
-LORA_MX4_PATH_TILES = 3
+LORA_MX4_PATH_ROWS = 1
+LORA_MX4_PATH_TILES = 2
 
 LORA_PLAN_SIMT = 1
 LORA_PLAN_TC = 2
@@ -154,7 +153,6 @@ _SIGNATURES = {
     "lora_mx4_quantize": (_i, [_vp, _i, _i64, _i64, _i, _vp, _vp, _vp]),
     "lora_mx4_dequantize": (_i, [_vp, _vp, _i64, _i, _vp, _i, _i64, _vp]),
     "lora_mx4_proj_workspace_bytes": (_sz, [_i, _rtp]),
-    "lora_mx4_proj_workspace_bytes_ex": (_sz, [_i, _rtp, _i]),
     "lora_mx4_proj_apply": (_i, [_vp, _i64, _vp, _vp, _i, _i, _i, _vp, _rtp, _vp, _i64, _vp, _sz, _vp]),
     "lora_mx4_proj_apply_ex": (_i, [_vp, _i64, _vp, _vp, _i, _i, _i, _vp, _rtp, _vp, _i64, _vp, _sz, _i, _vp]),
     "lora_logprobs_workspace_bytes": (_sz, [_i, _i, _i]),
@@ -406,10 +404,8 @@ def lora_mx4_dequantize(codes, scales, rows: int, K: int, w, dtype: int, w_strid
     _check(lib().lora_mx4_dequantize(_ptr(codes), _ptr(scales), rows, K, _ptr(w), dtype, w_stride, _stream(stream)))
 
 
-def lora_mx4_proj_workspace_bytes(M: int, rt: lora_route, path: int = LORA_MX4_PATH_AUTO) -> int:
-    if path == LORA_MX4_PATH_AUTO:
-        return int(lib().lora_mx4_proj_workspace_bytes(M, ctypes.byref(rt)))
-    return int(lib().lora_mx4_proj_workspace_bytes_ex(M, ctypes.byref(rt), path))
+def lora_mx4_proj_workspace_bytes(M: int, rt: lora_route) -> int:
+    return int(lib().lora_mx4_proj_workspace_bytes(M, ctypes.byref(rt)))
 
 
 def lora_mx4_proj_apply(x, x_stride: int, codes, scales, M: int, K: int, N: int, seq_slot, rt: lora_route, y,

@@ -22,7 +22,6 @@ namespace {
 constexpr uint64_t ROUTE_MAGIC = 0x6c6f72615f727431ull; // "lora_rt1"
 constexpr int MAX_LORAS = MAX_BUCKETS - 1;
 constexpr int MAX_RANK = 256;
-constexpr int MX4_STREAM_MAX_ROWS = 64; // LORA_MX4_PATH_AUTO: at most this many rows read the codes directly
 constexpr int SIMT_MAX_ROWS = 16; // LORA_PATH_AUTO: at most this many rows per segment -> GEMV
 
 thread_local std::string g_err;
@@ -1436,12 +1435,12 @@ lora_status check_mx4(const char *who, const void *w, int dtype, int64_t w_strid
     return LORA_OK;
 }
 
-// The path a call of M rows takes.
-int mx4_path(int M, int path)
+// The path a call takes.
+int mx4_path(int M, int K, int R, int path)
 {
-    if (path != LORA_MX4_PATH_AUTO)
-        return path;
-    return M <= MX4_STREAM_MAX_ROWS ? LORA_MX4_PATH_STREAM : LORA_MX4_PATH_EXPAND;
+    if (path == LORA_MX4_PATH_TILES || !mx4_rows_fit(M, K, R))
+        return LORA_MX4_PATH_TILES;
+    return LORA_MX4_PATH_ROWS;
 }
 
 } // namespace
@@ -1490,20 +1489,13 @@ lora_status lora_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int
     return ok();
 }
 
-size_t lora_mx4_proj_workspace_bytes_ex(int M, const lora_route *rt, int path)
+size_t lora_mx4_proj_workspace_bytes(int M, const lora_route *rt)
 {
     if (rt == nullptr || rt->magic != ROUTE_MAGIC || rt->kind != LORA_ROUTE_PROJ || M < 0)
         return 0;
-    if (mx4_path(M, path) == LORA_MX4_PATH_EXPAND) // the projection's, then the weight in bf16
-        return align256(lora_proj_workspace_bytes(M, rt)) + align256((size_t)rt->n_out * (size_t)rt->n_in * 2);
     // status, h in fp32, h in bf16
     return align256(256 + sizeof(float) * (size_t)M * (size_t)rt->max_rank) +
            align256(sizeof(uint16_t) * (size_t)M * (size_t)rt->max_rank);
-}
-
-size_t lora_mx4_proj_workspace_bytes(int M, const lora_route *rt)
-{
-    return lora_mx4_proj_workspace_bytes_ex(M, rt, LORA_MX4_PATH_AUTO);
 }
 
 lora_status lora_mx4_proj_apply(const void *x, int64_t x_stride, const uint8_t *codes, const uint8_t *scales, int M,
@@ -1539,8 +1531,7 @@ lora_status lora_mx4_proj_apply_ex(const void *x, int64_t x_stride, const uint8_
         return fail(LORA_ERR_ALIGN, "%s: codes must be 16-byte aligned", who);
     if ((s = check_io(who, x, x_stride, M, K, N, seq_slot, y, y_stride)) != LORA_OK)
         return s;
-    path = mx4_path(M, path);
-    const size_t need = lora_mx4_proj_workspace_bytes_ex(M, rt, path);
+    const size_t need = lora_mx4_proj_workspace_bytes(M, rt);
     if (ws == nullptr)
         return fail(LORA_ERR_NULL, "%s: workspace is NULL", who);
     if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
@@ -1553,14 +1544,6 @@ lora_status lora_mx4_proj_apply_ex(const void *x, int64_t x_stride, const uint8_
         return fail(LORA_ERR_CUDA, "%s: no CUDA device", who);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (path == LORA_MX4_PATH_EXPAND) {
-        const size_t proj = align256(lora_proj_workspace_bytes(M, rt));
-        uint8_t *W = static_cast<uint8_t *>(ws) + proj;
-        const Mx4DequantParams q{codes, scales, N, K, W, K};
-        if ((e = launch_mx4_dequantize(q, LORA_DTYPE_BF16, st)) != cudaSuccess)
-            return cuda_fail(e, who);
-        return proj_apply(x, x_stride, W, M, K, N, seq_slot, rt, y, y_stride, ws, proj, LORA_PATH_AUTO, stream);
-    }
     Mx4ProjParams q;
     memset(&q, 0, sizeof q);
     q.x = static_cast<const uint16_t *>(x);
@@ -1581,7 +1564,7 @@ lora_status lora_mx4_proj_apply_ex(const void *x, int64_t x_stride, const uint8_
     q.y_stride = y_stride;
     if ((e = launch_mx4_shrink(q, st)) != cudaSuccess)
         return cuda_fail(e, who);
-    if (path == LORA_MX4_PATH_TILES) {
+    if (mx4_path(M, K, q.R, path) == LORA_MX4_PATH_TILES) {
         const Mx4TcPlan plan = plan_mx4_tc(q, di.num_sms);
         Mx4TcMaps maps;
         memset(&maps, 0, sizeof maps);
@@ -1592,7 +1575,10 @@ lora_status lora_mx4_proj_apply_ex(const void *x, int64_t x_stride, const uint8_
                          make_map_bytes(&maps.scales, scales, (uint64_t)(K / 32), (uint64_t)N, 16, 128, false);
         e = launch_mx4_tc(q, plan, maps, st);
     } else {
-        e = launch_mx4_stream(q, di.num_sms, st);
+        CUtensorMap map;
+        if (!make_map_bytes(&map, codes, (uint64_t)(K / 2), (uint64_t)N, 128, 16, true))
+            return fail(LORA_ERR_CUDA, "%s: encoding the tensor map failed", who);
+        e = launch_mx4_rows(q, map, di.num_sms, st);
     }
     if (e != cudaSuccess)
         return cuda_fail(e, who);

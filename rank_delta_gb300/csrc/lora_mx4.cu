@@ -10,24 +10,14 @@
 //            from memory: 16 rank rows by up to 16 of the slot's rows a CTA and
 //            pass. The projection kernels start behind it at once and wait for
 //            h only where they need it.
-// stream     the product for few rows. The weight's 16-row fragments go from
-//            memory to the tensor cores' registers: a thread copies 16 bytes
-//            (one block of 32 codes) of two weight rows, 128 k of the tile's 16
-//            rows a warp and step, into a ring of its own in shared memory (no
-//            barrier: it reads back what it copied itself), widens them to bf16
-//            exactly, and multiplies. Which k a fragment's slots mean is free as
-//            long as both operands agree, so the codes stay in their natural
-//            order and x is read to match.
-#include <cooperative_groups.h>
-#include <cuda_fp16.h>
-
+// rows       the product for up to eight rows, on the tensor cores' registers
+//            (mma.sync): a warp's 16 weight rows need not pass through shared
+//            memory a second time once they are widened.
 #include "lora_mx4.cuh"
 #include "ptx.cuh"
 #include "vec.cuh"
 
 namespace rd {
-
-namespace cg = cooperative_groups;
 
 namespace {
 
@@ -377,8 +367,8 @@ __device__ __forceinline__ void shrink_tile(const Mx4ProjParams &p, const uint16
 
 } // namespace
 
-// Grid: 16-rank groups, by slots (or, for more than SH_ROWS of them, the u-th
-// distinct slot of the chunk), by 64-row chunks. Each thread multiplies 8
+// Grid: 16-rank groups, by slots (or, where there are more of them than rows in a
+// chunk, the u-th distinct slot of the chunk), by 64-row chunks. Each thread multiplies 8
 // consecutive k of two rank rows and of the slot's rows at a time: which k a
 // fragment's slots mean is free as long as both operands agree.
 __global__ void __launch_bounds__(SH_THREADS) mx4_shrink_kernel(Mx4ProjParams p)
@@ -395,7 +385,8 @@ __global__ void __launch_bounds__(SH_THREADS) mx4_shrink_kernel(Mx4ProjParams p)
     const int mine = tid < SH_ROWS && c0 + tid < p.M ? p.seq_slot[c0 + tid] : -1;
     SlotInfo si;
     int slot = u;
-    if (p.L <= SH_ROWS)
+    const bool direct = p.L <= min(p.M, SH_ROWS);
+    if (direct)
         si = slot_info(p.tab, slot, p.L); // on its way with the rows' slots
     if (blockIdx.x == 0 && u == 0 && c0 == 0) { // the call's status
         int bad = 0;
@@ -405,7 +396,7 @@ __global__ void __launch_bounds__(SH_THREADS) mx4_shrink_kernel(Mx4ProjParams p)
         if (tid == 0)
             status_begin(p.status, bad ? (uint32_t)LORA_FLAG_SLOT_RANGE : 0u);
     }
-    if (p.L > SH_ROWS) { // the u-th distinct slot among the chunk's rows
+    if (!direct) { // the u-th distinct slot among the chunk's rows
         present[lane] = 0u;
         if (tid == 0)
             slot_s = -1;
@@ -510,8 +501,8 @@ cudaError_t launch_mx4_shrink(const Mx4ProjParams &p, cudaStream_t st)
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    const int distinct = p.M < SH_ROWS ? p.M : SH_ROWS; // at most, in a chunk
-    cfg.gridDim = dim3((unsigned)((p.R + 15) / 16), (unsigned)(p.L <= SH_ROWS ? p.L : distinct),
+    const int distinct = p.M < SH_ROWS ? p.M : SH_ROWS; // slots in a chunk, at most
+    cfg.gridDim = dim3((unsigned)((p.R + 15) / 16), (unsigned)(p.L < distinct ? p.L : distinct),
                        (unsigned)((p.M + SH_ROWS - 1) / SH_ROWS));
     cfg.blockDim = dim3(SH_THREADS);
     cfg.stream = st;
@@ -520,33 +511,39 @@ cudaError_t launch_mx4_shrink(const Mx4ProjParams &p, cudaStream_t st)
     return cudaLaunchKernelEx(&cfg, mx4_shrink_kernel, p);
 }
 
-// ------------------------------------------------------------------ stream
+// -------------------------------------------------------------------- rows
 namespace {
 
-constexpr int ST_THREADS = 256;           // 8 warps, 16 features each
-constexpr int ST_FEATURES = 128;
-constexpr int ST_DEPTH = 6;               // 128-wide k chunks of codes in flight
-constexpr uint32_t ST_RING = ST_DEPTH * 2 * ST_THREADS * 16;
-constexpr uint32_t ST_X_BYTES = 96 * 1024; // x of a pass over part of K, at most
-constexpr int ST_TILE = ST_FEATURES + 4;  // floats of a token's row of the partial tile
+constexpr int RW_WARPS = 16, RW_FINISH = 4;  // compute, finish
+constexpr int RW_THREADS = (RW_WARPS + RW_FINISH) * 32;
+constexpr int RW_ROWS = 8;                   // batch rows: the n of one mma
+constexpr uint32_t RW_BOX = 16 * 128;        // codes of 16 weight rows x 256 k
+constexpr int RW_BUFS = 3;                   // steps whose partial sums may wait to be finished
+constexpr uint32_t RW_PART = 16 * RW_ROWS;   // floats of a warp's partial tile, [feature][row]
+constexpr int RW_MAX_DEPTH = 4;
+constexpr uint32_t RW_SMEM = 226 * 1024;
+constexpr int RW_FULL = 1, RW_FREE = RW_FULL + RW_BUFS, RW_X = RW_FREE + RW_BUFS, RW_H = RW_X + 1; // named barriers
 
-// Bytes of a token's x row over `chunks` chunks: every 64-byte block is
-// followed by 16 spare bytes, and rows lie 4 (mod 8) 16-byte units apart, so
-// that the eight lanes of a load phase touch eight different bank groups.
-__host__ __device__ inline uint32_t st_x_stride(int chunks)
+// How the warps share the work: a team of `team` warps splits K (boxes of 256)
+// of 16 features, and the CTA's teams take neighbouring features.
+struct RowsShape {
+    int boxes, team, depth;
+    uint32_t x_bytes, smem;
+};
+inline RowsShape rows_shape(int K, int R)
 {
-    uint32_t u = (uint32_t)chunks * 20u;
-    u += (4u + 8u - u % 8u) % 8u;
-    return u * 16u;
-}
-
-// Chunks of K a pass may stage for nt token tiles of 8.
-inline int st_pass_chunks(int nt)
-{
-    int c = 1;
-    while (c < 64 && (uint32_t)(nt * 8) * st_x_stride(c + 1) <= ST_X_BYTES)
-        ++c;
-    return c;
+    RowsShape r;
+    r.boxes = (K + 255) / 256;
+    r.team = 1;
+    while (r.team < RW_WARPS && r.team < r.boxes)
+        r.team *= 2;
+    r.x_bytes = (uint32_t)r.boxes * 512u * RW_ROWS;
+    const uint32_t fixed = 1024u + r.x_bytes + RW_BUFS * RW_WARPS * RW_PART * 4 + RW_ROWS * (uint32_t)R * 4;
+    r.depth = 0;
+    while (r.depth < RW_MAX_DEPTH && fixed + (uint32_t)(r.depth + 1) * RW_WARPS * RW_BOX <= RW_SMEM)
+        ++r.depth;
+    r.smem = fixed + (uint32_t)r.depth * RW_WARPS * RW_BOX;
+    return r;
 }
 
 __device__ __forceinline__ uint4 lds_16(uint32_t addr)
@@ -556,290 +553,260 @@ __device__ __forceinline__ uint4 lds_16(uint32_t addr)
     return v;
 }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, uint32_t bytes)
+// Eight codes of two weight rows -> bf16 pairs, times their blocks' scales.
+__device__ __forceinline__ void widen_pair(uint32_t a, uint32_t b, uint32_t fa, uint32_t fb, uint32_t (&u)[4], uint32_t (&v)[4])
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-
-// Scale bytes of 128 weight rows, blocks [b0, b0 + n) of each (zero past K), to
-// sc[row][n padded to 4]; W bytes an access, which the caller has checked for
-// alignment. Eight accesses of a thread are in flight at a time.
-template <typename W>
-__device__ __forceinline__ void stage_scales(const uint8_t *scales, int nblk, int N, int f0, int b0, int n, uint8_t *sc,
-                                             int scs, int tid)
-{
-    constexpr int B = sizeof(W);
-    const int each = (n + B - 1) / B, total = ST_FEATURES * each;
-    for (int i0 = tid; i0 < total; i0 += 8 * ST_THREADS) {
-        W v[8];
+    mx4_unpack8(a, u);
+    mx4_unpack8(b, v);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const int i = i0 + u * ST_THREADS, r = i / each, b = (i - r * each) * B;
-            v[u] = W{};
-            if (i < total && b0 + b < nblk)
-                v[u] = __ldg(reinterpret_cast<const W *>(scales + (size_t)min(f0 + r, N - 1) * nblk + b0 + b));
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const int i = i0 + u * ST_THREADS, r = i / each, b = (i - r * each) * B;
-            if (i < total)
-                *reinterpret_cast<W *>(sc + r * scs + b) = v[u];
-        }
+    for (int q = 0; q < 4; ++q) {
+        u[q] = mul_bf16x2(u[q], fa);
+        v[q] = mul_bf16x2(v[q], fb);
     }
 }
-
-// Two blocks' worth of a row pair's codes in registers -> bf16, times their scales.
-struct Widen {
-    uint32_t fa1, fa2, fb1, fb2;
-    bool twice;
-    __device__ __forceinline__ Widen(uint32_t sa, uint32_t sb)
-    {
-        mx4_factors(sa, fa1, fa2);
-        mx4_factors(sb, fb1, fb2);
-        twice = __any_sync(0xffffffffu, sa > MX4_ONE_FACTOR || sb > MX4_ONE_FACTOR);
-    }
-    __device__ __forceinline__ void operator()(uint32_t a, uint32_t b, uint32_t (&u)[4], uint32_t (&v)[4]) const
-    {
-        mx4_unpack8(a, u);
-        mx4_unpack8(b, v);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            u[q] = mul_bf16x2(u[q], fa1);
-            v[q] = mul_bf16x2(v[q], fb1);
-        }
-        if (twice) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                u[q] = mul_bf16x2(u[q], fa2);
-                v[q] = mul_bf16x2(v[q], fb2);
-            }
-        }
-    }
-};
 
 } // namespace
 
-// Grid: (feature tiles of 128) x kparts, by token tiles of 8 NT; the kparts
-// CTAs of a tile are a cluster, and each finishes 128 / kparts features.
-template <int NT>
-__global__ void __launch_bounds__(ST_THREADS) mx4_stream_kernel(Mx4ProjParams p, int kparts, int pass_chunks)
+// A CTA an SM; step s of CTA c takes the features of 16 * teams from
+// (s * gridDim + c) * 16 * teams on. Each compute warp has a ring of its own
+// of code boxes that its lane 0 keeps asking for by TMA, steps ahead, so
+// nothing in a CTA waits for anything but its own boxes; partial sums of a
+// step go to shared memory, and four more warps add them in order, add the
+// adapters and write y while the next steps are in work. x (8 rows, all of K)
+// stays in shared memory; within 64 bytes its 16-byte pieces are turned by
+// the row and the block so that the eight lanes of a load phase meet eight
+// different bank groups. Which k a fragment's slots mean is free as long as
+// both operands agree: thread t of four supplies the block t of 128 k.
+__global__ void __launch_bounds__(RW_THREADS, 1)
+    mx4_rows_kernel(const __grid_constant__ CUtensorMap codes, const __grid_constant__ Mx4ProjParams p, RowsShape shape)
 {
-    constexpr int TOK = NT * 8;
-    extern __shared__ __align__(128) uint8_t st_smem[];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    const int part = blockIdx.x % kparts, f0 = (blockIdx.x / kparts) * ST_FEATURES, t0 = blockIdx.y * TOK;
-    const int nblk = p.K / 32, nch = (nblk + 3) / 4, per = (nch + kparts - 1) / kparts;
-    const int cb = min(nch, part * per), ce = min(nch, cb + per);
-    const int fs = ST_FEATURES / kparts, fb = part * fs; // the features this CTA finishes
-    const uint32_t xstr = st_x_stride(pass_chunks);
-    const uint32_t smem = smem_u32(st_smem);
-    const uint32_t ring = smem + tid * 16;
-    const uint32_t xs = smem + ST_RING;
-    uint8_t *sc = st_smem + ST_RING + (uint32_t)TOK * xstr; // [128][4 pass_chunks] scale bytes
-    const int scs = (4 * pass_chunks + 15) & ~15;
+    extern __shared__ uint8_t rw_raw[];
+    __shared__ uint64_t full[RW_WARPS][RW_MAX_DEPTH];
+    __shared__ const uint16_t *brow[RW_ROWS]; // B of the row's slot, nullptr: no delta
+    __shared__ int bad;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t raw = smem_u32(rw_raw), base = (raw + 1023u) & ~1023u;
+    uint8_t *const smem = rw_raw + (base - raw);
+    const uint32_t ring = base, xs = base + (uint32_t)shape.depth * RW_WARPS * RW_BOX, xrow = (uint32_t)shape.boxes * 512u;
+    float *const part = reinterpret_cast<float *>(smem + (xs - base) + shape.x_bytes);
+    float *const hs = part + RW_BUFS * RW_WARPS * RW_PART;
+    const int T = shape.team, teams = RW_WARPS / T, nblk = p.K / 32;
+    const int tiles = (p.N + 15) / 16, groups = (tiles + teams - 1) / teams; // of 16 features, of a step's
+    const int steps = (groups - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+    if (tid < RW_WARPS * RW_MAX_DEPTH)
+        mbar_init(&full[tid / RW_MAX_DEPTH][tid % RW_MAX_DEPTH], 1);
+    if (tid == 0) {
+        bad = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
 
-    // this thread's two weight rows (rows past N repeat the last; their sums are dropped)
-    const int fa = f0 + warp * 16 + g;
-    const uint8_t *wa = p.codes + (size_t)min(fa, p.N - 1) * (p.K / 2) + t * 16;
-    const uint8_t *wb = p.codes + (size_t)min(fa + 8, p.N - 1) * (p.K / 2) + t * 16;
-    float acc[NT][4];
+    if (warp < RW_WARPS) {
+        const int wk = warp % T, team = warp / T, g = lane >> 2, t = lane & 3;
+        const int per = wk < shape.boxes ? (shape.boxes - wk + T - 1) / T : 0; // boxes of a step, 0 to 2
+        const int units = steps * per, depth = shape.depth;
+        const uint32_t mine = ring + (uint32_t)(warp * depth) * RW_BOX;
+        auto feature = [&](int s) { return ((s * (int)gridDim.x + (int)blockIdx.x) * teams + team) * 16; };
+        auto ask = [&](int u, int slot) {
+            const int s = per == 2 ? u >> 1 : u, box = wk + (per == 2 ? (u & 1) * T : 0);
+            mbar_arrive_expect_tx(&full[warp][slot], RW_BOX);
+            tma_load_2d(smem + (warp * depth + slot) * RW_BOX, &codes, box * 128, feature(s), &full[warp][slot]);
+        };
+        // scale bytes of unit u: rows g and g + 8, blocks t and t + 4 of the box
+        const bool eights = nblk % 8 == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 7u) == 0;
+        auto scales_of = [&](int u, uint32_t (&sc)[4]) {
+            const int s = per == 2 ? u >> 1 : u, b0 = (wk + (per == 2 ? (u & 1) * T : 0)) * 8, f = feature(s) + g;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            acc[n][i] = 0.0f;
-
-    auto fetch = [&](int c, int slot) { // codes of chunk c, zeros past K
-        const uint32_t have = c * 4 + t < nblk ? 16u : 0u;
-        const uint32_t d = ring + (uint32_t)slot * (2 * ST_THREADS * 16);
-        cp16(d, have ? wa + (size_t)c * 64 : p.codes, have);
-        cp16(d + ST_THREADS * 16, have ? wb + (size_t)c * 64 : p.codes, have);
-    };
-
-    for (int c0 = cb; c0 < ce; c0 += pass_chunks) {
-        const int nc = min(pass_chunks, ce - c0);
-        // the first chunks of codes, a group a chunk, also where there is none; x of
-        // the pass (zeros past K and M) goes with the first
-#pragma unroll
-        for (int d = 0; d < ST_DEPTH - 1; ++d) {
-            if (d < nc)
-                fetch(c0 + d, d);
-            if (d == 0) {
-                for (int i = tid; i < TOK * nc * 16; i += ST_THREADS) {
-                    const int tok = i / (nc * 16), q = i - tok * (nc * 16); // 16-byte piece q of the row
-                    const int k = c0 * 128 + q * 8;
-                    const bool have = t0 + tok < p.M && k < p.K;
-                    cp16(xs + (uint32_t)tok * xstr + (uint32_t)((q >> 2) * 80 + (q & 3) * 16),
-                         have ? p.x + (int64_t)(t0 + tok) * p.x_stride + k : p.x, have ? 16u : 0u);
+            for (int r = 0; r < 2; ++r) { // rows past N repeat the last; their sums are dropped
+                const uint8_t *row = p.scales + (size_t)min(f + 8 * r, p.N - 1) * nblk + b0;
+                if (eights) {
+                    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(row));
+                    sc[r] = v.x >> (8 * t) & 255u;
+                    sc[2 + r] = v.y >> (8 * t) & 255u;
+                } else {
+                    sc[r] = b0 + t < nblk ? __ldg(row + t) : 0u;
+                    sc[2 + r] = b0 + 4 + t < nblk ? __ldg(row + 4 + t) : 0u;
                 }
             }
-            cp_async_commit();
+        };
+        if (lane == 0)
+            for (int u = 0; u < min(depth, units); ++u)
+                ask(u, u);
+        uint32_t next[4] = {0, 0, 0, 0};
+        if (units > 0)
+            scales_of(0, next);
+        // x, zeros past K and M
+        for (int i = tid; i < RW_ROWS * shape.boxes * 32; i += RW_WARPS * 32) {
+            const int row = i / (shape.boxes * 32), piece = i - row * (shape.boxes * 32), block = piece >> 2;
+            const bool have = row < p.M && piece * 8 < p.K;
+            const int turn = (block >> 1 & 1) | (row & 1) << 1;
+            const uint4 v = have ? ld_nc_16(p.x + (int64_t)row * p.x_stride + piece * 8) : make_uint4(0, 0, 0, 0);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(xs + (uint32_t)row * xrow + (uint32_t)block * 64u +
+                                                                         (uint32_t)((piece & 3) ^ turn) * 16u),
+                         "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                         : "memory");
         }
-        if (nblk % 16 == 0 && nc % 4 == 0 && c0 % 4 == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 15u) == 0)
-            stage_scales<uint4>(p.scales, nblk, p.N, f0, c0 * 4, nc * 4, sc, scs, tid);
-        else if (nblk % 4 == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 3u) == 0)
-            stage_scales<uint32_t>(p.scales, nblk, p.N, f0, c0 * 4, nc * 4, sc, scs, tid);
-        else
-            stage_scales<uint8_t>(p.scales, nblk, p.N, f0, c0 * 4, nc * 4, sc, scs, tid);
-        cp_async_wait_group<ST_DEPTH - 2>();
-        __syncthreads();
-        for (int i = 0, slot = 0; i < nc; ++i) {
-            cp_async_wait_group<ST_DEPTH - 2>();
-            const uint4 a = lds_16(ring + (uint32_t)slot * (2 * ST_THREADS * 16));
-            const uint4 b = lds_16(ring + (uint32_t)slot * (2 * ST_THREADS * 16) + ST_THREADS * 16);
-            const int ahead = i + ST_DEPTH - 1;
-            if (ahead < nc)
-                fetch(c0 + ahead, slot == 0 ? ST_DEPTH - 1 : slot - 1);
-            cp_async_commit();
-            slot = slot + 1 == ST_DEPTH ? 0 : slot + 1;
-            const Widen widen(sc[(warp * 16 + g) * scs + i * 4 + t], sc[(warp * 16 + g + 8) * scs + i * 4 + t]);
-            const uint32_t xa = xs + (uint32_t)g * xstr + (uint32_t)(i * 4 + t) * 80;
+        named_bar_sync(RW_X, RW_WARPS * 32);
+
+        const uint32_t xg = xs + (uint32_t)g * xrow + (uint32_t)t * 64u;
+        const uint32_t turn = (uint32_t)((t >> 1) | (g & 1) << 1) << 4;
+        const uint32_t row_at = (uint32_t)g * 128u; // of a box; row g + 8 is 1024 further and turned alike
+        int slot = 0;
+        uint32_t parity = 0;
+        for (int s = 0, u = 0; s < steps; ++s) {
+            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int k = 0; k < per; ++k, ++u) {
+                const int box = wk + k * T;
+                uint32_t sc[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t u[4], v[4];
-                widen(j == 0 ? a.x : j == 1 ? a.y : j == 2 ? a.z : a.w, j == 0 ? b.x : j == 1 ? b.y : j == 2 ? b.z : b.w, u, v);
+                for (int i = 0; i < 4; ++i)
+                    sc[i] = next[i];
+                if (u + 1 < units)
+                    scales_of(u + 1, next);
+                wait_or_note(&full[warp][slot], parity, &bad);
+                const uint32_t at = mine + (uint32_t)slot * RW_BOX + row_at;
+                const bool twice = __any_sync(0xffffffffu, max(max(sc[0], sc[1]), max(sc[2], sc[3])) > MX4_ONE_FACTOR);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const uint4 xb = lds_16(xa + (uint32_t)(n * 8) * xstr + (uint32_t)j * 16);
-                    mma_16816(acc[n], u[0], v[0], u[1], v[1], xb.x, xb.y);
-                    mma_16816(acc[n], u[2], v[2], u[3], v[3], xb.z, xb.w);
+                for (int h = 0; h < 2; ++h) { // 128 k
+                    const uint32_t piece = (uint32_t)(((h * 4 + t) ^ (g & 7)) << 4);
+                    const uint4 a = lds_16(at + piece), b = lds_16(at + 1024u + piece);
+                    uint32_t fa, fa2, fb, fb2;
+                    mx4_factors(sc[2 * h], fa, fa2);
+                    mx4_factors(sc[2 * h + 1], fb, fb2);
+                    const uint32_t xa = xg + (uint32_t)(box * 8 + h * 4) * 64u;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint4 xv = lds_16(xa + (((uint32_t)j << 4) ^ turn));
+                        uint32_t w[4], v[4];
+                        widen_pair(j == 0 ? a.x : j == 1 ? a.y : j == 2 ? a.z : a.w, j == 0 ? b.x : j == 1 ? b.y : j == 2 ? b.z : b.w,
+                                   fa, fb, w, v);
+                        if (twice) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                w[q] = mul_bf16x2(w[q], fa2);
+                                v[q] = mul_bf16x2(v[q], fb2);
+                            }
+                        }
+                        mma_16816(acc, w[0], v[0], w[1], v[1], xv.x, xv.y);
+                        mma_16816(acc, w[2], v[2], w[3], v[3], xv.z, xv.w);
+                    }
+                }
+                __syncwarp(); // every lane has read the box
+                if (lane == 0 && u + depth < units)
+                    ask(u + depth, slot);
+                if (++slot == depth) {
+                    slot = 0;
+                    parity ^= 1u;
                 }
             }
+            const int buf = s % RW_BUFS;
+            if (s >= RW_BUFS) // the step that used the buffer before has been finished
+                named_bar_sync(RW_FREE + buf, RW_THREADS);
+            float *to = part + (size_t)(buf * RW_WARPS + warp) * RW_PART;
+            *reinterpret_cast<float2 *>(to + g * RW_ROWS + 2 * t) = make_float2(acc[0], acc[1]);
+            *reinterpret_cast<float2 *>(to + (g + 8) * RW_ROWS + 2 * t) = make_float2(acc[2], acc[3]);
+            named_bar_arrive(RW_FULL + buf, RW_THREADS);
         }
-        __syncthreads(); // x and the scales are overwritten
-    }
-    cp_async_wait_all();
-    __syncthreads();
-
-    // ---- partial tile, [token][128 + 4]; then s comp h of the tile's rows, [token][R], and the delta, [token][fs]
-    float *tile = reinterpret_cast<float *>(st_smem);
-    float *hs = tile + TOK * ST_TILE;
-    float *delta = hs + TOK * p.R;
-    __shared__ const uint16_t *brow_s[TOK]; // B of a row's slot, nullptr: no delta
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int f = warp * 16 + g, tok = n * 8 + 2 * t;
-        tile[tok * ST_TILE + f] = acc[n][0];
-        tile[(tok + 1) * ST_TILE + f] = acc[n][1];
-        tile[tok * ST_TILE + f + 8] = acc[n][2];
-        tile[(tok + 1) * ST_TILE + f + 8] = acc[n][3];
-    }
-    if (kparts > 1)
-        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    grid_dependency_wait(); // h is complete
-    const int rows = min(TOK, p.M - t0);
-#pragma unroll 4
-    for (int i = tid; i < rows * p.R; i += ST_THREADS) {
-        const int tok = i / p.R, r = i - tok * p.R, slot = p.seq_slot[t0 + tok];
-        const SlotInfo si = slot_info(p.tab, slot, p.L);
-        if (r == 0)
-            brow_s[tok] = si.on ? si.b : nullptr;
-        float v = 0.0f;
-        if (si.on && r < si.rank)
-            v = __ldcg(p.h + (size_t)(t0 + tok) * p.R + r);
-        hs[i] = v;
-    }
-    __syncthreads();
-    // a B row is `pieces` 16-byte pieces, a lane each: one row, or several
-    const int pieces = p.R / 8;
-    int lanes = 1;
-    while (lanes < pieces)
-        lanes *= 2;
-    const int sub = lane & (lanes - 1), each = 32 / lanes;
-    constexpr int AT_ONCE = 8;
-    for (int i0 = warp * each; i0 < rows * fs; i0 += (ST_THREADS / 32) * each * AT_ONCE) {
-        uint4 b[AT_ONCE];
-        int tok[AT_ONCE];
-#pragma unroll
-        for (int a = 0; a < AT_ONCE; ++a) {
-            const int i = i0 + a * (ST_THREADS / 32) * each + lane / lanes, f = i % fs;
-            tok[a] = i / fs;
-            const uint16_t *base = i < rows * fs && f0 + fb + f < p.N && sub < pieces ? brow_s[tok[a]] : nullptr;
-            b[a] = make_uint4(0, 0, 0, 0);
-            tok[a] = base != nullptr ? tok[a] : -1;
-            if (base != nullptr)
-                b[a] = ld_nc_16(base + (size_t)(f0 + fb + f) * p.R + sub * 8);
+    } else {
+        // ---- finish: the rows' slots, s h, then step by step
+        const int ft = tid - RW_WARPS * 32;
+        if (ft < RW_ROWS) {
+            const SlotInfo si = ft < p.M ? slot_info(p.tab, p.seq_slot[ft], p.L) : SlotInfo{nullptr, nullptr, 0.0f, 0, 0};
+            brow[ft] = si.on ? si.b : nullptr;
         }
+        named_bar_sync(RW_H, RW_FINISH * 32);
+        grid_dependency_wait(); // h is complete, and the call's status open
+        for (int i = ft; i < p.M * p.R; i += RW_FINISH * 32) {
+            const int row = i / p.R, r = i - row * p.R;
+            float v = 0.0f;
+            if (brow[row] != nullptr && r < p.tab.rank_table[p.seq_slot[row]])
+                v = __ldcg(p.h + i);
+            hs[i] = v;
+        }
+        named_bar_sync(RW_H, RW_FINISH * 32);
+        // an output takes `lanes` lanes: they share the team's partial sums, and
+        // the 16-byte pieces of its B row
+        const int pieces = p.R / 8, sums = min(T, shape.boxes);
+        int lanes = 8;
+        while (lanes < pieces)
+            lanes *= 2;
+        const int sub = lane & (lanes - 1), each = 32 / lanes, outs = teams * 16 * p.M;
+        constexpr int AT_ONCE = 4;
+        for (int s = 0; s < steps; ++s) {
+            const int buf = s % RW_BUFS, f0 = (s * (int)gridDim.x + (int)blockIdx.x) * teams * 16;
+            const float *from = part + (size_t)buf * RW_WARPS * RW_PART;
+            const int first = (ft >> 5) * each + lane / lanes;
+            bool waited = false;
+            for (int o0 = 0; o0 < outs; o0 += RW_FINISH * each * AT_ONCE) {
+                uint4 b[AT_ONCE];
+                int row[AT_ONCE], f[AT_ONCE];
 #pragma unroll
-        for (int a = 0; a < AT_ONCE; ++a) {
-            const int i = i0 + a * (ST_THREADS / 32) * each + lane / lanes;
-            float d = 0.0f;
-            if (tok[a] >= 0) {
-                const float4 *hp = reinterpret_cast<const float4 *>(hs + tok[a] * p.R + sub * 8);
-                d = dot8_bf_f32(0.0f, b[a], hp[0], hp[1]);
+                for (int a = 0; a < AT_ONCE; ++a) { // the B pieces, on their way before the sums are in
+                    const int o = o0 + a * RW_FINISH * each + first;
+                    row[a] = o / (teams * 16);
+                    f[a] = o - row[a] * (teams * 16);
+                    const bool have = o < outs && f0 + f[a] < p.N;
+                    row[a] = have ? row[a] : -1;
+                    b[a] = make_uint4(0, 0, 0, 0);
+                    if (have && sub < pieces && brow[row[a]] != nullptr)
+                        b[a] = ld_nc_16(brow[row[a]] + (size_t)(f0 + f[a]) * p.R + sub * 8);
+                }
+                if (!waited)
+                    named_bar_sync(RW_FULL + buf, RW_THREADS);
+                waited = true;
+#pragma unroll
+                for (int a = 0; a < AT_ONCE; ++a) {
+                    float v = 0.0f, d = 0.0f;
+                    if (row[a] >= 0) {
+                        const float *q = from + (size_t)((f[a] >> 4) * T) * RW_PART + (f[a] & 15) * RW_ROWS + row[a];
+                        for (int w = sub; w < sums; w += lanes)
+                            v += q[w * RW_PART];
+                        if (sub < pieces && brow[row[a]] != nullptr) {
+                            const float4 *h = reinterpret_cast<const float4 *>(hs + row[a] * p.R + sub * 8);
+                            d = dot8_bf_f32(0.0f, b[a], h[0], h[1]);
+                        }
+                    }
+                    for (int o = lanes / 2; o > 0; o >>= 1) {
+                        v += __shfl_xor_sync(0xffffffffu, v, o);
+                        d += __shfl_xor_sync(0xffffffffu, d, o);
+                    }
+                    if (row[a] >= 0 && sub == 0) {
+                        if (brow[row[a]] != nullptr) // else the base product to the bit
+                            v += d;
+                        p.y[(int64_t)row[a] * p.y_stride + f0 + f[a]] = f32_to_bf16_bits(v);
+                    }
+                }
             }
-            for (int o = lanes / 2; o > 0; o >>= 1)
-                d += __shfl_xor_sync(0xffffffffu, d, o);
-            if (i < rows * fs && sub == 0)
-                delta[i] = d;
+            if (s + RW_BUFS < steps)
+                named_bar_arrive(RW_FREE + buf, RW_THREADS);
         }
+        if (ft == 0 && *reinterpret_cast<volatile int *>(&bad) != 0)
+            atomicOr(p.status, (uint32_t)LORA_FLAG_WAIT_TIMEOUT);
     }
-    __syncthreads();
-    if (kparts > 1)
-        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    // ---- sum over the K parts (part order), the row's adapter, one rounding
-    for (int i = tid; i < rows * fs; i += ST_THREADS) {
-        const int tok = i / fs, f = i - tok * fs;
-        if (f0 + fb + f >= p.N)
-            continue;
-        float v = 0.0f;
-        if (kparts > 1) {
-            cg::cluster_group cl = cg::this_cluster();
-            for (int r = 0; r < kparts; ++r)
-                v += cl.map_shared_rank(tile, r)[tok * ST_TILE + fb + f];
-        } else {
-            v = tile[tok * ST_TILE + f];
-        }
-        if (brow_s[tok] != nullptr) // else the base product to the bit
-            v += delta[i];
-        p.y[(int64_t)(t0 + tok) * p.y_stride + f0 + fb + f] = f32_to_bf16_bits(v);
-    }
-    if (kparts > 1)
-        cg::this_cluster().sync(); // the parts' tiles are read until here
 }
 
-template <int NT> cudaError_t launch_st(const Mx4ProjParams &p, int num_sms, cudaStream_t st)
+// Whether a call can take the rows kernel: x and two boxes a warp have to fit.
+bool mx4_rows_fit(int M, int K, int R) { return M <= RW_ROWS && K <= 512 * RW_WARPS && rows_shape(K, R).depth >= 2; }
+
+cudaError_t launch_mx4_rows(const Mx4ProjParams &p, const CUtensorMap &codes, int num_sms, cudaStream_t st)
 {
-    const int tiles = (p.N + ST_FEATURES - 1) / ST_FEATURES, nch = (p.K / 32 + 3) / 4;
-    const int ttiles = (p.M + NT * 8 - 1) / (NT * 8);
-    int kparts = 1;
-    while (kparts < 8 && tiles * kparts * ttiles < num_sms && nch >= 4 * kparts)
-        kparts *= 2;
-    int pass = st_pass_chunks(NT);
-    const int per = (nch + kparts - 1) / kparts;
-    pass = pass < per ? pass : per;
-    uint32_t smem = ST_RING + (uint32_t)(NT * 8) * st_x_stride(pass) + ST_FEATURES * ((4 * (uint32_t)pass + 15) & ~15u);
-    const uint32_t end = (uint32_t)(NT * 8) * (ST_TILE + p.R + ST_FEATURES / kparts) * 4;
-    smem = smem > end ? smem : end;
+    const RowsShape shape = rows_shape(p.K, p.R);
     static std::atomic<uint64_t> raised{0};
-    cudaError_t e = raise_smem_limit(raised, mx4_stream_kernel<NT>, 224 * 1024);
+    cudaError_t e = raise_smem_limit(raised, mx4_rows_kernel, (int)RW_SMEM);
     if (e != cudaSuccess)
         return e;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)kparts;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    const int step = 16 * (RW_WARPS / shape.team), groups = (p.N + step - 1) / step;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * kparts), (unsigned)ttiles);
-    cfg.blockDim = dim3(ST_THREADS);
-    cfg.dynamicSmemBytes = smem;
+    cfg.gridDim = dim3((unsigned)(groups < num_sms ? groups : num_sms));
+    cfg.blockDim = dim3(RW_THREADS);
+    cfg.dynamicSmemBytes = shape.smem;
     cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, mx4_stream_kernel<NT>, p, kparts, pass);
-}
-
-cudaError_t launch_mx4_stream(const Mx4ProjParams &p, int num_sms, cudaStream_t st)
-{
-    if (p.M <= 8)
-        return launch_st<1>(p, num_sms, st);
-    if (p.M <= 16)
-        return launch_st<2>(p, num_sms, st);
-    if (p.M <= 32)
-        return launch_st<4>(p, num_sms, st);
-    return launch_st<8>(p, num_sms, st);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, mx4_rows_kernel, codes, p, shape);
 }
 
 } // namespace rd

@@ -6,6 +6,7 @@
 // consecutive values of a row share. Byte 255 makes its block NaN.
 #pragma once
 #include "lora_internal.cuh"
+#include "ptx.cuh"
 
 namespace rd {
 
@@ -43,7 +44,9 @@ struct Mx4ProjParams {
 cudaError_t launch_mx4_quantize(const Mx4QuantParams &p, int dtype, cudaStream_t st);
 cudaError_t launch_mx4_dequantize(const Mx4DequantParams &p, int dtype, cudaStream_t st);
 cudaError_t launch_mx4_shrink(const Mx4ProjParams &p, cudaStream_t st);
-cudaError_t launch_mx4_stream(const Mx4ProjParams &p, int num_sms, cudaStream_t st);
+// The product for up to 8 rows; `codes`: bytes [N][K / 2], boxes of 128 bytes x 16 rows, 128-byte swizzle.
+bool mx4_rows_fit(int M, int K, int R);
+cudaError_t launch_mx4_rows(const Mx4ProjParams &p, const CUtensorMap &codes, int num_sms, cudaStream_t st);
 // The tiles of a tensor-core launch: rows of a token tile (the host encodes x
 // in boxes of 64 k by that many rows) and K parts.
 struct Mx4TcPlan {
@@ -57,6 +60,24 @@ struct Mx4TcMaps {
     int scales_ok;      // 1: encoded
 };
 cudaError_t launch_mx4_tc(const Mx4ProjParams &p, const Mx4TcPlan &plan, const Mx4TcMaps &maps, cudaStream_t st);
+
+// Wait for a phase, at most WAIT_NS; the clock is read only every 256 polls
+// from the first on (a read of it takes longer than a stage).
+__device__ __forceinline__ void wait_or_note(uint64_t *bar, uint32_t parity, int *bad)
+{
+    const uint32_t a = smem_u32(bar);
+    uint64_t t0 = 0;
+    for (uint32_t i = 1; !mbar_try_wait(a, parity); ++i) {
+        if ((i & 255u) != 0)
+            continue;
+        const uint64_t t = globaltimer_ns();
+        t0 = t0 == 0 ? t : t0;
+        if (t - t0 > WAIT_NS || *reinterpret_cast<volatile int *>(bad) != 0) {
+            *reinterpret_cast<volatile int *>(bad) = 1;
+            return;
+        }
+    }
+}
 
 // The bf16 factors that turn value * 2^-126 (what mx4_unpack8 gives) into value
 // * 2^(byte - 127). The second is 1 unless the first would leave bf16's range

@@ -98,24 +98,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     return r;
 }
 
-// Wait for a phase, at most WAIT_NS; the clock is read only every 256 polls
-// from the first on (a read of it takes longer than a stage).
-__device__ __forceinline__ void wait_or_note(uint64_t *bar, uint32_t parity, int *bad)
-{
-    const uint32_t a = smem_u32(bar);
-    uint64_t t0 = 0;
-    for (uint32_t i = 1; !mbar_try_wait(a, parity); ++i) {
-        if ((i & 255u) != 0)
-            continue;
-        const uint64_t t = globaltimer_ns();
-        t0 = t0 == 0 ? t : t0;
-        if (t - t0 > WAIT_NS || *reinterpret_cast<volatile int *>(bad) != 0) {
-            *reinterpret_cast<volatile int *>(bad) = 1;
-            return;
-        }
-    }
-}
-
 // umma_bf16 and umma_commit by the lanes with lead != 0.
 __device__ __forceinline__ void umma_bf16_by(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                              uint32_t accumulate)

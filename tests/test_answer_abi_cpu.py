@@ -103,8 +103,6 @@ def test_mx4_projection_refusals():
     rt = fake_route(L=4, R=8, K=256, N=256)
     need = rd.lora_mx4_proj_workspace_bytes(8, rt)
     assert need > 0
-    many = rd.lora_mx4_proj_workspace_bytes(8, rt, rd.LORA_MX4_PATH_EXPAND)
-    assert many >= rd.lora_proj_workspace_bytes(8, rt) + 256 * 256 * 2
     assert rd.lora_mx4_proj_workspace_bytes(8, fake_route(kind=rd.LORA_ROUTE_EMBED)) == 0
     good = dict(x=4096, xs=256, codes=8192, scales=513, M=8, K=256, N=256, slots=4096, rt=rt, y=4096, ys=256, ws=1 << 20,
                 n=need, path=0)

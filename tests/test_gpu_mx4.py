@@ -19,7 +19,7 @@ from rank_delta_gb300 import torch_helpers as th
 pytestmark = pytest.mark.gpu
 
 GRID = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
-PATHS = [rd.LORA_MX4_PATH_STREAM, rd.LORA_MX4_PATH_EXPAND, rd.LORA_MX4_PATH_TILES]
+PATHS = [rd.LORA_MX4_PATH_ROWS, rd.LORA_MX4_PATH_TILES]
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -155,7 +155,7 @@ class Setup:
     def run(self, path, slots=None, y_pad=0, stream=None):
         slots = torch.tensor(self.slots if slots is None else slots).cuda()
         y = torch.full((self.M, self.N + y_pad), float("nan"), dtype=torch.bfloat16, device="cuda")
-        ws = torch.full((rd.lora_mx4_proj_workspace_bytes(self.M, self.route.rt, path),), 0x5A, dtype=torch.uint8,
+        ws = torch.full((rd.lora_mx4_proj_workspace_bytes(self.M, self.route.rt),), 0x5A, dtype=torch.uint8,
                         device="cuda")
         rd.lora_mx4_proj_apply(self.x, self.x.stride(0), self.codes, self.scales, self.M, self.K, self.N, slots,
                                self.route.rt, y, y.stride(0), ws, ws.numel(), stream, path)
