@@ -1435,10 +1435,20 @@ lora_status check_mx4(const char *who, const void *w, int dtype, int64_t w_strid
     return LORA_OK;
 }
 
-// The path a call takes.
+// The path a call takes: by itself, the rows kernel up to four rows. What both
+// take, rows kernel and tiles in us, every row of an adapter of its own of rank 64:
+//   K x N         1 row        4 rows       8 rows
+//   4096 x  4096   9.3  11.5   11.3  11.7   14.1  12.6
+//   4096 x 14336  21.3  24.2   27.3  26.5   39.9  28.5
+//   4096 x 32000  43.4  47.4   50.9  50.2   75.7  52.0
+//   8192 x  4096  13.5  15.7   14.3  16.0   17.9  17.8
+// The rows kernel reads a row's B on its own and multiplies on the CUDA cores, a
+// tile has them in its products: the wider the matrix, the earlier tiles win.
+// (Without adapters the rows kernel is ahead up to seven rows or so.)
 int mx4_path(int M, int K, int R, int path)
 {
-    if (path == LORA_MX4_PATH_TILES || !mx4_rows_fit(M, K, R))
+    constexpr int ROWS_AUTO = 4;
+    if (path == LORA_MX4_PATH_TILES || (path == LORA_MX4_PATH_AUTO && M > ROWS_AUTO) || !mx4_rows_fit(M, K, R))
         return LORA_MX4_PATH_TILES;
     return LORA_MX4_PATH_ROWS;
 }

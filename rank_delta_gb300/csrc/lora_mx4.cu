@@ -522,7 +522,7 @@ constexpr int RW_BUFS = 3;                   // steps whose partial sums may wai
 constexpr uint32_t RW_PART = 16 * RW_ROWS;   // floats of a warp's partial tile, [feature][row]
 constexpr int RW_MAX_DEPTH = 4;
 constexpr uint32_t RW_SMEM = 226 * 1024;
-constexpr int RW_FULL = 1, RW_FREE = RW_FULL + RW_BUFS, RW_X = RW_FREE + RW_BUFS, RW_H = RW_X + 1; // named barriers
+constexpr int RW_X = 1, RW_H = 2; // named barriers
 
 // How the warps share the work: a team of `team` warps splits K (boxes of 256)
 // of 16 features, and the CTA's teams take neighbouring features.
@@ -538,7 +538,8 @@ inline RowsShape rows_shape(int K, int R)
     while (r.team < RW_WARPS && r.team < r.boxes)
         r.team *= 2;
     r.x_bytes = (uint32_t)r.boxes * 512u * RW_ROWS;
-    const uint32_t fixed = 1024u + r.x_bytes + RW_BUFS * RW_WARPS * RW_PART * 4 + RW_ROWS * (uint32_t)R * 4;
+    const uint32_t fixed = 1024u + r.x_bytes + RW_BUFS * RW_WARPS * RW_PART * 4 + RW_ROWS * (uint32_t)R * 4 +
+                           RW_WARPS / (uint32_t)r.team * 16u * RW_ROWS * 4u;
     r.depth = 0;
     while (r.depth < RW_MAX_DEPTH && fixed + (uint32_t)(r.depth + 1) * RW_WARPS * RW_BOX <= RW_SMEM)
         ++r.depth;
@@ -581,7 +582,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
     mx4_rows_kernel(const __grid_constant__ CUtensorMap codes, const __grid_constant__ Mx4ProjParams p, RowsShape shape)
 {
     extern __shared__ uint8_t rw_raw[];
-    __shared__ uint64_t full[RW_WARPS][RW_MAX_DEPTH];
+    __shared__ uint64_t full[RW_WARPS][RW_MAX_DEPTH], part_full[RW_BUFS], part_free[RW_BUFS];
     __shared__ const uint16_t *brow[RW_ROWS]; // B of the row's slot, nullptr: no delta
     __shared__ int bad;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -589,16 +590,20 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
     uint8_t *const smem = rw_raw + (base - raw);
     const uint32_t ring = base, xs = base + (uint32_t)shape.depth * RW_WARPS * RW_BOX, xrow = (uint32_t)shape.boxes * 512u;
     float *const part = reinterpret_cast<float *>(smem + (xs - base) + shape.x_bytes);
-    float *const hs = part + RW_BUFS * RW_WARPS * RW_PART;
+    float *const hs = part + RW_BUFS * RW_WARPS * RW_PART, *const delta = hs + RW_ROWS * p.R; // s h; a step's B (s h)
     const int T = shape.team, teams = RW_WARPS / T, nblk = p.K / 32;
     const int tiles = (p.N + 15) / 16, groups = (tiles + teams - 1) / teams; // of 16 features, of a step's
     const int steps = (groups - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
     if (tid < RW_WARPS * RW_MAX_DEPTH)
         mbar_init(&full[tid / RW_MAX_DEPTH][tid % RW_MAX_DEPTH], 1);
     if (tid == 0) {
+        for (int b = 0; b < RW_BUFS; ++b) {
+            mbar_init(&part_full[b], RW_WARPS);
+            mbar_init(&part_free[b], RW_FINISH);
+        }
         bad = 0;
-        fence_barrier_init();
     }
+    fence_barrier_init();
     __syncthreads();
 
     if (warp < RW_WARPS) {
@@ -612,13 +617,15 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
             mbar_arrive_expect_tx(&full[warp][slot], RW_BOX);
             tma_load_2d(smem + (warp * depth + slot) * RW_BOX, &codes, box * 128, feature(s), &full[warp][slot]);
         };
-        // scale bytes of unit u: rows g and g + 8, blocks t and t + 4 of the box
+        // scale bytes of a box: rows g and g + 8, blocks t and t + 4
         const bool eights = nblk % 8 == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 7u) == 0;
-        auto scales_of = [&](int u, uint32_t (&sc)[4]) {
-            const int s = per == 2 ? u >> 1 : u, b0 = (wk + (per == 2 ? (u & 1) * T : 0)) * 8, f = feature(s) + g;
+        const int jump = (int)gridDim.x * teams * 16; // features from a step to the next
+        int sf = feature(0) + g, sk = 0;              // where the next are
+        auto next_scales = [&](uint32_t (&sc)[4]) {
+            const int b0 = (wk + sk * T) * 8;
 #pragma unroll
             for (int r = 0; r < 2; ++r) { // rows past N repeat the last; their sums are dropped
-                const uint8_t *row = p.scales + (size_t)min(f + 8 * r, p.N - 1) * nblk + b0;
+                const uint8_t *row = p.scales + (size_t)min(sf + 8 * r, p.N - 1) * nblk + b0;
                 if (eights) {
                     const uint2 v = __ldg(reinterpret_cast<const uint2 *>(row));
                     sc[r] = v.x >> (8 * t) & 255u;
@@ -628,13 +635,17 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
                     sc[2 + r] = b0 + 4 + t < nblk ? __ldg(row + 4 + t) : 0u;
                 }
             }
+            if (++sk == per) {
+                sk = 0;
+                sf += jump;
+            }
         };
         if (lane == 0)
             for (int u = 0; u < min(depth, units); ++u)
                 ask(u, u);
         uint32_t next[4] = {0, 0, 0, 0};
         if (units > 0)
-            scales_of(0, next);
+            next_scales(next);
         // x, zeros past K and M
         for (int i = tid; i < RW_ROWS * shape.boxes * 32; i += RW_WARPS * 32) {
             const int row = i / (shape.boxes * 32), piece = i - row * (shape.boxes * 32), block = piece >> 2;
@@ -662,7 +673,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
                 for (int i = 0; i < 4; ++i)
                     sc[i] = next[i];
                 if (u + 1 < units)
-                    scales_of(u + 1, next);
+                    next_scales(next);
                 wait_or_note(&full[warp][slot], parity, &bad);
                 const uint32_t at = mine + (uint32_t)slot * RW_BOX + row_at;
                 const bool twice = __any_sync(0xffffffffu, max(max(sc[0], sc[1]), max(sc[2], sc[3])) > MX4_ONE_FACTOR);
@@ -670,9 +681,11 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
                 for (int h = 0; h < 2; ++h) { // 128 k
                     const uint32_t piece = (uint32_t)(((h * 4 + t) ^ (g & 7)) << 4);
                     const uint4 a = lds_16(at + piece), b = lds_16(at + 1024u + piece);
-                    uint32_t fa, fa2, fb, fb2;
-                    mx4_factors(sc[2 * h], fa, fa2);
-                    mx4_factors(sc[2 * h + 1], fb, fb2);
+                    uint32_t fa = mx4_factor(sc[2 * h]), fb = mx4_factor(sc[2 * h + 1]), fa2 = 0u, fb2 = 0u;
+                    if (twice) {
+                        mx4_factors(sc[2 * h], fa, fa2);
+                        mx4_factors(sc[2 * h + 1], fb, fb2);
+                    }
                     const uint32_t xa = xg + (uint32_t)(box * 8 + h * 4) * 64u;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -699,13 +712,15 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
                     parity ^= 1u;
                 }
             }
-            const int buf = s % RW_BUFS;
-            if (s >= RW_BUFS) // the step that used the buffer before has been finished
-                named_bar_sync(RW_FREE + buf, RW_THREADS);
+            const int buf = s % RW_BUFS, use = s / RW_BUFS;
+            if (use > 0) // the step that used the buffer before has been finished
+                wait_or_note(&part_free[buf], (uint32_t)(use - 1) & 1u, &bad);
             float *to = part + (size_t)(buf * RW_WARPS + warp) * RW_PART;
             *reinterpret_cast<float2 *>(to + g * RW_ROWS + 2 * t) = make_float2(acc[0], acc[1]);
             *reinterpret_cast<float2 *>(to + (g + 8) * RW_ROWS + 2 * t) = make_float2(acc[2], acc[3]);
-            named_bar_arrive(RW_FULL + buf, RW_THREADS);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&part_full[buf]);
         }
     } else {
         // ---- finish: the rows' slots, s h, then step by step
@@ -724,61 +739,63 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
             hs[i] = v;
         }
         named_bar_sync(RW_H, RW_FINISH * 32);
-        // an output takes `lanes` lanes: they share the team's partial sums, and
-        // the 16-byte pieces of its B row
-        const int pieces = p.R / 8, sums = min(T, shape.boxes);
-        int lanes = 8;
+        // the adapter's part of an output takes `lanes` lanes, a 16-byte piece of its
+        // B row each; then a thread adds the team's partial sums of an output
+        const int pieces = p.R / 8, sums = min(T, shape.boxes), width = teams * 16, outs = width * p.M;
+        int lanes = 1;
         while (lanes < pieces)
             lanes *= 2;
-        const int sub = lane & (lanes - 1), each = 32 / lanes, outs = teams * 16 * p.M;
+        const int sub = lane & (lanes - 1), each = 32 / lanes, first = (ft >> 5) * each + lane / lanes;
         constexpr int AT_ONCE = 4;
         for (int s = 0; s < steps; ++s) {
-            const int buf = s % RW_BUFS, f0 = (s * (int)gridDim.x + (int)blockIdx.x) * teams * 16;
-            const float *from = part + (size_t)buf * RW_WARPS * RW_PART;
-            const int first = (ft >> 5) * each + lane / lanes;
-            bool waited = false;
+            const int buf = s % RW_BUFS, f0 = (s * (int)gridDim.x + (int)blockIdx.x) * width;
             for (int o0 = 0; o0 < outs; o0 += RW_FINISH * each * AT_ONCE) {
                 uint4 b[AT_ONCE];
-                int row[AT_ONCE], f[AT_ONCE];
-#pragma unroll
-                for (int a = 0; a < AT_ONCE; ++a) { // the B pieces, on their way before the sums are in
-                    const int o = o0 + a * RW_FINISH * each + first;
-                    row[a] = o / (teams * 16);
-                    f[a] = o - row[a] * (teams * 16);
-                    const bool have = o < outs && f0 + f[a] < p.N;
-                    row[a] = have ? row[a] : -1;
-                    b[a] = make_uint4(0, 0, 0, 0);
-                    if (have && sub < pieces && brow[row[a]] != nullptr)
-                        b[a] = ld_nc_16(brow[row[a]] + (size_t)(f0 + f[a]) * p.R + sub * 8);
-                }
-                if (!waited)
-                    named_bar_sync(RW_FULL + buf, RW_THREADS);
-                waited = true;
+                int row[AT_ONCE];
 #pragma unroll
                 for (int a = 0; a < AT_ONCE; ++a) {
-                    float v = 0.0f, d = 0.0f;
+                    const int o = o0 + a * RW_FINISH * each + first, r = o / width, f = f0 + o - r * width;
+                    const bool have = o < outs && f < p.N && sub < pieces && brow[r & (RW_ROWS - 1)] != nullptr;
+                    row[a] = have ? r : -1;
+                    b[a] = make_uint4(0, 0, 0, 0);
+                    if (have)
+                        b[a] = ld_nc_16(brow[r] + (size_t)f * p.R + sub * 8);
+                }
+#pragma unroll
+                for (int a = 0; a < AT_ONCE; ++a) {
+                    if (o0 + a * RW_FINISH * each >= outs) // none of the warp's lanes has one
+                        break;
+                    float d = 0.0f;
                     if (row[a] >= 0) {
-                        const float *q = from + (size_t)((f[a] >> 4) * T) * RW_PART + (f[a] & 15) * RW_ROWS + row[a];
-                        for (int w = sub; w < sums; w += lanes)
-                            v += q[w * RW_PART];
-                        if (sub < pieces && brow[row[a]] != nullptr) {
-                            const float4 *h = reinterpret_cast<const float4 *>(hs + row[a] * p.R + sub * 8);
-                            d = dot8_bf_f32(0.0f, b[a], h[0], h[1]);
-                        }
+                        const float4 *h = reinterpret_cast<const float4 *>(hs + row[a] * p.R + sub * 8);
+                        d = dot8_bf_f32(0.0f, b[a], h[0], h[1]);
                     }
-                    for (int o = lanes / 2; o > 0; o >>= 1) {
-                        v += __shfl_xor_sync(0xffffffffu, v, o);
+                    for (int o = lanes / 2; o > 0; o >>= 1)
                         d += __shfl_xor_sync(0xffffffffu, d, o);
-                    }
-                    if (row[a] >= 0 && sub == 0) {
-                        if (brow[row[a]] != nullptr) // else the base product to the bit
-                            v += d;
-                        p.y[(int64_t)row[a] * p.y_stride + f0 + f[a]] = f32_to_bf16_bits(v);
-                    }
+                    const int o = o0 + a * RW_FINISH * each + first;
+                    if (sub == 0 && o < outs)
+                        delta[o] = d;
                 }
             }
-            if (s + RW_BUFS < steps)
-                named_bar_arrive(RW_FREE + buf, RW_THREADS);
+            named_bar_sync(RW_H, RW_FINISH * 32);
+            wait_or_note(&part_full[buf], (uint32_t)(s / RW_BUFS) & 1u, &bad);
+            const float *from = part + (size_t)buf * RW_WARPS * RW_PART;
+            for (int o = ft; o < outs; o += RW_FINISH * 32) {
+                const int row = o / width, f = o - row * width;
+                const float *q = from + (size_t)((f >> 4) * T) * RW_PART + (f & 15) * RW_ROWS + row;
+                float v = q[0];
+#pragma unroll 4
+                for (int w = 1; w < sums; ++w)
+                    v += q[w * RW_PART];
+                if (brow[row] != nullptr) // else the base product to the bit
+                    v += delta[o];
+                if (f0 + f < p.N)
+                    p.y[(int64_t)row * p.y_stride + f0 + f] = f32_to_bf16_bits(v);
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&part_free[buf]);
+            named_bar_sync(RW_H, RW_FINISH * 32); // delta is written again
         }
         if (ft == 0 && *reinterpret_cast<volatile int *>(&bad) != 0)
             atomicOr(p.status, (uint32_t)LORA_FLAG_WAIT_TIMEOUT);

@@ -95,6 +95,9 @@ __device__ __forceinline__ void mx4_factors(uint32_t byte, uint32_t &f1, uint32_
     f2 |= f2 << 16;
 }
 
+// The first of them alone, for byte <= MX4_ONE_FACTOR: twice (byte + 126) << 7.
+__device__ __forceinline__ uint32_t mx4_factor(uint32_t byte) { return byte * 0x00800080u + 0x3F003F00u; }
+
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
 {
     uint32_t r;

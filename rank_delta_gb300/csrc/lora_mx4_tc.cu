@@ -5,9 +5,12 @@
 // A CTA takes 128 features by one tile of up to 256 rows and a part of K.
 // The codes come by TMA, 256 k of 128 rows a box; sixteen warps widen them to
 // bf16 exactly and store them as the swizzled K-major operand of tcgen05.mma; x
-// comes by TMA in the same layout; one thread issues the products into TMEM. The weight is
-// widened once for all rows of the tile, so from some 100 rows on the tensor
-// cores are the bound and below it the codes' way from HBM.
+// comes by TMA in the same layout; one thread issues the products into TMEM. The
+// weight is widened once for all rows of the tile. With tiles of 256 rows the
+// tensor cores bound it (8192x4096x14336: 733 us without adapters, 1.31 PFLOP/s);
+// with fewer rows it is the widening and what a call takes in any case, shrink,
+// set-up and epilogue (one row of K = 1024: 7.2 us; 64x4096x4096: 16.6 us;
+// 256x4096x6144: 28.5 us).
 //
 // The adapters are more K: s h of the tile's rows (rounded to bf16, as y
 // itself is; the sums stay fp32) against the B rows of each slot in the tile,
@@ -123,10 +126,12 @@ __device__ __forceinline__ void umma_commit_by(uint32_t lead, uint64_t *bar)
 // with the row goes into the address once.
 __device__ __forceinline__ void widen_store(const uint4 (&codes)[2], uint32_t s0, uint32_t s1, uint32_t row_at)
 {
-    uint32_t f1[2], f2[2];
-    mx4_factors(s0, f1[0], f2[0]);
-    mx4_factors(s1, f1[1], f2[1]);
+    uint32_t f1[2] = {mx4_factor(s0), mx4_factor(s1)}, f2[2] = {0u, 0u};
     const bool twice = __any_sync(0xffffffffu, s0 > MX4_ONE_FACTOR || s1 > MX4_ONE_FACTOR);
+    if (twice) {
+        mx4_factors(s0, f1[0], f2[0]);
+        mx4_factors(s1, f1[1], f2[1]);
+    }
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
         const uint32_t w[4] = {codes[b].x, codes[b].y, codes[b].z, codes[b].w};
