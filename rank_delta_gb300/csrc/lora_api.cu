@@ -1435,20 +1435,19 @@ lora_status check_mx4(const char *who, const void *w, int dtype, int64_t w_strid
     return LORA_OK;
 }
 
-// The path a call takes: by itself, the rows kernel up to four rows. What both
-// take, rows kernel and tiles in us, every row of an adapter of its own of rank 64:
-//   K x N         1 row        4 rows       8 rows
-//   4096 x  4096   9.3  11.5   11.3  11.7   14.1  12.6
-//   4096 x 14336  21.3  24.2   27.3  26.5   39.9  28.5
-//   4096 x 32000  43.4  47.4   50.9  50.2   75.7  52.0
-//   8192 x  4096  13.5  15.7   14.3  16.0   17.9  17.8
-// The rows kernel reads a row's B on its own and multiplies on the CUDA cores, a
-// tile has them in its products: the wider the matrix, the earlier tiles win.
-// (Without adapters the rows kernel is ahead up to seven rows or so.)
+// The path a call takes: the rows kernel where it can. What it and tiles take
+// in us, every row of an adapter of its own of rank 64 (K = 1024: 16):
+//   K x N         1 row        2 rows       4 rows
+//   1024 x  4096   6.4   8.0    6.3   8.1    6.4   8.1
+//   4096 x  4096   8.7  11.4    9.1  11.6   10.1  11.7
+//   4096 x 14336  17.3  24.1   18.9  25.1   22.6  26.5
+//   4096 x 32000  31.8  47.2   35.6  48.0   41.5  50.1
+//   8192 x  4096  12.4  15.6   12.5  15.7   13.0  16.0
+// (For up to eight rows, with twice the room for x, it took 39.9 us for
+// 8 x 4096 x 14336 and tiles 28.5.)
 int mx4_path(int M, int K, int R, int path)
 {
-    constexpr int ROWS_AUTO = 4;
-    if (path == LORA_MX4_PATH_TILES || (path == LORA_MX4_PATH_AUTO && M > ROWS_AUTO) || !mx4_rows_fit(M, K, R))
+    if (path == LORA_MX4_PATH_TILES || !mx4_rows_fit(M, K, R))
         return LORA_MX4_PATH_TILES;
     return LORA_MX4_PATH_ROWS;
 }

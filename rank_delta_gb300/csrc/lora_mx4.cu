@@ -10,7 +10,7 @@
 //            from memory: 16 rank rows by up to 16 of the slot's rows a CTA and
 //            pass. The projection kernels start behind it at once and wait for
 //            h only where they need it.
-// rows       the product for up to eight rows, on the tensor cores' registers
+// rows       the product for up to four rows, on the tensor cores' registers
 //            (mma.sync): a warp's 16 weight rows need not pass through shared
 //            memory a second time once they are widened.
 #include "lora_mx4.cuh"
@@ -516,7 +516,7 @@ namespace {
 
 constexpr int RW_WARPS = 16, RW_FINISH = 4;  // compute, finish
 constexpr int RW_THREADS = (RW_WARPS + RW_FINISH) * 32;
-constexpr int RW_ROWS = 8;                   // batch rows: the n of one mma
+constexpr int RW_ROWS = 4;                   // batch rows: half the n of one mma
 constexpr uint32_t RW_BOX = 16 * 128;        // codes of 16 weight rows x 256 k
 constexpr int RW_BUFS = 3;                   // steps whose partial sums may wait to be finished
 constexpr uint32_t RW_PART = 16 * RW_ROWS;   // floats of a warp's partial tile, [feature][row]
@@ -573,10 +573,10 @@ __device__ __forceinline__ void widen_pair(uint32_t a, uint32_t b, uint32_t fa, 
 // of code boxes that its lane 0 keeps asking for by TMA, steps ahead, so
 // nothing in a CTA waits for anything but its own boxes; partial sums of a
 // step go to shared memory, and four more warps add them in order, add the
-// adapters and write y while the next steps are in work. x (8 rows, all of K)
+// adapters and write y while the next steps are in work. x (4 rows, all of K)
 // stays in shared memory; within 64 bytes its 16-byte pieces are turned by
-// the row and the block so that the eight lanes of a load phase meet eight
-// different bank groups. Which k a fragment's slots mean is free as long as
+// the row and the block so that the eight lanes of a load phase meet different
+// bank groups. Which k a fragment's slots mean is free as long as
 // both operands agree: thread t of four supplies the block t of 128 k.
 __global__ void __launch_bounds__(RW_THREADS, 1)
     mx4_rows_kernel(const __grid_constant__ CUtensorMap codes, const __grid_constant__ Mx4ProjParams p, RowsShape shape)
@@ -621,18 +621,19 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
         const bool eights = nblk % 8 == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 7u) == 0;
         const int jump = (int)gridDim.x * teams * 16; // features from a step to the next
         int sf = feature(0) + g, sk = 0;              // where the next are
-        auto next_scales = [&](uint32_t (&sc)[4]) {
+        const int byte_at = eights ? 8 * t : 0;
+        // The bytes are cut out where they are used: here the cut would wait for
+        // the load, a quarter of the time of a step.
+        auto next_scales = [&](uint2 (&sc)[2]) {
             const int b0 = (wk + sk * T) * 8;
 #pragma unroll
             for (int r = 0; r < 2; ++r) { // rows past N repeat the last; their sums are dropped
                 const uint8_t *row = p.scales + (size_t)min(sf + 8 * r, p.N - 1) * nblk + b0;
-                if (eights) {
-                    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(row));
-                    sc[r] = v.x >> (8 * t) & 255u;
-                    sc[2 + r] = v.y >> (8 * t) & 255u;
-                } else {
-                    sc[r] = b0 + t < nblk ? __ldg(row + t) : 0u;
-                    sc[2 + r] = b0 + 4 + t < nblk ? __ldg(row + 4 + t) : 0u;
+                if (eights)
+                    sc[r] = __ldg(reinterpret_cast<const uint2 *>(row));
+                else {
+                    sc[r].x = b0 + t < nblk ? __ldg(row + t) : 0u;
+                    sc[r].y = b0 + 4 + t < nblk ? __ldg(row + 4 + t) : 0u;
                 }
             }
             if (++sk == per) {
@@ -643,7 +644,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
         if (lane == 0)
             for (int u = 0; u < min(depth, units); ++u)
                 ask(u, u);
-        uint32_t next[4] = {0, 0, 0, 0};
+        uint2 next[2] = {};
         if (units > 0)
             next_scales(next);
         // x, zeros past K and M
@@ -659,7 +660,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
         }
         named_bar_sync(RW_X, RW_WARPS * 32);
 
-        const uint32_t xg = xs + (uint32_t)g * xrow + (uint32_t)t * 64u;
+        const uint32_t xg = xs + (uint32_t)(g & (RW_ROWS - 1)) * xrow + (uint32_t)t * 64u; // columns 4 to 7 repeat
         const uint32_t turn = (uint32_t)((t >> 1) | (g & 1) << 1) << 4;
         const uint32_t row_at = (uint32_t)g * 128u; // of a box; row g + 8 is 1024 further and turned alike
         int slot = 0;
@@ -670,8 +671,10 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
                 const int box = wk + k * T;
                 uint32_t sc[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sc[i] = next[i];
+                for (int r = 0; r < 2; ++r) {
+                    sc[r] = next[r].x >> byte_at & 255u;
+                    sc[2 + r] = next[r].y >> byte_at & 255u;
+                }
                 if (u + 1 < units)
                     next_scales(next);
                 wait_or_note(&full[warp][slot], parity, &bad);
@@ -716,8 +719,10 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
             if (use > 0) // the step that used the buffer before has been finished
                 wait_or_note(&part_free[buf], (uint32_t)(use - 1) & 1u, &bad);
             float *to = part + (size_t)(buf * RW_WARPS + warp) * RW_PART;
-            *reinterpret_cast<float2 *>(to + g * RW_ROWS + 2 * t) = make_float2(acc[0], acc[1]);
-            *reinterpret_cast<float2 *>(to + (g + 8) * RW_ROWS + 2 * t) = make_float2(acc[2], acc[3]);
+            if (t < RW_ROWS / 2) {
+                *reinterpret_cast<float2 *>(to + g * RW_ROWS + 2 * t) = make_float2(acc[0], acc[1]);
+                *reinterpret_cast<float2 *>(to + (g + 8) * RW_ROWS + 2 * t) = make_float2(acc[2], acc[3]);
+            }
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&part_full[buf]);
@@ -741,47 +746,55 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
         named_bar_sync(RW_H, RW_FINISH * 32);
         // the adapter's part of an output takes `lanes` lanes, a 16-byte piece of its
         // B row each; then a thread adds the team's partial sums of an output
+        // (a step's first pieces are asked for while the step before is in work)
         const int pieces = p.R / 8, sums = min(T, shape.boxes), width = teams * 16, outs = width * p.M;
+        const int wide = 31 - __clz(width); // a power of two
         int lanes = 1;
         while (lanes < pieces)
             lanes *= 2;
         const int sub = lane & (lanes - 1), each = 32 / lanes, first = (ft >> 5) * each + lane / lanes;
         constexpr int AT_ONCE = 4;
+        uint4 b[AT_ONCE];
+        auto ask = [&](int s, int o0) {
+            const int f0 = (s * (int)gridDim.x + (int)blockIdx.x) * width;
+#pragma unroll
+            for (int a = 0; a < AT_ONCE; ++a) {
+                const int o = o0 + a * RW_FINISH * each + first, r = o >> wide, f = f0 + (o & (width - 1));
+                b[a] = make_uint4(0, 0, 0, 0);
+                if (o < outs && f < p.N && sub < pieces && brow[r] != nullptr)
+                    b[a] = ld_nc_16(brow[r] + (size_t)f * p.R + sub * 8);
+            }
+        };
+        if (steps > 0)
+            ask(0, 0);
         for (int s = 0; s < steps; ++s) {
             const int buf = s % RW_BUFS, f0 = (s * (int)gridDim.x + (int)blockIdx.x) * width;
             for (int o0 = 0; o0 < outs; o0 += RW_FINISH * each * AT_ONCE) {
-                uint4 b[AT_ONCE];
-                int row[AT_ONCE];
-#pragma unroll
-                for (int a = 0; a < AT_ONCE; ++a) {
-                    const int o = o0 + a * RW_FINISH * each + first, r = o / width, f = f0 + o - r * width;
-                    const bool have = o < outs && f < p.N && sub < pieces && brow[r & (RW_ROWS - 1)] != nullptr;
-                    row[a] = have ? r : -1;
-                    b[a] = make_uint4(0, 0, 0, 0);
-                    if (have)
-                        b[a] = ld_nc_16(brow[r] + (size_t)f * p.R + sub * 8);
-                }
+                if (o0 > 0)
+                    ask(s, o0);
 #pragma unroll
                 for (int a = 0; a < AT_ONCE; ++a) {
                     if (o0 + a * RW_FINISH * each >= outs) // none of the warp's lanes has one
                         break;
+                    const int o = o0 + a * RW_FINISH * each + first;
                     float d = 0.0f;
-                    if (row[a] >= 0) {
-                        const float4 *h = reinterpret_cast<const float4 *>(hs + row[a] * p.R + sub * 8);
+                    if (o < outs && sub < pieces) {
+                        const float4 *h = reinterpret_cast<const float4 *>(hs + (o >> wide) * p.R + sub * 8);
                         d = dot8_bf_f32(0.0f, b[a], h[0], h[1]);
                     }
-                    for (int o = lanes / 2; o > 0; o >>= 1)
-                        d += __shfl_xor_sync(0xffffffffu, d, o);
-                    const int o = o0 + a * RW_FINISH * each + first;
+                    for (int i = lanes / 2; i > 0; i >>= 1)
+                        d += __shfl_xor_sync(0xffffffffu, d, i);
                     if (sub == 0 && o < outs)
                         delta[o] = d;
                 }
             }
+            if (s + 1 < steps)
+                ask(s + 1, 0);
             named_bar_sync(RW_H, RW_FINISH * 32);
             wait_or_note(&part_full[buf], (uint32_t)(s / RW_BUFS) & 1u, &bad);
             const float *from = part + (size_t)buf * RW_WARPS * RW_PART;
             for (int o = ft; o < outs; o += RW_FINISH * 32) {
-                const int row = o / width, f = o - row * width;
+                const int row = o >> wide, f = o & (width - 1);
                 const float *q = from + (size_t)((f >> 4) * T) * RW_PART + (f & 15) * RW_ROWS + row;
                 float v = q[0];
 #pragma unroll 4
