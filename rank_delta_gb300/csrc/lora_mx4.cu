@@ -641,9 +641,10 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
                 sf += jump;
             }
         };
-        if (lane == 0)
+        if (elected())
             for (int u = 0; u < min(depth, units); ++u)
                 ask(u, u);
+        __syncwarp();
         uint2 next[2] = {};
         if (units > 0)
             next_scales(next);
@@ -708,7 +709,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
                     }
                 }
                 __syncwarp(); // every lane has read the box
-                if (lane == 0 && u + depth < units)
+                if (u + depth < units && elected())
                     ask(u + depth, slot);
                 if (++slot == depth) {
                     slot = 0;

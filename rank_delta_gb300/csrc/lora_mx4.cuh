@@ -79,6 +79,16 @@ __device__ __forceinline__ void wait_or_note(uint64_t *bar, uint32_t parity, int
     }
 }
 
+// One lane of the converged warp, by the instruction that tells the compiler so:
+// what follows in its branch needs no loop over lanes that might differ (with
+// lane == 0 instead a product took 80 cycles to issue: 8192x4096x14336 748 us, not 690).
+__device__ __forceinline__ bool elected()
+{
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.b32 %0, 1, 0, e;\n\t}" : "=r"(one));
+    return one != 0u;
+}
+
 // The bf16 factors that turn value * 2^-126 (what mx4_unpack8 gives) into value
 // * 2^(byte - 127). The second is 1 unless the first would leave bf16's range
 // (byte > MX4_ONE_FACTOR).

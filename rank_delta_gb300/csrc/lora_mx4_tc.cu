@@ -4,13 +4,14 @@
 //
 // A CTA takes 128 features by one tile of up to 256 rows and a part of K.
 // The codes come by TMA, 256 k of 128 rows a box; sixteen warps widen them to
-// bf16 exactly and store them as the swizzled K-major operand of tcgen05.mma; x
-// comes by TMA in the same layout; one thread issues the products into TMEM. The
-// weight is widened once for all rows of the tile. With tiles of 256 rows the
-// tensor cores bound it (8192x4096x14336: 733 us without adapters, 1.31 PFLOP/s);
-// with fewer rows it is the widening and what a call takes in any case, shrink,
-// set-up and epilogue (one row of K = 1024: 7.2 us; 64x4096x4096: 16.6 us;
-// 256x4096x6144: 28.5 us).
+// bf16 exactly and store them in tensor memory, where tcgen05.mma takes its first
+// operand from (a thread has a row there as it has here: no swizzle, no fence, and
+// shared memory is left to x); x comes by TMA, and one thread issues the products.
+// The weight is widened once for all rows of the tile. With tiles of 256 rows
+// the tensor cores and what a tile takes before and after them bound it
+// (8192x4096x14336: 623 us without adapters, 1.55 PFLOP/s; a stage of 64 k takes
+// 555 cycles, its products 512); with fewer rows it is the widening and what a
+// call takes in any case, shrink, set-up and epilogue.
 //
 // The adapters are more K: s h of the tile's rows (rounded to bf16, as y
 // itself is; the sums stay fp32) against the B rows of each slot in the tile,
@@ -33,23 +34,33 @@ namespace cg = cooperative_groups;
 namespace {
 
 constexpr int BM = 128;             // features of a tile: the UMMA M
-// Three rings between TMA, the widening warps and the products. A stage is SUB
-// sub-tiles of 64 k: AS slots of widened weights (16 KB a sub-tile), XS slots of
-// tn rows of x (tn 128 bytes), CS steps of codes (256 k of 128 rows, and 16 scale
-// bytes a row). Groups of four warps (128 rows) widen, sub-tile m by group m mod
-// GROUPS, and drain the accumulators.
+// The rings between TMA, the widening warps and the products. A stage is SUB
+// sub-tiles of 64 k. There are S of them: widened weights in tensor memory (32
+// columns a sub-tile, from column A_COL on) and tn rows of x in shared memory (tn
+// 128 bytes a sub-tile), with one barrier for "both are there" and one for "the
+// products are through". CS steps of codes (256 k of 128 rows, and 16 scale
+// bytes a row) and DS slots of the adapters' rows come besides. Groups of four
+// warps (128 rows) widen, sub-tile m by group m mod GROUPS, and drain the
+// accumulators.
 //
-// The thread that issues the products spends some 100 cycles on each wait and
-// more on a commit, which is longer than the products of 64 k take for up to
-// about 128 rows: there a stage has two sub-tiles.
-template <int SUB_, int AS_, int XS_, int CS_> struct Rings {
-    static constexpr int SUB = SUB_, AS = AS_, XS = XS_, CS = CS_;
-    static constexpr int GROUPS = SUB == 1 && AS < 4 ? AS : 4, WARPS = GROUPS * 4, THREADS = (WARPS + 4) * 32;
+// 64 k take 2 tn cycles of the tensor cores. Up to about 128 rows that is less
+// than a stage's waits and commits, so a stage has two sub-tiles there
+// (64x4096x14336: 30.5 us, with one 32.4); above, two would leave two stages
+// only (256x4096x14336: 45 us with one, 53 with two).
+//
+// Up to 128 rows the widened weights lie behind both accumulators; above it
+// they take the columns of the adapters' accumulator (ALIAS), which is not written
+// before the last base product has read them.
+template <int SUB_, int S_, int CS_, int DS_, int A_COL_, bool ALIAS_> struct Rings {
+    static constexpr int SUB = SUB_, S = S_, CS = CS_, DS = DS_, A_COL = A_COL_;
+    static constexpr bool ALIAS = ALIAS_;
+    static constexpr int GROUPS = 4, WARPS = GROUPS * 4, THREADS = (WARPS + 4) * 32;
     // A group that waits for its stage's slot has been told, by the wait for its
     // stage before (GROUPS / SUB stages earlier), that the slot's use before the
     // last is through; were that still open, the parity of the last use would
     // not tell the two apart.
-    static_assert(AS >= GROUPS / SUB && XS >= AS, "parity of a slot's last use");
+    static_assert(S >= GROUPS / SUB && S >= DS, "parity of a slot's last use");
+    static_assert(A_COL + S * SUB * 32 <= 512, "tensor memory");
 };
 constexpr int MAX_RING = 16;
 constexpr uint32_t CODE_BYTES = BM * 128, SCALE_BYTES = BM * 16;
@@ -57,8 +68,7 @@ constexpr uint32_t A_BYTES = BM * 128;
 constexpr int MAX_TN = 256;
 
 struct TcShared {
-    uint64_t x_full[MAX_RING], x_free[MAX_RING], a_full[MAX_RING], a_free[MAX_RING], c_full[MAX_RING], c_free[MAX_RING];
-    uint64_t d_full[MAX_RING], routed, done;
+    uint64_t full[MAX_RING], free[MAX_RING], c_full[MAX_RING], c_free[MAX_RING], d_full[MAX_RING], routed, base_done, done;
     uint32_t tmem;
     int bad;                          // a wait gave up
     int nseg;
@@ -81,10 +91,6 @@ __device__ __forceinline__ uint4 lds_16(uint32_t addr)
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
 }
-__device__ __forceinline__ void sts_16(uint32_t addr, uint4 v)
-{
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
 __device__ __forceinline__ uint32_t lds_2(uint32_t addr)
 {
     uint16_t v;
@@ -101,30 +107,32 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     return r;
 }
 
-// umma_bf16 and umma_commit by the lanes with lead != 0.
-__device__ __forceinline__ void umma_bf16_by(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate)
+// umma_bf16 with A in tensor memory: 128 lanes, two k a column.
+__device__ __forceinline__ void umma_bf16_tmem(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate)
 {
-    asm volatile("{\n\t.reg .pred p, q;\n\t"
-                 "setp.ne.b32 q, %5, 0;\n\t"
+    asm volatile("{\n\t.reg .pred p;\n\t"
                  "setp.ne.b32 p, %4, 0;\n\t"
-                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+                 "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
                  : "memory");
 }
-__device__ __forceinline__ void umma_commit_by(uint32_t lead, uint64_t *bar)
+// 32 columns of the warp's 32 lanes.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32])
 {
-    asm volatile("{\n\t.reg .pred q;\n\t"
-                 "setp.ne.b32 q, %1, 0;\n\t"
-                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
-                 "r"(lead)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+                 "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+                 "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+                 "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+                 "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+                 "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
                  : "memory");
 }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Two blocks of a row, 32 codes each, and their scale bytes -> the row's 128
-// bytes of bf16. row_at is where its piece 0 lies: the swizzle's exclusive or
-// with the row goes into the address once.
-__device__ __forceinline__ void widen_store(const uint4 (&codes)[2], uint32_t s0, uint32_t s1, uint32_t row_at)
+// Two blocks of a row, 32 codes each, and their scale bytes -> 64 k in bf16.
+__device__ __forceinline__ void widen(const uint4 (&codes)[2], uint32_t s0, uint32_t s1, uint32_t (&out)[32])
 {
     uint32_t f1[2] = {mx4_factor(s0), mx4_factor(s1)}, f2[2] = {0u, 0u};
     const bool twice = __any_sync(0xffffffffu, s0 > MX4_ONE_FACTOR || s1 > MX4_ONE_FACTOR);
@@ -141,14 +149,13 @@ __device__ __forceinline__ void widen_store(const uint4 (&codes)[2], uint32_t s0
             mx4_unpack8(w[j], o);
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                o[q] = mul_bf16x2(o[q], f1[b]);
-            if (twice) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    o[q] = mul_bf16x2(o[q], f2[b]);
-            }
-            sts_16(row_at ^ (uint32_t)((b * 4 + j) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+                out[b * 16 + j * 4 + q] = mul_bf16x2(o[q], f1[b]);
         }
+    }
+    if (twice) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            out[i] = mul_bf16x2(out[i], f2[i / 16]);
     }
 }
 
@@ -212,39 +219,35 @@ template <typename RINGS>
 __global__ void __launch_bounds__(RINGS::THREADS, 1)
     mx4_tc_kernel(const __grid_constant__ Mx4TcMaps maps, const __grid_constant__ Mx4ProjParams p, int tn, int kparts)
 {
-    constexpr int SUB = RINGS::SUB, AS = RINGS::AS, XS = RINGS::XS, CS = RINGS::CS, GROUPS = RINGS::GROUPS, WIDEN_WARPS = RINGS::WARPS;
+    constexpr int SUB = RINGS::SUB, S = RINGS::S, CS = RINGS::CS, DS = RINGS::DS, GROUPS = RINGS::GROUPS, WIDEN_WARPS = RINGS::WARPS;
     extern __shared__ uint8_t tc_smem_raw[];
     __shared__ TcShared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t raw = smem_u32(tc_smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *const smem = tc_smem_raw + (base - raw);
     const uint32_t x_bytes = (uint32_t)tn * 128u;
-    const uint32_t a_at = base, x_at = base + AS * SUB * A_BYTES, codes_at = x_at + XS * SUB * x_bytes,
+    const uint32_t d_at = base, x_at = base + DS * SUB * A_BYTES, codes_at = x_at + S * SUB * x_bytes,
                    scales_at = codes_at + CS * CODE_BYTES;
     const int part = blockIdx.x % kparts, f0 = (blockIdx.x / kparts) * BM, t0 = blockIdx.y * tn;
     const int nblk = p.K / 32, nst = (nblk + 1) / 2, nsteps = (nst + 3) / 4; // blocks of 32 k, sub-tiles of 64, steps of 256
     const int j0 = (int)((int64_t)nsteps * part / kparts), j1 = (int)((int64_t)nsteps * (part + 1) / kparts);
     // sub-tiles of the part, whole stages (past K both operands are zeros)
     const int m0 = 4 * j0, mbase = (min(nst, 4 * j1) - m0 + SUB - 1) / SUB * SUB, nbase = mbase / SUB;
-    uint32_t cols = 32;
-    while ((int)cols < 2 * tn)
-        cols *= 2;
+    constexpr uint32_t cols = 512; // no second CTA fits on the SM by its shared memory
 
     if (tid == 0) {
-        for (int s = 0; s < XS; ++s) {
-            mbar_init(&sh.x_full[s], 1);
-            mbar_init(&sh.x_free[s], 1);
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&sh.full[s], 1 + 4 * SUB); // x, and the groups' warps
+            mbar_init(&sh.free[s], 1);
         }
-        for (int s = 0; s < AS; ++s) {
-            mbar_init(&sh.a_full[s], 4 * SUB); // the groups' warps
-            mbar_init(&sh.a_free[s], 1);
+        for (int s = 0; s < DS; ++s)
             mbar_init(&sh.d_full[s], WIDEN_WARPS * 32);
-        }
         for (int s = 0; s < CS; ++s) {
             mbar_init(&sh.c_full[s], 1);
             mbar_init(&sh.c_free[s], 16); // four warps for each of the step's four stages
         }
         mbar_init(&sh.routed, 1);
+        mbar_init(&sh.base_done, 1);
         mbar_init(&sh.done, 1);
         sh.bad = 0;
         fence_barrier_init();
@@ -256,6 +259,8 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
 
+    // stage n's products are through (stage n - S is known to be)
+    auto stage_free = [&](int n) { wait_or_note(&sh.free[n % S], (uint32_t)(n / S) & 1u, &sh.bad); };
     if (warp < WIDEN_WARPS) {
         // ---- widen: every GROUPS-th sub-tile
         const int group = warp >> 2, row = (warp & 3) * 32 + lane;
@@ -280,15 +285,19 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&sh.c_free[cs]);
-            const int n = m / SUB, s = n % AS, use = n / AS;
-            if (use > 0)
-                wait_or_note(&sh.a_free[s], (uint32_t)(use - 1) & 1u, &sh.bad);
+            const int n = m / SUB, s = n % S;
+            if (n >= S)
+                stage_free(n - S);
             __syncwarp();
-            widen_store(c, sc & 255u, (sc >> 8) & 255u, a_at + (uint32_t)(s * SUB + m % SUB) * A_BYTES + own);
-            fence_proxy_async_smem();
+            tc_fence_after();
+            uint32_t out[32];
+            widen(c, sc & 255u, (sc >> 8) & 255u, out);
+            tmem_st32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(RINGS::A_COL + (s * SUB + m % SUB) * 32), out);
+            tmem_wait_st();
+            tc_fence_before();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&sh.a_full[s]);
+                mbar_arrive(&sh.full[s]);
         }
 
         // ---- the adapters' operands: 4 SUB segments of 16 ranks a stage, every
@@ -303,17 +312,17 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
             grid_dependency_wait(); // h is complete
         int q = q0 + group, lo = 0; // this group's next segment, and the slot it belongs to
         for (int d = 0; d < ndelta; ++d) {
-            const int n = nbase + d, s = n % AS, use = n / AS, xslot = n % XS, xuse = n / XS;
-            if (use > 0)
-                wait_or_note(&sh.a_free[s], (uint32_t)(use - 1) & 1u, &sh.bad);
-            if (xuse > 0)
-                wait_or_note(&sh.x_free[xslot], (uint32_t)(xuse - 1) & 1u, &sh.bad);
+            const int n = nbase + d, s = d % DS, xslot = n % S;
+            if (d >= DS) // then n - S is, too
+                stage_free(n - DS);
+            else if (n >= S)
+                stage_free(n - S);
             for (; q < min(q1, q0 + 4 * SUB * (d + 1)); q += GROUPS) {
                 const int j = q - q0 - 4 * SUB * d;
                 while (lo + 1 < sh.nslot && sh.seg_start[lo + 1] <= q)
                     ++lo;
                 const int r = (q - sh.seg_start[lo]) * 16, slot = sh.slot_id[lo];
-                const uint32_t two = r + 8 < p.R ? 16u : 0u, at = a_at + (uint32_t)(s * SUB + (j >> 2)) * A_BYTES,
+                const uint32_t two = r + 8 < p.R ? 16u : 0u, at = d_at + (uint32_t)(s * SUB + (j >> 2)) * A_BYTES,
                                xt = x_at + (uint32_t)(xslot * SUB + (j >> 2)) * x_bytes;
                 const uint16_t *b = sh.slot_b[lo] + (size_t)rowi * p.R + r;
                 cp16(at + sw128(row, 2 * (j & 3)), b, 16u);
@@ -331,79 +340,90 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         __syncwarp();
     } else if (warp == WIDEN_WARPS) {
         // ---- x
-        if (lane == 0) {
+        if (elected()) {
             prefetch_tmap(&maps.x);
             for (int n = 0; n < nbase; ++n) {
-                const int s = n % XS, use = n / XS;
-                if (use > 0)
-                    wait_or_note(&sh.x_free[s], (uint32_t)(use - 1) & 1u, &sh.bad);
-                mbar_arrive_expect_tx(&sh.x_full[s], SUB * x_bytes);
+                const int s = n % S;
+                if (n >= S)
+                    stage_free(n - S);
+                mbar_arrive_expect_tx(&sh.full[s], SUB * x_bytes);
                 for (int h = 0; h < SUB; ++h)
-                    tma_load_2d(smem + AS * SUB * A_BYTES + (uint32_t)(s * SUB + h) * x_bytes, &maps.x, (m0 + n * SUB + h) * 64,
-                                t0, &sh.x_full[s]);
+                    tma_load_2d(smem + DS * SUB * A_BYTES + (uint32_t)(s * SUB + h) * x_bytes, &maps.x, (m0 + n * SUB + h) * 64,
+                                t0, &sh.full[s]);
             }
         }
         __syncwarp();
     } else if (warp == WIDEN_WARPS + 1) {
-        // ---- products: the whole warp goes along, so that what the instructions
-        // take is known to be the same in all lanes; lane 0 issues
-        const uint32_t lead = lane == 0 ? 1u : 0u, idesc = idesc_bf16_f32(BM, (uint32_t)tn);
-        const uint64_t adesc = sw128_kmajor_desc(a_at), xdesc = sw128_kmajor_desc(x_at);
-        auto stage = [&](uint32_t d_tmem, int s, int xslot, int steps, bool first) {
-            const uint64_t ad = adesc + (uint64_t)(uint32_t)(s * SUB) * (A_BYTES >> 4);
-            const uint64_t xd = xdesc + (uint64_t)((uint32_t)(xslot * SUB) * (x_bytes >> 4));
-#pragma unroll
-            for (int j = 0; j < 4 * SUB; ++j)
-                if (j < steps)
-                    umma_bf16_by(lead, d_tmem, ad + (uint64_t)((j >> 2) * (A_BYTES >> 4) + (j & 3) * 2),
-                                 xd + (uint64_t)((uint32_t)(j >> 2) * (x_bytes >> 4) + (uint32_t)(j & 3) * 2u), idesc,
-                                 first && j == 0 ? 0u : 1u);
-            umma_commit_by(lead, &sh.a_free[s]);
-            umma_commit_by(lead, &sh.x_free[xslot]);
-        };
-        int s = 0, xslot = 0;
-        uint32_t a_parity = 0, x_parity = 0;
-        auto advance = [&] {
-            if (++s == AS) {
+        // ---- products
+        const uint32_t idesc = idesc_bf16_f32(BM, (uint32_t)tn);
+        const uint64_t ddesc = sw128_kmajor_desc(d_at), xdesc = sw128_kmajor_desc(x_at);
+        const uint32_t widened = tmem + RINGS::A_COL, delta = tmem + (uint32_t)(RINGS::ALIAS ? MAX_TN : tn);
+        int s = 0;
+        uint32_t parity = 0;
+        auto x_of = [&] { return xdesc + (uint64_t)((uint32_t)(s * SUB) * (x_bytes >> 4)); };
+        auto next = [&] {
+            if (++s == S) {
                 s = 0;
-                a_parity ^= 1u;
-            }
-            if (++xslot == XS) {
-                xslot = 0;
-                x_parity ^= 1u;
+                parity ^= 1u;
             }
         };
         for (int n = 0; n < nbase; ++n) {
-            // both polls on their way at once
-            const bool x_in = mbar_try_wait(smem_u32(&sh.x_full[xslot]), x_parity), a_in = mbar_try_wait(smem_u32(&sh.a_full[s]), a_parity);
-            if (!x_in)
-                wait_or_note(&sh.x_full[xslot], x_parity, &sh.bad);
-            if (!a_in)
-                wait_or_note(&sh.a_full[s], a_parity, &sh.bad);
+            wait_or_note(&sh.full[s], parity, &sh.bad);
+            __syncwarp();
             tc_fence_after();
-            stage(tmem, s, xslot, 4 * SUB, n == 0);
-            advance();
+            const uint64_t xd = x_of();
+            if (elected()) {
+#pragma unroll
+                for (int j = 0; j < 4 * SUB; ++j)
+                    umma_bf16_tmem(tmem, widened + (uint32_t)(s * SUB * 32 + j * 8),
+                                   xd + (uint64_t)((uint32_t)(j >> 2) * (x_bytes >> 4) + (uint32_t)(j & 3) * 2u), idesc,
+                                   n == 0 && j == 0 ? 0u : 1u);
+                umma_commit(&sh.free[s]);
+            }
+            __syncwarp();
+            next();
         }
         wait_or_note(&sh.routed, 0, &sh.bad);
         const int q0 = sh.nseg * part / kparts, q1 = sh.nseg * (part + 1) / kparts;
-        for (int q = q0; q < q1 && !__any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&sh.bad) != 0); q += 4 * SUB) {
-            wait_or_note(&sh.d_full[s], (uint32_t)((q - q0) / (4 * SUB) / AS) & 1u, &sh.bad);
+        if (RINGS::ALIAS && q1 > q0) {
+            __syncwarp();
+            if (elected())
+                umma_commit(&sh.base_done);
+            __syncwarp();
+            wait_or_note(&sh.base_done, 0, &sh.bad);
+            tc_fence_after();
+        }
+        for (int q = q0, d = 0; q < q1 && !__any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&sh.bad) != 0); q += 4 * SUB, ++d) {
+            const int ds = d % DS;
+            wait_or_note(&sh.d_full[ds], (uint32_t)(d / DS) & 1u, &sh.bad);
+            __syncwarp();
             fence_proxy_async_smem(); // cp.async (generic proxy) wrote both operands
             tc_fence_after();
-            stage(tmem + (uint32_t)tn, s, xslot, q1 - q, q == q0);
-            advance();
+            const uint64_t dd = ddesc + (uint64_t)(uint32_t)(ds * SUB) * (A_BYTES >> 4), xd = x_of();
+            if (elected()) {
+#pragma unroll
+                for (int j = 0; j < 4 * SUB; ++j)
+                    if (j < q1 - q)
+                        umma_bf16(delta, dd + (uint64_t)((j >> 2) * (A_BYTES >> 4) + (j & 3) * 2),
+                                  xd + (uint64_t)((uint32_t)(j >> 2) * (x_bytes >> 4) + (uint32_t)(j & 3) * 2u), idesc,
+                                  d == 0 && j == 0 ? 0u : 1u);
+                umma_commit(&sh.free[s]);
+            }
+            __syncwarp();
+            next();
         }
-        umma_commit_by(lead, &sh.done);
+        if (elected())
+            umma_commit(&sh.done);
         __syncwarp();
     } else if (warp == WIDEN_WARPS + 2) {
         // ---- codes and scales
-        if (lane == 0) {
+        if (elected()) {
             for (int j = 0; 4 * j < mbase; ++j) {
                 const int cs = j % CS, use = j / CS;
                 if (use > 0)
                     wait_or_note(&sh.c_free[cs], (uint32_t)(use - 1) & 1u, &sh.bad);
                 mbar_arrive_expect_tx(&sh.c_full[cs], CODE_BYTES + (maps.scales_ok ? SCALE_BYTES : 0u));
-                uint8_t *at = smem + AS * SUB * A_BYTES + XS * SUB * x_bytes;
+                uint8_t *at = smem + DS * SUB * A_BYTES + S * SUB * x_bytes;
                 tma_load_2d(at + (uint32_t)cs * CODE_BYTES, &maps.codes, (j0 + j) * 128, f0, &sh.c_full[cs]);
                 if (maps.scales_ok) // the 16 bytes that hold the step's eight
                     tma_load_2d(at + CS * CODE_BYTES + (uint32_t)cs * SCALE_BYTES, &maps.scales, ((j0 + j) * 8) & ~15, f0,
@@ -437,7 +457,7 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
             uint32_t v[16], d[16];
             tmem_ld16_nowait(tmem + lanes + (uint32_t)(c * 16), v);
             if (adapted)
-                tmem_ld16_nowait(tmem + lanes + (uint32_t)(tn + c * 16), d);
+                tmem_ld16_nowait(tmem + lanes + (uint32_t)((RINGS::ALIAS ? MAX_TN : tn) + c * 16), d);
             const uint32_t on = adapted ? sh.adapted[c >> 1] >> ((c & 1) * 16) : 0u;
             tmem_wait_ld();
 #pragma unroll
@@ -511,7 +531,7 @@ cudaError_t launch(const Mx4ProjParams &p, const Mx4TcPlan &plan, const Mx4TcMap
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((p.N + BM - 1) / BM * plan.kparts), (unsigned)((p.M + plan.tn - 1) / plan.tn));
     cfg.blockDim = dim3((unsigned)RINGS::THREADS);
-    cfg.dynamicSmemBytes = 1024u + RINGS::SUB * (RINGS::AS * A_BYTES + RINGS::XS * (uint32_t)plan.tn * 128u) +
+    cfg.dynamicSmemBytes = 1024u + RINGS::SUB * (RINGS::DS * A_BYTES + RINGS::S * (uint32_t)plan.tn * 128u) +
                            RINGS::CS * (CODE_BYTES + SCALE_BYTES);
     cfg.stream = st;
     cfg.attrs = attr;
@@ -536,8 +556,9 @@ Mx4TcPlan plan_mx4_tc(const Mx4ProjParams &p, int num_sms)
 cudaError_t launch_mx4_tc(const Mx4ProjParams &p, const Mx4TcPlan &plan, const Mx4TcMaps &maps, cudaStream_t st)
 {
     if (plan.tn <= 64)
-        return launch<Rings<2, 3, 4, 3>>(p, plan, maps, st); // what fits in 227 KB
-    return plan.tn <= 128 ? launch<Rings<2, 2, 3, 3>>(p, plan, maps, st) : launch<Rings<1, 3, 4, 2>>(p, plan, maps, st);
+        return launch<Rings<2, 4, 4, 2, 128, false>>(p, plan, maps, st); // what fits in 227 KB
+    return plan.tn <= 128 ? launch<Rings<2, 3, 3, 2, 256, false>>(p, plan, maps, st)
+                          : launch<Rings<1, 4, 2, 2, 256, true>>(p, plan, maps, st);
 }
 
 } // namespace rd
