@@ -117,6 +117,28 @@ __device__ __forceinline__ void umma_bf16_tmem(uint32_t d_tmem, uint32_t a_tmem,
                  "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
                  : "memory");
 }
+// 16 lanes x 16 columns as four 8 x 8 fragments: thread t has columns 2 (t % 4)
+// and the next of lane t / 4 in r[0], r[1], of lane t / 4 + 8 in r[2], r[3], and
+// of the next eight columns in r[4..7]. Valid after tmem_wait_ld().
+__device__ __forceinline__ void tmem_ld_16x16(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+// Four 8 x 8 matrices of 16-bit values, transposed; lane l has the address of
+// row l % 8 of matrix l / 8.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, const uint32_t (&r)[4])
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+// `bytes` (a multiple of 16) from the 16-byte aligned p on into L2.
+__device__ __forceinline__ void prefetch_l2_bulk(const void *p, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 // 32 columns of the warp's 32 lanes.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32])
 {
@@ -300,38 +322,42 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
                 mbar_arrive(&sh.full[s]);
         }
 
-        // ---- the adapters' operands: 4 SUB segments of 16 ranks a stage, every
-        // GROUPS-th by this group
+        // ---- the adapters' operands: 4 SUB segments of 16 ranks a stage. Eight
+        // lanes copy a row's 128 bytes of a sub-tile, which for a rank of 64 lie in
+        // one piece: a warp's copy meets 4 lines (a row a lane, 32: 64x4096x14336 took
+        // 3 us longer)
         wait_or_note(&sh.routed, 0, &sh.bad);
         const int q0 = sh.nseg * part / kparts, q1 = sh.nseg * (part + 1) / kparts;
         const int ndelta = __any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&sh.bad) != 0)
                                ? 0
                                : (q1 - q0 + 4 * SUB - 1) / (4 * SUB);
-        const int rows = min(tn, p.M - t0);
         if (ndelta > 0)
             grid_dependency_wait(); // h is complete
-        int q = q0 + group, lo = 0; // this group's next segment, and the slot it belongs to
+        constexpr int SUB_WARPS = WIDEN_WARPS / SUB, ROWS = SUB_WARPS * 4; // that copy a sub-tile, rows at a time
+        const int sub = warp / SUB_WARPS, piece = lane & 7, first = (warp % SUB_WARPS) * 4 + (lane >> 3);
+        int lo = 0; // the slot of this thread's segment
         for (int d = 0; d < ndelta; ++d) {
             const int n = nbase + d, s = d % DS, xslot = n % S;
             if (d >= DS) // then n - S is, too
                 stage_free(n - DS);
             else if (n >= S)
                 stage_free(n - S);
-            for (; q < min(q1, q0 + 4 * SUB * (d + 1)); q += GROUPS) {
-                const int j = q - q0 - 4 * SUB * d;
+            const int q = q0 + 4 * (SUB * d + sub) + (piece >> 1);
+            if (q < q1) {
                 while (lo + 1 < sh.nslot && sh.seg_start[lo + 1] <= q)
                     ++lo;
-                const int r = (q - sh.seg_start[lo]) * 16, slot = sh.slot_id[lo];
-                const uint32_t two = r + 8 < p.R ? 16u : 0u, at = d_at + (uint32_t)(s * SUB + (j >> 2)) * A_BYTES,
-                               xt = x_at + (uint32_t)(xslot * SUB + (j >> 2)) * x_bytes;
-                const uint16_t *b = sh.slot_b[lo] + (size_t)rowi * p.R + r;
-                cp16(at + sw128(row, 2 * (j & 3)), b, 16u);
-                cp16(at + sw128(row, 2 * (j & 3) + 1), two ? b + 8 : b, two);
-                for (int tok = row; tok < tn; tok += 128) { // zeros for the other slots' rows
+                const int r = (q - sh.seg_start[lo]) * 16 + (piece & 1) * 8, slot = sh.slot_id[lo];
+                const uint32_t have = r < p.R ? 16u : 0u; // else zeros
+                const uint32_t at = d_at + (uint32_t)(s * SUB + sub) * A_BYTES, xt = x_at + (uint32_t)(xslot * SUB + sub) * x_bytes;
+                const uint16_t *b = sh.slot_b[lo] + (have ? r : 0), *h = p.hs + (size_t)t0 * p.R + (have ? r : 0);
+#pragma unroll
+                for (int i = 0; i < BM / ROWS; ++i) {
+                    const int f = first + i * ROWS;
+                    cp16(at + sw128(f, piece), b + (size_t)min(f0 + f, p.N - 1) * p.R, have);
+                }
+                for (int tok = first; tok < tn; tok += ROWS) { // zeros for the other slots' rows
                     const bool mine = sh.tok_slot[tok] == slot;
-                    const uint16_t *h = p.hs + (size_t)(t0 + (mine ? tok : 0)) * p.R + r;
-                    cp16(xt + sw128(tok, 2 * (j & 3)), h, mine ? 16u : 0u);
-                    cp16(xt + sw128(tok, 2 * (j & 3) + 1), two ? h + 8 : h, mine ? two : 0u);
+                    cp16(xt + sw128(tok, piece), h + (size_t)(mine ? tok : 0) * p.R, mine ? have : 0u);
                 }
             }
             cp_async_mbar_arrive_noinc(&sh.d_full[s]); // when this thread's copies have landed
@@ -435,29 +461,104 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         route_tile(p, sh, t0, tn, lane);
         if (lane == 0)
             mbar_arrive(&sh.routed);
+        // the slots' B rows of this tile are one piece each: on their way into L2
+        // while the base is multiplied
+        const uint32_t bytes = (uint32_t)(min(BM, p.N - f0) * p.R) * 2u;
+        for (int i = lane; i < sh.nslot; i += 32)
+            if (sh.seg_start[i + 1] > sh.nseg * part / kparts && sh.seg_start[i] < sh.nseg * (part + 1) / kparts)
+                prefetch_l2_bulk(sh.slot_b[i] + (size_t)f0 * p.R, bytes);
         __syncwarp();
+    }
+
+    const int rows = min(tn, p.M - t0);
+    const bool vec = (reinterpret_cast<uintptr_t>(p.y) & 15u) == 0 && p.y_stride % 8 == 0;
+    const uint32_t delta_col = (uint32_t)(RINGS::ALIAS ? MAX_TN : tn);
+    if (kparts == 1) {
+        // ---- the accumulators, turned by stmatrix into rows of 128 features in
+        // bf16, 272 bytes apart in shared memory, which every product has left;
+        // a group of four warps has 16 rows at a time, every GROUPS-th. (Through
+        // fp32 a tile of 256 rows took 8100 cycles.)
+        if (warp < WIDEN_WARPS) {
+            constexpr uint32_t Y_ROW = BM * 2 + 16;
+            const int group = warp >> 2;
+            const bool adapted = sh.nseg > 0;
+            const uint32_t quad = (uint32_t)(warp & 3) * 32;
+            // the lane's row of the four 8 x 8 matrices of a store: 8 features of a batch row
+            const uint32_t to = base + (uint32_t)((lane >> 4) * 8 + (lane & 7)) * Y_ROW + (quad + (uint32_t)(lane >> 3 & 1) * 8) * 2;
+            tc_fence_after();
+            for (int c = group; c < tn / 16; c += GROUPS) {
+                uint32_t v[2][8], d[2][8];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t at = tmem + ((quad + (uint32_t)h * 16) << 16) + (uint32_t)(c * 16);
+                    tmem_ld_16x16(at, v[h]);
+                    if (adapted)
+                        tmem_ld_16x16(at + delta_col, d[h]);
+                }
+                const uint32_t on = adapted ? sh.adapted[c >> 1] >> ((c & 1) * 16 + (lane & 3) * 2) : 0u;
+                tmem_wait_ld();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) { // rows 2 (lane % 4) and the next of 8: the first 8, features 0 and 8; the second
+                        float a = __uint_as_float(v[h][2 * q]), b = __uint_as_float(v[h][2 * q + 1]);
+                        if (on >> (q >> 1) * 8 & 1u)
+                            a += __uint_as_float(d[h][2 * q]);
+                        if (on >> (q >> 1) * 8 & 2u)
+                            b += __uint_as_float(d[h][2 * q + 1]);
+                        o[q] = pack2(a, b);
+                    }
+                    stmatrix_x4_trans(to + (uint32_t)(c * 16) * Y_ROW + (uint32_t)h * 32, o);
+                }
+            }
+            named_bar_sync(1u + (uint32_t)group, 128);
+            for (int i = tid & 127; i < tn / GROUPS * 16 + 256; i += 128) {
+                const int tok = ((i >> 8) * GROUPS + group) * 16 + (i >> 4 & 15), f = (i & 15) * 8, feature = f0 + f;
+                if (tok >= rows)
+                    break;
+                const uint4 o = lds_16(base + (uint32_t)tok * Y_ROW + (uint32_t)f * 2);
+                uint16_t *y = p.y + (int64_t)(t0 + tok) * p.y_stride + feature;
+                if (vec && feature + 8 <= p.N) {
+                    *reinterpret_cast<uint4 *>(y) = o;
+                } else {
+                    const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (feature + k < p.N)
+                            y[k] = (uint16_t)(w[k >> 1] >> (k & 1) * 16);
+                }
+            }
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (warp == WIDEN_WARPS + 1)
+            tmem_dealloc(tmem, cols);
+        if (tid == 0 && sh.bad) {
+            grid_dependency_wait(); // the call's status is open
+            atomicOr(p.status, (uint32_t)LORA_FLAG_WAIT_TIMEOUT);
+        }
+        return;
     }
 
     // ---- the accumulators: each part finishes 128 / kparts features, and gets
     // them from every part in its shared memory, [part][row][features + 4]
     cg::cluster_group cl = cg::this_cluster();
-    if (kparts > 1)
-        cl.sync(); // every part's products have read their operands
-    else
-        __syncthreads();
-    const int fs = BM / kparts, stride = fs + 4, rows = min(tn, p.M - t0);
+    cl.sync(); // every part's products have read their operands
+    const int fs = BM / kparts, stride = fs + 4;
     float *const tile = reinterpret_cast<float *>(smem);
     if (warp < WIDEN_WARPS) {
         tc_fence_after();
         const bool adapted = sh.nseg * (part + 1) / kparts > sh.nseg * part / kparts;
         const int f = (warp & 3) * 32 + lane, owner = f / fs;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        float *const to = (kparts > 1 ? cl.map_shared_rank(tile, owner) : tile) + (size_t)part * tn * stride + (f - owner * fs);
+        float *const to = cl.map_shared_rank(tile, owner) + (size_t)part * tn * stride + (f - owner * fs);
         for (int c = warp >> 2; c < tn / 16; c += GROUPS) {
             uint32_t v[16], d[16];
             tmem_ld16_nowait(tmem + lanes + (uint32_t)(c * 16), v);
             if (adapted)
-                tmem_ld16_nowait(tmem + lanes + (uint32_t)((RINGS::ALIAS ? MAX_TN : tn) + c * 16), d);
+                tmem_ld16_nowait(tmem + lanes + delta_col + (uint32_t)(c * 16), d);
             const uint32_t on = adapted ? sh.adapted[c >> 1] >> ((c & 1) * 16) : 0u;
             tmem_wait_ld();
 #pragma unroll
@@ -469,14 +570,10 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
             }
         }
     }
-    if (kparts > 1)
-        cl.sync();
-    else
-        __syncthreads();
+    cl.sync();
     // ---- the parts' sum, in part order, and one rounding; 8 features of a row at a time
     {
         const int eights = fs / 8, log_eights = 31 - __clz(eights), b0 = part * fs;
-        const bool vec = (reinterpret_cast<uintptr_t>(p.y) & 15u) == 0 && p.y_stride % 8 == 0;
 #pragma unroll 4
         for (int i = tid; i < rows * eights; i += RINGS::THREADS) {
             const int tok = i >> log_eights, f = (i & (eights - 1)) * 8, feature = f0 + b0 + f;
