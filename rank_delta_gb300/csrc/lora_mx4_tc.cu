@@ -20,16 +20,13 @@
 // the base product to the bit.
 //
 // With few feature tiles K is split over a cluster of CTAs, whose partial
-// tiles are summed in part order through distributed shared memory.
-#include <cooperative_groups.h>
-
+// tiles are exchanged through distributed shared memory: each part sums and writes
+// some of the features.
 #include "lora_mx4.cuh"
 #include "ptx.cuh"
 #include "vec.cuh"
 
 namespace rd {
-
-namespace cg = cooperative_groups;
 
 namespace {
 
@@ -51,7 +48,8 @@ constexpr int BM = 128;             // features of a tile: the UMMA M
 // Up to 128 rows the widened weights lie behind both accumulators; above it
 // they take the columns of the adapters' accumulator (ALIAS), which is not written
 // before the last base product has read them.
-template <int SUB_, int S_, int CS_, int DS_, int A_COL_, bool ALIAS_> struct Rings {
+template <int MAX_ROWS_, int SUB_, int S_, int CS_, int DS_, int A_COL_, bool ALIAS_> struct Rings {
+    static constexpr int MAX_ROWS = MAX_ROWS_; // of a tile
     static constexpr int SUB = SUB_, S = S_, CS = CS_, DS = DS_, A_COL = A_COL_;
     static constexpr bool ALIAS = ALIAS_;
     static constexpr int GROUPS = 4, WARPS = GROUPS * 4, THREADS = (WARPS + 4) * 32;
@@ -62,13 +60,13 @@ template <int SUB_, int S_, int CS_, int DS_, int A_COL_, bool ALIAS_> struct Ri
     static_assert(S >= GROUPS / SUB && S >= DS, "parity of a slot's last use");
     static_assert(A_COL + S * SUB * 32 <= 512, "tensor memory");
 };
-constexpr int MAX_RING = 16;
+constexpr int MAX_RING = 16, MAX_KPARTS = 8;
 constexpr uint32_t CODE_BYTES = BM * 128, SCALE_BYTES = BM * 16;
 constexpr uint32_t A_BYTES = BM * 128;
 constexpr int MAX_TN = 256;
 
 struct TcShared {
-    uint64_t full[MAX_RING], free[MAX_RING], c_full[MAX_RING], c_free[MAX_RING], d_full[MAX_RING], routed, base_done, done;
+    uint64_t full[MAX_RING], free[MAX_RING], c_full[MAX_RING], c_free[MAX_RING], d_full[MAX_RING], routed, base_done, done, joined;
     uint32_t tmem;
     int bad;                          // a wait gave up
     int nseg;
@@ -117,6 +115,30 @@ __device__ __forceinline__ void umma_bf16_tmem(uint32_t d_tmem, uint32_t a_tmem,
                  "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
                  : "memory");
 }
+// The shared-memory address of CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+// `bytes` (a multiple of 16) from this CTA's shared memory to another's, whose barrier they complete on.
+__device__ __forceinline__ void copy_to_cluster(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "r"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+// Features that each of `kparts` parts of K finishes (the last has what is left).
+__host__ __device__ constexpr int part_features(int kparts) { return (BM / 8 + kparts - 1) / kparts * 8; }
+__host__ __device__ constexpr int part_owns(int kparts, int part)
+{
+    const int fs = part_features(kparts), left = BM - part * fs;
+    return left < 0 ? 0 : left < fs ? left : fs;
+}
+
 // 16 lanes x 16 columns as four 8 x 8 fragments: thread t has columns 2 (t % 4)
 // and the next of lane t / 4 in r[0], r[1], of lane t / 4 + 8 in r[2], r[3], and
 // of the next eight columns in r[4..7]. Valid after tmem_wait_ld().
@@ -179,6 +201,21 @@ __device__ __forceinline__ void widen(const uint4 (&codes)[2], uint32_t s0, uint
         for (int i = 0; i < 32; ++i)
             out[i] = mul_bf16x2(out[i], f2[i / 16]);
     }
+}
+
+// Eight bf16 values to y, of which `left` are wanted (0 or less: none), by one
+// store where y is 16-byte aligned (`vec`).
+__device__ __forceinline__ void store_8(uint16_t *y, uint4 v, int left, bool vec)
+{
+    if (vec && left >= 8) {
+        *reinterpret_cast<uint4 *>(y) = v;
+        return;
+    }
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (k < left)
+            y[k] = (uint16_t)(w[k >> 1] >> (k & 1) * 16);
 }
 
 // The tile's rows and slots, by one warp: each row's slot, the distinct slots
@@ -271,8 +308,11 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         mbar_init(&sh.routed, 1);
         mbar_init(&sh.base_done, 1);
         mbar_init(&sh.done, 1);
+        mbar_init(&sh.joined, 1);
         sh.bad = 0;
         fence_barrier_init();
+        if (kparts > 1 && part_owns(kparts, part) > 0)
+            mbar_arrive_expect_tx(&sh.joined, (uint32_t)((kparts - 1) * part_owns(kparts, part) * (tn + 1)) * 4u);
     }
     if (warp == WIDEN_WARPS + 1)
         tmem_alloc(&sh.tmem, cols);
@@ -335,6 +375,16 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
             grid_dependency_wait(); // h is complete
         constexpr int SUB_WARPS = WIDEN_WARPS / SUB, ROWS = SUB_WARPS * 4; // that copy a sub-tile, rows at a time
         const int sub = warp / SUB_WARPS, piece = lane & 7, first = (warp % SUB_WARPS) * 4 + (lane >> 3);
+        constexpr int AT_ONCE = RINGS::MAX_ROWS / ROWS;
+        size_t b_row[BM / ROWS]; // element offsets of the rows this thread copies
+#pragma unroll
+        for (int i = 0; i < BM / ROWS; ++i)
+            b_row[i] = (size_t)min(f0 + first + i * ROWS, p.N - 1) * p.R;
+        int h_slot[AT_ONCE];
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i)
+            h_slot[i] = first + i * ROWS < tn ? sh.tok_slot[first + i * ROWS] : -1;
+        const uint32_t into = sw128(first, piece); // rows ROWS further are swizzled alike
         int lo = 0; // the slot of this thread's segment
         for (int d = 0; d < ndelta; ++d) {
             const int n = nbase + d, s = d % DS, xslot = n % S;
@@ -348,17 +398,18 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
                     ++lo;
                 const int r = (q - sh.seg_start[lo]) * 16 + (piece & 1) * 8, slot = sh.slot_id[lo];
                 const uint32_t have = r < p.R ? 16u : 0u; // else zeros
-                const uint32_t at = d_at + (uint32_t)(s * SUB + sub) * A_BYTES, xt = x_at + (uint32_t)(xslot * SUB + sub) * x_bytes;
-                const uint16_t *b = sh.slot_b[lo] + (have ? r : 0), *h = p.hs + (size_t)t0 * p.R + (have ? r : 0);
+                const uint32_t at = d_at + (uint32_t)(s * SUB + sub) * A_BYTES + into,
+                               xt = x_at + (uint32_t)(xslot * SUB + sub) * x_bytes + into;
+                const uint16_t *b = sh.slot_b[lo] + (have ? r : 0), *h = p.hs + (size_t)(t0 + first) * p.R + (have ? r : 0);
 #pragma unroll
-                for (int i = 0; i < BM / ROWS; ++i) {
-                    const int f = first + i * ROWS;
-                    cp16(at + sw128(f, piece), b + (size_t)min(f0 + f, p.N - 1) * p.R, have);
-                }
-                for (int tok = first; tok < tn; tok += ROWS) { // zeros for the other slots' rows
-                    const bool mine = sh.tok_slot[tok] == slot;
-                    cp16(xt + sw128(tok, piece), h + (size_t)(mine ? tok : 0) * p.R, mine ? have : 0u);
-                }
+                for (int i = 0; i < BM / ROWS; ++i)
+                    cp16(at + (uint32_t)(i * ROWS * 128), b + b_row[i], have);
+#pragma unroll
+                for (int i = 0; i < AT_ONCE; ++i) // zeros for the other slots' rows
+                    if (first + i * ROWS < tn) {
+                        const bool mine = h_slot[i] == slot;
+                        cp16(xt + (uint32_t)(i * ROWS * 128), mine ? h + i * ROWS * p.R : p.hs, mine ? have : 0u);
+                    }
             }
             cp_async_mbar_arrive_noinc(&sh.d_full[s]); // when this thread's copies have landed
         }
@@ -518,16 +569,7 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
                 if (tok >= rows)
                     break;
                 const uint4 o = lds_16(base + (uint32_t)tok * Y_ROW + (uint32_t)f * 2);
-                uint16_t *y = p.y + (int64_t)(t0 + tok) * p.y_stride + feature;
-                if (vec && feature + 8 <= p.N) {
-                    *reinterpret_cast<uint4 *>(y) = o;
-                } else {
-                    const uint32_t w[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (feature + k < p.N)
-                            y[k] = (uint16_t)(w[k >> 1] >> (k & 1) * 16);
-                }
+                store_8(p.y + (int64_t)(t0 + tok) * p.y_stride + feature, o, p.N - feature, vec);
             }
         }
         tc_fence_before();
@@ -542,18 +584,18 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         return;
     }
 
-    // ---- the accumulators: each part finishes 128 / kparts features, and gets
-    // them from every part in its shared memory, [part][row][features + 4]
-    cg::cluster_group cl = cg::this_cluster();
-    cl.sync(); // every part's products have read their operands
-    const int fs = BM / kparts, stride = fs + 4;
-    float *const tile = reinterpret_cast<float *>(smem);
+    // ---- the accumulators, [feature][row + 1] floats in shared memory. Each part
+    // finishes fs features: it gets the others' sums of them as one bulk copy from
+    // each, once its own products have left their rings. (The cluster's
+    // barriers order no memory: the copies complete on a barrier of their own.)
+    const int fs = part_features(kparts), own = part_owns(kparts, part), stride = tn + 1;
+    const uint32_t chunk = (uint32_t)(fs * stride) * 4u, recv = base + (uint32_t)(BM * stride) * 4u;
+    cluster_arrive();
     if (warp < WIDEN_WARPS) {
         tc_fence_after();
         const bool adapted = sh.nseg * (part + 1) / kparts > sh.nseg * part / kparts;
-        const int f = (warp & 3) * 32 + lane, owner = f / fs;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        float *const to = cl.map_shared_rank(tile, owner) + (size_t)part * tn * stride + (f - owner * fs);
+        float *const to = reinterpret_cast<float *>(smem) + ((warp & 3) * 32 + lane) * stride;
         for (int c = warp >> 2; c < tn / 16; c += GROUPS) {
             uint32_t v[16], d[16];
             tmem_ld16_nowait(tmem + lanes + (uint32_t)(c * 16), v);
@@ -566,39 +608,40 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
                 float o = __uint_as_float(v[i]);
                 if (on >> i & 1u)
                     o += __uint_as_float(d[i]);
-                to[(c * 16 + i) * stride] = o;
+                to[c * 16 + i] = o;
             }
         }
+        fence_proxy_async_smem();
     }
-    cl.sync();
+    __syncthreads();
+    cluster_wait();
+    if (warp == WIDEN_WARPS && lane < kparts && lane != part && part_owns(kparts, lane) > 0)
+        copy_to_cluster(cluster_addr(recv + (uint32_t)(part - (part > lane)) * chunk, (uint32_t)lane), base + (uint32_t)lane * chunk,
+                        (uint32_t)(part_owns(kparts, lane) * stride) * 4u, cluster_addr(smem_u32(&sh.joined), (uint32_t)lane));
+    __syncwarp();
     // ---- the parts' sum, in part order, and one rounding; 8 features of a row at a time
+    if (own > 0)
+        wait_or_note(&sh.joined, 0, &sh.bad);
+    __syncwarp();
+    cluster_arrive(); // this part has its copies
     {
-        const int eights = fs / 8, log_eights = 31 - __clz(eights), b0 = part * fs;
-#pragma unroll 4
+        const int eights = own / 8;
+        const float *const tile = reinterpret_cast<const float *>(smem);
         for (int i = tid; i < rows * eights; i += RINGS::THREADS) {
-            const int tok = i >> log_eights, f = (i & (eights - 1)) * 8, feature = f0 + b0 + f;
-            float v[8];
-            const float4 *src = reinterpret_cast<const float4 *>(tile + tok * stride + f);
-            const float4 first = src[0], second = src[1];
-            v[0] = first.x; v[1] = first.y; v[2] = first.z; v[3] = first.w;
-            v[4] = second.x; v[5] = second.y; v[6] = second.z; v[7] = second.w;
-            for (int r = 1; r < kparts; ++r) {
-                const float4 *more = src + r * (tn * stride / 4);
-                const float4 a = more[0], b = more[1];
-                v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-                v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
-            }
-            uint16_t *y = p.y + (int64_t)(t0 + tok) * p.y_stride + feature;
-            if (vec && feature + 8 <= p.N) {
-                *reinterpret_cast<uint4 *>(y) = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
-            } else {
+            const int tok = i / eights, u = i - tok * eights, feature = f0 + part * fs + u * 8;
+            float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+            for (int r = 0; r < kparts; ++r) {
+                const int at = r == part ? part * fs : BM + (r - (r > part)) * fs;
+                const float *src = tile + (at + u * 8) * stride + tok;
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    if (feature + k < p.N)
-                        y[k] = f32_to_bf16_bits(v[k]);
+                    v[k] += src[k * stride];
             }
+            store_8(p.y + (int64_t)(t0 + tok) * p.y_stride + feature,
+                    make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7])), p.N - feature, vec);
         }
     }
+    cluster_wait(); // every part has its copies, which read the others' shared memory
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -612,29 +655,82 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
 
 namespace {
 
+constexpr uint32_t SMEM_LIMIT = 217 * 1024; // besides TcShared
+// The rings, and later the exchange.
+template <typename RINGS> uint32_t smem_bytes(int tn, int kparts)
+{
+    const uint32_t rings = RINGS::SUB * (RINGS::DS * A_BYTES + RINGS::S * (uint32_t)tn * 128u) + RINGS::CS * (CODE_BYTES + SCALE_BYTES);
+    const uint32_t exchange = kparts > 1 ? (uint32_t)((BM + (kparts - 1) * part_features(kparts)) * (tn + 1)) * 4u : 0u;
+    return 1024u + (rings > exchange ? rings : exchange);
+}
+
+// The cluster of the kernel's grid, and that it may begin before the call's shrink is through.
+struct TcLaunch {
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg;
+    template <typename RINGS> cudaError_t fill(int tn, int kparts, dim3 grid, cudaStream_t st)
+    {
+        static std::atomic<uint64_t> raised{0};
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)kparts;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg = {};
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3((unsigned)RINGS::THREADS);
+        cfg.dynamicSmemBytes = smem_bytes<RINGS>(tn, kparts);
+        cfg.stream = st;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        return raise_smem_limit(raised, mx4_tc_kernel<RINGS>, (int)SMEM_LIMIT);
+    }
+};
+
+// How many clusters of `kparts` CTAs the device runs at a time: its SMs come in
+// groups that a cluster does not cross.
+template <typename RINGS> int clusters_at_once(int kparts, int num_sms)
+{
+    static std::atomic<int> known[MAX_KPARTS + 1];
+    int n = known[kparts].load();
+    if (n == 0) {
+        TcLaunch l;
+        if (l.fill<RINGS>(16, kparts, dim3((unsigned)(kparts * num_sms)), nullptr) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, mx4_tc_kernel<RINGS>, &l.cfg) != cudaSuccess || n < 1) {
+            (void)cudaGetLastError();
+            n = -1;
+        }
+        known[kparts].store(n);
+    }
+    return n;
+}
+
+// Parts of K: as many as fill the device with one CTA an SM, whole steps of 256 k
+// each, and of those the fewest whose longest part is as short.
+template <typename RINGS> int parts(const Mx4ProjParams &p, int tn, int tiles, int num_sms)
+{
+    const int ctas = (p.N + BM - 1) / BM * tiles, nst = (p.K / 32 + 1) / 2, nsteps = (nst + 3) / 4;
+    int best = 1;
+    for (int k = 2; k <= MAX_KPARTS && k <= nsteps && ctas * k <= num_sms; ++k)
+        if ((nsteps + k - 1) / k < (nsteps + best - 1) / best && smem_bytes<RINGS>(tn, k) <= SMEM_LIMIT &&
+            clusters_at_once<RINGS>(k, num_sms) >= ctas)
+            best = k;
+    return best;
+}
+
 template <typename RINGS>
 cudaError_t launch(const Mx4ProjParams &p, const Mx4TcPlan &plan, const Mx4TcMaps &maps, cudaStream_t st)
 {
-    static std::atomic<uint64_t> raised{0};
-    cudaError_t e = raise_smem_limit(raised, mx4_tc_kernel<RINGS>, 217 * 1024);
-    if (e != cudaSuccess)
-        return e;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)plan.kparts;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.N + BM - 1) / BM * plan.kparts), (unsigned)((p.M + plan.tn - 1) / plan.tn));
-    cfg.blockDim = dim3((unsigned)RINGS::THREADS);
-    cfg.dynamicSmemBytes = 1024u + RINGS::SUB * (RINGS::DS * A_BYTES + RINGS::S * (uint32_t)plan.tn * 128u) +
-                           RINGS::CS * (CODE_BYTES + SCALE_BYTES);
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, mx4_tc_kernel<RINGS>, maps, p, plan.tn, plan.kparts);
+    TcLaunch l;
+    const cudaError_t e = l.fill<RINGS>(plan.tn, plan.kparts,
+                                        dim3((unsigned)((p.N + BM - 1) / BM * plan.kparts), (unsigned)((p.M + plan.tn - 1) / plan.tn)), st);
+    return e != cudaSuccess ? e : cudaLaunchKernelEx(&l.cfg, mx4_tc_kernel<RINGS>, maps, p, plan.tn, plan.kparts);
 }
+
+// What fits in 227 KB of shared memory and 512 columns of tensor memory.
+using Rings64 = Rings<64, 2, 4, 4, 2, 128, false>;
+using Rings128 = Rings<128, 2, 3, 3, 2, 256, false>;
+using Rings256 = Rings<256, 1, 4, 2, 2, 256, true>;
 
 } // namespace
 
@@ -643,19 +739,17 @@ Mx4TcPlan plan_mx4_tc(const Mx4ProjParams &p, int num_sms)
     Mx4TcPlan plan;
     const int tiles = (p.M + MAX_TN - 1) / MAX_TN, each = (p.M + tiles - 1) / tiles;
     plan.tn = (each + 15) / 16 * 16;
-    const int ctas = (p.N + BM - 1) / BM * tiles, nst = (p.K / 32 + 1) / 2;
-    plan.kparts = 1;
-    while (plan.kparts < 8 && ctas * plan.kparts * 2 <= num_sms && nst >= 8 * plan.kparts)
-        plan.kparts *= 2;
+    plan.kparts = plan.tn <= 64    ? parts<Rings64>(p, plan.tn, tiles, num_sms)
+                  : plan.tn <= 128 ? parts<Rings128>(p, plan.tn, tiles, num_sms)
+                                   : parts<Rings256>(p, plan.tn, tiles, num_sms);
     return plan;
 }
 
 cudaError_t launch_mx4_tc(const Mx4ProjParams &p, const Mx4TcPlan &plan, const Mx4TcMaps &maps, cudaStream_t st)
 {
-    if (plan.tn <= 64)
-        return launch<Rings<2, 4, 4, 2, 128, false>>(p, plan, maps, st); // what fits in 227 KB
-    return plan.tn <= 128 ? launch<Rings<2, 3, 3, 2, 256, false>>(p, plan, maps, st)
-                          : launch<Rings<1, 4, 2, 2, 256, true>>(p, plan, maps, st);
+    return plan.tn <= 64    ? launch<Rings64>(p, plan, maps, st)
+           : plan.tn <= 128 ? launch<Rings128>(p, plan, maps, st)
+                            : launch<Rings256>(p, plan, maps, st);
 }
 
 } // namespace rd
