@@ -36,7 +36,8 @@ constexpr int BM = 128;             // features of a tile: the UMMA M
 // columns a sub-tile, from column A_COL on) and tn rows of x in shared memory (tn
 // 128 bytes a sub-tile), with one barrier for "both are there" and one for "the
 // products are through". CS steps of codes (256 k of 128 rows, and 16 scale
-// bytes a row) and DS slots of the adapters' rows come besides. Groups of four
+// bytes a row) and DS slots of the adapters' rows come besides, S of
+// them with the codes' place once those are widened. Groups of four
 // warps (128 rows) widen, sub-tile m by group m mod GROUPS, and drain the
 // accumulators.
 //
@@ -57,7 +58,8 @@ template <int MAX_ROWS_, int SUB_, int S_, int CS_, int DS_, int A_COL_, bool AL
     // stage before (GROUPS / SUB stages earlier), that the slot's use before the
     // last is through; were that still open, the parity of the last use would
     // not tell the two apart.
-    static_assert(S >= GROUPS / SUB && S >= DS, "parity of a slot's last use");
+    static_assert(S >= GROUPS / SUB, "parity of a slot's last use");
+    static_assert(DS + CS / SUB >= S, "slots of the adapters' rows: one a stage");
     static_assert(A_COL + S * SUB * 32 <= 512, "tensor memory");
 };
 constexpr int MAX_RING = 16, MAX_KPARTS = 8;
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
             mbar_init(&sh.full[s], 1 + 4 * SUB); // x, and the groups' warps
             mbar_init(&sh.free[s], 1);
         }
-        for (int s = 0; s < DS; ++s)
+        for (int s = 0; s < S; ++s)
             mbar_init(&sh.d_full[s], WIDEN_WARPS * 32);
         for (int s = 0; s < CS; ++s) {
             mbar_init(&sh.c_full[s], 1);
@@ -321,6 +323,7 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
 
+    auto d_slot = [&](int s) { return s < DS ? d_at + (uint32_t)(s * SUB) * A_BYTES : codes_at + (uint32_t)((s - DS) * SUB) * A_BYTES; };
     // stage n's products are through (stage n - S is known to be)
     auto stage_free = [&](int n) { wait_or_note(&sh.free[n % S], (uint32_t)(n / S) & 1u, &sh.bad); };
     if (warp < WIDEN_WARPS) {
@@ -385,30 +388,44 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         for (int i = 0; i < AT_ONCE; ++i)
             h_slot[i] = first + i * ROWS < tn ? sh.tok_slot[first + i * ROWS] : -1;
         const uint32_t into = sw128(first, piece); // rows ROWS further are swizzled alike
-        int lo = 0; // the slot of this thread's segment
+        // the slot of this thread's segment, the lo-th, its segments, and the slots of
+        // the last S stages
+        int lo = -1, begin = 0, end = 0, slot = -1;
+        const uint16_t *slot_b = nullptr;
+        uint64_t held = 0;
         for (int d = 0; d < ndelta; ++d) {
-            const int n = nbase + d, s = d % DS, xslot = n % S;
-            if (d >= DS) // then n - S is, too
-                stage_free(n - DS);
-            else if (n >= S)
+            const int n = nbase + d, s = d % S, xslot = n % S;
+            if (n >= S)
                 stage_free(n - S);
+            if (d == DS) // the further slots are where the codes were
+                named_bar_sync(5u, WIDEN_WARPS * 32);
             const int q = q0 + 4 * (SUB * d + sub) + (piece >> 1);
             if (q < q1) {
-                while (lo + 1 < sh.nslot && sh.seg_start[lo + 1] <= q)
-                    ++lo;
-                const int r = (q - sh.seg_start[lo]) * 16 + (piece & 1) * 8, slot = sh.slot_id[lo];
+                if (q >= end) { // another slot
+                    do {
+                        begin = end;
+                        end = sh.seg_start[++lo + 1];
+                    } while (q >= end);
+                    slot = sh.slot_id[lo];
+                    slot_b = sh.slot_b[lo];
+                }
+                const int r = (q - begin) * 16 + (piece & 1) * 8;
                 const uint32_t have = r < p.R ? 16u : 0u; // else zeros
-                const uint32_t at = d_at + (uint32_t)(s * SUB + sub) * A_BYTES + into,
-                               xt = x_at + (uint32_t)(xslot * SUB + sub) * x_bytes + into;
-                const uint16_t *b = sh.slot_b[lo] + (have ? r : 0), *h = p.hs + (size_t)(t0 + first) * p.R + (have ? r : 0);
+                // rows of x that are not the slot's are zeros: all of a slot at first, then
+                // those that the stage S before had
+                const int before = (int16_t)(held >> 16 * (S - 1));
+                held = held << 16 | (uint16_t)slot;
+                const uint32_t at = d_slot(s) + (uint32_t)sub * A_BYTES + into, xt = x_at + (uint32_t)(xslot * SUB + sub) * x_bytes + into;
+                const uint16_t *b = slot_b + (have ? r : 0), *h = p.hs + (size_t)(t0 + first) * p.R + (have ? r : 0);
 #pragma unroll
                 for (int i = 0; i < BM / ROWS; ++i)
                     cp16(at + (uint32_t)(i * ROWS * 128), b + b_row[i], have);
 #pragma unroll
-                for (int i = 0; i < AT_ONCE; ++i) // zeros for the other slots' rows
+                for (int i = 0; i < AT_ONCE; ++i)
                     if (first + i * ROWS < tn) {
                         const bool mine = h_slot[i] == slot;
-                        cp16(xt + (uint32_t)(i * ROWS * 128), mine ? h + i * ROWS * p.R : p.hs, mine ? have : 0u);
+                        if (mine || d < S || h_slot[i] == before)
+                            cp16(xt + (uint32_t)(i * ROWS * 128), mine ? h + i * ROWS * p.R : p.hs, mine ? have : 0u);
                     }
             }
             cp_async_mbar_arrive_noinc(&sh.d_full[s]); // when this thread's copies have landed
@@ -433,7 +450,7 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
     } else if (warp == WIDEN_WARPS + 1) {
         // ---- products
         const uint32_t idesc = idesc_bf16_f32(BM, (uint32_t)tn);
-        const uint64_t ddesc = sw128_kmajor_desc(d_at), xdesc = sw128_kmajor_desc(x_at);
+        const uint64_t xdesc = sw128_kmajor_desc(x_at);
         const uint32_t widened = tmem + RINGS::A_COL, delta = tmem + (uint32_t)(RINGS::ALIAS ? MAX_TN : tn);
         int s = 0;
         uint32_t parity = 0;
@@ -471,12 +488,12 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
             tc_fence_after();
         }
         for (int q = q0, d = 0; q < q1 && !__any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&sh.bad) != 0); q += 4 * SUB, ++d) {
-            const int ds = d % DS;
-            wait_or_note(&sh.d_full[ds], (uint32_t)(d / DS) & 1u, &sh.bad);
+            const int ds = d % S;
+            wait_or_note(&sh.d_full[ds], (uint32_t)(d / S) & 1u, &sh.bad);
             __syncwarp();
             fence_proxy_async_smem(); // cp.async (generic proxy) wrote both operands
             tc_fence_after();
-            const uint64_t dd = ddesc + (uint64_t)(uint32_t)(ds * SUB) * (A_BYTES >> 4), xd = x_of();
+            const uint64_t dd = sw128_kmajor_desc(d_slot(ds)), xd = x_of();
             if (elected()) {
 #pragma unroll
                 for (int j = 0; j < 4 * SUB; ++j)
@@ -705,19 +722,6 @@ template <typename RINGS> int clusters_at_once(int kparts, int num_sms)
     return n;
 }
 
-// Parts of K: as many as fill the device with one CTA an SM, whole steps of 256 k
-// each, and of those the fewest whose longest part is as short.
-template <typename RINGS> int parts(const Mx4ProjParams &p, int tn, int tiles, int num_sms)
-{
-    const int ctas = (p.N + BM - 1) / BM * tiles, nst = (p.K / 32 + 1) / 2, nsteps = (nst + 3) / 4;
-    int best = 1;
-    for (int k = 2; k <= MAX_KPARTS && k <= nsteps && ctas * k <= num_sms; ++k)
-        if ((nsteps + k - 1) / k < (nsteps + best - 1) / best && smem_bytes<RINGS>(tn, k) <= SMEM_LIMIT &&
-            clusters_at_once<RINGS>(k, num_sms) >= ctas)
-            best = k;
-    return best;
-}
-
 template <typename RINGS>
 cudaError_t launch(const Mx4ProjParams &p, const Mx4TcPlan &plan, const Mx4TcMaps &maps, cudaStream_t st)
 {
@@ -727,6 +731,12 @@ cudaError_t launch(const Mx4ProjParams &p, const Mx4TcPlan &plan, const Mx4TcMap
     return e != cudaSuccess ? e : cudaLaunchKernelEx(&l.cfg, mx4_tc_kernel<RINGS>, maps, p, plan.tn, plan.kparts);
 }
 
+// Whether clusters of k parts for all tiles run at once, and their exchange fits.
+template <typename RINGS> bool fits(int tn, int k, int64_t ctas, int num_sms)
+{
+    return smem_bytes<RINGS>(tn, k) <= SMEM_LIMIT && clusters_at_once<RINGS>(k, num_sms) >= ctas;
+}
+
 // What fits in 227 KB of shared memory and 512 columns of tensor memory.
 using Rings64 = Rings<64, 2, 4, 4, 2, 128, false>;
 using Rings128 = Rings<128, 2, 3, 3, 2, 256, false>;
@@ -734,14 +744,33 @@ using Rings256 = Rings<256, 1, 4, 2, 2, 256, true>;
 
 } // namespace
 
+// Tiles of 128 or 256 rows and the parts of K, by an estimate of the cycles of the
+// CTAs that an SM runs one after another: what 64 k take (the widening up to 64
+// rows, the products from some 170 on), 4000 for the rest of a tile, and what
+// the exchange adds. 256x4096x4096 with 16 adapters takes 27.7 us as 256 rows in
+// two parts and 23.5 as twice 128 rows.
 Mx4TcPlan plan_mx4_tc(const Mx4ProjParams &p, int num_sms)
 {
-    Mx4TcPlan plan;
-    const int tiles = (p.M + MAX_TN - 1) / MAX_TN, each = (p.M + tiles - 1) / tiles;
-    plan.tn = (each + 15) / 16 * 16;
-    plan.kparts = plan.tn <= 64    ? parts<Rings64>(p, plan.tn, tiles, num_sms)
-                  : plan.tn <= 128 ? parts<Rings128>(p, plan.tn, tiles, num_sms)
-                                   : parts<Rings256>(p, plan.tn, tiles, num_sms);
+    const int ftiles = (p.N + BM - 1) / BM, nst = (p.K / 32 + 1) / 2, nsteps = (nst + 3) / 4;
+    Mx4TcPlan plan{0, 1};
+    int64_t least = 0;
+    for (int most = MAX_TN; most >= MAX_TN / 2; most /= 2) {
+        const int tiles = (p.M + most - 1) / most, each = (p.M + tiles - 1) / tiles, tn = (each + 15) / 16 * 16;
+        const int64_t ctas = (int64_t)ftiles * tiles;
+        const int sub = tn <= 128 ? 335 + (tn > 64 ? (tn - 64) * 7 / 8 : 0) : 2 * tn + 45 > 390 ? 2 * tn + 45 : 390;
+        for (int k = 1; k <= MAX_KPARTS && k <= nsteps && (k == 1 || ctas * k <= num_sms); ++k) {
+            const int64_t waves = (ctas * k + num_sms - 1) / num_sms;
+            const int64_t cost = waves * (4000 + (int64_t)((nsteps + k - 1) / k) * 4 * sub + (k > 1 ? 2000 + 16 * tn : 0));
+            if ((plan.tn == 0 || cost < least) &&
+                (k == 1 || (tn <= 64    ? fits<Rings64>(tn, k, ctas, num_sms)
+                            : tn <= 128 ? fits<Rings128>(tn, k, ctas, num_sms)
+                                        : fits<Rings256>(tn, k, ctas, num_sms)))) {
+                least = cost;
+                plan.tn = tn;
+                plan.kparts = k;
+            }
+        }
+    }
     return plan;
 }
 
