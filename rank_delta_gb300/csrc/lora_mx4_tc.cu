@@ -9,9 +9,9 @@
 // shared memory is left to x); x comes by TMA, and one thread issues the products.
 // The weight is widened once for all rows of the tile. With tiles of 256 rows
 // the tensor cores and what a tile takes before and after them bound it
-// (8192x4096x14336: 623 us without adapters, 1.55 PFLOP/s; a stage of 64 k takes
-// 555 cycles, its products 512); with fewer rows it is the widening and what a
-// call takes in any case, shrink, set-up and epilogue.
+// (8192x4096x14336: 626 us, 574 without adapters, 1.68 PFLOP/s; a stage of 64 k
+// takes 555 cycles, its products 512); with fewer rows it is the widening and what a
+// call takes in any case, shrink, set-up and epilogue (64x4096x4096: 14.5 us).
 //
 // The adapters are more K: s h of the tile's rows (rounded to bf16, as y
 // itself is; the sums stay fp32) against the B rows of each slot in the tile,
@@ -31,6 +31,7 @@ namespace rd {
 namespace {
 
 constexpr int BM = 128;             // features of a tile: the UMMA M
+constexpr int TEAMS = 2;            // of the widening warps, that copy the adapters' rows
 // The rings between TMA, the widening warps and the products. A stage is SUB
 // sub-tiles of 64 k. There are S of them: widened weights in tensor memory (32
 // columns a sub-tile, from column A_COL on) and tn rows of x in shared memory (tn
@@ -58,7 +59,9 @@ template <int MAX_ROWS_, int SUB_, int S_, int CS_, int DS_, int A_COL_, bool AL
     // stage before (GROUPS / SUB stages earlier), that the slot's use before the
     // last is through; were that still open, the parity of the last use would
     // not tell the two apart.
-    static_assert(S >= GROUPS / SUB, "parity of a slot's last use");
+    // (The adapters' stages: the group that copies to stage d, of team d mod TEAMS, has
+    // widened for stage d - 4 / SUB or a later one, as bases are whole steps.)
+    static_assert(S >= GROUPS / SUB && S >= TEAMS, "parity of a slot's last use");
     static_assert(DS + CS / SUB >= S, "slots of the adapters' rows: one a stage");
     static_assert(A_COL + S * SUB * 32 <= 512, "tensor memory");
 };
@@ -292,8 +295,8 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
     const int part = blockIdx.x % kparts, f0 = (blockIdx.x / kparts) * BM, t0 = blockIdx.y * tn;
     const int nblk = p.K / 32, nst = (nblk + 1) / 2, nsteps = (nst + 3) / 4; // blocks of 32 k, sub-tiles of 64, steps of 256
     const int j0 = (int)((int64_t)nsteps * part / kparts), j1 = (int)((int64_t)nsteps * (part + 1) / kparts);
-    // sub-tiles of the part, whole stages (past K both operands are zeros)
-    const int m0 = 4 * j0, mbase = (min(nst, 4 * j1) - m0 + SUB - 1) / SUB * SUB, nbase = mbase / SUB;
+    // sub-tiles of the part: whole steps (past K both operands are zeros)
+    const int m0 = 4 * j0, mbase = 4 * (j1 - j0), nbase = mbase / SUB;
     constexpr uint32_t cols = 512; // no second CTA fits on the SM by its shared memory
 
     if (tid == 0) {
@@ -302,7 +305,7 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
             mbar_init(&sh.free[s], 1);
         }
         for (int s = 0; s < S; ++s)
-            mbar_init(&sh.d_full[s], WIDEN_WARPS * 32);
+            mbar_init(&sh.d_full[s], WIDEN_WARPS / TEAMS * 32);
         for (int s = 0; s < CS; ++s) {
             mbar_init(&sh.c_full[s], 1);
             mbar_init(&sh.c_free[s], 16); // four warps for each of the step's four stages
@@ -376,8 +379,12 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
                                : (q1 - q0 + 4 * SUB - 1) / (4 * SUB);
         if (ndelta > 0)
             grid_dependency_wait(); // h is complete
-        constexpr int SUB_WARPS = WIDEN_WARPS / SUB, ROWS = SUB_WARPS * 4; // that copy a sub-tile, rows at a time
-        const int sub = warp / SUB_WARPS, piece = lane & 7, first = (warp % SUB_WARPS) * 4 + (lane >> 3);
+        // The warps work in teams, a stage each: finding its slot and waiting take
+        // as long as the copies (256x4096x14336 39.9 us, 40.7 with all on every stage).
+        constexpr int TEAM_WARPS = WIDEN_WARPS / TEAMS;
+        constexpr int SUB_WARPS = TEAM_WARPS / SUB, ROWS = SUB_WARPS * 4; // that copy a sub-tile, rows at a time
+        const int team = warp / TEAM_WARPS, sub = warp % TEAM_WARPS / SUB_WARPS, piece = lane & 7,
+                  first = (warp % SUB_WARPS) * 4 + (lane >> 3);
         constexpr int AT_ONCE = RINGS::MAX_ROWS / ROWS;
         size_t b_row[BM / ROWS]; // element offsets of the rows this thread copies
 #pragma unroll
@@ -388,17 +395,19 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         for (int i = 0; i < AT_ONCE; ++i)
             h_slot[i] = first + i * ROWS < tn ? sh.tok_slot[first + i * ROWS] : -1;
         const uint32_t into = sw128(first, piece); // rows ROWS further are swizzled alike
-        // the slot of this thread's segment, the lo-th, its segments, and the slots of
-        // the last S stages
-        int lo = -1, begin = 0, end = 0, slot = -1;
+        // the slot of this thread's segment, the lo-th, its segments, and the slot that
+        // had the stage's place before
+        int lo = -1, begin = 0, end = 0, slot = -1, lo_before = -1, end_before = 0, before = -1;
         const uint16_t *slot_b = nullptr;
-        uint64_t held = 0;
-        for (int d = 0; d < ndelta; ++d) {
+        bool codes_left = false;
+        for (int d = team; d < ndelta; d += TEAMS) {
             const int n = nbase + d, s = d % S, xslot = n % S;
             if (n >= S)
                 stage_free(n - S);
-            if (d == DS) // the further slots are where the codes were
+            if (d >= DS && !codes_left) { // the further slots are where the codes were
                 named_bar_sync(5u, WIDEN_WARPS * 32);
+                codes_left = true;
+            }
             const int q = q0 + 4 * (SUB * d + sub) + (piece >> 1);
             if (q < q1) {
                 if (q >= end) { // another slot
@@ -413,8 +422,12 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
                 const uint32_t have = r < p.R ? 16u : 0u; // else zeros
                 // rows of x that are not the slot's are zeros: all of a slot at first, then
                 // those that the stage S before had
-                const int before = (int16_t)(held >> 16 * (S - 1));
-                held = held << 16 | (uint16_t)slot;
+                if (d >= S && q - 4 * SUB * S >= end_before) {
+                    do
+                        end_before = sh.seg_start[++lo_before + 1];
+                    while (q - 4 * SUB * S >= end_before);
+                    before = sh.slot_id[lo_before];
+                }
                 const uint32_t at = d_slot(s) + (uint32_t)sub * A_BYTES + into, xt = x_at + (uint32_t)(xslot * SUB + sub) * x_bytes + into;
                 const uint16_t *b = slot_b + (have ? r : 0), *h = p.hs + (size_t)(t0 + first) * p.R + (have ? r : 0);
 #pragma unroll
@@ -430,6 +443,8 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
             }
             cp_async_mbar_arrive_noinc(&sh.d_full[s]); // when this thread's copies have landed
         }
+        if (ndelta > DS && !codes_left) // the other teams wait here
+            named_bar_sync(5u, WIDEN_WARPS * 32);
         wait_or_note(&sh.done, 0, &sh.bad);
         __syncwarp();
     } else if (warp == WIDEN_WARPS) {
