@@ -17,7 +17,8 @@
 // itself is; the sums stay fp32) against the B rows of each slot in the tile,
 // a row's columns zero for every slot but its own, into an accumulator of
 // their own, which is added to the rows that have an adapter: the others keep
-// the base product to the bit.
+// the base product to the bit. Where that sum is not finite, the row's part is
+// computed alone, so that no adapter reaches another's rows.
 //
 // With few feature tiles K is split over a cluster of CTAs, whose partial
 // tiles are exchanged through distributed shared memory: each part sums and writes
@@ -142,6 +143,22 @@ __host__ __device__ constexpr int part_owns(int kparts, int part)
 {
     const int fs = part_features(kparts), left = BM - part * fs;
     return left < 0 ? 0 : left < fs ? left : fs;
+}
+
+// An adapter's part of y over segments q0 .. q1 of the tile, row tok and feature
+// f, once more by itself: the zeros that keep a slot's B from the other slots'
+// rows make a NaN of an infinity or a NaN in it.
+__device__ __noinline__ float delta_alone(const Mx4ProjParams &p, const TcShared &sh, int t0, int tok, int f, int q0, int q1)
+{
+    int i = 0;
+    while (i + 1 < sh.nslot && sh.slot_id[i] != sh.tok_slot[tok])
+        ++i;
+    const int begin = max(q0, sh.seg_start[i]) - sh.seg_start[i], end = min(q1, sh.seg_start[i + 1]) - sh.seg_start[i];
+    const uint16_t *b = sh.slot_b[i] + (size_t)min(f, p.N - 1) * p.R, *h = p.hs + (size_t)(t0 + tok) * p.R;
+    float sum = 0.0f;
+    for (int r = begin * 16; r < min(end * 16, p.R); ++r)
+        sum = fmaf(bf_lo(h[r]), bf_lo(b[r]), sum);
+    return sum;
 }
 
 // 16 lanes x 16 columns as four 8 x 8 fragments: thread t has columns 2 (t % 4)
@@ -580,6 +597,20 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
                 }
                 const uint32_t on = adapted ? sh.adapted[c >> 1] >> ((c & 1) * 16 + (lane & 3) * 2) : 0u;
                 tmem_wait_ld();
+                if (adapted) {
+                    float probe = 0.0f; // NaN if a delta is not finite
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        probe = fmaf(__uint_as_float(d[j >> 3][j & 7]), 0.0f, probe);
+                    if (probe != probe) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (on >> ((j >> 2 & 1) * 8 + (j & 1)) & 1u && isnan(__uint_as_float(d[j >> 3][j & 7])))
+                                d[j >> 3][j & 7] = __float_as_uint(
+                                    delta_alone(p, sh, t0, c * 16 + (j >> 2 & 1) * 8 + (lane & 3) * 2 + (j & 1),
+                                                f0 + (int)quad + (j >> 3) * 16 + (lane >> 2) + (j >> 1 & 1) * 8, 0, sh.nseg));
+                    }
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t o[4];
@@ -635,6 +666,19 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
                 tmem_ld16_nowait(tmem + lanes + delta_col + (uint32_t)(c * 16), d);
             const uint32_t on = adapted ? sh.adapted[c >> 1] >> ((c & 1) * 16) : 0u;
             tmem_wait_ld();
+            if (adapted) {
+                float probe = 0.0f; // NaN if a delta is not finite
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    probe = fmaf(__uint_as_float(d[i]), 0.0f, probe);
+                if (probe != probe) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (on >> i & 1u && isnan(__uint_as_float(d[i])))
+                            d[i] = __float_as_uint(delta_alone(p, sh, t0, c * 16 + i, f0 + (warp & 3) * 32 + lane,
+                                                               sh.nseg * part / kparts, sh.nseg * (part + 1) / kparts));
+                }
+            }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 float o = __uint_as_float(v[i]);

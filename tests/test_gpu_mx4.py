@@ -256,3 +256,72 @@ def test_same_bytes_on_every_run_and_on_another_stream(path):
     side.wait_stream(torch.cuda.current_stream())
     c = s.run(path, stream=side)
     assert torch.equal(a.view(torch.int16), b.view(torch.int16)) and torch.equal(a.view(torch.int16), c.view(torch.int16))
+
+
+# More slots than a chunk of rows has, ranks that end inside a segment of 16, one slot with every row, every
+# adapter in a tile, several parts of K with a tail, one and two tiles of rows.
+LARGER = [
+    (48, 512, 150, 80, 16), (40, 384, 130, 200, 8), (230, 1024, 300, 1, 64), (130, 768, 260, 40, 40), (20, 512, 128, 20, 256),
+    (256, 4224, 300, 32, 64), (150, 4096, 1100, 16, 24), (256, 2048, 2048, 8, 16), (64, 4096, 520, 16, 56), (192, 1056, 130, 64, 64),
+    (300, 800, 200, 24, 72)]
+
+
+@pytest.mark.parametrize("M,K,N,L,R", LARGER)
+def test_many_adapters_and_large_ranks(M, K, N, L, R):
+    s = Setup(M, K, N, L, R, seed=M + R)
+    s.check(s.run(rd.LORA_MX4_PATH_TILES, y_pad=8 * (M % 2)))
+    assert s.flags == 0
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("M", [3, 40, 150])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_an_adapter_that_is_not_finite_stays_with_its_rows(path, M, value):
+    """Slot 0 with such values in A and in B: rows of the other slots get what they should, those of none the same bytes."""
+    s = Setup(M, 1024, 300, 4, 24, seed=M)
+    slots = np.arange(M, dtype=np.int32) % 5 - 1  # -1 .. 3
+    clean = s.run(path, slots)
+    rng = np.random.default_rng(1)
+    bf = lambda a: torch.tensor(a).to(torch.bfloat16).cuda()  # noqa: E731
+    A, B = bf(rng.standard_normal((24, 1024)) / 32), bf(rng.standard_normal((300, 24)))
+    A[3, 5] = value
+    B[7, 2] = B[299, 23] = value
+    rd.lora_pool_pack(s.route.rt, 0, A, B, 24, 0.0, False, 1.0)
+    y = s.run(path, slots)
+    own = torch.tensor(slots == 0).cuda()
+    assert not bool(torch.isfinite(y[own].float()).any())
+    s.check(torch.where(own[:, None], clean, y), slots)
+    none = torch.tensor(slots == -1).cuda()
+    assert torch.equal(y[none].view(torch.int16), clean[none].view(torch.int16))
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("M", [2, 70])
+def test_bases_that_no_tile_load_takes(path, M):
+    """Scales on an odd address, a base of y that is 2 bytes off, K with a tail."""
+    s = Setup(M, 2080, 200, 4, 16, seed=M)
+    odd = torch.empty(s.scales.numel() + 1, dtype=torch.uint8, device="cuda")[1:].view_as(s.scales)
+    odd.copy_(s.scales)
+    s.scales = odd
+    s.check(s.run(path, y_pad=3))
+
+
+@pytest.mark.parametrize("M", [1, 64, 200])
+def test_replayed_from_a_graph(M):
+    s = Setup(M, 1024, 384, 8, 32, seed=M)
+    want = s.run(rd.LORA_MX4_PATH_AUTO)
+    y = torch.empty(M, 384, dtype=torch.bfloat16, device="cuda")
+    ws = th.workspace(rd.lora_mx4_proj_workspace_bytes(M, s.route.rt))
+    slots = torch.tensor(s.slots).cuda()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        for _ in range(2):
+            rd.lora_mx4_proj_apply(s.x, s.x.stride(0), s.codes, s.scales, M, 1024, 384, slots, s.route.rt, y, 384, ws, ws.numel(),
+                                   torch.cuda.current_stream())
+    for _ in range(3):
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y.view(torch.int16), want.view(torch.int16))
