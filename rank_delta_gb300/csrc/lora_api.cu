@@ -1571,7 +1571,7 @@ lora_status lora_mx4_proj_apply_ex(const void *x, int64_t x_stride, const uint8_
     q.hs = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(ws) + align256(256 + sizeof(float) * (size_t)M * (size_t)q.R));
     q.y = static_cast<uint16_t *>(y);
     q.y_stride = y_stride;
-    if ((e = launch_mx4_shrink(q, st)) != cudaSuccess)
+    if ((e = launch_mx4_shrink(q, di.num_sms, st)) != cudaSuccess)
         return cuda_fail(e, who);
     if (mx4_path(M, K, q.R, path) == LORA_MX4_PATH_TILES) {
         const Mx4TcPlan plan = plan_mx4_tc(q, di.num_sms);

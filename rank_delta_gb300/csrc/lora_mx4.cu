@@ -329,6 +329,59 @@ constexpr int SH_PAIR = 16;      // rows whose sums are joined at a time
 
 __device__ __forceinline__ void grid_dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// The call's status, by one CTA.
+__device__ __forceinline__ void open_status(const Mx4ProjParams &p, int tid)
+{
+    int bad = 0;
+    for (int i = tid; i < p.M; i += SH_THREADS)
+        bad |= p.seq_slot[i] >= p.L;
+    bad = __syncthreads_or(bad);
+    if (tid == 0)
+        status_begin(p.status, bad ? (uint32_t)LORA_FLAG_SLOT_RANGE : 0u);
+}
+
+// The u-th slot that a chunk of up to ROWS rows may have, and what is in it; -1:
+// there are not as many. With more slots than rows it is the u-th distinct one
+// of the rows (`mine`: this thread's). Whole CTA.
+template <int ROWS>
+__device__ __forceinline__ int shrink_slot(const Mx4ProjParams &p, int u, int mine, int tid, uint32_t *present, int &slot_s,
+                                           SlotInfo &si)
+{
+    if (p.L <= min(p.M, ROWS)) {
+        si = slot_info(p.tab, u, p.L);
+        return u;
+    }
+    const int lane = tid & 31;
+    present[lane] = 0u;
+    if (tid == 0)
+        slot_s = -1;
+    __syncthreads();
+    if (mine >= 0 && mine < p.L)
+        atomicOr(&present[mine >> 5], 1u << (mine & 31));
+    __syncthreads();
+    if (tid < 32) {
+        const uint32_t w = present[lane];
+        int incl = __popc(w);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += v;
+        }
+        const int before = incl - __popc(w);
+        if (u >= before && u < incl) {
+            uint32_t rest = w;
+            for (int i = before; i < u; ++i)
+                rest &= rest - 1;
+            slot_s = lane * 32 + __ffs(rest) - 1;
+        }
+    }
+    __syncthreads();
+    if (slot_s >= 0)
+        si = slot_info(p.tab, slot_s, p.L);
+    return slot_s;
+}
+
 // NT * 8 rows of the slot (from i0; past the last they repeat it) against 16
 // rank rows over the warp's blocks of 32 k, `AHEAD` blocks' loads in flight.
 template <int NT, int AHEAD>
@@ -383,50 +436,12 @@ __global__ void __launch_bounds__(SH_THREADS) mx4_shrink_kernel(Mx4ProjParams p)
     grid_dependency_wait();
     grid_dependents_launch();
     const int mine = tid < SH_ROWS && c0 + tid < p.M ? p.seq_slot[c0 + tid] : -1;
+    if (blockIdx.x == 0 && u == 0 && c0 == 0)
+        open_status(p, tid);
     SlotInfo si;
-    int slot = u;
-    const bool direct = p.L <= min(p.M, SH_ROWS);
-    if (direct)
-        si = slot_info(p.tab, slot, p.L); // on its way with the rows' slots
-    if (blockIdx.x == 0 && u == 0 && c0 == 0) { // the call's status
-        int bad = 0;
-        for (int i = tid; i < p.M; i += SH_THREADS)
-            bad |= p.seq_slot[i] >= p.L;
-        bad = __syncthreads_or(bad);
-        if (tid == 0)
-            status_begin(p.status, bad ? (uint32_t)LORA_FLAG_SLOT_RANGE : 0u);
-    }
-    if (!direct) { // the u-th distinct slot among the chunk's rows
-        present[lane] = 0u;
-        if (tid == 0)
-            slot_s = -1;
-        __syncthreads();
-        if (mine >= 0 && mine < p.L)
-            atomicOr(&present[mine >> 5], 1u << (mine & 31));
-        __syncthreads();
-        if (warp == 0) {
-            const uint32_t w = present[lane];
-            int incl = __popc(w);
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o)
-                    incl += v;
-            }
-            const int before = incl - __popc(w);
-            if (u >= before && u < incl) {
-                uint32_t rest = w;
-                for (int i = before; i < u; ++i)
-                    rest &= rest - 1;
-                slot_s = lane * 32 + __ffs(rest) - 1;
-            }
-        }
-        __syncthreads();
-        slot = slot_s;
-        if (slot < 0)
-            return;
-        si = slot_info(p.tab, slot, p.L);
-    }
+    const int slot = shrink_slot<SH_ROWS>(p, u, mine, tid, present, slot_s, si);
+    if (slot < 0)
+        return;
     if (!si.on || r0 >= si.rank)
         return;
     if (tid < SH_ROWS) { // the slot's rows, in order
@@ -495,12 +510,190 @@ __global__ void __launch_bounds__(SH_THREADS) mx4_shrink_kernel(Mx4ProjParams p)
     }
 }
 
-cudaError_t launch_mx4_shrink(const Mx4ProjParams &p, cudaStream_t st)
+namespace {
+
+constexpr int SM_CHUNK = 256;              // rows that a group of CTAs sorts by slot
+constexpr int SM_ROWS = 64, SM_RANKS = 64; // of a product, by slabs of 64 k
+constexpr int SM_STAGES = 12;
+constexpr int SM_MOST = 16;                // CTAs of a chunk, at most
+constexpr uint32_t SM_TILE = 64 * 128, SM_BYTES = SM_STAGES * 2 * SM_TILE + 1024;
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+} // namespace
+
+// The same for many rows. The CTAs of a chunk of 256 rows sort it by slot and take
+// turns with what that gives: up to 64 rows of a slot against up to 64 ranks, both
+// through shared memory, so x is read once and A once for 64 rows. A warp has 32
+// ranks by 32 rows of one k16 of each slab (16 by 16 of all four, which reads shared
+// memory twice as often: 4 us longer for 8192 rows). (A grid over
+// slots would be mostly empty CTAs: 8192 rows of 16 slots, 8192 of them.)
+// Grid: groups of 64 ranks, CTAs of a chunk, chunks.
+__global__ void __launch_bounds__(SH_THREADS, 1) mx4_shrink_many_kernel(Mx4ProjParams p)
+{
+    extern __shared__ uint8_t sm_raw[];
+    __shared__ int slots_s[SM_CHUNK], sorted_s[SM_CHUNK], unit_s[SM_CHUNK];
+    __shared__ uint32_t starts_s[SM_CHUNK / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int r0 = blockIdx.x * SM_RANKS, c0 = (int)blockIdx.z * SM_CHUNK;
+    grid_dependency_wait();
+    grid_dependents_launch();
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+        open_status(p, tid);
+    int mine = -1;
+    if (tid < SM_CHUNK) {
+        mine = c0 + tid < p.M ? p.seq_slot[c0 + tid] : -1;
+        mine = mine < p.L ? mine : -1;
+        slots_s[tid] = mine;
+    }
+    if (tid < SM_CHUNK / 32)
+        starts_s[tid] = 0u;
+    __syncthreads();
+    int less = 0, before = 0, all = 0; // rows of lower slots, earlier rows of this one, rows of this one
+    if (tid < SM_CHUNK) {
+#pragma unroll 4
+        for (int j = 0; j < SM_CHUNK; j += 4) {
+            const int4 v = *reinterpret_cast<const int4 *>(slots_s + j);
+            less += (v.x < mine) + (v.y < mine) + (v.z < mine) + (v.w < mine);
+            const int e[4] = {v.x == mine, v.y == mine, v.z == mine, v.w == mine};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                all += e[i];
+                before += e[i] && j + i < tid;
+            }
+        }
+        const int at = less + before;
+        sorted_s[at] = c0 + tid;
+        if (mine >= 0 && before % SM_ROWS == 0) // a unit begins
+            atomicOr(&starts_s[at >> 5], 1u << (at & 31));
+    }
+    __syncthreads();
+    int units = 0, nth = 0;
+#pragma unroll
+    for (int w = 0; w < SM_CHUNK / 32; ++w) {
+        const int n = __popc(starts_s[w]);
+        nth += w < (less + before) >> 5 ? n : 0;
+        units += n;
+    }
+    if (mine >= 0 && before % SM_ROWS == 0)
+        unit_s[nth + __popc(starts_s[(less + before) >> 5] & ((1u << ((less + before) & 31)) - 1u))] =
+            mine << 16 | (less + before) << 8 | (min(all - before, SM_ROWS) - 1);
+    __syncthreads();
+
+    const uint32_t raw = smem_u32(sm_raw), base = (raw + 1023u) & ~1023u;
+    uint8_t *const smem = sm_raw + (base - raw);
+    const int row = tid >> 3, piece = tid & 7, slabs = (p.K + 63) / 64;
+    const uint32_t into = (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4));
+    const int rg = (warp & 1) * 32, xg = (warp >> 1 & 1) * 32, k16 = warp >> 2;
+    const int lr = lane & 7, lm = lane >> 3; // row and matrix of a load
+    const int a_row = rg + lr + (lm & 1) * 8, x_row = xg + lr + (lm >> 1) * 8;
+    const uint32_t a_at = SM_TILE + (uint32_t)(a_row * 128 + (((k16 * 2 + (lm >> 1)) ^ (a_row & 7)) << 4)),
+                   x_at = (uint32_t)(x_row * 128 + (((k16 * 2 + (lm & 1)) ^ (x_row & 7)) << 4));
+    for (int unit = blockIdx.y; unit < units; unit += gridDim.y) {
+        const int slot = unit_s[unit] >> 16, count = (unit_s[unit] & 255) + 1;
+        const int *const rows_s = sorted_s + (unit_s[unit] >> 8 & 255);
+        const SlotInfo si = slot_info(p.tab, slot, p.L);
+        if (!si.on || r0 >= si.rank)
+            continue;
+        const bool have_x = row < count, have_a = r0 + row < si.rank;
+        const uint16_t *xr = p.x + (int64_t)rows_s[have_x ? row : 0] * p.x_stride + piece * 8;
+        const uint16_t *ar = si.a + (size_t)(have_a ? r0 + row : 0) * p.K + piece * 8;
+        auto load = [&](int b) {
+            if (b < slabs) {
+                uint8_t *const to = smem + (uint32_t)(b % SM_STAGES) * 2 * SM_TILE + into;
+                const bool in = b * 64 + piece * 8 < p.K;
+                const int k = in ? b * 64 : 0;
+                cp_async_16(to, in ? xr + k : p.x, in && have_x ? 16u : 0u);
+                cp_async_16(to + SM_TILE, in ? ar + k : p.x, in && have_a ? 16u : 0u);
+            }
+            cp_async_commit();
+        };
+        __syncthreads(); // the unit before has been read
+        for (int b = 0; b < SM_STAGES - 1; ++b)
+            load(b);
+        const bool work = r0 + rg < si.rank && xg < count;
+        float acc[2][4][4] = {};
+        for (int b = 0; b < slabs; ++b) {
+            cp_async_wait_group<SM_STAGES - 2>();
+            __syncthreads(); // slab b is there, and slab b - 1 has been read
+            load(b + SM_STAGES - 1);
+            if (work) {
+                const uint32_t at = base + (uint32_t)(b % SM_STAGES) * 2 * SM_TILE;
+                uint32_t a[2][4], x[2][4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) { // 16 rows further: 2048 bytes, turned alike
+                    ldmatrix_x4(at + a_at + (uint32_t)i * 2048, a[i]);
+                    ldmatrix_x4(at + x_at + (uint32_t)i * 2048, x[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+                        mma_16816(acc[i][n], a[i][0], a[i][1], a[i][2], a[i][3], x[n >> 1][(n & 1) * 2], x[n >> 1][(n & 1) * 2 + 1]);
+            }
+        }
+        // the four k16's sums, in order, where the slabs were
+        __syncthreads();
+        float *const red = reinterpret_cast<float *>(smem);
+        constexpr int RED_ROW = SM_ROWS + 1, RED = SM_RANKS * RED_ROW;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    red[k16 * RED + (rg + i * 16 + g + (j >> 1) * 8) * RED_ROW + xg + n * 8 + 2 * t + (j & 1)] = acc[i][n][j];
+        __syncthreads();
+        const float *comp = p.tab.comp_table + (size_t)slot * LORA_COMP_STRIDE;
+        const int ranks = min(p.R - r0, SM_RANKS);
+        for (int i = tid; i < count * SM_RANKS; i += SH_THREADS) {
+            const int r = i & (SM_RANKS - 1), q = i / SM_RANKS;
+            if (r < ranks) {
+                const float *v = red + r * RED_ROW + q;
+                const float h = r0 + r < si.rank ? si.scale * __ldg(comp + r0 + r) * (v[0] + v[RED] + v[2 * RED] + v[3 * RED]) : 0.0f;
+                const size_t to = (size_t)rows_s[q] * p.R + r0 + r;
+                p.h[to] = h;
+                p.hs[to] = f32_to_bf16_bits(h);
+            }
+        }
+    }
+}
+
+cudaError_t launch_mx4_shrink(const Mx4ProjParams &p, int num_sms, cudaStream_t st)
 {
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
+    // Many rows and more than 16 ranks, of which the other kernel reads x for each:
+    // a call of K = N = 4096, 16 slots of rank 64 (then 32 of rank 16), takes
+    //   rows  2048         4096          8192
+    //   many  61.0  60.1   110.9 109.6   199.0 199.1 us
+    //   other 65.5  54.7   123.8 106.7   235.7 199.4
+    if (p.M >= 2048 && p.R > 16) {
+        static std::atomic<uint64_t> raised{0};
+        const cudaError_t e = raise_smem_limit(raised, mx4_shrink_many_kernel, (int)SM_BYTES);
+        if (e != cudaSuccess)
+            return e;
+        // some two CTAs an SM; a chunk of one slot has four units, of many more
+        const int groups = (p.R + SM_RANKS - 1) / SM_RANKS, chunks = (p.M + SM_CHUNK - 1) / SM_CHUNK;
+        const int each = std::max(4, std::min(SM_MOST, 2 * num_sms / (groups * chunks)));
+        cfg.gridDim = dim3((unsigned)groups, (unsigned)each, (unsigned)chunks);
+        cfg.blockDim = dim3(SH_THREADS);
+        cfg.dynamicSmemBytes = SM_BYTES;
+        cfg.stream = st;
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, mx4_shrink_many_kernel, p);
+    }
     const int distinct = p.M < SH_ROWS ? p.M : SH_ROWS; // slots in a chunk, at most
     cfg.gridDim = dim3((unsigned)((p.R + 15) / 16), (unsigned)(p.L < distinct ? p.L : distinct),
                        (unsigned)((p.M + SH_ROWS - 1) / SH_ROWS));

@@ -316,7 +316,27 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
     const int m0 = 4 * j0, mbase = 4 * (j1 - j0), nbase = mbase / SUB;
     constexpr uint32_t cols = 512; // no second CTA fits on the SM by its shared memory
 
-    if (tid == 0) {
+    // the loads of a stage of x, and of a step of codes and scales
+    auto load_x = [&](int n) {
+        const int s = n % S;
+        mbar_arrive_expect_tx(&sh.full[s], SUB * x_bytes);
+        for (int h = 0; h < SUB; ++h)
+            tma_load_2d(smem + DS * SUB * A_BYTES + (uint32_t)(s * SUB + h) * x_bytes, &maps.x, (m0 + n * SUB + h) * 64, t0,
+                        &sh.full[s]);
+    };
+    auto load_codes = [&](int j) {
+        const int cs = j % CS;
+        uint8_t *at = smem + DS * SUB * A_BYTES + S * SUB * x_bytes;
+        mbar_arrive_expect_tx(&sh.c_full[cs], CODE_BYTES + (maps.scales_ok ? SCALE_BYTES : 0u));
+        tma_load_2d(at + (uint32_t)cs * CODE_BYTES, &maps.codes, (j0 + j) * 128, f0, &sh.c_full[cs]);
+        if (maps.scales_ok) // the 16 bytes that hold the step's eight
+            tma_load_2d(at + CS * CODE_BYTES + (uint32_t)cs * SCALE_BYTES, &maps.scales, ((j0 + j) * 8) & ~15, f0, &sh.c_full[cs]);
+    };
+
+    // The first loads are on their way before anything else is set up.
+    if (warp == WIDEN_WARPS + 2 && elected()) {
+        prefetch_tmap(&maps.codes);
+        prefetch_tmap(&maps.x);
         for (int s = 0; s < S; ++s) {
             mbar_init(&sh.full[s], 1 + 4 * SUB); // x, and the groups' warps
             mbar_init(&sh.free[s], 1);
@@ -335,6 +355,10 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         fence_barrier_init();
         if (kparts > 1 && part_owns(kparts, part) > 0)
             mbar_arrive_expect_tx(&sh.joined, (uint32_t)((kparts - 1) * part_owns(kparts, part) * (tn + 1)) * 4u);
+        for (int j = 0; j < CS && j < j1 - j0; ++j)
+            load_codes(j);
+        for (int n = 0; n < S && n < nbase; ++n)
+            load_x(n);
     }
     if (warp == WIDEN_WARPS + 1)
         tmem_alloc(&sh.tmem, cols);
@@ -466,18 +490,11 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         __syncwarp();
     } else if (warp == WIDEN_WARPS) {
         // ---- x
-        if (elected()) {
-            prefetch_tmap(&maps.x);
-            for (int n = 0; n < nbase; ++n) {
-                const int s = n % S;
-                if (n >= S)
-                    stage_free(n - S);
-                mbar_arrive_expect_tx(&sh.full[s], SUB * x_bytes);
-                for (int h = 0; h < SUB; ++h)
-                    tma_load_2d(smem + DS * SUB * A_BYTES + (uint32_t)(s * SUB + h) * x_bytes, &maps.x, (m0 + n * SUB + h) * 64,
-                                t0, &sh.full[s]);
+        if (elected())
+            for (int n = S; n < nbase; ++n) {
+                stage_free(n - S);
+                load_x(n);
             }
-        }
         __syncwarp();
     } else if (warp == WIDEN_WARPS + 1) {
         // ---- products
@@ -543,19 +560,11 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         __syncwarp();
     } else if (warp == WIDEN_WARPS + 2) {
         // ---- codes and scales
-        if (elected()) {
-            for (int j = 0; 4 * j < mbase; ++j) {
-                const int cs = j % CS, use = j / CS;
-                if (use > 0)
-                    wait_or_note(&sh.c_free[cs], (uint32_t)(use - 1) & 1u, &sh.bad);
-                mbar_arrive_expect_tx(&sh.c_full[cs], CODE_BYTES + (maps.scales_ok ? SCALE_BYTES : 0u));
-                uint8_t *at = smem + DS * SUB * A_BYTES + S * SUB * x_bytes;
-                tma_load_2d(at + (uint32_t)cs * CODE_BYTES, &maps.codes, (j0 + j) * 128, f0, &sh.c_full[cs]);
-                if (maps.scales_ok) // the 16 bytes that hold the step's eight
-                    tma_load_2d(at + CS * CODE_BYTES + (uint32_t)cs * SCALE_BYTES, &maps.scales, ((j0 + j) * 8) & ~15, f0,
-                                &sh.c_full[cs]);
+        if (elected())
+            for (int j = CS; j < j1 - j0; ++j) {
+                wait_or_note(&sh.c_free[j % CS], (uint32_t)(j / CS - 1) & 1u, &sh.bad);
+                load_codes(j);
             }
-        }
         __syncwarp();
     } else {
         route_tile(p, sh, t0, tn, lane);

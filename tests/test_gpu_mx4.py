@@ -325,3 +325,14 @@ def test_replayed_from_a_graph(M):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("M,K,N,L,R,runs", [(2048, 288, 40, 5, 64, True), (2050, 320, 24, 300, 24, False), (2500, 96, 72, 2, 136, True),
+                                            (2304, 2080, 16, 24, 32, False)])
+def test_calls_of_thousands_of_rows(M, K, N, L, R, runs):
+    """Slots in runs as prefill has them, and rows of any slot; chunks with more slots than CTAs, a last chunk that ends early."""
+    s = Setup(M, K, N, L, R, seed=M)
+    if runs:
+        s.slots = np.repeat(np.arange(-1, L, dtype=np.int32), -(-M // (L + 1)))[:M].copy()
+    s.check(s.run(rd.LORA_MX4_PATH_AUTO))
+    assert s.flags == 0
