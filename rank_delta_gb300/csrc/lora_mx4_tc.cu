@@ -178,11 +178,6 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, const uint32_t 
                  "r"(r[2]), "r"(r[3])
                  : "memory");
 }
-// `bytes` (a multiple of 16) from the 16-byte aligned p on into L2.
-__device__ __forceinline__ void prefetch_l2_bulk(const void *p, uint32_t bytes)
-{
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
 // 32 columns of the warp's 32 lanes.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32])
 {
@@ -418,8 +413,6 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         const int ndelta = __any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&sh.bad) != 0)
                                ? 0
                                : (q1 - q0 + 4 * SUB - 1) / (4 * SUB);
-        if (ndelta > 0)
-            grid_dependency_wait(); // h is complete
         // The warps work in teams, a stage each: finding its slot and waiting take
         // as long as the copies (256x4096x14336 39.9 us, 40.7 with all on every stage).
         constexpr int TEAM_WARPS = WIDEN_WARPS / TEAMS;
@@ -440,6 +433,32 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         // had the stage's place before
         int lo = -1, begin = 0, end = 0, slot = -1, lo_before = -1, end_before = 0, before = -1;
         const uint16_t *slot_b = nullptr;
+        auto find = [&](int q) {
+            if (q >= end) { // another slot
+                do {
+                    begin = end;
+                    end = sh.seg_start[++lo + 1];
+                } while (q >= end);
+                slot = sh.slot_id[lo];
+                slot_b = sh.slot_b[lo];
+            }
+            return (q - begin) * 16 + (piece & 1) * 8; // the rank
+        };
+        auto copy_b = [&](int s, int r) {
+            const uint32_t at = d_slot(s) + (uint32_t)sub * A_BYTES + into;
+            const uint16_t *b = slot_b + (r < p.R ? r : 0);
+#pragma unroll
+            for (int i = 0; i < BM / ROWS; ++i)
+                cp16(at + (uint32_t)(i * ROWS * 128), b + b_row[i], r < p.R ? 16u : 0u); // else zeros
+        };
+        static_assert(DS >= TEAMS, "B of a team's first stage, which has its place from the start");
+        const int q_first = q0 + 4 * (SUB * team + sub) + (piece >> 1);
+        if (team < ndelta && q_first < q1) {
+            const int r = find(q_first);
+            copy_b(team, r);
+        }
+        if (ndelta > 0)
+            grid_dependency_wait(); // h is complete
         bool codes_left = false;
         for (int d = team; d < ndelta; d += TEAMS) {
             const int n = nbase + d, s = d % S, xslot = n % S;
@@ -451,16 +470,9 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
             }
             const int q = q0 + 4 * (SUB * d + sub) + (piece >> 1);
             if (q < q1) {
-                if (q >= end) { // another slot
-                    do {
-                        begin = end;
-                        end = sh.seg_start[++lo + 1];
-                    } while (q >= end);
-                    slot = sh.slot_id[lo];
-                    slot_b = sh.slot_b[lo];
-                }
-                const int r = (q - begin) * 16 + (piece & 1) * 8;
-                const uint32_t have = r < p.R ? 16u : 0u; // else zeros
+                const int r = find(q);
+                if (d != team)
+                    copy_b(s, r);
                 // rows of x that are not the slot's are zeros: all of a slot at first, then
                 // those that the stage S before had
                 if (d >= S && q - 4 * SUB * S >= end_before) {
@@ -469,11 +481,8 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
                     while (q - 4 * SUB * S >= end_before);
                     before = sh.slot_id[lo_before];
                 }
-                const uint32_t at = d_slot(s) + (uint32_t)sub * A_BYTES + into, xt = x_at + (uint32_t)(xslot * SUB + sub) * x_bytes + into;
-                const uint16_t *b = slot_b + (have ? r : 0), *h = p.hs + (size_t)(t0 + first) * p.R + (have ? r : 0);
-#pragma unroll
-                for (int i = 0; i < BM / ROWS; ++i)
-                    cp16(at + (uint32_t)(i * ROWS * 128), b + b_row[i], have);
+                const uint32_t xt = x_at + (uint32_t)(xslot * SUB + sub) * x_bytes + into, have = r < p.R ? 16u : 0u;
+                const uint16_t *h = p.hs + (size_t)(t0 + first) * p.R + (have ? r : 0);
 #pragma unroll
                 for (int i = 0; i < AT_ONCE; ++i)
                     if (first + i * ROWS < tn) {
@@ -570,12 +579,6 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         route_tile(p, sh, t0, tn, lane);
         if (lane == 0)
             mbar_arrive(&sh.routed);
-        // the slots' B rows of this tile are one piece each: on their way into L2
-        // while the base is multiplied
-        const uint32_t bytes = (uint32_t)(min(BM, p.N - f0) * p.R) * 2u;
-        for (int i = lane; i < sh.nslot; i += 32)
-            if (sh.seg_start[i + 1] > sh.nseg * part / kparts && sh.seg_start[i] < sh.nseg * (part + 1) / kparts)
-                prefetch_l2_bulk(sh.slot_b[i] + (size_t)f0 * p.R, bytes);
         __syncwarp();
     }
 
