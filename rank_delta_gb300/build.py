@@ -18,7 +18,7 @@ LIB = os.path.join(OUT, "librank_delta.so")
 SOURCES = ["lora_api.cu", "lora_prep.cu", "lora_simt.cu", "lora_tc.cu", "lora_embed.cu", "lora_act.cu", "lora_gather.cu",
            "lora_static_ws.cu", "lora_dec.cu", "lora_logprob.cu",
            "lora_mx4.cu", "lora_mx4_tc.cu"]
-HEADERS = ["lora_internal.cuh", "lora_logprob.cuh", "lora_mx4.cuh", "ptx.cuh", "shrink.cuh", "shrink_tc.cuh", "vec.cuh"]
+HEADERS = ["behind.cuh", "lora_internal.cuh", "lora_logprob.cuh", "lora_mx4.cuh", "ptx.cuh", "shrink.cuh", "shrink_tc.cuh", "vec.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "nvcc")
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

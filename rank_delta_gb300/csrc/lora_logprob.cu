@@ -27,6 +27,7 @@
 //     distributed shared memory. Nothing depends on timing in either.
 #include <cooperative_groups.h>
 
+#include "behind.cuh"
 #include "lora_logprob.cuh"
 #include "ptx.cuh"
 #include "vec.cuh"
@@ -633,6 +634,7 @@ __global__ void __launch_bounds__(ROW_THREADS, ROW_CTAS) logprob_rows_kernel(Log
     constexpr int PER = ROW_READERS / 32; // threads a lane of the last warp answers for
     __shared__ Left<TOP> left[2];
     __shared__ Key held[TOP ? 64 : 1];
+    begin_behind();
     const int tid = threadIdx.x, lane = tid & 31, step = gridDim.x;
     const float c = p.inv_t * LOG2E;
     if (blockIdx.x == 0)
@@ -754,6 +756,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprob_split_kernel(LogprobPar
 {
     constexpr int E = Vec<T>::E;
     __shared__ SplitShared<TOP> sm;
+    begin_behind();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int part = blockIdx.x % parts, row = blockIdx.x / parts;
     const float c = p.inv_t * LOG2E;
@@ -880,6 +883,7 @@ template <typename T, bool BONUS>
 __global__ void __launch_bounds__(LP_THREADS, 6) logprob_grad_kernel(LogprobGradParams p, int segs)
 {
     constexpr int E = Vec<T>::E;
+    begin_behind();
     const int row = blockIdx.x / segs, seg = blockIdx.x % segs;
     const T *x = static_cast<const T *>(p.logits) + (int64_t)row * p.stride;
     T *dx = static_cast<T *>(p.dlogits) + (int64_t)row * p.d_stride;
@@ -978,25 +982,11 @@ template <typename T> cudaError_t launch_lp(const LogprobParams &p, int num_sms,
     while (parts < 8 && (int64_t)p.M * parts < 2 * num_sms && nvec >= 2 * parts * LP_THREADS)
         parts *= 2;
     if (parts == 1) { // as many CTAs as stay resident, each with rows one after another
-        const int grid = p.M < ROW_CTAS * num_sms ? p.M : ROW_CTAS * num_sms;
-        if (p.top_k > 0)
-            logprob_rows_kernel<T, true><<<grid, ROW_THREADS, 0, st>>>(p);
-        else
-            logprob_rows_kernel<T, false><<<grid, ROW_THREADS, 0, st>>>(p);
-        return cudaGetLastError();
+        const dim3 grid((unsigned)(p.M < ROW_CTAS * num_sms ? p.M : ROW_CTAS * num_sms));
+        return launch_behind(p.top_k > 0 ? logprob_rows_kernel<T, true> : logprob_rows_kernel<T, false>, grid, ROW_THREADS, 0, 1, st, p);
     }
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)parts;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.M * parts));
-    cfg.blockDim = dim3(LP_THREADS);
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return p.top_k > 0 ? cudaLaunchKernelEx(&cfg, logprob_split_kernel<T, true>, p, parts)
-                       : cudaLaunchKernelEx(&cfg, logprob_split_kernel<T, false>, p, parts);
+    return launch_behind(p.top_k > 0 ? logprob_split_kernel<T, true> : logprob_split_kernel<T, false>, dim3((unsigned)(p.M * parts)),
+                         LP_THREADS, 0, (unsigned)parts, st, p, parts);
 }
 
 cudaError_t launch_logprob(const LogprobParams &p, int dtype, int num_sms, cudaStream_t st)
@@ -1009,11 +999,8 @@ template <typename T> cudaError_t launch_grad(const LogprobGradParams &p, cudaSt
     // one vector more than V fills, for rows that start inside one
     const int64_t nvec = ((int64_t)p.V + Vec<T>::E - 1) / Vec<T>::E + 1;
     const int segs = (int)((nvec + LP_UNROLL * LP_THREADS - 1) / (LP_UNROLL * LP_THREADS));
-    if (p.g_entropy != nullptr)
-        logprob_grad_kernel<T, true><<<(unsigned)(p.M * segs), LP_THREADS, 0, st>>>(p, segs);
-    else
-        logprob_grad_kernel<T, false><<<(unsigned)(p.M * segs), LP_THREADS, 0, st>>>(p, segs);
-    return cudaGetLastError();
+    return launch_behind(p.g_entropy != nullptr ? logprob_grad_kernel<T, true> : logprob_grad_kernel<T, false>,
+                         dim3((unsigned)(p.M * segs)), LP_THREADS, 0, 1, st, p, segs);
 }
 
 cudaError_t launch_logprob_grad(const LogprobGradParams &p, int dtype, cudaStream_t st)

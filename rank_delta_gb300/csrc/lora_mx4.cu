@@ -13,6 +13,9 @@
 // rows       the product for up to four rows, on the tensor cores' registers
 //            (mma.sync): a warp's 16 weight rows need not pass through shared
 //            memory a second time once they are widened.
+#include <algorithm>
+
+#include "behind.cuh"
 #include "lora_mx4.cuh"
 #include "ptx.cuh"
 #include "vec.cuh"
@@ -139,6 +142,7 @@ __device__ __forceinline__ uint4 quantize_block(const uint32_t (&w)[16], uint32_
 // 14336x4096: 24 us, 6.1 TB/s (four threads a block, through fp32: 40 us).
 __global__ void __launch_bounds__(Q_THREADS) mx4_quantize_blocks_kernel(Mx4QuantParams p)
 {
+    begin_behind();
     const int bpr = p.K / 32;
     const int64_t b = (int64_t)blockIdx.x * Q_THREADS + threadIdx.x;
     if (b >= p.rows * bpr)
@@ -161,6 +165,7 @@ __global__ void __launch_bounds__(Q_THREADS) mx4_quantize_blocks_kernel(Mx4Quant
 // 6.8 TB/s) and rows on any boundary: four threads a block.
 template <typename T> __global__ void __launch_bounds__(Q_THREADS) mx4_quantize_kernel(Mx4QuantParams p, int vec)
 {
+    begin_behind();
     const int upr = p.K / 8;
     const int64_t total = p.rows * upr; // a multiple of 4: the threads of a block go together
     const bool packed = p.w_stride == p.K;
@@ -249,6 +254,7 @@ template <typename T> __global__ void __launch_bounds__(Q_THREADS) mx4_dequantiz
 {
     using Codes = typename Back<T>::Codes;
     constexpr int EACH = 2 * sizeof(Codes); // values
+    begin_behind();
     const int upr = p.K / EACH;
     const int64_t total = p.rows * upr;
     const bool packed = p.w_stride == p.K;
@@ -291,23 +297,19 @@ cudaError_t launch_mx4_quantize(const Mx4QuantParams &p, int dtype, cudaStream_t
 {
     const unsigned pairs = grid_for(p.rows * (p.K / 8), 2);
     if (dtype == LORA_DTYPE_F32)
-        mx4_quantize_kernel<float><<<pairs, Q_THREADS, 0, st>>>(p, vec_rows<float>(p.w, p.w_stride));
-    else if (vec_rows<uint16_t>(p.w, p.w_stride))
-        mx4_quantize_blocks_kernel<<<grid_for(p.rows * (p.K / 32), 1), Q_THREADS, 0, st>>>(p);
-    else
-        mx4_quantize_kernel<uint16_t><<<pairs, Q_THREADS, 0, st>>>(p, 0);
-    return cudaGetLastError();
+        return launch_behind(mx4_quantize_kernel<float>, dim3(pairs), Q_THREADS, 0, 1, st, p, (int)vec_rows<float>(p.w, p.w_stride));
+    if (vec_rows<uint16_t>(p.w, p.w_stride))
+        return launch_behind(mx4_quantize_blocks_kernel, dim3(grid_for(p.rows * (p.K / 32), 1)), Q_THREADS, 0, 1, st, p);
+    return launch_behind(mx4_quantize_kernel<uint16_t>, dim3(pairs), Q_THREADS, 0, 1, st, p, 0);
 }
 
 cudaError_t launch_mx4_dequantize(const Mx4DequantParams &p, int dtype, cudaStream_t st)
 {
     if (dtype == LORA_DTYPE_F32)
-        mx4_dequantize_kernel<float>
-            <<<grid_for(p.rows * (p.K / 4), Q_UNROLL), Q_THREADS, 0, st>>>(p, vec_rows<float>(p.w, p.w_stride));
-    else
-        mx4_dequantize_kernel<uint16_t>
-            <<<grid_for(p.rows * (p.K / 8), Q_UNROLL), Q_THREADS, 0, st>>>(p, vec_rows<uint16_t>(p.w, p.w_stride));
-    return cudaGetLastError();
+        return launch_behind(mx4_dequantize_kernel<float>, dim3(grid_for(p.rows * (p.K / 4), Q_UNROLL)), Q_THREADS, 0, 1, st, p,
+                             (int)vec_rows<float>(p.w, p.w_stride));
+    return launch_behind(mx4_dequantize_kernel<uint16_t>, dim3(grid_for(p.rows * (p.K / 8), Q_UNROLL)), Q_THREADS, 0, 1, st, p,
+                         (int)vec_rows<uint16_t>(p.w, p.w_stride));
 }
 
 // ------------------------------------------------------------------ shrink
@@ -326,8 +328,6 @@ constexpr int SH_WARPS = 16;     // they share K
 constexpr int SH_THREADS = SH_WARPS * 32;
 constexpr int SH_ROWS = 64;      // rows a CTA looks through for its slot
 constexpr int SH_PAIR = 16;      // rows whose sums are joined at a time
-
-__device__ __forceinline__ void grid_dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // The call's status, by one CTA.
 __device__ __forceinline__ void open_status(const Mx4ProjParams &p, int tid)
@@ -433,8 +433,7 @@ __global__ void __launch_bounds__(SH_THREADS) mx4_shrink_kernel(Mx4ProjParams p)
     const int r0 = blockIdx.x * 16, u = blockIdx.y, c0 = blockIdx.z * SH_ROWS;
     // Launched early behind whatever the stream ran before; nothing is read
     // until that is complete, and only then may the projection kernel start.
-    grid_dependency_wait();
-    grid_dependents_launch();
+    begin_behind();
     const int mine = tid < SH_ROWS && c0 + tid < p.M ? p.seq_slot[c0 + tid] : -1;
     if (blockIdx.x == 0 && u == 0 && c0 == 0)
         open_status(p, tid);
@@ -542,8 +541,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1) mx4_shrink_many_kernel(Mx4ProjP
     __shared__ uint32_t starts_s[SM_CHUNK / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int r0 = blockIdx.x * SM_RANKS, c0 = (int)blockIdx.z * SM_CHUNK;
-    grid_dependency_wait();
-    grid_dependents_launch();
+    begin_behind();
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
         open_status(p, tid);
     int mine = -1;
@@ -667,10 +665,6 @@ __global__ void __launch_bounds__(SH_THREADS, 1) mx4_shrink_many_kernel(Mx4ProjP
 
 cudaError_t launch_mx4_shrink(const Mx4ProjParams &p, int num_sms, cudaStream_t st)
 {
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
     // Many rows and more than 16 ranks, of which the other kernel reads x for each:
     // a call of K = N = 4096, 16 slots of rank 64 (then 32 of rank 16), takes
     //   rows  2048         4096          8192
@@ -684,24 +678,14 @@ cudaError_t launch_mx4_shrink(const Mx4ProjParams &p, int num_sms, cudaStream_t 
         // some two CTAs an SM; a chunk of one slot has four units, of many more
         const int groups = (p.R + SM_RANKS - 1) / SM_RANKS, chunks = (p.M + SM_CHUNK - 1) / SM_CHUNK;
         const int each = std::max(4, std::min(SM_MOST, 2 * num_sms / (groups * chunks)));
-        cfg.gridDim = dim3((unsigned)groups, (unsigned)each, (unsigned)chunks);
-        cfg.blockDim = dim3(SH_THREADS);
-        cfg.dynamicSmemBytes = SM_BYTES;
-        cfg.stream = st;
-        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr.val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, mx4_shrink_many_kernel, p);
+        return launch_behind(mx4_shrink_many_kernel, dim3((unsigned)groups, (unsigned)each, (unsigned)chunks), SH_THREADS, SM_BYTES, 1,
+                             st, p);
     }
     const int distinct = p.M < SH_ROWS ? p.M : SH_ROWS; // slots in a chunk, at most
-    cfg.gridDim = dim3((unsigned)((p.R + 15) / 16), (unsigned)(p.L < distinct ? p.L : distinct),
-                       (unsigned)((p.M + SH_ROWS - 1) / SH_ROWS));
-    cfg.blockDim = dim3(SH_THREADS);
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, mx4_shrink_kernel, p);
+    return launch_behind(mx4_shrink_kernel,
+                         dim3((unsigned)((p.R + 15) / 16), (unsigned)(p.L < distinct ? p.L : distinct),
+                              (unsigned)((p.M + SH_ROWS - 1) / SH_ROWS)),
+                         SH_THREADS, 0, 1, st, p);
 }
 
 // -------------------------------------------------------------------- rows
@@ -1020,17 +1004,8 @@ cudaError_t launch_mx4_rows(const Mx4ProjParams &p, const CUtensorMap &codes, in
     if (e != cudaSuccess)
         return e;
     const int step = 16 * (RW_WARPS / shape.team), groups = (p.N + step - 1) / step;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(groups < num_sms ? groups : num_sms));
-    cfg.blockDim = dim3(RW_THREADS);
-    cfg.dynamicSmemBytes = shape.smem;
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, mx4_rows_kernel, codes, p, shape);
+    return launch_behind(mx4_rows_kernel, dim3((unsigned)(groups < num_sms ? groups : num_sms)), RW_THREADS, shape.smem, 1, st, codes, p,
+                         shape);
 }
 
 } // namespace rd

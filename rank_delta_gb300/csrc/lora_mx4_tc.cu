@@ -579,6 +579,7 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         route_tile(p, sh, t0, tn, lane);
         if (lane == 0)
             mbar_arrive(&sh.routed);
+        grid_dependency_wait(); // a call is not over before its shrink is
         __syncwarp();
     }
 
@@ -815,23 +816,25 @@ using Rings256 = Rings<256, 1, 4, 2, 2, 256, true>;
 
 } // namespace
 
-// Tiles of 128 or 256 rows and the parts of K, by an estimate of the cycles of the
-// CTAs that an SM runs one after another: what 64 k take (the widening up to 64
-// rows, the products from some 170 on), 4000 for the rest of a tile, and what
-// the exchange adds. 256x4096x4096 with 16 adapters takes 27.7 us as 256 rows in
-// two parts and 23.5 as twice 128 rows.
+// The tiles' rows and the parts of K, by an estimate of the cycles of the CTAs that
+// an SM runs one after another: set-up, what 64 k take (the widening up to 64
+// rows, the products from some 170 on), and the epilogue, with the exchange if
+// there is one. Measured where it decides, 16 adapters of rank 64:
+// 256x4096x4096 27.7 us as 256 rows in two parts, 23.5 as twice 128;
+// 512x4096x6144 with 32 adapters 55.3 us as twice 256, 51.5 as three times 176.
 Mx4TcPlan plan_mx4_tc(const Mx4ProjParams &p, int num_sms)
 {
     const int ftiles = (p.N + BM - 1) / BM, nst = (p.K / 32 + 1) / 2, nsteps = (nst + 3) / 4;
     Mx4TcPlan plan{0, 1};
     int64_t least = 0;
-    for (int most = MAX_TN; most >= MAX_TN / 2; most /= 2) {
-        const int tiles = (p.M + most - 1) / most, each = (p.M + tiles - 1) / tiles, tn = (each + 15) / 16 * 16;
-        const int64_t ctas = (int64_t)ftiles * tiles;
-        const int sub = tn <= 128 ? 335 + (tn > 64 ? (tn - 64) * 7 / 8 : 0) : 2 * tn + 45 > 390 ? 2 * tn + 45 : 390;
+    const int fewest = (p.M + MAX_TN - 1) / MAX_TN;
+    for (int t = fewest; t <= 4 * fewest; ++t) {
+        const int each = (p.M + t - 1) / t, tn = (each + 15) / 16 * 16;
+        const int64_t ctas = (int64_t)ftiles * ((p.M + tn - 1) / tn);
+        const int sub = tn <= 128 ? 335 + (tn > 64 ? (tn - 64) * 7 / 8 : 0) : 2 * tn + 5 > 390 ? 2 * tn + 5 : 390;
         for (int k = 1; k <= MAX_KPARTS && k <= nsteps && (k == 1 || ctas * k <= num_sms); ++k) {
             const int64_t waves = (ctas * k + num_sms - 1) / num_sms;
-            const int64_t cost = waves * (4000 + (int64_t)((nsteps + k - 1) / k) * 4 * sub + (k > 1 ? 2000 + 16 * tn : 0));
+            const int64_t cost = waves * (4000 + (int64_t)((nsteps + k - 1) / k) * 4 * sub + (k > 1 ? 2700 + 28 * tn : 600 + 15 * tn));
             if ((plan.tn == 0 || cost < least) &&
                 (k == 1 || (tn <= 64    ? fits<Rings64>(tn, k, ctas, num_sms)
                             : tn <= 128 ? fits<Rings128>(tn, k, ctas, num_sms)
@@ -841,6 +844,8 @@ Mx4TcPlan plan_mx4_tc(const Mx4ProjParams &p, int num_sms)
                 plan.kparts = k;
             }
         }
+        if (tn <= 16)
+            break;
     }
     return plan;
 }
