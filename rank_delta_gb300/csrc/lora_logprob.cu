@@ -42,8 +42,8 @@ constexpr int LP_THREADS = 256;     // gradient, and rows spread over a cluster
 constexpr int LP_WARPS = LP_THREADS / 32;
 // Whole rows: reading threads of a CTA (one warp more finishes), CTAs resident
 // a SM and 16-byte vectors of a thread in flight. 256 x 3 x 4 reads 8192 rows
-// of 32000 bf16 in 95 us; 128 x 6 in 160, 192 x 4 in 104, 384 x 2 in 110, 512 x
-// 2 in 157 (small groups scatter the reads, large ones leave a row two steps).
+// of 32000 bf16 in 88 us; 128 x 6 took 68 % longer, 192 x 4 9, 384 x 2 16, 512 x
+// 2 65 (small groups scatter the reads, large ones leave a row two steps).
 constexpr int ROW_READERS = 256;
 constexpr int ROW_THREADS = ROW_READERS + 32;
 constexpr int ROW_CTAS = 3;
@@ -628,6 +628,8 @@ template <bool TOP> struct Left {
 
 } // namespace
 
+// 8192 x 32000 bf16: 88 us, 6.0 TB/s, and 105 with the best element; issue slots
+// and the exponentials bound it. 4096 x 32000 f32: 80 us, 6.6 TB/s, HBM.
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(ROW_THREADS, ROW_CTAS) logprob_rows_kernel(LogprobParams p)
 {
@@ -751,6 +753,8 @@ template <bool TOP> struct SplitShared {
 
 } // namespace
 
+// Latency bounds it. 1 x 32000 bf16: 4 us, 8 with the best 20; 64 x 32003 f32 with
+// the best 5: 9.7 us.
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(LP_THREADS, 4) logprob_split_kernel(LogprobParams p, int parts)
 {
@@ -879,6 +883,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprob_split_kernel(LogprobPar
 //   dx = 2^a (q + r a),  q = -t (g + g_H H),  r = -t g_H ln 2,
 // and the token's own gets t g on top. a = x c - (m c + log S log2 e), the
 // latter held as two fp32 numbers so that p is as good as fp32 allows.
+// 8192 x 32000 bf16: 150 us, 7.0 TB/s, HBM; 96 x 32003 f32 with entropy 4.9 us.
 template <typename T, bool BONUS>
 __global__ void __launch_bounds__(LP_THREADS, 6) logprob_grad_kernel(LogprobGradParams p, int segs)
 {

@@ -7,9 +7,11 @@
 //            rounded to nearest even and saturate.
 // dequantize the reverse, eight values a thread and step.
 // shrink     h = A_s x_i for the rows of each slot, on the tensor cores straight
-//            from memory: 16 rank rows by up to 16 of the slot's rows a CTA and
-//            pass. The projection kernels start behind it at once and wait for
-//            h only where they need it.
+//            from memory: 16 rank rows by up to 32 of the slot's rows a CTA and
+//            pass (64 rows, 16 slots of rank 64, K = 4096: 6.4 us, latency); for
+//            thousands of rows 64 by 64 through shared memory. The projection
+//            kernels start behind it at once and wait for h only where they need
+//            it.
 // rows       the product for up to four rows, on the tensor cores' registers
 //            (mma.sync): a warp's 16 weight rows need not pass through shared
 //            memory a second time once they are widened.
@@ -139,7 +141,7 @@ __device__ __forceinline__ uint4 quantize_block(const uint32_t (&w)[16], uint32_
 
 // bf16 rows on 16-byte boundaries: a block of 32 values a thread, whose 16
 // bytes of codes and scale byte are neighbours of the next thread's.
-// 14336x4096: 24 us, 6.1 TB/s (four threads a block, through fp32: 40 us).
+// 14336x4096: 23 us, 6.4 TB/s (four threads a block, through fp32: 40 us).
 __global__ void __launch_bounds__(Q_THREADS) mx4_quantize_blocks_kernel(Mx4QuantParams p)
 {
     begin_behind();
@@ -249,7 +251,7 @@ template <> struct Back<float> {
 
 } // namespace
 
-// 14336x4096 to bf16: 24 us, 6.3 TB/s.
+// 14336x4096 to bf16: 23 us, 6.4 TB/s.
 template <typename T> __global__ void __launch_bounds__(Q_THREADS) mx4_dequantize_kernel(Mx4DequantParams p, int vec)
 {
     using Codes = typename Back<T>::Codes;
@@ -755,6 +757,8 @@ __device__ __forceinline__ void widen_pair(uint32_t a, uint32_t b, uint32_t fa, 
 // the row and the block so that the eight lanes of a load phase meet different
 // bank groups. Which k a fragment's slots mean is free as long as
 // both operands agree: thread t of four supplies the block t of 128 k.
+// What bounds it is the widening, 19 instructions for 8 codes: 1x4096x32000 takes
+// 31 us (2.2 TB/s of codes), 1x4096x4096 8.5 with its shrink.
 __global__ void __launch_bounds__(RW_THREADS, 1)
     mx4_rows_kernel(const __grid_constant__ CUtensorMap codes, const __grid_constant__ Mx4ProjParams p, RowsShape shape)
 {

@@ -81,7 +81,7 @@ __device__ __forceinline__ void wait_or_note(uint64_t *bar, uint32_t parity, int
 
 // One lane of the converged warp, by the instruction that tells the compiler so:
 // what follows in its branch needs no loop over lanes that might differ (with
-// lane == 0 instead a product took 80 cycles to issue: 8192x4096x14336 748 us, not 690).
+// lane == 0 instead a product took 80 cycles to issue, and 8192x4096x14336 8 % longer).
 __device__ __forceinline__ bool elected()
 {
     uint32_t one;

@@ -9,8 +9,8 @@
 // shared memory is left to x); x comes by TMA, and one thread issues the products.
 // The weight is widened once for all rows of the tile. With tiles of 256 rows
 // the tensor cores and what a tile takes before and after them bound it
-// (8192x4096x14336: 626 us, 574 without adapters, 1.68 PFLOP/s; a stage of 64 k
-// takes 555 cycles, its products 512); with fewer rows it is the widening and what a
+// (8192x4096x14336: 586 us, 550 without adapters, 1.75 PFLOP/s; a stage of 64 k
+// takes 515 to 555 cycles, its products 512); with fewer rows it is the widening and what a
 // call takes in any case, shrink, set-up and epilogue (64x4096x4096: 14.5 us).
 //
 // The adapters are more K: s h of the tile's rows (rounded to bf16, as y
@@ -45,8 +45,8 @@ constexpr int TEAMS = 2;            // of the widening warps, that copy the adap
 //
 // 64 k take 2 tn cycles of the tensor cores. Up to about 128 rows that is less
 // than a stage's waits and commits, so a stage has two sub-tiles there
-// (64x4096x14336: 30.5 us, with one 32.4); above, two would leave two stages
-// only (256x4096x14336: 45 us with one, 53 with two).
+// (64x4096x14336: 25.4 us, 6 % longer with one); above, two would leave two stages
+// only (256x4096x14336: 37.8 us with one, 19 % longer with two).
 //
 // Up to 128 rows the widened weights lie behind both accumulators; above it
 // they take the columns of the adapters' accumulator (ALIAS), which is not written
@@ -407,14 +407,14 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         // ---- the adapters' operands: 4 SUB segments of 16 ranks a stage. Eight
         // lanes copy a row's 128 bytes of a sub-tile, which for a rank of 64 lie in
         // one piece: a warp's copy meets 4 lines (a row a lane, 32: 64x4096x14336 took
-        // 3 us longer)
+        // 10 % longer)
         wait_or_note(&sh.routed, 0, &sh.bad);
         const int q0 = sh.nseg * part / kparts, q1 = sh.nseg * (part + 1) / kparts;
         const int ndelta = __any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&sh.bad) != 0)
                                ? 0
                                : (q1 - q0 + 4 * SUB - 1) / (4 * SUB);
         // The warps work in teams, a stage each: finding its slot and waiting take
-        // as long as the copies (256x4096x14336 39.9 us, 40.7 with all on every stage).
+        // as long as the copies (256x4096x14336: 2 % longer with all on every stage).
         constexpr int TEAM_WARPS = WIDEN_WARPS / TEAMS;
         constexpr int SUB_WARPS = TEAM_WARPS / SUB, ROWS = SUB_WARPS * 4; // that copy a sub-tile, rows at a time
         const int team = warp / TEAM_WARPS, sub = warp % TEAM_WARPS / SUB_WARPS, piece = lane & 7,
