@@ -20,7 +20,7 @@
 // bound, k elements and a few, is then put in order.
 //
 // logprob_rows_kernel   many rows: a CTA takes whole rows, one after another;
-//     eight warps read, a ninth finishes the row before while they are in the
+//     eight warps read, a ninth (and tenth) finishes the row before while they are in the
 //     next one, so neither the joins nor the alternatives stop the loads.
 // logprob_split_kernel  few rows: a row is spread over a cluster of up to 8
 //     CTAs, all warps finish it together, and the parts are joined through
@@ -487,6 +487,97 @@ __device__ __forceinline__ Key gather_top(const Part<T> &r, int who, int npicked
     return merge_desc(list, warp_sort_desc(rest, lane), lane);
 }
 
+// What a warp keeps of the shares it looks through: vectors with an element
+// that may reach the bound, and the elements that do.
+struct Finds {
+    static constexpr int VECS = 64, KEYS = 96;
+    uint4 raw[VECS];
+    int at[VECS];
+    Key key[KEYS];
+};
+
+// gather_top for a warp by itself where no more than that reaches the bound (else
+// false): a key's place is how many precede it.
+template <int THREADS, typename T>
+__device__ __forceinline__ bool gather_few(const Part<T> &r, int who, int npicked, Key bound, Finds &f, int lane, Key &top)
+{
+    constexpr int E = Vec<T>::E, AHEAD = 5;
+    const int share = (r.ve - r.vb + THREADS - 1) / THREADS, items = npicked * share;
+    const float least = bound == 1ull ? neg_inf() : key_value(bound);
+    const uint32_t before = (1u << lane) - 1u;
+    int vecs = 0, keys = 0;
+    for (int i0 = 0; i0 < items; i0 += AHEAD * 32) {
+        uint4 raw[AHEAD];
+        int at[AHEAD];
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+            const int i = i0 + a * 32 + lane, pick = min(i / share, 31);
+            const int v = r.vb + __shfl_sync(0xffffffffu, who, pick) + (i - pick * share) * THREADS;
+            at[a] = v * E - r.lead;
+            raw[a] = i < items && v < r.ve ? load_vec(r.x, r.V, r.lead, v) : empty_vec<T>();
+        }
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+            const float most = Vec<T>::largest(raw[a]);
+            const bool hit = most >= least && most > neg_inf();
+            const uint32_t all = __ballot_sync(0xffffffffu, hit);
+            const int n = vecs + __popc(all);
+            if (n > Finds::VECS)
+                return false;
+            if (hit) {
+                const int to = vecs + __popc(all & before);
+                f.raw[to] = raw[a];
+                f.at[to] = at[a];
+            }
+            vecs = n;
+        }
+    }
+    __syncwarp();
+    for (int g = 0; g < vecs; g += 32) {
+        const bool have = g + lane < vecs;
+        const uint4 raw = have ? f.raw[g + lane] : empty_vec<T>();
+        const int at = have ? f.at[g + lane] : 0;
+        float x[E];
+        Vec<T>::unpack(raw, x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const Key k = x[e] > neg_inf() ? order_key(x[e], at + e) : 0ull;
+            const bool in = k >= bound;
+            const uint32_t all = __ballot_sync(0xffffffffu, in);
+            const int n = keys + __popc(all);
+            if (n > Finds::KEYS)
+                return false;
+            if (in)
+                f.key[keys + __popc(all & before)] = k;
+            keys = n;
+        }
+    }
+    __syncwarp();
+    Key k[Finds::KEYS / 32];
+    int to[Finds::KEYS / 32];
+#pragma unroll
+    for (int q = 0; q < Finds::KEYS / 32; ++q) {
+        k[q] = q * 32 + lane < keys ? f.key[q * 32 + lane] : 0ull;
+        to[q] = 0;
+    }
+#pragma unroll 4
+    for (int i = 0; i < keys; ++i) {
+        const Key other = f.key[i];
+#pragma unroll
+        for (int q = 0; q < Finds::KEYS / 32; ++q)
+            to[q] += other > k[q];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < Finds::KEYS / 32; ++q)
+        if (k[q] != 0ull && to[q] < 32)
+            f.key[to[q]] = k[q];
+    __syncwarp();
+    top = lane < keys ? f.key[lane] : 0ull;
+    __syncwarp(); // the lists are written again for the next row
+    return true;
+}
+
 // The key that every element has to reach: the last element of the vector of
 // the k-th best thread (its vector may hold the value more than once), or any
 // element where fewer than k threads hold one.
@@ -629,18 +720,21 @@ template <bool TOP> struct Left {
 } // namespace
 
 // 8192 x 32000 bf16: 88 us, 6.0 TB/s, and 105 with the best element; issue slots
-// and the exponentials bound it. 4096 x 32000 f32: 80 us, 6.6 TB/s, HBM.
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(ROW_THREADS, ROW_CTAS) logprob_rows_kernel(LogprobParams p)
+// and the exponentials bound it. 4096 x 32000 f32: 80 us, 6.6 TB/s, HBM. FIN warps
+// finish rows in turn: with more than FEW alternatives that takes longer than
+// reading, and two are worth the registers they take from the others (the best
+// 20: 145 us, 179 with one; the best 5: 119 with one, 132 with two).
+template <typename T, bool TOP, int FIN>
+__global__ void __launch_bounds__(ROW_READERS + FIN * 32, ROW_CTAS) logprob_rows_kernel(LogprobParams p)
 {
     constexpr int PER = ROW_READERS / 32; // threads a lane of the last warp answers for
     __shared__ Left<TOP> left[2];
-    __shared__ Key held[TOP ? 64 : 1];
+    __shared__ Finds finds[TOP ? FIN : 1];
     begin_behind();
     const int tid = threadIdx.x, lane = tid & 31, step = gridDim.x;
     const float c = p.inv_t * LOG2E;
     if (blockIdx.x == 0)
-        open_status(p, tid, ROW_THREADS);
+        open_status(p, tid, ROW_READERS + FIN * 32);
     if (tid < ROW_READERS) {
         Reader<T, ROW_READERS> reader{p, tid};
         reader.enter(blockIdx.x, 0, 1);
@@ -660,7 +754,7 @@ __global__ void __launch_bounds__(ROW_THREADS, ROW_CTAS) logprob_rows_kernel(Log
             l.sums[tid] = make_float4(sums.m, st.m, st.s, st.u);
             if (TOP) {
                 Key best = best_vec >= 0 && sums.m > neg_inf() ? order_key(sums.m, best_vec) : 0ull;
-                if (p.top_k > FEW)
+                if (FIN == 2)
                     best = warp_sort_desc(best, tid & 31); // a warp's share of what would keep the last warp too long
                 l.best[tid] = best;
             }
@@ -668,7 +762,9 @@ __global__ void __launch_bounds__(ROW_THREADS, ROW_CTAS) logprob_rows_kernel(Log
         }
         return;
     }
-    for (int row = blockIdx.x, turn = 0; row < p.M; row += step, ++turn) {
+    const int fin = (tid - ROW_READERS) / 32;
+    Finds &found = finds[TOP ? fin : 0];
+    for (int row = blockIdx.x + fin * step, turn = fin; row < p.M; row += FIN * step, turn += FIN) {
         Left<TOP> &l = left[turn & 1];
         Part<T> r;
         r.x = static_cast<const T *>(p.logits) + (int64_t)row * p.stride;
@@ -692,7 +788,7 @@ __global__ void __launch_bounds__(ROW_THREADS, ROW_CTAS) logprob_rows_kernel(Log
             named_bar_arrive(BAR_FREE + (turn & 1), ROW_THREADS);
         Key top = 0ull;
         if (TOP) { // the k best threads, lane by lane
-            if (p.top_k <= FEW) {
+            if (FIN == 1) { // top_k <= FEW
                 for (int i = 0; i < p.top_k; ++i) {
                     Key mine = key[0];
 #pragma unroll
@@ -715,7 +811,9 @@ __global__ void __launch_bounds__(ROW_THREADS, ROW_CTAS) logprob_rows_kernel(Log
             const int npicked = __popc(__ballot_sync(0xffffffffu, best != 0ull));
             const Key bound = bound_of<T>(__shfl_sync(0xffffffffu, best, p.top_k - 1), r.lead);
             const int who = best != 0ull ? key_index(best) % ROW_READERS : 0;
-            top = gather_top<ROW_READERS>(r, who, npicked, 0, 32, bound, p.top_k, held, lane);
+            // for a few the one pass is shorter; else only where a share holds much of the best
+            if (FIN == 1 || !gather_few<ROW_READERS>(r, who, npicked, bound, found, lane, top))
+                top = gather_top<ROW_READERS>(r, who, npicked, 0, 32, bound, p.top_k, found.key, lane);
         }
         float m = q[0].x;
 #pragma unroll
@@ -988,7 +1086,10 @@ template <typename T> cudaError_t launch_lp(const LogprobParams &p, int num_sms,
         parts *= 2;
     if (parts == 1) { // as many CTAs as stay resident, each with rows one after another
         const dim3 grid((unsigned)(p.M < ROW_CTAS * num_sms ? p.M : ROW_CTAS * num_sms));
-        return launch_behind(p.top_k > 0 ? logprob_rows_kernel<T, true> : logprob_rows_kernel<T, false>, grid, ROW_THREADS, 0, 1, st, p);
+        return launch_behind(p.top_k > FEW  ? logprob_rows_kernel<T, true, 2>
+                             : p.top_k > 0 ? logprob_rows_kernel<T, true, 1>
+                                           : logprob_rows_kernel<T, false, 1>,
+                             grid, p.top_k > FEW ? ROW_THREADS + 32 : ROW_THREADS, 0, 1, st, p);
     }
     return launch_behind(p.top_k > 0 ? logprob_split_kernel<T, true> : logprob_split_kernel<T, false>, dim3((unsigned)(p.M * parts)),
                          LP_THREADS, 0, (unsigned)parts, st, p, parts);

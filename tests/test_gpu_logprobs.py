@@ -295,3 +295,26 @@ def test_gradient_against_differences_of_the_forward_kernel():
     val = (g[0] * f["logprob"].double() + h[0] * f["entropy"].double()).cpu().numpy()
     diff = (val[0::2] - val[1::2]) / (2 * step)
     assert np.abs(diff - d).max() < 0.012
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("k", [9, 20, 32])
+def test_many_rows_whose_best_lie_together(dtype, k):
+    """Whole rows by one CTA: the best in one thread's share, in a run, all equal, few distinct values, rising, masked but for
+    fewer than k, one value apart; a CTA takes more than one row."""
+    M, V = 700, 2500
+    rng = np.random.default_rng(k)
+    x = rng.standard_normal((M, V)).astype(np.float32)
+    e = 16 // (2 if dtype == torch.bfloat16 else 4) * 8  # a vector of every eighth
+    x[0::9] = 1.5
+    x[1::9] = rng.integers(0, 3, x[1::9].shape)
+    x[2::9] = np.arange(V) / 64
+    x[3::9] = -np.arange(V) / 64
+    x[4::9, 100:160] += 20
+    x[5::9, ::e] += 20
+    x[6::9, 5:] = -INF
+    x[7::9] = np.finfo(np.float32).min if dtype == torch.float32 else -3.3895313892515355e38
+    x[7::9, -1] = 0.0
+    t = place(torch.tensor(x), dtype, 1, 3)
+    tokens = rng.integers(-1, V, M).astype(np.int32)
+    check(forward(t, torch.tensor(tokens).cuda(), 1.0, k), define(t, tokens, 1.0, k), V)
