@@ -573,7 +573,7 @@ lora_status lora_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int
 
 /* Path of lora_mx4_proj_apply_ex (lora_mx4_proj_apply uses LORA_MX4_PATH_AUTO). */
 enum {
-    LORA_MX4_PATH_AUTO = 0,  /* LORA_MX4_PATH_ROWS where it is possible */
+    LORA_MX4_PATH_AUTO = 0,  /* the faster of the two as measured: by M and N */
     LORA_MX4_PATH_ROWS = 1,  /* up to 4 rows and n_in 8192: codes widened into the tensor cores' registers (other
                                 calls take LORA_MX4_PATH_TILES) */
     LORA_MX4_PATH_TILES = 2  /* codes widened into the shared-memory operand tiles of tcgen05 */

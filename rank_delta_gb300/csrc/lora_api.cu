@@ -1435,21 +1435,21 @@ lora_status check_mx4(const char *who, const void *w, int dtype, int64_t w_strid
     return LORA_OK;
 }
 
-// The path a call takes: the rows kernel where it can. What it and tiles take
-// in us, every row of an adapter of its own of rank 64 (K = 1024: 16):
+// The path a call takes by itself. The rows kernel and tiles in us, every row of
+// an adapter of its own of rank 64 (K = 1024: 16):
 //   K x N         1 row        2 rows       4 rows
-//   1024 x  4096   6.4   8.0    6.3   8.1    6.4   8.1
-//   4096 x  4096   8.7  11.4    9.1  11.6   10.1  11.7
-//   4096 x 14336  17.3  24.1   18.9  25.1   22.6  26.5
-//   4096 x 32000  31.8  47.2   35.6  48.0   41.5  50.1
-//   8192 x  4096  12.4  15.6   12.5  15.7   13.0  16.0
-// (For up to eight rows, with twice the room for x, it took 39.9 us for
-// 8 x 4096 x 14336 and tiles 28.5.)
-int mx4_path(int M, int K, int R, int path)
+//   1024 x  4096   6.3   7.2    6.4   7.4    6.3   7.7
+//   4096 x  4096   8.4   9.5    8.9   9.7    9.9   9.8
+//   8192 x  4096  12.1  12.6   12.2  12.8   12.6  12.9
+//   4096 x 14336  15.8  18.5   17.8  19.4   21.8  20.2
+//   4096 x 32000  30.8  36.1   34.1  36.4   40.6  37.5
+// The rows kernel multiplies each row by its B on the CUDA cores: three and four
+// rows of many features are for tiles.
+int mx4_path(int M, int K, int N, int R, int path)
 {
     if (path == LORA_MX4_PATH_TILES || !mx4_rows_fit(M, K, R))
         return LORA_MX4_PATH_TILES;
-    return LORA_MX4_PATH_ROWS;
+    return path == LORA_MX4_PATH_ROWS || M <= 2 || N <= 4096 ? LORA_MX4_PATH_ROWS : LORA_MX4_PATH_TILES;
 }
 
 } // namespace
@@ -1573,7 +1573,7 @@ lora_status lora_mx4_proj_apply_ex(const void *x, int64_t x_stride, const uint8_
     q.y_stride = y_stride;
     if ((e = launch_mx4_shrink(q, di.num_sms, st)) != cudaSuccess)
         return cuda_fail(e, who);
-    if (mx4_path(M, K, q.R, path) == LORA_MX4_PATH_TILES) {
+    if (mx4_path(M, K, N, q.R, path) == LORA_MX4_PATH_TILES) {
         const Mx4TcPlan plan = plan_mx4_tc(q, di.num_sms);
         Mx4TcMaps maps;
         memset(&maps, 0, sizeof maps);

@@ -733,11 +733,27 @@ __device__ __forceinline__ uint4 lds_16(uint32_t addr)
     return v;
 }
 
+// mx4_unpack8 with the pairs (0, 4), (1, 5), (2, 6), (3, 7): codes four apart lie
+// in the two halves of a word as they are, so none are moved.
+__device__ __forceinline__ void unpack8_apart(uint32_t w, uint32_t (&o)[4])
+{
+    const uint32_t v = w >> 8;
+    o[0] = ((w & 0x000F000Fu) * 0x1040u) & 0x81C081C0u;
+    o[1] = ((w & 0x00F000F0u) * 0x0104u) & 0x81C081C0u;
+    o[2] = ((v & 0x000F000Fu) * 0x1040u) & 0x81C081C0u;
+    o[3] = ((v & 0x00F000F0u) * 0x0104u) & 0x81C081C0u;
+}
+// Eight values of x in the same pairs.
+__device__ __forceinline__ uint4 pairs_apart(uint4 v)
+{
+    return make_uint4(prmt<0x5410>(v.x, v.z), prmt<0x7632>(v.x, v.z), prmt<0x5410>(v.y, v.w), prmt<0x7632>(v.y, v.w));
+}
+
 // Eight codes of two weight rows -> bf16 pairs, times their blocks' scales.
 __device__ __forceinline__ void widen_pair(uint32_t a, uint32_t b, uint32_t fa, uint32_t fb, uint32_t (&u)[4], uint32_t (&v)[4])
 {
-    mx4_unpack8(a, u);
-    mx4_unpack8(b, v);
+    unpack8_apart(a, u);
+    unpack8_apart(b, v);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         u[q] = mul_bf16x2(u[q], fa);
@@ -757,7 +773,7 @@ __device__ __forceinline__ void widen_pair(uint32_t a, uint32_t b, uint32_t fa, 
 // the row and the block so that the eight lanes of a load phase meet different
 // bank groups. Which k a fragment's slots mean is free as long as
 // both operands agree: thread t of four supplies the block t of 128 k.
-// What bounds it is the widening, 19 instructions for 8 codes: 1x4096x32000 takes
+// What bounds it is the widening, 17 instructions for 8 codes: 1x4096x32000 takes
 // 31 us (2.2 TB/s of codes), 1x4096x4096 8.5 with its shrink.
 __global__ void __launch_bounds__(RW_THREADS, 1)
     mx4_rows_kernel(const __grid_constant__ CUtensorMap codes, const __grid_constant__ Mx4ProjParams p, RowsShape shape)
@@ -834,7 +850,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
             const int row = i / (shape.boxes * 32), piece = i - row * (shape.boxes * 32), block = piece >> 2;
             const bool have = row < p.M && piece * 8 < p.K;
             const int turn = (block >> 1 & 1) | (row & 1) << 1;
-            const uint4 v = have ? ld_nc_16(p.x + (int64_t)row * p.x_stride + piece * 8) : make_uint4(0, 0, 0, 0);
+            const uint4 v = pairs_apart(have ? ld_nc_16(p.x + (int64_t)row * p.x_stride + piece * 8) : make_uint4(0, 0, 0, 0));
             asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(xs + (uint32_t)row * xrow + (uint32_t)block * 64u +
                                                                          (uint32_t)((piece & 3) ^ turn) * 16u),
                          "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
