@@ -576,7 +576,7 @@ enum {
     LORA_MX4_PATH_AUTO = 0,  /* the faster of the two as measured: by M and N */
     LORA_MX4_PATH_ROWS = 1,  /* up to 4 rows and n_in 8192: codes widened into the tensor cores' registers (other
                                 calls take LORA_MX4_PATH_TILES) */
-    LORA_MX4_PATH_TILES = 2  /* codes widened into the shared-memory operand tiles of tcgen05 */
+    LORA_MX4_PATH_TILES = 2  /* codes widened into operand tiles of tcgen05 in tensor memory */
 };
 
 /* Workspace of lora_mx4_proj_apply for M rows on route `rt`: the status word
