@@ -774,7 +774,7 @@ __device__ __forceinline__ void widen_pair(uint32_t a, uint32_t b, uint32_t fa, 
 // bank groups. Which k a fragment's slots mean is free as long as
 // both operands agree: thread t of four supplies the block t of 128 k.
 // What bounds it is the widening, 17 instructions for 8 codes: 1x4096x32000 takes
-// 31 us (2.2 TB/s of codes), 1x4096x4096 8.5 with its shrink.
+// 30 us (2.3 TB/s of codes), 1x4096x4096 8.1 with its shrink.
 __global__ void __launch_bounds__(RW_THREADS, 1)
     mx4_rows_kernel(const __grid_constant__ CUtensorMap codes, const __grid_constant__ Mx4ProjParams p, RowsShape shape)
 {
@@ -991,16 +991,17 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
             named_bar_sync(RW_H, RW_FINISH * 32);
             wait_or_note(&part_full[buf], (uint32_t)(s / RW_BUFS) & 1u, &bad);
             const float *from = part + (size_t)buf * RW_WARPS * RW_PART;
-            for (int o = ft; o < outs; o += RW_FINISH * 32) {
-                const int row = o >> wide, f = o & (width - 1);
+            for (int i = ft; i < 2 * outs; i += RW_FINISH * 32) { // two threads an output
+                const int o = i >> 1, row = o >> wide, f = o & (width - 1);
                 const float *q = from + (size_t)((f >> 4) * T) * RW_PART + (f & 15) * RW_ROWS + row;
-                float v = q[0];
-#pragma unroll 4
-                for (int w = 1; w < sums; ++w)
+                float v = 0.0f;
+#pragma unroll 8
+                for (int w = i & 1; w < sums; w += 2)
                     v += q[w * RW_PART];
+                v += __shfl_xor_sync(0xffffffffu, v, 1);
                 if (brow[row] != nullptr) // else the base product to the bit
                     v += delta[o];
-                if (f0 + f < p.N)
+                if ((i & 1) == 0 && f0 + f < p.N)
                     p.y[(int64_t)row * p.y_stride + f0 + f] = f32_to_bf16_bits(v);
             }
             __syncwarp();
