@@ -328,7 +328,7 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
 
 constexpr int SH_WARPS = 16;     // they share K
 constexpr int SH_THREADS = SH_WARPS * 32;
-constexpr int SH_ROWS = 64;      // rows a CTA looks through for its slot
+constexpr int SH_ROWS = 64;      // a CTA takes, of the 64 or 256 rows of a chunk
 constexpr int SH_PAIR = 16;      // rows whose sums are joined at a time
 
 // The call's status, by one CTA.
@@ -423,40 +423,45 @@ __device__ __forceinline__ void shrink_tile(const Mx4ProjParams &p, const uint16
 } // namespace
 
 // Grid: 16-rank groups, by slots (or, where there are more of them than rows in a
-// chunk, the u-th distinct slot of the chunk), by 64-row chunks. Each thread multiplies 8
+// chunk, the u-th distinct slot of the chunk), by chunks of CHUNK rows and `takes` CTAs
+// for 64 rows of the slot each. Each thread multiplies 8
 // consecutive k of two rank rows and of the slot's rows at a time: which k a
 // fragment's slots mean is free as long as both operands agree.
-__global__ void __launch_bounds__(SH_THREADS) mx4_shrink_kernel(Mx4ProjParams p)
+template <int CHUNK> __global__ void __launch_bounds__(SH_THREADS) mx4_shrink_kernel(Mx4ProjParams p, int takes)
 {
     __shared__ uint32_t present[MAX_BUCKETS / 32];
     __shared__ int slot_s, rows_s[SH_ROWS];
     __shared__ float red[SH_WARPS][16][SH_PAIR + 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    const int r0 = blockIdx.x * 16, u = blockIdx.y, c0 = blockIdx.z * SH_ROWS;
+    const int r0 = blockIdx.x * 16, u = blockIdx.y, c0 = (int)blockIdx.z / takes * CHUNK, from = (int)blockIdx.z % takes * SH_ROWS;
     // Launched early behind whatever the stream ran before; nothing is read
     // until that is complete, and only then may the projection kernel start.
     begin_behind();
-    const int mine = tid < SH_ROWS && c0 + tid < p.M ? p.seq_slot[c0 + tid] : -1;
-    if (blockIdx.x == 0 && u == 0 && c0 == 0)
+    const int mine = tid < CHUNK && c0 + tid < p.M ? p.seq_slot[c0 + tid] : -1;
+    if (blockIdx.x == 0 && u == 0 && blockIdx.z == 0)
         open_status(p, tid);
     SlotInfo si;
-    const int slot = shrink_slot<SH_ROWS>(p, u, mine, tid, present, slot_s, si);
-    if (slot < 0)
+    const int slot = shrink_slot<CHUNK>(p, u, mine, tid, present, slot_s, si);
+    if (slot < 0 || !si.on || r0 >= si.rank)
         return;
-    if (!si.on || r0 >= si.rank)
-        return;
-    if (tid < SH_ROWS) { // the slot's rows, in order
-        const uint32_t m = __ballot_sync(0xffffffffu, mine == slot);
-        if (lane == 0)
-            present[warp] = m;
+    const uint32_t match = __ballot_sync(0xffffffffu, mine == slot);
+    __syncthreads(); // slot_s and the distinct slots have been read
+    if (lane == 0 && warp < CHUNK / 32)
+        present[warp] = match;
+    __syncthreads();
+    int before = 0, total = 0; // the slot's rows of the chunk, in order
+#pragma unroll
+    for (int w = 0; w < CHUNK / 32; ++w) {
+        const int n = __popc(present[w]);
+        before += w < warp ? n : 0;
+        total += n;
     }
-    __syncthreads();
-    if (tid < SH_ROWS && mine == slot)
-        rows_s[(warp == 1 ? __popc(present[0]) : 0) + __popc(present[warp] & ((1u << lane) - 1u))] = c0 + tid;
-    const int count = __popc(present[0]) + __popc(present[1]);
-    __syncthreads();
-    if (count == 0)
+    const int count = min(total - from, SH_ROWS), at = before + __popc(match & ((1u << lane) - 1u)) - from;
+    if (count <= 0)
         return;
+    if (mine == slot && at >= 0 && at < SH_ROWS)
+        rows_s[at] = c0 + tid;
+    __syncthreads();
     const int nb = p.K / 32;
     const int b0 = (int)((int64_t)nb * warp / SH_WARPS), b1 = (int)((int64_t)nb * (warp + 1) / SH_WARPS); // this warp's blocks of 32 k
     // rank rows past the rank read the last one; what comes of them is dropped
@@ -683,11 +688,18 @@ cudaError_t launch_mx4_shrink(const Mx4ProjParams &p, int num_sms, cudaStream_t 
         return launch_behind(mx4_shrink_many_kernel, dim3((unsigned)groups, (unsigned)each, (unsigned)chunks), SH_THREADS, SM_BYTES, 1,
                              st, p);
     }
-    const int distinct = p.M < SH_ROWS ? p.M : SH_ROWS; // slots in a chunk, at most
-    return launch_behind(mx4_shrink_kernel,
-                         dim3((unsigned)((p.R + 15) / 16), (unsigned)(p.L < distinct ? p.L : distinct),
-                              (unsigned)((p.M + SH_ROWS - 1) / SH_ROWS)),
-                         SH_THREADS, 0, 1, st, p);
+    // A CTA takes all registers of its SM, and the projection's have to wait for it: the
+    // fewer have work the better. Chunks of 64 and of 256 rows, 16 adapters of rank 64 at
+    // N = 4096, then 32 of rank 64 and 32 of rank 16 at N = 6144:
+    //   128 rows   17.5  17.3   27.4  25.9   20.4  19.7 us
+    //   256 rows   22.7  21.1   36.0  33.4   25.7  25.9
+    //   512 rows   33.0  29.7   51.5  46.2   34.4  32.3
+    const int chunk = p.M > SH_ROWS ? 256 : SH_ROWS;
+    const int takes = std::min((p.M + SH_ROWS - 1) / SH_ROWS, chunk / SH_ROWS);
+    return launch_behind(chunk == 256 ? mx4_shrink_kernel<256> : mx4_shrink_kernel<SH_ROWS>,
+                         dim3((unsigned)((p.R + 15) / 16), (unsigned)std::min(p.L, std::min(p.M, chunk)),
+                              (unsigned)((p.M + chunk - 1) / chunk * takes)),
+                         SH_THREADS, 0, 1, st, p, takes);
 }
 
 // -------------------------------------------------------------------- rows
