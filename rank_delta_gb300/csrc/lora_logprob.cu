@@ -19,10 +19,10 @@
 // into 64 bits, which orders them totally; -0 equals +0. What reaches the
 // bound, k elements and a few, is then put in order.
 //
-// logprob_rows_kernel   many rows: a CTA takes whole rows, one after another;
+// logprob_rows_kernel   many rows or short ones: a CTA takes whole rows, one after another;
 //     eight warps read, a ninth (and tenth) finishes the row before while they are in the
 //     next one, so neither the joins nor the alternatives stop the loads.
-// logprob_split_kernel  few rows: a row is spread over a cluster of up to 8
+// logprob_split_kernel  few long rows: a row is spread over a cluster of up to 8
 //     CTAs, all warps finish it together, and the parts are joined through
 //     distributed shared memory. Nothing depends on timing in either.
 #include <cooperative_groups.h>
@@ -851,8 +851,8 @@ template <bool TOP> struct SplitShared {
 
 } // namespace
 
-// Latency bounds it. 1 x 32000 bf16: 4 us, 8 with the best 20; 64 x 32003 f32 with
-// the best 5: 9.7 us.
+// Latency bounds it. 1 x 32000 bf16: 3.5 us, 8 with the best 20; 64 x 32003 f32 with
+// the best 20: 8.5 us.
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(LP_THREADS, 4) logprob_split_kernel(LogprobParams p, int parts)
 {
@@ -1079,10 +1079,20 @@ __global__ void __launch_bounds__(LP_THREADS, 6) logprob_grad_kernel(LogprobGrad
 
 template <typename T> cudaError_t launch_lp(const LogprobParams &p, int num_sms, cudaStream_t st)
 {
-    // parts of a row: enough CTAs for two a SM, each part at least one vector a thread
-    const int nvec = (int)(((int64_t)p.V + Vec<T>::E - 1) / Vec<T>::E);
+    // Parts of a row, each at least one vector a thread: none of a row that a CTA is
+    // through with before a cluster has met, else enough CTAs for one an SM, and for
+    // two where a part is longer than `longest`. us for the best 0, 5 and 20 with two for
+    // all, one for all, and this:
+    //    90 x   8000 bf16   3.9  8.1  8.6   3.9  8.1  8.6   2.7  5.1  6.4
+    //    64 x  32000 f32    4.2  9.6 10.2   4.1  8.0  8.4   4.0  7.1  8.5
+    //   200 x  32000 f32    7.6 12.0 13.4   7.5 10.1 15.3   7.6 10.1 13.4
+    //    90 x 131072 f32   10.9 15.6 17.8  14.2 18.8 21.1  10.8 15.7 17.9
+    const bool few = p.top_k > 0 && p.top_k <= FEW;
+    const int64_t shortest = few ? 140 << 10 : 40 << 10, longest = p.top_k > FEW ? 112 << 10 : 224 << 10;
+    const int64_t nvec = ((int64_t)p.V + Vec<T>::E - 1) / Vec<T>::E;
     int parts = 1;
-    while (parts < 8 && (int64_t)p.M * parts < 2 * num_sms && nvec >= 2 * parts * LP_THREADS)
+    while (parts < 8 && nvec * 16 > shortest && nvec >= 2 * parts * LP_THREADS &&
+           ((int64_t)p.M * parts < num_sms || ((int64_t)p.M * parts < 2 * num_sms && nvec * 16 / parts > longest)))
         parts *= 2;
     if (parts == 1) { // as many CTAs as stay resident, each with rows one after another
         const dim3 grid((unsigned)(p.M < ROW_CTAS * num_sms ? p.M : ROW_CTAS * num_sms));
