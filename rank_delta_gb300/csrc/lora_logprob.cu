@@ -2,7 +2,8 @@
 // alternatives of rows of logits, and the gradient of the first two.
 //
 // With z_v = x_v t (t = inv_temperature), m = max x, d_v = (x_v - m) t:
-//   S = sum e^{d_v},  log p_v = d_v - log S,  H = log S - (sum e^{d_v} d_v) / S,
+//   S = sum e^{d_v},  log p_v = d_v - log S,  H = log S - (sum e^{d_v} d_v) / S
+// (S is carried as 1 + the rest, the 1 one element that is the maximum),
 //   dx_v = t [ g (1[v = token] - p_v) - g_H p_v (log p_v + H) ].
 //
 // A row is read once: every thread keeps its maximum, and S and sum e^d d
@@ -42,7 +43,7 @@ constexpr int LP_THREADS = 256;     // gradient, and rows spread over a cluster
 constexpr int LP_WARPS = LP_THREADS / 32;
 // Whole rows: reading threads of a CTA (one warp more finishes), CTAs resident
 // a SM and 16-byte vectors of a thread in flight. 256 x 3 x 4 reads 8192 rows
-// of 32000 bf16 in 88 us; 128 x 6 took 68 % longer, 192 x 4 9, 384 x 2 16, 512 x
+// of 32000 bf16 in 91 us; 128 x 6 took 68 % longer, 192 x 4 9, 384 x 2 16, 512 x
 // 2 65 (small groups scatter the reads, large ones leave a row two steps).
 constexpr int ROW_READERS = 256;
 constexpr int ROW_THREADS = ROW_READERS + 32;
@@ -249,13 +250,20 @@ __device__ __forceinline__ float warp_max_nan(float v)
     return v;
 }
 
-// The lanes' parts as one whose maximum is that of the lanes' m.
-__device__ __forceinline__ Stat warp_join(Stat st, float m, float c)
+// The lanes' parts as one, where a part's s leaves out one element that is its maximum (1
+// itself): in a row that one element dominates, the sum of the others keeps its
+// digits, log S is log1p of it, and the entropy, which is as small, is as good.
+__device__ __forceinline__ Stat warp_join_rest(Stat st, float c)
 {
-    rescale(st, warp_max_nan(m), c);
-    st.s = warp_sum(st.s);
-    st.u = warp_sum(st.u);
-    return st;
+    const float top = warp_max_nan(st.m);
+    const int holder = __ffs(__ballot_sync(0xffffffffu, st.m == top)) - 1;
+    if (st.m == neg_inf()) // no elements
+        st.s = st.u = 0.0f;
+    else if ((int)(threadIdx.x & 31) != holder) {
+        st.s += 1.0f;
+        rescale(st, top, c);
+    }
+    return Stat{top, warp_sum(st.s), warp_sum(st.u)};
 }
 
 // What a thread has summed of its elements, relative to a reference `at` that
@@ -420,6 +428,42 @@ template <typename T> struct Part {
     const T *x;
     int V, lead, vb, ve;
 };
+
+// The first vector that a lane takes of thread `who`'s share, for share_rest.
+template <int THREADS, typename T> __device__ __forceinline__ uint4 share_first(const Part<T> &r, int who, int lane)
+{
+    const int v = r.vb + who + lane * THREADS;
+    return v < r.ve ? load_vec(r.x, r.V, r.lead, v) : empty_vec<T>();
+}
+// What thread `who` of THREADS sums of its share, but relative to `top`, which is its
+// maximum, and with one element that is it left out; over the lanes. (This, instead
+// of taking 1 from the sum, costs 8192 rows of 32000 bf16 3 us, and keeps log S and the
+// entropy of a row of entropy 0.001 within 6e-7 of themselves instead of 6e-5.)
+template <int THREADS, typename T>
+__device__ __forceinline__ Stat share_rest(const Part<T> &r, int who, uint4 raw, float top, float c, int lane)
+{
+    constexpr int E = Vec<T>::E;
+    Stat st{top, 0.0f, 0.0f};
+    int equal = 0;
+    for (int v = r.vb + who + lane * THREADS; v < r.ve;) {
+        float f[E];
+        Vec<T>::unpack(raw, f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const bool is = f[e] == top;
+            const float d = is ? -1000.0f : max_nan((f[e] - top) * c, -1000.0f), w = exp2_fast(d);
+            equal += is;
+            st.s += w;
+            st.u = fmaf(w, d, st.u);
+        }
+        v += 32 * THREADS;
+        if (v < r.ve)
+            raw = load_vec(r.x, r.V, r.lead, v);
+    }
+    const int first = __ffs(__ballot_sync(0xffffffffu, equal > 0)) - 1;
+    st.s += (float)(equal - (lane == first));
+    return st;
+}
 
 // The elements that reach `bound` in the shares of `npicked` of THREADS
 // threads, the k best in descending order (of those this warp takes: vectors
@@ -672,7 +716,8 @@ __device__ __forceinline__ void write_row(const LogprobParams &p, int row, int t
                                           Key top, int lane)
 {
     const bool empty = st.m == neg_inf();
-    const float logsum = empty ? 0.0f : logf(st.s); // NaN when the row holds a NaN or +infinity
+    // NaN when the row holds one, in the sums if not in the maximum, or +infinity
+    const float logsum = empty ? 0.0f : st.m < -neg_inf() ? log1pf(st.s) : quiet_nan();
     const bool none = !(logsum == logsum);
     if (lane == 0) {
         if (p.stats != nullptr) {
@@ -680,7 +725,7 @@ __device__ __forceinline__ void write_row(const LogprobParams &p, int row, int t
             p.stats[2 * (int64_t)row + 1] = logsum;
         }
         if (p.entropy != nullptr)
-            p.entropy[row] = empty ? 0.0f : logsum - LN2 * (st.u / st.s);
+            p.entropy[row] = empty ? 0.0f : logsum - LN2 * (st.u / (1.0f + st.s));
         if (p.logprob != nullptr) {
             float lp = 0.0f;
             if (token >= 0 && token < p.V)
@@ -719,11 +764,11 @@ template <bool TOP> struct Left {
 
 } // namespace
 
-// 8192 x 32000 bf16: 88 us, 6.0 TB/s, and 105 with the best element; issue slots
+// 8192 x 32000 bf16: 91 us, 5.7 TB/s, and 109 with the best element; issue slots
 // and the exponentials bound it. 4096 x 32000 f32: 80 us, 6.6 TB/s, HBM. FIN warps
 // finish rows in turn: with more than FEW alternatives that takes longer than
 // reading, and two are worth the registers they take from the others (the best
-// 20: 145 us, 179 with one; the best 5: 119 with one, 132 with two).
+// 20: 151 us, some 35 more with one; the best 5: 128, some 13 more with two).
 template <typename T, bool TOP, int FIN>
 __global__ void __launch_bounds__(ROW_READERS + FIN * 32, ROW_CTAS) logprob_rows_kernel(LogprobParams p)
 {
@@ -786,6 +831,18 @@ __global__ void __launch_bounds__(ROW_READERS + FIN * 32, ROW_CTAS) logprob_rows
         }
         if (row + 2 * (int64_t)step < p.M)
             named_bar_arrive(BAR_FREE + (turn & 1), ROW_THREADS);
+        float m = q[0].x;
+#pragma unroll
+        for (int i = 1; i < PER; ++i)
+            m = max_nan(m, q[i].x);
+        m = warp_max_nan(m);
+        int holder = 0; // the thread whose maximum it is
+#pragma unroll
+        for (int i = PER - 1; i >= 0; --i) {
+            const uint32_t is = __ballot_sync(0xffffffffu, q[i].x == m);
+            holder = is != 0u ? i * 32 + __ffs(is) - 1 : holder;
+        }
+        const uint4 raw = share_first<ROW_READERS>(r, holder, lane);
         Key top = 0ull;
         if (TOP) { // the k best threads, lane by lane
             if (FIN == 1) { // top_k <= FEW
@@ -815,18 +872,15 @@ __global__ void __launch_bounds__(ROW_READERS + FIN * 32, ROW_CTAS) logprob_rows
             if (FIN == 1 || !gather_few<ROW_READERS>(r, who, npicked, bound, found, lane, top))
                 top = gather_top<ROW_READERS>(r, who, npicked, 0, 32, bound, p.top_k, found.key, lane);
         }
-        float m = q[0].x;
-#pragma unroll
-        for (int i = 1; i < PER; ++i)
-            m = max_nan(m, q[i].x);
-        m = warp_max_nan(m);
-        Stat st{m, 0.0f, 0.0f};
+        Stat st = share_rest<ROW_READERS>(r, holder, raw, m, c, lane);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             Stat one{q[i].y, q[i].z, q[i].w};
             rescale(one, m, c);
-            st.s += one.s;
-            st.u += one.u;
+            if (i * 32 + lane != holder) {
+                st.s += one.s;
+                st.u += one.u;
+            }
         }
         st.s = warp_sum(st.s);
         st.u = warp_sum(st.u);
@@ -851,8 +905,8 @@ template <bool TOP> struct SplitShared {
 
 } // namespace
 
-// Latency bounds it. 1 x 32000 bf16: 3.5 us, 8 with the best 20; 64 x 32003 f32 with
-// the best 20: 8.5 us.
+// Latency bounds it. 1 x 32000 bf16: 4 us, 8.7 with the best 20; 64 x 32003 f32 with
+// the best 20: 9 us.
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(LP_THREADS, 4) logprob_split_kernel(LogprobParams p, int parts)
 {
@@ -882,13 +936,22 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprob_split_kernel(LogprobPar
     sums.scale(c);
     sums.clear();
     reader.template read<TOP>(sums, best_vec, [] {});
-    const Stat ws = warp_join(sums.stat(), sums.m, c);
-    if (lane == 0)
-        sm.warp[warp] = ws;
+    Stat ws{warp_max_nan(sums.m), 0.0f, 0.0f};
+    const int holder = max(__ffs(__ballot_sync(0xffffffffu, sums.m == ws.m)) - 1, 0);
+    const uint4 raw = share_first<LP_THREADS>(r, warp * 32 + holder, lane);
     Key best = 0ull;
     if (TOP) {
         best = warp_top(best_vec >= 0 && sums.m > neg_inf() ? order_key(sums.m, best_vec) : 0ull, p.top_k, lane);
         sm.lists[warp][lane] = best;
+    }
+    {
+        Stat one = sums.stat();
+        rescale(one, ws.m, c);
+        const Stat rest = share_rest<LP_THREADS>(r, warp * 32 + holder, raw, ws.m, c, lane);
+        ws.s = warp_sum(rest.s + (lane != holder ? one.s : 0.0f));
+        ws.u = warp_sum(rest.u + (lane != holder ? one.u : 0.0f));
+        if (lane == 0)
+            sm.warp[warp] = ws;
     }
     __syncthreads();
     if (TOP) {
@@ -948,7 +1011,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprob_split_kernel(LogprobPar
     if (warp == 0) {
         if (lane < LP_WARPS)
             st = sm.warp[lane];
-        st = warp_join(st, st.m, c);
+        st = warp_join_rest(st, c);
         if (lane == 0)
             sm.cta = st;
     }
@@ -958,7 +1021,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprob_split_kernel(LogprobPar
     if (part == 0) {
         if (warp == 0) {
             st = lane < parts ? cl.map_shared_rank(&sm, lane)->cta : Stat{neg_inf(), 0.0f, 0.0f};
-            st = warp_join(st, st.m, c);
+            st = warp_join_rest(st, c);
         }
         if (TOP) {
             const Key k = warp < parts && lane < p.top_k ? cl.map_shared_rank(&sm, warp)->fin[lane] : 0ull;

@@ -318,3 +318,29 @@ def test_many_rows_whose_best_lie_together(dtype, k):
     t = place(torch.tensor(x), dtype, 1, 3)
     tokens = rng.integers(-1, V, M).astype(np.int32)
     check(forward(t, torch.tensor(tokens).cuda(), 1.0, k), define(t, tokens, 1.0, k), V)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,V", [(4, 32000), (400, 6000), (3, 131072)])
+def test_rows_that_one_element_dominates(dtype, M, V):
+    """Log S and the entropy relative to themselves, down to some 1e-4: 1 is left out of S before it is summed, so the
+    tolerance of the sums of the others holds for them."""
+    gen = torch.Generator().manual_seed(V)
+    x = torch.randn(M, V, generator=gen)
+    at = torch.randint(V, (M,), generator=gen)
+    x[torch.arange(M), at] = 14 + 12 * torch.rand(M, generator=gen)
+    x[::3, 5] = x[::3].amax(1) - 9  # a second one, far above the rest, 1e-4 of it
+    t = place(x, dtype, 0, 0)
+    tokens = at.to(torch.int32).cuda()
+    got, want = forward(t, tokens, 1.0, 1), define(t, at.numpy(), 1.0, 1)
+    for name, w in (("stats", want["stats"][:, 1]), ("entropy", want["entropy"]), ("logprob", want["logprob"])):
+        g = got[name].double().cpu().numpy()
+        g = g[:, 1] if name == "stats" else g
+        if name == "stats":  # the sums of the others in 64 bits: log1p keeps what log of the whole loses
+            d = t.double().cpu().numpy()
+            d = np.exp(d - d.max(1, keepdims=True))
+            d[np.arange(M), d.argmax(1)] = 0.0
+            w = np.log1p(d.sum(1))
+        elif name == "logprob":
+            w = -np.log1p(d.sum(1))
+        assert (np.abs(g - w) <= LOG_TOL * np.abs(w)).all(), (name, g[:4], w[:4])
