@@ -640,6 +640,14 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
                 }
             }
             named_bar_sync(1u + (uint32_t)group, 128);
+            if (!vec) { // a feature a thread: a warp's stores lie in one piece
+                const int f = tid & 127;
+                if (f0 + f < p.N)
+                    for (int c = group; c < tn / 16; c += GROUPS)
+#pragma unroll 8
+                        for (int tok = c * 16; tok < min(c * 16 + 16, rows); ++tok)
+                            p.y[(int64_t)(t0 + tok) * p.y_stride + f0 + f] = (uint16_t)lds_2(base + (uint32_t)tok * Y_ROW + (uint32_t)f * 2);
+            } else
             for (int i = tid & 127; i < tn / GROUPS * 16 + 256; i += 128) {
                 const int tok = ((i >> 8) * GROUPS + group) * 16 + (i >> 4 & 15), f = (i & 15) * 8, feature = f0 + f;
                 if (tok >= rows)
