@@ -23,6 +23,7 @@
 // logprob_rows_kernel   many rows or short ones: a CTA takes whole rows, one after another;
 //     eight warps read, a ninth (and tenth) finishes the row before while they are in the
 //     next one, so neither the joins nor the alternatives stop the loads.
+// logprob_short_kernel  many short rows: a warp takes a row.
 // logprob_split_kernel  few long rows: a row is spread over a cluster of up to 8
 //     CTAs, all warps finish it together, and the parts are joined through
 //     distributed shared memory. Nothing depends on timing in either.
@@ -49,6 +50,7 @@ constexpr int ROW_READERS = 256;
 constexpr int ROW_THREADS = ROW_READERS + 32;
 constexpr int ROW_CTAS = 3;
 constexpr int LP_UNROLL = 4;
+constexpr int SHORT_VECS = 1024;    // of a row that one warp takes where there are many
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xff800000u); }
@@ -888,6 +890,51 @@ __global__ void __launch_bounds__(ROW_READERS + FIN * 32, ROW_CTAS) logprob_rows
     }
 }
 
+// Many short rows: a row a warp, which reads and finishes it, so the finishing, which
+// takes longer than reading, goes on in all warps of an SM. Latency and issue bound it:
+// 8170 x 3188 bf16 in 16 us, 26 with the best five.
+template <typename T, bool TOP> __global__ void __launch_bounds__(LP_THREADS) logprob_short_kernel(LogprobParams p)
+{
+    __shared__ Finds finds[TOP ? LP_WARPS : 1];
+    begin_behind();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t at = (int64_t)blockIdx.x * LP_WARPS + warp;
+    const float c = p.inv_t * LOG2E;
+    if (blockIdx.x == 0)
+        open_status(p, tid, LP_THREADS);
+    if (at >= p.M)
+        return;
+    const int row = (int)at;
+    Reader<T, 32> reader{p, lane};
+    reader.enter(row, 0, 1);
+    const Part<T> r = reader.r;
+    const int token = p.logprob != nullptr ? p.tokens[row] : -1;
+    const float given = token >= 0 && token < p.V ? Vec<T>::widen(r.x[token]) : 0.0f;
+    Sums<T> sums;
+    int best_vec;
+    sums.scale(c);
+    sums.clear();
+    reader.template read<TOP>(sums, best_vec, [] {});
+    const float m = warp_max_nan(sums.m);
+    const int holder = max(__ffs(__ballot_sync(0xffffffffu, sums.m == m)) - 1, 0);
+    const uint4 raw = share_first<32>(r, holder, lane);
+    Key top = 0ull;
+    if (TOP) {
+        Key best = warp_top(best_vec >= 0 && sums.m > neg_inf() ? order_key(sums.m, best_vec) : 0ull, p.top_k, lane);
+        best = lane < p.top_k ? best : 0ull;
+        const int npicked = __popc(__ballot_sync(0xffffffffu, best != 0ull));
+        const Key bound = bound_of<T>(__shfl_sync(0xffffffffu, best, p.top_k - 1), r.lead);
+        const int who = best != 0ull ? key_index(best) % 32 : 0;
+        if (!gather_few<32>(r, who, npicked, bound, finds[warp], lane, top))
+            top = gather_top<32>(r, who, npicked, 0, 32, bound, p.top_k, finds[warp].key, lane);
+    }
+    Stat one = sums.stat(), st = share_rest<32>(r, holder, raw, m, c, lane);
+    rescale(one, m, c);
+    st.s = warp_sum(st.s + (lane != holder ? one.s : 0.0f));
+    st.u = warp_sum(st.u + (lane != holder ? one.u : 0.0f));
+    write_row<T, TOP>(p, row, token, given, st, top, lane);
+}
+
 namespace {
 
 constexpr int CAND = 256; // elements that reach the bound, gathered by the whole CTA
@@ -1157,6 +1204,15 @@ template <typename T> cudaError_t launch_lp(const LogprobParams &p, int num_sms,
     while (parts < 8 && nvec * 16 > shortest && nvec >= 2 * parts * LP_THREADS &&
            ((int64_t)p.M * parts < num_sms || ((int64_t)p.M * parts < 2 * num_sms && nvec * 16 / parts > longest)))
         parts *= 2;
+    // More short rows than CTAs that take whole ones: a warp each. us for the best 0, 5
+    // and 20, whole rows by CTAs and by warps:
+    //   1000 x  8000 bf16   7.4 15.4 14.8    6.7  8.5 12.7
+    //   8170 x  3188 bf16  41.4 81.9 87.8   15.6 26.2 34.4
+    //   2000 x 14000 bf16  16.2 29.3 31.9   14.8 22.5 34.3
+    //   2000 x  8000 f32   13.5 24.0 25.5   15.2 20.2 34.0
+    if (parts == 1 && nvec <= SHORT_VECS && p.M > ROW_CTAS * num_sms)
+        return launch_behind(p.top_k > 0 ? logprob_short_kernel<T, true> : logprob_short_kernel<T, false>,
+                             dim3((unsigned)(((int64_t)p.M + LP_WARPS - 1) / LP_WARPS)), LP_THREADS, 0, 1, st, p);
     if (parts == 1) { // as many CTAs as stay resident, each with rows one after another
         const dim3 grid((unsigned)(p.M < ROW_CTAS * num_sms ? p.M : ROW_CTAS * num_sms));
         return launch_behind(p.top_k > FEW  ? logprob_rows_kernel<T, true, 2>

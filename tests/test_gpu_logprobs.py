@@ -344,3 +344,28 @@ def test_rows_that_one_element_dominates(dtype, M, V):
         elif name == "logprob":
             w = -np.log1p(d.sum(1))
         assert (np.abs(g - w) <= LOG_TOL * np.abs(w)).all(), (name, g[:4], w[:4])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,V", [(520, 9000), (3000, 257), (1000, 4)])
+@pytest.mark.parametrize("k", [0, 3, 20])
+def test_many_rows_of_different_lengths(dtype, M, V, k):
+    """Whole rows by CTAs that take several, and by warps; ties, masks, rows without a distribution, shares held by one thread."""
+    k = min(k, V)
+    rng = np.random.default_rng(M + k)
+    x = rng.standard_normal((M, V)).astype(np.float32) * 3
+    x[0::11] = -1.5
+    x[1::11] = rng.integers(0, 2, x[1::11].shape)
+    x[2::11] = np.arange(V) / 32
+    x[3::11, V // 3:V // 3 + 70] += 15
+    x[4::11, 1:] = -INF
+    x[5::11] = -INF
+    x[6::11, V - 1] = np.nan
+    x[7::11, 0] = INF
+    e = 16 // (2 if dtype == torch.bfloat16 else 4)
+    x[8::11, ::32 * e] += 30
+    t = place(torch.tensor(x), dtype, 3, 1)
+    tokens = rng.integers(-1, V, M).astype(np.int32)
+    got = forward(t, torch.tensor(tokens).cuda(), 0.75, k)
+    check(got, define(t, tokens, 0.75, k), V)
+    assert got["flags"] == 0
