@@ -580,13 +580,15 @@ enum {
 };
 
 /* Workspace of lora_mx4_proj_apply for M rows on route `rt`: the status word
- * and h. 0 if rt is NULL, not initialised or not a projection route. */
+ * and s A_s x_i. 0 if rt is NULL, not initialised or not a projection route. */
 size_t lora_mx4_proj_workspace_bytes(int M, const lora_route *rt);
 
 /*
  * y[i, :] = dq(W) x_i + s * B_s (A_s x_i), s = seq_slot[i]: lora_proj_apply with
  * the base [N][K] as codes and scales. The codes are widened to bf16 exactly;
- * x, the adapters and y are bf16, accumulation is fp32, y is rounded once.
+ * x, the adapters and y are bf16, accumulation is fp32, y is rounded once. In
+ * between, s A_s x_i is held in fp32 (LORA_MX4_PATH_ROWS) or as the sum of two
+ * bf16, within 2^-17 of it (LORA_MX4_PATH_TILES).
  * Every row rule, the status word (lora_status_get(ws)) and the errors are
  * those of lora_proj_apply; besides, K must be a multiple of 32, and codes and
  * scales non-NULL, codes 16-byte aligned. y rows may have any stride >= N.
@@ -594,8 +596,9 @@ size_t lora_mx4_proj_workspace_bytes(int M, const lora_route *rt);
 lora_status lora_mx4_proj_apply(const void *x, int64_t x_stride, const uint8_t *codes, const uint8_t *scales, int M,
                                 int K, int N, const int32_t *seq_slot, const lora_route *rt, void *y,
                                 int64_t y_stride, void *ws, size_t ws_bytes, lora_stream_t stream);
-/* The same on an explicit path (LORA_MX4_PATH_*); paths agree within the
- * fp32 accumulation-order tolerance, not bit for bit. */
+/* The same on an explicit path (LORA_MX4_PATH_*); paths agree within the fp32
+ * accumulation-order tolerance and that 2^-17 of the adapter's part, not bit
+ * for bit. */
 lora_status lora_mx4_proj_apply_ex(const void *x, int64_t x_stride, const uint8_t *codes, const uint8_t *scales, int M,
                                    int K, int N, const int32_t *seq_slot, const lora_route *rt, void *y,
                                    int64_t y_stride, void *ws, size_t ws_bytes, int path, lora_stream_t stream);

@@ -1502,9 +1502,8 @@ size_t lora_mx4_proj_workspace_bytes(int M, const lora_route *rt)
 {
     if (rt == nullptr || rt->magic != ROUTE_MAGIC || rt->kind != LORA_ROUTE_PROJ || M < 0)
         return 0;
-    // status, h in fp32, h in bf16
-    return align256(256 + sizeof(float) * (size_t)M * (size_t)rt->max_rank) +
-           align256(sizeof(uint16_t) * (size_t)M * (size_t)rt->max_rank);
+    // status, h in fp32 or in two planes of bf16
+    return align256(256 + sizeof(float) * (size_t)M * (size_t)rt->max_rank);
 }
 
 lora_status lora_mx4_proj_apply(const void *x, int64_t x_stride, const uint8_t *codes, const uint8_t *scales, int M,
@@ -1567,13 +1566,18 @@ lora_status lora_mx4_proj_apply_ex(const void *x, int64_t x_stride, const uint8_
     q.seq_slot = seq_slot;
     q.tab = tables_of(*rt);
     q.status = static_cast<uint32_t *>(ws);
-    q.h = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + 256);
-    q.hs = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(ws) + align256(256 + sizeof(float) * (size_t)M * (size_t)q.R));
+    const bool tiles = mx4_path(M, K, N, q.R, path) == LORA_MX4_PATH_TILES;
+    if (tiles) {
+        q.hs = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(ws) + 256);
+        q.ls = q.hs + (size_t)M * (size_t)q.R;
+    } else {
+        q.h = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + 256);
+    }
     q.y = static_cast<uint16_t *>(y);
     q.y_stride = y_stride;
     if ((e = launch_mx4_shrink(q, di.num_sms, st)) != cudaSuccess)
         return cuda_fail(e, who);
-    if (mx4_path(M, K, N, q.R, path) == LORA_MX4_PATH_TILES) {
+    if (tiles) {
         const Mx4TcPlan plan = plan_mx4_tc(q, di.num_sms);
         Mx4TcMaps maps;
         memset(&maps, 0, sizeof maps);

@@ -488,9 +488,7 @@ template <int CHUNK> __global__ void __launch_bounds__(SH_THREADS) mx4_shrink_ke
                 for (int w = 0; w < SH_WARPS; ++w)
                     v += red[w][q][row];
                 v = r0 + q < si.rank ? si.scale * __ldg(comp + r0 + q) * v : 0.0f;
-                const size_t at = (size_t)rows_s[i0 + row] * p.R + r0 + q;
-                p.h[at] = v;
-                p.hs[at] = f32_to_bf16_bits(v);
+                store_h(p, (size_t)rows_s[i0 + row] * p.R + r0 + q, v);
             }
         }
         __syncthreads();
@@ -662,9 +660,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1) mx4_shrink_many_kernel(Mx4ProjP
             if (r < ranks) {
                 const float *v = red + r * RED_ROW + q;
                 const float h = r0 + r < si.rank ? si.scale * __ldg(comp + r0 + r) * (v[0] + v[RED] + v[2 * RED] + v[3 * RED]) : 0.0f;
-                const size_t to = (size_t)rows_s[q] * p.R + r0 + r;
-                p.h[to] = h;
-                p.hs[to] = f32_to_bf16_bits(h);
+                store_h(p, (size_t)rows_s[q] * p.R + r0 + r, h);
             }
         }
     }

@@ -7,6 +7,7 @@
 #pragma once
 #include "lora_internal.cuh"
 #include "ptx.cuh"
+#include "vec.cuh"
 
 namespace rd {
 
@@ -34,8 +35,10 @@ struct Mx4ProjParams {
     int M, K, N, L, R;
     const int32_t *seq_slot;
     Tables tab;
-    float *h;      // [M][R]: s comp (A_s x_i) of every adapted row
-    uint16_t *hs;  // the same rounded to bf16
+    // s comp (A_s x_i) of every adapted row, [M][R]: in fp32 for the rows kernel, or for
+    // tiles (h null) as two bf16 whose sum it is to 2^-17 of itself
+    float *h;
+    uint16_t *hs, *ls;
     uint16_t *y;
     int64_t y_stride;
     uint32_t *status;
@@ -60,6 +63,23 @@ struct Mx4TcMaps {
     int scales_ok;      // 1: encoded
 };
 cudaError_t launch_mx4_tc(const Mx4ProjParams &p, const Mx4TcPlan &plan, const Mx4TcMaps &maps, cudaStream_t st);
+
+// An element of h to where the call's product takes it from. One bf16 would be
+// 2^-9 off, as much as the rounding of y itself; the second takes that up. (A value past
+// the largest bf16 stays finite; an infinity or a NaN is in the first alone.)
+__device__ __forceinline__ void store_h(const Mx4ProjParams &p, size_t at, float v)
+{
+    if (p.h != nullptr) {
+        p.h[at] = v;
+        return;
+    }
+    uint16_t hi = f32_to_bf16_bits(v);
+    const bool finite = (__float_as_uint(v) & 0x7F800000u) != 0x7F800000u;
+    if (finite && (hi & 0x7FFFu) == 0x7F80u)
+        --hi;
+    p.hs[at] = hi;
+    p.ls[at] = finite ? f32_to_bf16_bits(v - __uint_as_float((uint32_t)hi << 16)) : (uint16_t)0;
+}
 
 // Wait for a phase, at most WAIT_NS; the clock is read only every 256 polls
 // from the first on (a read of it takes longer than a stage).

@@ -13,8 +13,8 @@
 // takes 515 to 555 cycles, its products 512); with fewer rows it is the widening and what a
 // call takes in any case, shrink, set-up and epilogue (64x4096x4096: 14.5 us).
 //
-// The adapters are more K: s h of the tile's rows (rounded to bf16, as y
-// itself is; the sums stay fp32) against the B rows of each slot in the tile,
+// The adapters are more K: s h of the tile's rows (as two bf16, whose sum is good to
+// 2^-17; the sums stay fp32) against the B rows of each slot in the tile,
 // a row's columns zero for every slot but its own, into an accumulator of
 // their own, which is added to the rows that have an adapter: the others keep
 // the base product to the bit. Where that sum is not finite, the row's part is
@@ -33,6 +33,9 @@ namespace {
 
 constexpr int BM = 128;             // features of a tile: the UMMA M
 constexpr int TEAMS = 2;            // of the widening warps, that copy the adapters' rows
+// 16-rank segments of the adapters in a sub-tile of 64 k: of h the first bf16 of SEGS
+// segments, then the second; of B the segments alone, once for both.
+constexpr int SEGS = 2;
 // The rings between TMA, the widening warps and the products. A stage is SUB
 // sub-tiles of 64 k. There are S of them: widened weights in tensor memory (32
 // columns a sub-tile, from column A_COL on) and tn rows of x in shared memory (tn
@@ -154,10 +157,11 @@ __device__ __noinline__ float delta_alone(const Mx4ProjParams &p, const TcShared
     while (i + 1 < sh.nslot && sh.slot_id[i] != sh.tok_slot[tok])
         ++i;
     const int begin = max(q0, sh.seg_start[i]) - sh.seg_start[i], end = min(q1, sh.seg_start[i + 1]) - sh.seg_start[i];
-    const uint16_t *b = sh.slot_b[i] + (size_t)min(f, p.N - 1) * p.R, *h = p.hs + (size_t)(t0 + tok) * p.R;
+    const uint16_t *b = sh.slot_b[i] + (size_t)min(f, p.N - 1) * p.R;
+    const size_t h = (size_t)(t0 + tok) * p.R;
     float sum = 0.0f;
     for (int r = begin * 16; r < min(end * 16, p.R); ++r)
-        sum = fmaf(bf_lo(h[r]), bf_lo(b[r]), sum);
+        sum = fmaf(bf_lo(p.hs[h + r]) + bf_lo(p.ls[h + r]), bf_lo(b[r]), sum);
     return sum;
 }
 
@@ -404,31 +408,33 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
                 mbar_arrive(&sh.full[s]);
         }
 
-        // ---- the adapters' operands: 4 SUB segments of 16 ranks a stage. Eight
-        // lanes copy a row's 128 bytes of a sub-tile, which for a rank of 64 lie in
-        // one piece: a warp's copy meets 4 lines (a row a lane, 32: 64x4096x14336 took
-        // 10 % longer)
+        // ---- the adapters' operands: SEGS SUB segments of 16 ranks a stage. Eight
+        // lanes copy a row's 128 bytes of h in a sub-tile, four a row's 64 of B, so a warp's
+        // copy meets 8 pieces of memory (a row a lane, 32: 64x4096x14336 took 10 % longer)
         wait_or_note(&sh.routed, 0, &sh.bad);
         const int q0 = sh.nseg * part / kparts, q1 = sh.nseg * (part + 1) / kparts;
         const int ndelta = __any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&sh.bad) != 0)
                                ? 0
-                               : (q1 - q0 + 4 * SUB - 1) / (4 * SUB);
+                               : (q1 - q0 + SEGS * SUB - 1) / (SEGS * SUB);
         // The warps work in teams, a stage each: finding its slot and waiting take
         // as long as the copies (256x4096x14336: 2 % longer with all on every stage).
         constexpr int TEAM_WARPS = WIDEN_WARPS / TEAMS;
         constexpr int SUB_WARPS = TEAM_WARPS / SUB, ROWS = SUB_WARPS * 4; // that copy a sub-tile, rows at a time
-        const int team = warp / TEAM_WARPS, sub = warp % TEAM_WARPS / SUB_WARPS, piece = lane & 7,
+        const int team = warp / TEAM_WARPS, sub = warp % TEAM_WARPS / SUB_WARPS, piece = lane & 7, half = piece >> 2,
                   first = (warp % SUB_WARPS) * 4 + (lane >> 3);
-        constexpr int AT_ONCE = RINGS::MAX_ROWS / ROWS;
-        size_t b_row[BM / ROWS]; // element offsets of the rows this thread copies
+        const int own_seg = sub * SEGS + (piece >> 1 & 1); // of a stage
+        constexpr int AT_ONCE = RINGS::MAX_ROWS / ROWS, B_AT_ONCE = BM / ROWS / 2;
+        size_t b_row[B_AT_ONCE]; // element offsets of the rows this thread copies
 #pragma unroll
-        for (int i = 0; i < BM / ROWS; ++i)
-            b_row[i] = (size_t)min(f0 + first + i * ROWS, p.N - 1) * p.R;
+        for (int i = 0; i < B_AT_ONCE; ++i)
+            b_row[i] = (size_t)min(f0 + first + (2 * i + half) * ROWS, p.N - 1) * p.R;
         int h_slot[AT_ONCE];
 #pragma unroll
         for (int i = 0; i < AT_ONCE; ++i)
             h_slot[i] = first + i * ROWS < tn ? sh.tok_slot[first + i * ROWS] : -1;
-        const uint32_t into = sw128(first, piece); // rows ROWS further are swizzled alike
+        // rows ROWS further are swizzled alike
+        const uint32_t into = sw128(first, piece), b_into = sw128(first, piece & 3) + (uint32_t)(half * ROWS * 128);
+        const uint16_t *const plane = half == 0 ? p.hs : p.ls;
         // the slot of this thread's segment, the lo-th, its segments, and the slot that
         // had the stage's place before
         int lo = -1, begin = 0, end = 0, slot = -1, lo_before = -1, end_before = 0, before = -1;
@@ -445,56 +451,62 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
             return (q - begin) * 16 + (piece & 1) * 8; // the rank
         };
         auto copy_b = [&](int s, int r) {
-            const uint32_t at = d_slot(s) + (uint32_t)sub * A_BYTES + into;
+            const uint32_t at = d_slot(s) + (uint32_t)sub * A_BYTES + b_into;
             const uint16_t *b = slot_b + (r < p.R ? r : 0);
 #pragma unroll
-            for (int i = 0; i < BM / ROWS; ++i)
-                cp16(at + (uint32_t)(i * ROWS * 128), b + b_row[i], r < p.R ? 16u : 0u); // else zeros
+            for (int i = 0; i < B_AT_ONCE; ++i)
+                cp16(at + (uint32_t)(2 * i * ROWS * 128), b + b_row[i], r < p.R ? 16u : 0u); // else zeros
         };
-        static_assert(DS >= TEAMS, "B of a team's first stage, which has its place from the start");
-        const int q_first = q0 + 4 * (SUB * team + sub) + (piece >> 1);
+        // B of the stages that have their places from the start, or from when all codes
+        // are widened, is copied while h is waited for
+        static_assert(DS >= TEAMS && S <= 2 * TEAMS, "a team's first stage, and one more");
+        int rank0 = 0, rank1 = 0, slot0 = -1;
+        const int q_first = q0 + SEGS * SUB * team + own_seg, q_second = q_first + SEGS * SUB * TEAMS;
         if (team < ndelta && q_first < q1) {
-            const int r = find(q_first);
-            copy_b(team, r);
+            rank0 = find(q_first);
+            slot0 = slot;
+            copy_b(team, rank0);
+        }
+        if (ndelta > DS) // the further places are where the codes were
+            named_bar_sync(5u, WIDEN_WARPS * 32);
+        if (team + TEAMS < min(ndelta, S) && q_second < q1) {
+            rank1 = find(q_second);
+            copy_b(team + TEAMS, rank1);
         }
         if (ndelta > 0)
             grid_dependency_wait(); // h is complete
-        bool codes_left = false;
         for (int d = team; d < ndelta; d += TEAMS) {
             const int n = nbase + d, s = d % S, xslot = n % S;
             if (n >= S)
                 stage_free(n - S);
-            if (d >= DS && !codes_left) { // the further slots are where the codes were
-                named_bar_sync(5u, WIDEN_WARPS * 32);
-                codes_left = true;
-            }
-            const int q = q0 + 4 * (SUB * d + sub) + (piece >> 1);
+            const int q = q0 + SEGS * SUB * d + own_seg;
             if (q < q1) {
-                const int r = find(q);
-                if (d != team)
+                int r = d == team ? rank0 : rank1;
+                if (d >= min(team + 2 * TEAMS, S)) {
+                    r = find(q);
                     copy_b(s, r);
+                }
+                const int now = d == team ? slot0 : slot;
                 // rows of x that are not the slot's are zeros: all of a slot at first, then
                 // those that the stage S before had
-                if (d >= S && q - 4 * SUB * S >= end_before) {
+                if (d >= S && q - SEGS * SUB * S >= end_before) {
                     do
                         end_before = sh.seg_start[++lo_before + 1];
-                    while (q - 4 * SUB * S >= end_before);
+                    while (q - SEGS * SUB * S >= end_before);
                     before = sh.slot_id[lo_before];
                 }
                 const uint32_t xt = x_at + (uint32_t)(xslot * SUB + sub) * x_bytes + into, have = r < p.R ? 16u : 0u;
-                const uint16_t *h = p.hs + (size_t)(t0 + first) * p.R + (have ? r : 0);
+                const uint16_t *h = plane + (size_t)(t0 + first) * p.R + (have ? r : 0);
 #pragma unroll
                 for (int i = 0; i < AT_ONCE; ++i)
                     if (first + i * ROWS < tn) {
-                        const bool mine = h_slot[i] == slot;
+                        const bool mine = h_slot[i] == now;
                         if (mine || d < S || h_slot[i] == before)
                             cp16(xt + (uint32_t)(i * ROWS * 128), mine ? h + i * ROWS * p.R : p.hs, mine ? have : 0u);
                     }
             }
             cp_async_mbar_arrive_noinc(&sh.d_full[s]); // when this thread's copies have landed
         }
-        if (ndelta > DS && !codes_left) // the other teams wait here
-            named_bar_sync(5u, WIDEN_WARPS * 32);
         wait_or_note(&sh.done, 0, &sh.bad);
         __syncwarp();
     } else if (warp == WIDEN_WARPS) {
@@ -545,7 +557,7 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
             wait_or_note(&sh.base_done, 0, &sh.bad);
             tc_fence_after();
         }
-        for (int q = q0, d = 0; q < q1 && !__any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&sh.bad) != 0); q += 4 * SUB, ++d) {
+        for (int q = q0, d = 0; q < q1 && !__any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&sh.bad) != 0); q += SEGS * SUB, ++d) {
             const int ds = d % S;
             wait_or_note(&sh.d_full[ds], (uint32_t)(d / S) & 1u, &sh.bad);
             __syncwarp();
@@ -554,9 +566,9 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
             const uint64_t dd = sw128_kmajor_desc(d_slot(ds)), xd = x_of();
             if (elected()) {
 #pragma unroll
-                for (int j = 0; j < 4 * SUB; ++j)
-                    if (j < q1 - q)
-                        umma_bf16(delta, dd + (uint64_t)((j >> 2) * (A_BYTES >> 4) + (j & 3) * 2),
+                for (int j = 0; j < 4 * SUB; ++j) // both parts of h against the same segment of B
+                    if ((j >> 2) * SEGS + (j & 1) < q1 - q)
+                        umma_bf16(delta, dd + (uint64_t)((j >> 2) * (A_BYTES >> 4) + (j & 1) * 2),
                                   xd + (uint64_t)((uint32_t)(j >> 2) * (x_bytes >> 4) + (uint32_t)(j & 3) * 2u), idesc,
                                   d == 0 && j == 0 ? 0u : 1u);
                 umma_commit(&sh.free[s]);
