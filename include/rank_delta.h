@@ -639,8 +639,10 @@ size_t lora_logprobs_workspace_bytes(int M, int V, int top_k);
  * to the entropy and is no alternative: places without one hold id -1 and
  * -infinity. A row with nothing but -infinity has entropy 0, log probabilities
  * of -infinity and stats { -infinity, 0 }. A row that holds a NaN or +infinity
- * has no distribution: its floats are NaN and its ids -1. The type's lowest
- * value is an ordinary element: a row of it alone is uniform.
+ * has no distribution: its floats are NaN (the logprob of a negative token
+ * stays 0) and its ids -1. The type's lowest value is an ordinary element: a
+ * row of it alone is uniform, and it is an alternative with its id also where
+ * its log probability is beyond fp32 and -infinity.
  * Results are the same on every run. M = 0 is a no-op. Enqueued on `stream`
  * only (no allocation, no synchronisation; graph-safe).
  * Errors: NULL logits or ws, M < 0, V < 1, stride < V, an unknown dtype, an

@@ -736,9 +736,11 @@ __device__ __forceinline__ void write_row(const LogprobParams &p, int row, int t
         }
     }
     if (TOP && lane < p.top_k) {
-        const float lp = top != 0ull ? (key_value(top) - st.m) * p.inv_t - logsum : neg_inf();
+        // an element is one also where its log probability leaves fp32's range
+        const bool one = top != 0ull && !none;
+        const float lp = one ? (key_value(top) - st.m) * p.inv_t - logsum : neg_inf();
         p.top_logprobs[(int64_t)row * p.top_k + lane] = none ? quiet_nan() : lp;
-        p.top_ids[(int64_t)row * p.top_k + lane] = lp > neg_inf() ? key_index(top) : -1;
+        p.top_ids[(int64_t)row * p.top_k + lane] = one ? key_index(top) : -1;
     }
 }
 
