@@ -724,7 +724,10 @@ lora_status lora_proj_plan(int M, const lora_route *rt, int gated, int path, lor
  * setting covers the tensor-core kernel's split-K wait (LORA_PATH_TC with K
  * parts) and, from 2048 rows, its wait for the launch's shrink tiles: those
  * waits run out, the call returns with LORA_FLAG_WAIT_TIMEOUT and y is not
- * (fully) written. Nothing faults or hangs.
+ * (fully) written. In lora_mx4_proj_apply extra_flags = 1 keeps an arrival from
+ * the adapters' stages (LORA_MX4_PATH_ROWS: from the sums of a step), 2 or more
+ * from the base's; the call returns with LORA_FLAG_WAIT_TIMEOUT and y is not
+ * valid. Nothing faults or hangs.
  * wait_ns = 0 restores normal operation. Process-wide; for tests only.
  */
 void lora_test_wait_hook(uint64_t wait_ns, int extra_flags);

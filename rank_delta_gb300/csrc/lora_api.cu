@@ -1575,6 +1575,9 @@ lora_status lora_mx4_proj_apply_ex(const void *x, int64_t x_stride, const uint8_
     }
     q.y = static_cast<uint16_t *>(y);
     q.y_stride = y_stride;
+    test_hook_get(q.wait_ns, q.never);
+    if (q.wait_ns == 0)
+        q.wait_ns = WAIT_NS;
     if ((e = launch_mx4_shrink(q, di.num_sms, st)) != cudaSuccess)
         return cuda_fail(e, who);
     if (tiles) {

@@ -800,10 +800,10 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
     const int tiles = (p.N + 15) / 16, groups = (tiles + teams - 1) / teams; // of 16 features, of a step's
     const int steps = (groups - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
     if (tid < RW_WARPS * RW_MAX_DEPTH)
-        mbar_init(&full[tid / RW_MAX_DEPTH][tid % RW_MAX_DEPTH], 1);
+        mbar_init(&full[tid / RW_MAX_DEPTH][tid % RW_MAX_DEPTH], 1 + (p.never > 1));
     if (tid == 0) {
         for (int b = 0; b < RW_BUFS; ++b) {
-            mbar_init(&part_full[b], RW_WARPS);
+            mbar_init(&part_full[b], RW_WARPS + (p.never == 1));
             mbar_init(&part_free[b], RW_FINISH);
         }
         bad = 0;
@@ -869,9 +869,10 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
         const uint32_t xg = xs + (uint32_t)(g & (RW_ROWS - 1)) * xrow + (uint32_t)t * 64u; // columns 4 to 7 repeat
         const uint32_t turn = (uint32_t)((t >> 1) | (g & 1) << 1) << 4;
         const uint32_t row_at = (uint32_t)g * 128u; // of a box; row g + 8 is 1024 further and turned alike
-        int slot = 0;
+        int slot = 0, u = 0;
         uint32_t parity = 0;
-        for (int s = 0, u = 0; s < steps; ++s) {
+        bool ok = true; // no wait gave up
+        for (int s = 0; s < steps; ++s) {
             float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             for (int k = 0; k < per; ++k, ++u) {
                 const int box = wk + k * T;
@@ -883,7 +884,8 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
                 }
                 if (u + 1 < units)
                     next_scales(next);
-                wait_or_note(&full[warp][slot], parity, &bad);
+                if (!(ok = warp_wait(&full[warp][slot], parity, &bad, p.wait_ns)))
+                    break;
                 const uint32_t at = mine + (uint32_t)slot * RW_BOX + row_at;
                 const bool twice = __any_sync(0xffffffffu, max(max(sc[0], sc[1]), max(sc[2], sc[3])) > MX4_ONE_FACTOR);
 #pragma unroll
@@ -922,8 +924,10 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
                 }
             }
             const int buf = s % RW_BUFS, use = s / RW_BUFS;
-            if (use > 0) // the step that used the buffer before has been finished
-                wait_or_note(&part_free[buf], (uint32_t)(use - 1) & 1u, &bad);
+            if (ok && use > 0) // the step that used the buffer before has been finished
+                ok = warp_wait(&part_free[buf], (uint32_t)(use - 1) & 1u, &bad, p.wait_ns);
+            if (!ok)
+                break;
             float *to = part + (size_t)(buf * RW_WARPS + warp) * RW_PART;
             if (t < RW_ROWS / 2) {
                 *reinterpret_cast<float2 *>(to + g * RW_ROWS + 2 * t) = make_float2(acc[0], acc[1]);
@@ -933,6 +937,9 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
             if (lane == 0)
                 mbar_arrive(&part_full[buf]);
         }
+        if (!ok) // the boxes on their way land before the CTA ends
+            for (int v = u; v < min(u + depth, units); ++v)
+                mbar_wait(&full[warp][v % depth], (uint32_t)(v / depth) & 1u, p.wait_ns);
     } else {
         // ---- finish: the rows' slots, s h, then step by step
         const int ft = tid - RW_WARPS * 32;
@@ -997,7 +1004,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1)
             if (s + 1 < steps)
                 ask(s + 1, 0);
             named_bar_sync(RW_H, RW_FINISH * 32);
-            wait_or_note(&part_full[buf], (uint32_t)(s / RW_BUFS) & 1u, &bad);
+            wait_or_note(&part_full[buf], (uint32_t)(s / RW_BUFS) & 1u, &bad, p.wait_ns); // goes on with what there is
             const float *from = part + (size_t)buf * RW_WARPS * RW_PART;
             for (int i = ft; i < 2 * outs; i += RW_FINISH * 32) { // two threads an output
                 const int o = i >> 1, row = o >> wide, f = o & (width - 1);

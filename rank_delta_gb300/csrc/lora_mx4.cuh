@@ -42,6 +42,10 @@ struct Mx4ProjParams {
     uint16_t *y;
     int64_t y_stride;
     uint32_t *status;
+    // limit of a wait; test hook: 1, the adapters' stages (rows kernel: the steps' sums) wait
+    // for an arrival that never comes; more, the base's do
+    uint64_t wait_ns;
+    int never;
 };
 
 cudaError_t launch_mx4_quantize(const Mx4QuantParams &p, int dtype, cudaStream_t st);
@@ -81,9 +85,10 @@ __device__ __forceinline__ void store_h(const Mx4ProjParams &p, size_t at, float
     p.ls[at] = finite ? f32_to_bf16_bits(v - __uint_as_float((uint32_t)hi << 16)) : (uint16_t)0;
 }
 
-// Wait for a phase, at most WAIT_NS; the clock is read only every 256 polls
+// Wait for a phase, at most `limit` ns, or (`heed`) until another wait of the CTA has given
+// up; false: not complete, and noted. The clock is read only every 256 polls
 // from the first on (a read of it takes longer than a stage).
-__device__ __forceinline__ void wait_or_note(uint64_t *bar, uint32_t parity, int *bad)
+__device__ __forceinline__ bool wait_or_note(uint64_t *bar, uint32_t parity, int *bad, uint64_t limit, bool heed = true)
 {
     const uint32_t a = smem_u32(bar);
     uint64_t t0 = 0;
@@ -92,11 +97,29 @@ __device__ __forceinline__ void wait_or_note(uint64_t *bar, uint32_t parity, int
             continue;
         const uint64_t t = globaltimer_ns();
         t0 = t0 == 0 ? t : t0;
-        if (t - t0 > WAIT_NS || *reinterpret_cast<volatile int *>(bad) != 0) {
+        if (t - t0 > limit || (heed && *reinterpret_cast<volatile int *>(bad) != 0)) {
             *reinterpret_cast<volatile int *>(bad) = 1;
-            return;
+            return false;
         }
     }
+    return true;
+}
+// The same for a whole warp, which goes on together.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int *bad, uint64_t limit)
+{
+    const uint32_t a = smem_u32(bar);
+    uint64_t t0 = 0;
+    for (uint32_t i = 1; !__all_sync(0xffffffffu, mbar_try_wait(a, parity)); ++i) {
+        if ((i & 255u) != 0)
+            continue;
+        const uint64_t t = globaltimer_ns();
+        t0 = t0 == 0 ? t : t0;
+        if (__any_sync(0xffffffffu, t - t0 > limit || *reinterpret_cast<volatile int *>(bad) != 0)) {
+            *reinterpret_cast<volatile int *>(bad) = 1;
+            return false;
+        }
+    }
+    return true;
 }
 
 // One lane of the converged warp, by the instruction that tells the compiler so:

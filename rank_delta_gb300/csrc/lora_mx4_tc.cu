@@ -78,6 +78,8 @@ struct TcShared {
     uint64_t full[MAX_RING], free[MAX_RING], c_full[MAX_RING], c_free[MAX_RING], d_full[MAX_RING], routed, base_done, done, joined;
     uint32_t tmem;
     int bad;                          // a wait gave up
+    int verdict;                      // whether the adapters are taken: 0 not decided, 1, 2 not
+    int x_asked, codes_asked;         // stages of x and steps of codes that were asked for
     int nseg;
     uint32_t present[MAX_BUCKETS / 32];
     int16_t tok_slot[MAX_TN];         // the row's slot, -1: no delta
@@ -337,11 +339,11 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         prefetch_tmap(&maps.codes);
         prefetch_tmap(&maps.x);
         for (int s = 0; s < S; ++s) {
-            mbar_init(&sh.full[s], 1 + 4 * SUB); // x, and the groups' warps
+            mbar_init(&sh.full[s], 1 + 4 * SUB + (p.never > 1)); // x, and the groups' warps
             mbar_init(&sh.free[s], 1);
         }
         for (int s = 0; s < S; ++s)
-            mbar_init(&sh.d_full[s], WIDEN_WARPS / TEAMS * 32);
+            mbar_init(&sh.d_full[s], WIDEN_WARPS / TEAMS * 32 + (p.never == 1));
         for (int s = 0; s < CS; ++s) {
             mbar_init(&sh.c_full[s], 1);
             mbar_init(&sh.c_free[s], 16); // four warps for each of the step's four stages
@@ -350,7 +352,7 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         mbar_init(&sh.base_done, 1);
         mbar_init(&sh.done, 1);
         mbar_init(&sh.joined, 1);
-        sh.bad = 0;
+        sh.bad = sh.verdict = 0;
         fence_barrier_init();
         if (kparts > 1 && part_owns(kparts, part) > 0)
             mbar_arrive_expect_tx(&sh.joined, (uint32_t)((kparts - 1) * part_owns(kparts, part) * (tn + 1)) * 4u);
@@ -368,7 +370,11 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
 
     auto d_slot = [&](int s) { return s < DS ? d_at + (uint32_t)(s * SUB) * A_BYTES : codes_at + (uint32_t)((s - DS) * SUB) * A_BYTES; };
     // stage n's products are through (stage n - S is known to be)
-    auto stage_free = [&](int n) { wait_or_note(&sh.free[n % S], (uint32_t)(n / S) & 1u, &sh.bad); };
+    auto stage_free = [&](int n) { return wait_or_note(&sh.free[n % S], (uint32_t)(n / S) & 1u, &sh.bad, p.wait_ns); };
+    auto warp_stage_free = [&](int n) { return warp_wait(&sh.free[n % S], (uint32_t)(n / S) & 1u, &sh.bad, p.wait_ns); };
+    // A role leaves its loop where a wait gives up, and what it left is seen to at the end.
+    int m = warp >> 2;       // a widening warp's next sub-tile
+    bool adapters = false;   // the widening warps': the adapters are taken
     if (warp < WIDEN_WARPS) {
         // ---- widen: every GROUPS-th sub-tile
         const int group = warp >> 2, row = (warp & 3) * 32 + lane;
@@ -380,9 +386,11 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         };
         uint32_t sc_next = !maps.scales_ok && group < mbase ? byte_scales(group) : 0u;
         const uint32_t own = sw128(row, 0);
-        for (int m = group; m < mbase; m += GROUPS) {
+        bool ok = true;
+        for (; m < mbase; m += GROUPS) {
             const int j = m >> 2, cs = j % CS, quarter = m & 3;
-            wait_or_note(&sh.c_full[cs], (uint32_t)(j / CS) & 1u, &sh.bad);
+            if (!(ok = warp_wait(&sh.c_full[cs], (uint32_t)(j / CS) & 1u, &sh.bad, p.wait_ns)))
+                break;
             const uint32_t at = codes_at + (uint32_t)cs * CODE_BYTES;
             const uint4 c[2] = {lds_16((at + own) ^ (uint32_t)(quarter << 5)), lds_16((at + own) ^ (uint32_t)(quarter << 5 | 16))};
             uint32_t sc = sc_next;
@@ -394,9 +402,8 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
             if (lane == 0)
                 mbar_arrive(&sh.c_free[cs]);
             const int n = m / SUB, s = n % S;
-            if (n >= S)
-                stage_free(n - S);
-            __syncwarp();
+            if (n >= S && !(ok = warp_stage_free(n - S)))
+                break;
             tc_fence_after();
             uint32_t out[32];
             widen(c, sc & 255u, (sc >> 8) & 255u, out);
@@ -411,11 +418,21 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         // ---- the adapters' operands: SEGS SUB segments of 16 ranks a stage. Eight
         // lanes copy a row's 128 bytes of h in a sub-tile, four a row's 64 of B, so a warp's
         // copy meets 8 pieces of memory (a row a lane, 32: 64x4096x14336 took 10 % longer)
-        wait_or_note(&sh.routed, 0, &sh.bad);
-        const int q0 = sh.nseg * part / kparts, q1 = sh.nseg * (part + 1) / kparts;
-        const int ndelta = __any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&sh.bad) != 0)
-                               ? 0
-                               : (q1 - q0 + SEGS * SUB - 1) / (SEGS * SUB);
+        ok = ok && warp_wait(&sh.routed, 0, &sh.bad, p.wait_ns);
+        // The warps meet at a barrier below, so all of them take the answer of the first to
+        // get here. Where it is yes, the routing was seen to be complete.
+        int verdict = 0;
+        if (lane == 0) {
+            __threadfence_block();
+            verdict = atomicCAS(&sh.verdict, 0, ok ? 1 : 2);
+            if (verdict == 0)
+                verdict = ok ? 1 : 2;
+            __threadfence_block();
+        }
+        adapters = __shfl_sync(0xffffffffu, verdict, 0) == 1;
+        __syncwarp();
+        const int q0 = adapters ? sh.nseg * part / kparts : 0, q1 = adapters ? sh.nseg * (part + 1) / kparts : 0;
+        const int ndelta = (q1 - q0 + SEGS * SUB - 1) / (SEGS * SUB);
         // The warps work in teams, a stage each: finding its slot and waiting take
         // as long as the copies (256x4096x14336: 2 % longer with all on every stage).
         constexpr int TEAM_WARPS = WIDEN_WARPS / TEAMS;
@@ -431,7 +448,7 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         int h_slot[AT_ONCE];
 #pragma unroll
         for (int i = 0; i < AT_ONCE; ++i)
-            h_slot[i] = first + i * ROWS < tn ? sh.tok_slot[first + i * ROWS] : -1;
+            h_slot[i] = adapters && first + i * ROWS < tn ? sh.tok_slot[first + i * ROWS] : -1;
         // rows ROWS further are swizzled alike
         const uint32_t into = sw128(first, piece), b_into = sw128(first, piece & 3) + (uint32_t)(half * ROWS * 128);
         const uint16_t *const plane = half == 0 ? p.hs : p.ls;
@@ -462,23 +479,23 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         static_assert(DS >= TEAMS && S <= 2 * TEAMS, "a team's first stage, and one more");
         int rank0 = 0, rank1 = 0, slot0 = -1;
         const int q_first = q0 + SEGS * SUB * team + own_seg, q_second = q_first + SEGS * SUB * TEAMS;
-        if (team < ndelta && q_first < q1) {
+        if (ok && team < ndelta && q_first < q1) {
             rank0 = find(q_first);
             slot0 = slot;
             copy_b(team, rank0);
         }
         if (ndelta > DS) // the further places are where the codes were
             named_bar_sync(5u, WIDEN_WARPS * 32);
-        if (team + TEAMS < min(ndelta, S) && q_second < q1) {
+        if (ok && team + TEAMS < min(ndelta, S) && q_second < q1) {
             rank1 = find(q_second);
             copy_b(team + TEAMS, rank1);
         }
         if (ndelta > 0)
             grid_dependency_wait(); // h is complete
-        for (int d = team; d < ndelta; d += TEAMS) {
+        for (int d = team; ok && d < ndelta; d += TEAMS) {
             const int n = nbase + d, s = d % S, xslot = n % S;
-            if (n >= S)
-                stage_free(n - S);
+            if (n >= S && !(ok = warp_stage_free(n - S)))
+                break;
             const int q = q0 + SEGS * SUB * d + own_seg;
             if (q < q1) {
                 int r = d == team ? rank0 : rank1;
@@ -507,15 +524,16 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
             }
             cp_async_mbar_arrive_noinc(&sh.d_full[s]); // when this thread's copies have landed
         }
-        wait_or_note(&sh.done, 0, &sh.bad);
+        wait_or_note(&sh.done, 0, &sh.bad, p.wait_ns, false); // the products end whether or not a wait gave up
         __syncwarp();
     } else if (warp == WIDEN_WARPS) {
         // ---- x
-        if (elected())
-            for (int n = S; n < nbase; ++n) {
-                stage_free(n - S);
+        if (elected()) {
+            int n = S;
+            for (; n < nbase && stage_free(n - S); ++n)
                 load_x(n);
-            }
+            sh.x_asked = min(n, nbase);
+        }
         __syncwarp();
     } else if (warp == WIDEN_WARPS + 1) {
         // ---- products
@@ -531,8 +549,10 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
                 parity ^= 1u;
             }
         };
+        bool ok = true;
         for (int n = 0; n < nbase; ++n) {
-            wait_or_note(&sh.full[s], parity, &sh.bad);
+            if (!(ok = warp_wait(&sh.full[s], parity, &sh.bad, p.wait_ns)))
+                break;
             __syncwarp();
             tc_fence_after();
             const uint64_t xd = x_of();
@@ -547,19 +567,20 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
             __syncwarp();
             next();
         }
-        wait_or_note(&sh.routed, 0, &sh.bad);
-        const int q0 = sh.nseg * part / kparts, q1 = sh.nseg * (part + 1) / kparts;
+        ok = ok && warp_wait(&sh.routed, 0, &sh.bad, p.wait_ns);
+        const int q0 = ok ? sh.nseg * part / kparts : 0, q1 = ok ? sh.nseg * (part + 1) / kparts : 0;
         if (RINGS::ALIAS && q1 > q0) {
             __syncwarp();
             if (elected())
                 umma_commit(&sh.base_done);
             __syncwarp();
-            wait_or_note(&sh.base_done, 0, &sh.bad);
+            ok = warp_wait(&sh.base_done, 0, &sh.bad, p.wait_ns);
             tc_fence_after();
         }
-        for (int q = q0, d = 0; q < q1 && !__any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&sh.bad) != 0); q += SEGS * SUB, ++d) {
+        for (int q = q0, d = 0; ok && q < q1; q += SEGS * SUB, ++d) {
             const int ds = d % S;
-            wait_or_note(&sh.d_full[ds], (uint32_t)(d / S) & 1u, &sh.bad);
+            if (!(ok = warp_wait(&sh.d_full[ds], (uint32_t)(d / S) & 1u, &sh.bad, p.wait_ns)))
+                break;
             __syncwarp();
             fence_proxy_async_smem(); // cp.async (generic proxy) wrote both operands
             tc_fence_after();
@@ -581,11 +602,12 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         __syncwarp();
     } else if (warp == WIDEN_WARPS + 2) {
         // ---- codes and scales
-        if (elected())
-            for (int j = CS; j < j1 - j0; ++j) {
-                wait_or_note(&sh.c_free[j % CS], (uint32_t)(j / CS - 1) & 1u, &sh.bad);
+        if (elected()) {
+            int j = CS;
+            for (; j < j1 - j0 && wait_or_note(&sh.c_free[j % CS], (uint32_t)(j / CS - 1) & 1u, &sh.bad, p.wait_ns); ++j)
                 load_codes(j);
-            }
+            sh.codes_asked = min(j, j1 - j0);
+        }
         __syncwarp();
     } else {
         route_tile(p, sh, t0, tn, lane);
@@ -595,6 +617,28 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         __syncwarp();
     }
 
+    // Where a wait gave up: everything on its way ends (with the same limit) before the
+    // CTA does. The stages whose x was asked for get the arrivals that the widening
+    // warps still owe them. Whole CTA, behind a barrier that all waits lie before.
+    auto unwind = [&] {
+        if (warp < WIDEN_WARPS) {
+            cp_async_wait_all();
+            if (lane == 0)
+                for (; m < mbase && m / SUB < sh.x_asked; m += GROUPS)
+                    mbar_arrive(&sh.full[m / SUB % S]);
+        }
+        __syncthreads();
+        if (tid == 0) {
+            for (int n = max(0, sh.x_asked - S); n < sh.x_asked; ++n)
+                mbar_wait(&sh.full[n % S], (uint32_t)(n / S) & 1u, p.wait_ns);
+            for (int j = max(0, sh.codes_asked - CS); j < sh.codes_asked; ++j)
+                mbar_wait(&sh.c_full[j % CS], (uint32_t)(j / CS) & 1u, p.wait_ns);
+            mbar_wait(&sh.done, 0, p.wait_ns); // the products
+            grid_dependency_wait();            // the call's status is open
+            atomicOr(p.status, (uint32_t)LORA_FLAG_WAIT_TIMEOUT);
+        }
+        __syncthreads();
+    };
     const int rows = min(tn, p.M - t0);
     const bool vec = (reinterpret_cast<uintptr_t>(p.y) & 15u) == 0 && p.y_stride % 8 == 0;
     const uint32_t delta_col = (uint32_t)(RINGS::ALIAS ? MAX_TN : tn);
@@ -606,7 +650,7 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         if (warp < WIDEN_WARPS) {
             constexpr uint32_t Y_ROW = BM * 2 + 16;
             const int group = warp >> 2;
-            const bool adapted = sh.nseg > 0;
+            const bool adapted = adapters && sh.nseg > 0;
             const uint32_t quad = (uint32_t)(warp & 3) * 32;
             // the lane's row of the four 8 x 8 matrices of a store: 8 features of a batch row
             const uint32_t to = base + (uint32_t)((lane >> 4) * 8 + (lane & 7)) * Y_ROW + (quad + (uint32_t)(lane >> 3 & 1) * 8) * 2;
@@ -671,12 +715,10 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
+        if (sh.bad)
+            unwind();
         if (warp == WIDEN_WARPS + 1)
             tmem_dealloc(tmem, cols);
-        if (tid == 0 && sh.bad) {
-            grid_dependency_wait(); // the call's status is open
-            atomicOr(p.status, (uint32_t)LORA_FLAG_WAIT_TIMEOUT);
-        }
         return;
     }
 
@@ -689,7 +731,7 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
     cluster_arrive();
     if (warp < WIDEN_WARPS) {
         tc_fence_after();
-        const bool adapted = sh.nseg * (part + 1) / kparts > sh.nseg * part / kparts;
+        const bool adapted = adapters && sh.nseg * (part + 1) / kparts > sh.nseg * part / kparts;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         float *const to = reinterpret_cast<float *>(smem) + ((warp & 3) * 32 + lane) * stride;
         for (int c = warp >> 2; c < tn / 16; c += GROUPS) {
@@ -730,7 +772,7 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
     __syncwarp();
     // ---- the parts' sum, in part order, and one rounding; 8 features of a row at a time
     if (own > 0)
-        wait_or_note(&sh.joined, 0, &sh.bad);
+        wait_or_note(&sh.joined, 0, &sh.bad, p.wait_ns, false); // so do the copies come
     __syncwarp();
     cluster_arrive(); // this part has its copies
     {
@@ -754,12 +796,10 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (sh.bad)
+        unwind();
     if (warp == WIDEN_WARPS + 1)
         tmem_dealloc(tmem, cols);
-    if (tid == 0 && sh.bad) {
-        grid_dependency_wait(); // the call's status is open
-        atomicOr(p.status, (uint32_t)LORA_FLAG_WAIT_TIMEOUT);
-    }
 }
 
 namespace {

@@ -81,8 +81,8 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar_addr, uint32_t parity
 // Wait until the phase with the given parity of `bar` has completed. Spins on
 // try_wait (which itself parks the thread briefly in hardware) without
 // sleeping, so a pipeline handoff costs no more than the barrier latency.
-// Returns false after WAIT_NS.
-__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity)
+// Returns false after `limit` ns.
+__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64_t limit = WAIT_NS)
 {
     const uint32_t a = smem_u32(bar);
     if (mbar_try_wait(a, parity))
@@ -91,7 +91,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity)
     for (uint32_t i = 1;; ++i) {
         if (mbar_try_wait(a, parity))
             return true;
-        if ((i & 255u) == 0 && globaltimer_ns() - t0 > WAIT_NS)
+        if ((i & 255u) == 0 && globaltimer_ns() - t0 > limit)
             return false;
     }
 }
