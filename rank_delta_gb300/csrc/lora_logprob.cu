@@ -1091,7 +1091,8 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprob_split_kernel(LogprobPar
 // A CTA takes LP_UNROLL * LP_THREADS vectors of one row of dlogits. With
 // a = log2 p and one factor for each row, an element is
 //   dx = 2^a (q + r a),  q = -t (g + g_H H),  r = -t g_H ln 2,
-// and the token's own gets t g on top. a = x c - (m c + log S log2 e), the
+// but the token's own, whose g (1 - p) is -g expm1(log p): where p is near 1 the
+// difference of g and g p would keep few digits. a = x c - (m c + log S log2 e), the
 // latter held as two fp32 numbers so that p is as good as fp32 allows.
 // 8192 x 32000 bf16: 150 us, 7.0 TB/s, HBM; 96 x 32003 f32 with entropy 4.9 us.
 template <typename T, bool BONUS>
@@ -1133,13 +1134,15 @@ __global__ void __launch_bounds__(LP_THREADS, 6) logprob_grad_kernel(LogprobGrad
     const float H = BONUS ? p.entropy[row] : 0.0f;
     const bool empty = m == neg_inf();
     const float c = p.inv_t * LOG2E;
-    const float qf = -p.inv_t * (g + gh * H), rf = -p.inv_t * gh * LN2, own = p.inv_t * g;
+    const float qf = -p.inv_t * (g + gh * H), rf = -p.inv_t * gh * LN2;
     // m c + logsum log2 e in two parts; rows of huge values take the difference first
     const float mc = m * c, ml = fmaf(m, c, -mc), ls = logsum * LOG2E;
     const float hi = mc + ls, part = hi - mc, lo = ((mc - (hi - part)) + (ls - part)) + ml;
     const bool huge = !(fabsf(mc) <= 65536.0f);
     const f2 c2 = make_f2(c, c), hi2 = make_f2(-hi, -hi), lo2 = make_f2(-lo, -lo), q2 = make_f2(qf, qf), r2 = make_f2(rf, rf);
     const f2 nm2 = make_f2(-m, -m), ls2 = make_f2(-ls, -ls);
+    bool mine = false; // this thread has the token's element, which is xt
+    float xt = 0.0f;
 #pragma unroll
     for (int q = 0; q < LP_UNROLL; ++q) {
         const int v = v0 + q * LP_THREADS, i0 = v * E - lead;
@@ -1147,6 +1150,12 @@ __global__ void __launch_bounds__(LP_THREADS, 6) logprob_grad_kernel(LogprobGrad
             break;
         float f[E];
         Vec<T>::unpack(raw[q], f);
+        if (t >= max(i0, 0) && t < i0 + E) { // none, -1, may lie before the row in its first vector
+            mine = true;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                xt = i0 + e == t ? f[e] : xt;
+        }
 #pragma unroll
         for (int e = 0; e < E; e += 2) {
             const f2 x2 = make_f2(f[e], f[e + 1]);
@@ -1168,11 +1177,6 @@ __global__ void __launch_bounds__(LP_THREADS, 6) logprob_grad_kernel(LogprobGrad
             d2 = mul_f2(make_f2(exp2_fast(a0), exp2_fast(a1)), d2);
             split_f2(d2, f[e], f[e + 1]);
         }
-        if (t >= i0 && t < i0 + E) {
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                f[e] += i0 + e == t ? own : 0.0f;
-        }
         if (empty) {
 #pragma unroll
             for (int e = 0; e < E; ++e)
@@ -1186,6 +1190,17 @@ __global__ void __launch_bounds__(LP_THREADS, 6) logprob_grad_kernel(LogprobGrad
                 if (i0 + e >= 0 && i0 + e < p.V)
                     dx[i0 + e] = Vec<T>::narrow(f[e]);
         }
+    }
+    // Over what was stored there. The row's numbers are read again: kept through the loop
+    // they took registers that it needs (8192 x 32000 bf16 with entropy: 169 us, 155).
+    if (mine && !empty) {
+        const float lp = (xt - p.stats[2 * (int64_t)row]) * p.inv_t - p.stats[2 * (int64_t)row + 1];
+        float d = p.g_logprob != nullptr ? -p.inv_t * p.g_logprob[row] * expm1f(lp) : 0.0f;
+        if (BONUS) {
+            const float l = max_nan(lp, -700.0f);
+            d = fmaf(exp2_fast(l * LOG2E), -p.inv_t * p.g_entropy[row] * (l + p.entropy[row]), d);
+        }
+        dx[t] = Vec<T>::narrow(d);
     }
 }
 
