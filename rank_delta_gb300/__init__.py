@@ -193,7 +193,7 @@ def _ptr(v) -> int:
     if v is None:
         return 0
     try:
-        return v.data_ptr()
+        return int(v.data_ptr())
     except AttributeError:
         return int(v)
 
@@ -202,7 +202,7 @@ def _stream(s) -> int:
     if s is None:
         return 0
     try:
-        return s.cuda_stream
+        return int(s.cuda_stream)
     except AttributeError:
         return int(s)
 
