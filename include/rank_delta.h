@@ -646,7 +646,7 @@ size_t lora_logprobs_workspace_bytes(int M, int V, int top_k);
  * Results are the same on every run. M = 0 is a no-op. Enqueued on `stream`
  * only (no allocation, no synchronisation; graph-safe).
  * Errors: NULL logits or ws, M < 0, V < 1, stride < V, an unknown dtype, an
- * inv_temperature that is not positive and finite, top_k outside [0,
+ * inv_temperature that is not positive or above 2^127, top_k outside [0,
  * min(V, LORA_MAX_TOP)], NULL top arrays with top_k > 0, logprob without
  * tokens, logits not aligned to their type, ws too small or not 256-byte
  * aligned.

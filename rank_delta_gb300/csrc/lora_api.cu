@@ -1614,8 +1614,8 @@ lora_status check_logits(const char *who, const void *logits, int dtype, int64_t
         return fail(LORA_ERR_SHAPE, "%s: need M %d >= 0 and V %d >= 1", who, M, V);
     if (stride < V)
         return fail(LORA_ERR_SHAPE, "%s: stride %lld must be >= V %d", who, (long long)stride, V);
-    if (!(inv_t > 0.0f) || !std::isfinite(inv_t))
-        return fail(LORA_ERR_RANGE, "%s: inv_temperature %g must be positive and finite", who, (double)inv_t);
+    if (!(inv_t > 0.0f && inv_t <= 0x1p127f)) // its product with log2 e, which scales the logits, has to be finite
+        return fail(LORA_ERR_RANGE, "%s: inv_temperature %g must be positive and at most 2^127", who, (double)inv_t);
     if (V > (1 << 30) || (int64_t)M * (V / 4096 + 8) > 0x7fffffff)
         return fail(LORA_ERR_UNSUPPORTED, "%s: M %d rows of V %d elements are more than one launch takes", who, M, V);
     if (M > 0 && logits == nullptr)

@@ -71,3 +71,14 @@ def test_the_gradient_of_a_token_that_dominates_its_row(dtype, V, g, h):
     unit = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -23
     bad = ~(np.abs(got - want) <= (2 * LOG_TOL + 2.0 ** -21) * size + unit * np.abs(want))
     assert not bad.any(), (np.argwhere(bad)[:4].tolist(), got[bad][:4], want[bad][:4], one_less[bad][:4])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,V", [(2, 40000), (3, 300), (3000, 257)])
+@pytest.mark.parametrize("inv_t", [2.0 ** 127, 1e30, 2.0 ** -149])
+def test_inverse_temperatures_at_their_ends(dtype, M, V, inv_t):
+    """Greedy choice, with ties, and a uniform one."""
+    rng = np.random.default_rng(V)
+    t = place(torch.tensor(rng.integers(-9, 9, (M, V)).astype(np.float64)), dtype, 1, 0)
+    tokens = rng.integers(0, V, M).astype(np.int32)
+    check(forward(t, torch.tensor(tokens).cuda(), inv_t, 5), in_fp32(define(t, tokens, inv_t, 5)), V)
