@@ -590,8 +590,8 @@ size_t lora_mx4_proj_workspace_bytes(int M, const lora_route *rt);
  * between, s A_s x_i is held in fp32 (LORA_MX4_PATH_ROWS) or as the sum of two
  * bf16, within 2^-17 of it (LORA_MX4_PATH_TILES).
  * Every row rule, the status word (lora_status_get(ws)) and the errors are
- * those of lora_proj_apply; besides, K must be a multiple of 32, and codes and
- * scales non-NULL, codes 16-byte aligned. y rows may have any stride >= N.
+ * those of lora_proj_apply; besides, K must be a multiple of 32, M at most
+ * 65535 * 256, and codes and scales non-NULL, codes 16-byte aligned. y rows may have any stride >= N.
  */
 lora_status lora_mx4_proj_apply(const void *x, int64_t x_stride, const uint8_t *codes, const uint8_t *scales, int M,
                                 int K, int N, const int32_t *seq_slot, const lora_route *rt, void *y,

@@ -1531,6 +1531,8 @@ lora_status lora_mx4_proj_apply_ex(const void *x, int64_t x_stride, const uint8_
                     M, K, N, K, rt->n_out, rt->n_in);
     if (K % LORA_MX4_BLOCK != 0)
         return fail(LORA_ERR_SHAPE, "%s: K %d must be a multiple of %d", who, K, LORA_MX4_BLOCK);
+    if (M > MX4_MAX_ROWS)
+        return fail(LORA_ERR_UNSUPPORTED, "%s: M %d rows are more than the %d that one launch takes", who, M, MX4_MAX_ROWS);
     if (M == 0)
         return ok();
     if (codes == nullptr || scales == nullptr)

@@ -673,7 +673,8 @@ cudaError_t launch_mx4_shrink(const Mx4ProjParams &p, int num_sms, cudaStream_t 
     //   rows  2048         4096          8192
     //   many  61.0  60.1   110.9 109.6   199.0 199.1 us
     //   other 65.5  54.7   123.8 106.7   235.7 199.4
-    if (p.M >= 2048 && p.R > 16) {
+    // (and of more than 65535 times 64 rows the other's chunks are not a grid's)
+    if (p.M >= 2048 && (p.R > 16 || p.M > 65535 * SH_ROWS)) {
         static std::atomic<uint64_t> raised{0};
         const cudaError_t e = raise_smem_limit(raised, mx4_shrink_many_kernel, (int)SM_BYTES);
         if (e != cudaSuccess)

@@ -51,6 +51,8 @@ struct Mx4ProjParams {
 cudaError_t launch_mx4_quantize(const Mx4QuantParams &p, int dtype, cudaStream_t st);
 cudaError_t launch_mx4_dequantize(const Mx4DequantParams &p, int dtype, cudaStream_t st);
 cudaError_t launch_mx4_shrink(const Mx4ProjParams &p, int num_sms, cudaStream_t st);
+// Most rows of a call: tiles of rows, and chunks of the shrink, are a grid's y and z.
+constexpr int MX4_MAX_ROWS = 65535 * 256;
 // The product for up to four rows; `codes`: bytes [N][K / 2], boxes of 128 bytes x 16 rows, 128-byte swizzle.
 bool mx4_rows_fit(int M, int K, int R);
 cudaError_t launch_mx4_rows(const Mx4ProjParams &p, const CUtensorMap &codes, int num_sms, cudaStream_t st);

@@ -888,7 +888,7 @@ Mx4TcPlan plan_mx4_tc(const Mx4ProjParams &p, int num_sms)
     Mx4TcPlan plan{0, 1};
     int64_t least = 0;
     const int fewest = (p.M + MAX_TN - 1) / MAX_TN;
-    for (int t = fewest; t <= 4 * fewest; ++t) {
+    for (int t = fewest; t <= 4 * fewest && t <= 65535; ++t) {
         const int each = (p.M + t - 1) / t, tn = (each + 15) / 16 * 16;
         const int64_t ctas = (int64_t)ftiles * ((p.M + tn - 1) / tn);
         const int sub = tn <= 128 ? 335 + (tn > 64 ? (tn - 64) * 7 / 8 : 0) : 2 * tn + 5 > 390 ? 2 * tn + 5 : 390;

@@ -19,3 +19,10 @@ def test_inverse_temperatures_that_the_arithmetic_does_not_take(inv_t):
            contains=("inv_temperature",))
     expect(rd.LORA_ERR_RANGE, lambda: rd.lora_logprobs_grad(4096, rd.LORA_DTYPE_F32, 100, 0, 100, 256, inv_t, 256, 256, 256, 256, 8192,
                                                             100), contains=("inv_temperature",))
+
+
+def test_projections_of_more_rows_than_a_launch_takes():
+    from tests.test_abi_cpu import fake_route
+    rt = fake_route(L=4, R=8, K=256, N=256)
+    expect(rd.LORA_ERR_UNSUPPORTED, lambda: rd.lora_mx4_proj_apply(4096, 256, 8192, 513, 65535 * 256 + 1, 256, 256, 4096, rt, 4096, 256,
+                                                                   1 << 20, 1 << 62), contains=("16776961",))
