@@ -45,6 +45,7 @@ lora_status ok()
 
 lora_status cuda_fail(cudaError_t e, const char *what)
 {
+    (void)cudaGetLastError(); // it is reported here; left behind, the next call would report it once more
     return fail(LORA_ERR_CUDA, "%s: CUDA error %d (%s)", what, (int)e, cudaGetErrorString(e));
 }
 
