@@ -1581,24 +1581,23 @@ lora_status lora_mx4_proj_apply_ex(const void *x, int64_t x_stride, const uint8_
     test_hook_get(q.wait_ns, q.never);
     if (q.wait_ns == 0)
         q.wait_ns = WAIT_NS;
-    if ((e = launch_mx4_shrink(q, di.num_sms, st)) != cudaSuccess)
-        return cuda_fail(e, who);
+    // the maps first: where one cannot be encoded, nothing has been enqueued
+    Mx4TcPlan plan{0, 0};
+    Mx4TcMaps maps;
+    memset(&maps, 0, sizeof maps);
     if (tiles) {
-        const Mx4TcPlan plan = plan_mx4_tc(q, di.num_sms);
-        Mx4TcMaps maps;
-        memset(&maps, 0, sizeof maps);
-        if (!make_map(&maps.x, x, (uint64_t)K, (uint64_t)M, (uint64_t)x_stride, 64, (uint32_t)plan.tn) ||
-            !make_map_bytes(&maps.codes, codes, (uint64_t)(K / 2), (uint64_t)N, 128, 128, true))
-            return fail(LORA_ERR_CUDA, "%s: encoding the tensor maps failed", who);
+        plan = plan_mx4_tc(q, di.num_sms);
+        const int64_t map_stride = M > 1 ? x_stride : K; // one row has none, and a map's ends at 2^40 bytes
+        if (!make_map(&maps.x, x, (uint64_t)K, (uint64_t)M, (uint64_t)map_stride, 64, (uint32_t)plan.tn))
+            return fail(LORA_ERR_CUDA, "%s: encoding the tensor map of x failed", who);
         maps.scales_ok = K % 512 == 0 && aligned16(scales) &&
                          make_map_bytes(&maps.scales, scales, (uint64_t)(K / 32), (uint64_t)N, 16, 128, false);
-        e = launch_mx4_tc(q, plan, maps, st);
-    } else {
-        CUtensorMap map;
-        if (!make_map_bytes(&map, codes, (uint64_t)(K / 2), (uint64_t)N, 128, 16, true))
-            return fail(LORA_ERR_CUDA, "%s: encoding the tensor map failed", who);
-        e = launch_mx4_rows(q, map, di.num_sms, st);
     }
+    if (!make_map_bytes(&maps.codes, codes, (uint64_t)(K / 2), (uint64_t)N, 128, tiles ? 128 : 16, true))
+        return fail(LORA_ERR_CUDA, "%s: encoding the tensor map of the codes failed", who);
+    e = launch_mx4_shrink(q, di.num_sms, st);
+    if (e == cudaSuccess)
+        e = tiles ? launch_mx4_tc(q, plan, maps, st) : launch_mx4_rows(q, maps.codes, di.num_sms, st);
     if (e != cudaSuccess)
         return cuda_fail(e, who);
     return ok();

@@ -1,4 +1,5 @@
-"""The 4-bit projection of millions of rows: more chunks of 64 rows than a grid's last dimension has.
+"""The 4-bit projection at the ends of its row counts and strides: more chunks of 64 rows than a
+grid's last dimension has, and one row with any stride.
 
 Tolerance as in test_gpu_mx4_adapters: the fp32 sums, 2^-17 of the adapter's part,
 and one rounding of y to bf16, 2^-8 of it."""
@@ -7,7 +8,7 @@ import torch
 
 import rank_delta_gb300 as rd
 from rank_delta_gb300 import torch_helpers as th
-from tests.test_gpu_mx4 import lib, nibbles, quantise, values  # noqa: F401
+from tests.test_gpu_mx4 import Setup, lib, nibbles, quantise, values  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -36,3 +37,15 @@ def test_millions_of_rows(M):
     assert rd.lora_status_get(ws) == 0
     bad = (y.double() - want).abs() > 2.0 ** -8 * want.abs() + (2.0 ** -16 + 66 * 2.0 ** -24) * size
     assert not bool(bad.any()), (int(bad.sum()), torch.nonzero(bad)[:3].tolist())
+
+
+@pytest.mark.parametrize("path", [rd.LORA_MX4_PATH_ROWS, rd.LORA_MX4_PATH_TILES])
+@pytest.mark.parametrize("stride", [1 << 39, 1 << 50])
+def test_one_row_may_have_any_stride(path, stride):
+    s = Setup(1, 512, 200, 2, 16, seed=4)
+    want = s.run(path)
+    y, ws = torch.empty_like(want), th.workspace(rd.lora_mx4_proj_workspace_bytes(1, s.route.rt))
+    rd.lora_mx4_proj_apply(s.x, stride, s.codes, s.scales, 1, 512, 200, torch.tensor(s.slots).cuda(), s.route.rt, y, stride + 1, ws,
+                           ws.numel(), None, path)
+    torch.cuda.synchronize()
+    assert torch.equal(y.view(torch.int16), want.view(torch.int16))
