@@ -542,7 +542,8 @@ __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4])
 __global__ void __launch_bounds__(SH_THREADS, 1) mx4_shrink_many_kernel(Mx4ProjParams p)
 {
     extern __shared__ uint8_t sm_raw[];
-    __shared__ int slots_s[SM_CHUNK], sorted_s[SM_CHUNK], unit_s[SM_CHUNK];
+    __shared__ alignas(16) int slots_s[SM_CHUNK]; // read four at a time
+    __shared__ int sorted_s[SM_CHUNK], unit_s[SM_CHUNK];
     __shared__ uint32_t starts_s[SM_CHUNK / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int r0 = blockIdx.x * SM_RANKS, c0 = (int)blockIdx.z * SM_CHUNK;
