@@ -836,21 +836,27 @@ struct TcLaunch {
     }
 };
 
-// How many clusters of `kparts` CTAs the device runs at a time: its SMs come in
-// groups that a cluster does not cross.
+// How many clusters of `kparts` CTAs the current device runs at a time: its SMs come
+// in groups that a cluster does not cross. Asked once a device; an answer that could
+// not be had (0) is asked for again.
+constexpr int MAX_DEVICES = 64;
 template <typename RINGS> int clusters_at_once(int kparts, int num_sms)
 {
-    static std::atomic<int> known[MAX_KPARTS + 1];
-    int n = known[kparts].load();
-    if (n == 0) {
-        TcLaunch l;
-        if (l.fill<RINGS>(16, kparts, dim3((unsigned)(kparts * num_sms)), nullptr) != cudaSuccess ||
-            cudaOccupancyMaxActiveClusters(&n, mx4_tc_kernel<RINGS>, &l.cfg) != cudaSuccess || n < 1) {
-            (void)cudaGetLastError();
-            n = -1;
-        }
-        known[kparts].store(n);
+    static std::atomic<int> known[MAX_DEVICES][MAX_KPARTS + 1];
+    int dev = -1, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) {
+        (void)cudaGetLastError();
+        return 0;
     }
+    if ((n = known[dev][kparts].load()) > 0)
+        return n;
+    TcLaunch l;
+    if (l.fill<RINGS>(16, kparts, dim3((unsigned)(kparts * num_sms)), nullptr) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, mx4_tc_kernel<RINGS>, &l.cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return 0;
+    }
+    known[dev][kparts].store(n);
     return n;
 }
 
