@@ -23,6 +23,8 @@
 // With few feature tiles K is split over a cluster of CTAs, whose partial
 // tiles are exchanged through distributed shared memory: each part sums and writes
 // some of the features.
+#include <algorithm>
+
 #include "lora_mx4.cuh"
 #include "ptx.cuh"
 #include "vec.cuh"
@@ -886,15 +888,25 @@ using Rings256 = Rings<256, 1, 4, 2, 2, 256, true>;
 // an SM runs one after another: set-up, what 64 k take (the widening up to 64
 // rows, the products from some 170 on), and the epilogue, with the exchange if
 // there is one. Measured where it decides, 16 adapters of rank 64:
-// 256x4096x4096 27.7 us as 256 rows in two parts, 23.5 as twice 128;
-// 512x4096x6144 with 32 adapters 55.3 us as twice 256, 51.5 as three times 176.
+// 256x4096x4096 26.0 us as 256 rows in two parts, 22.9 as twice 128;
+// 512x4096x6144 with 32 adapters 57.4 us as twice 256, 54.8 as three times 176.
+// Where the fewest tiles are more CTAs than SMs it is no guide to heights that differ
+// by little: the shrink's CTAs take SMs from the first wave, and tiles that begin in the
+// middle of an adapter's run of rows meet more of them. Only tiles of up to 256 and of
+// up to 128 rows are compared there. Us with adapters, these and any height by the estimate:
+//   rows       1100       1536        2048        4096        6000
+//   N  4096    54.6 54.5  64.4  63.0  63.4  76.4  112.7 126.3 165.2 169.3
+//   N  6144    54.2 56.6  63.9  63.8  81.3  85.2  155.8 160.4 216.9 214.5
+//   N 14336   105.7 105.8 131.8 142.8 170.9 170.8
 Mx4TcPlan plan_mx4_tc(const Mx4ProjParams &p, int num_sms)
 {
     const int ftiles = (p.N + BM - 1) / BM, nst = (p.K / 32 + 1) / 2, nsteps = (nst + 3) / 4;
     Mx4TcPlan plan{0, 1};
     int64_t least = 0;
     const int fewest = (p.M + MAX_TN - 1) / MAX_TN;
-    for (int t = fewest; t <= 4 * fewest && t <= 65535; ++t) {
+    const bool waves = (int64_t)ftiles * fewest > num_sms;
+    const int last = waves ? std::min((p.M + 127) / 128, 65535) : 4 * fewest;
+    for (int t = fewest; t <= last; t = waves && t < last ? last : t + 1) {
         const int each = (p.M + t - 1) / t, tn = (each + 15) / 16 * 16;
         const int64_t ctas = (int64_t)ftiles * ((p.M + tn - 1) / tn);
         const int sub = tn <= 128 ? 335 + (tn > 64 ? (tn - 64) * 7 / 8 : 0) : 2 * tn + 5 > 390 ? 2 * tn + 5 : 390;
