@@ -1439,11 +1439,11 @@ lora_status check_mx4(const char *who, const void *w, int dtype, int64_t w_strid
 // The path a call takes by itself. The rows kernel and tiles in us, every row of
 // an adapter of its own of rank 64 (K = 1024: 16):
 //   K x N         1 row        2 rows       4 rows
-//   1024 x  4096   6.3   7.2    6.3   7.4    6.3   7.7
-//   4096 x  4096   8.1   9.5    8.5   9.7    9.7   9.8
-//   8192 x  4096  11.8  12.6   11.9  12.8   12.4  12.9
-//   4096 x 14336  15.3  18.5   17.4  19.4   21.8  20.2
-//   4096 x 32000  29.9  36.1   33.3  36.4   40.2  37.5
+//   1024 x  4096   6.4   7.7    6.7   7.9    7.3   8.4
+//   4096 x  4096   8.7  10.0    8.9  10.2    9.9  10.4
+//   8192 x  4096  12.2  12.8   12.3  13.1   12.6  13.2
+//   4096 x 14336  16.2  18.7   17.4  19.4   21.5  20.6
+//   4096 x 32000  30.9  35.7   33.1  36.3   40.3  38.4
 // The rows kernel multiplies each row by its B on the CUDA cores: three and four
 // rows of many features are for tiles.
 int mx4_path(int M, int K, int N, int R, int path)

@@ -772,7 +772,9 @@ template <bool TOP> struct Left {
 // and the exponentials bound it. 4096 x 32000 f32: 80 us, 6.6 TB/s, HBM. FIN warps
 // finish rows in turn: with more than FEW alternatives that takes longer than
 // reading, and two are worth the registers they take from the others (the best
-// 20: 151 us, some 35 more with one; the best 5: 128, some 13 more with two).
+// 20: 151 us, some 35 more with one; the best 5: 128, some 13 more with two). What does
+// not fit the registers of three CTAs an SM is in local memory: up to 48 bytes a thread
+// with one of them, 144 with two.
 template <typename T, bool TOP, int FIN>
 __global__ void __launch_bounds__(ROW_READERS + FIN * 32, ROW_CTAS) logprob_rows_kernel(LogprobParams p)
 {
@@ -1094,7 +1096,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprob_split_kernel(LogprobPar
 // but the token's own, whose g (1 - p) is -g expm1(log p): where p is near 1 the
 // difference of g and g p would keep few digits. a = x c - (m c + log S log2 e), the
 // latter held as two fp32 numbers so that p is as good as fp32 allows.
-// 8192 x 32000 bf16: 150 us, 7.0 TB/s, HBM; 96 x 32003 f32 with entropy 4.9 us.
+// 8192 x 32000 bf16: 150 us, 7.0 TB/s, HBM; 96 x 32003 f32 with entropy 4.5 us.
 template <typename T, bool BONUS>
 __global__ void __launch_bounds__(LP_THREADS, 6) logprob_grad_kernel(LogprobGradParams p, int segs)
 {
@@ -1214,6 +1216,14 @@ template <typename T> cudaError_t launch_lp(const LogprobParams &p, int num_sms,
     //    64 x  32000 f32    4.2  9.6 10.2   4.1  8.0  8.4   4.0  7.1  8.5
     //   200 x  32000 f32    7.6 12.0 13.4   7.5 10.1 15.3   7.6 10.1 13.4
     //    90 x 131072 f32   10.9 15.6 17.8  14.2 18.8 21.1  10.8 15.7 17.9
+    // Around `shortest`, us for the best 1, 5 and 20 with 1, 2, 4 and 8 parts (f32):
+    //     1 x  32003    6.2  7.4 12.2   8.0  8.3  9.2   7.4  7.8  8.2   7.2  7.7  8.0
+    //    64 x  32003    6.5  7.9 12.8   8.4  8.5  9.6   8.1  8.5  9.0   9.6 10.2 10.8
+    //     1 x  50000    7.5  9.4 16.1   8.6  8.9  9.7   7.9  8.1  8.8   7.4  7.8  8.2
+    //    64 x  50000    8.3  9.4 16.6   9.0  9.0 10.1   8.8  9.1 10.1  10.3 10.9 11.7
+    //   200 x  65536   15.3 17.9 27.4  15.8 16.5 18.5  22.5 23.3 25.8  29.7 31.1 33.3
+    // (Rows of 256 KB in bf16 would rather stay whole in a call of 200 with up to eight
+    // alternatives: 200 x 131072 16.4 and 19.1 us whole, 20.8 and 21.6 in two parts.)
     const bool few = p.top_k > 0 && p.top_k <= FEW;
     const int64_t shortest = few ? 140 << 10 : 40 << 10, longest = p.top_k > FEW ? 112 << 10 : 224 << 10;
     const int64_t nvec = ((int64_t)p.V + Vec<T>::E - 1) / Vec<T>::E;
@@ -1221,12 +1231,20 @@ template <typename T> cudaError_t launch_lp(const LogprobParams &p, int num_sms,
     while (parts < 8 && nvec * 16 > shortest && nvec >= 2 * parts * LP_THREADS &&
            ((int64_t)p.M * parts < num_sms || ((int64_t)p.M * parts < 2 * num_sms && nvec * 16 / parts > longest)))
         parts *= 2;
-    // More short rows than CTAs that take whole ones: a warp each. us for the best 0, 5
+    // More short rows than CTAs that take whole ones: a warp each. us for the best 0, 1, 5
     // and 20, whole rows by CTAs and by warps:
-    //   1000 x  8000 bf16   7.4 15.4 14.8    6.7  8.5 12.7
-    //   8170 x  3188 bf16  41.4 81.9 87.8   15.6 26.2 34.4
-    //   2000 x 14000 bf16  16.2 29.3 31.9   14.8 22.5 34.3
-    //   2000 x  8000 f32   13.5 24.0 25.5   15.2 20.2 34.0
+    //   1000 x  8000 bf16   7.5 13.8 15.4 15.2    6.8  8.5  8.8 13.0
+    //   8170 x  3188 bf16  41.4 73.2 82.4 87.9   15.5 24.8 26.3 34.4
+    //   1000 x 14000 bf16  10.1 16.7 18.6 20.0   12.5 14.0 15.7 22.7
+    //   2000 x 14000 bf16  16.3 25.8 29.3 32.0   14.9 20.2 23.0 34.6
+    //   8170 x 14000 bf16  57.9 84.7 98.0  102   43.2 53.4 62.8 96.5
+    //   8170 x 20000 bf16  73.9 96.3  110  126   61.0 72.9 96.6  183
+    //   2000 x  8000 f32   13.5 20.3 23.9 25.5   15.2 17.2 20.1 33.9
+    //   8170 x  8000 f32   42.3 66.0 80.6 79.7   45.1 55.2 68.1  120
+    // The cut is at 16 KB, below which warps take down to a third of the time (and up to
+    // 1.7 us longer in calls of 500 rows). Between that and 40 KB thousands of rows with few
+    // alternatives would be up to 37 % shorter by warps, hundreds of rows or twenty
+    // alternatives up to half as long again.
     if (parts == 1 && nvec <= SHORT_VECS && p.M > ROW_CTAS * num_sms)
         return launch_behind(p.top_k > 0 ? logprob_short_kernel<T, true> : logprob_short_kernel<T, false>,
                              dim3((unsigned)(((int64_t)p.M + LP_WARPS - 1) / LP_WARPS)), LP_THREADS, 0, 1, st, p);

@@ -426,7 +426,8 @@ __device__ __forceinline__ void shrink_tile(const Mx4ProjParams &p, const uint16
 // chunk, the u-th distinct slot of the chunk), by chunks of CHUNK rows and `takes` CTAs
 // for 64 rows of the slot each. Each thread multiplies 8
 // consecutive k of two rank rows and of the slot's rows at a time: which k a
-// fragment's slots mean is free as long as both operands agree.
+// fragment's slots mean is free as long as both operands agree. (16 warps have 128
+// registers a thread; 56 bytes more are in local memory.)
 template <int CHUNK> __global__ void __launch_bounds__(SH_THREADS) mx4_shrink_kernel(Mx4ProjParams p, int takes)
 {
     __shared__ uint32_t present[MAX_BUCKETS / 32];
@@ -672,8 +673,8 @@ cudaError_t launch_mx4_shrink(const Mx4ProjParams &p, int num_sms, cudaStream_t 
     // Many rows and more than 16 ranks, of which the other kernel reads x for each:
     // a call of K = N = 4096, 16 slots of rank 64 (then 32 of rank 16), takes
     //   rows  2048         4096          8192
-    //   many  61.0  60.1   110.9 109.6   199.0 199.1 us
-    //   other 65.5  54.7   123.8 106.7   235.7 199.4
+    //   many  63.6  61.8   112.7 111.9   203.3 202.9 us
+    //   other 69.6  57.7   132.2 111.6   248.4 209.0
     // (and of more than 65535 times 64 rows the other's chunks are not a grid's)
     if (p.M >= 2048 && (p.R > 16 || p.M > 65535 * SH_ROWS)) {
         static std::atomic<uint64_t> raised{0};
@@ -689,9 +690,9 @@ cudaError_t launch_mx4_shrink(const Mx4ProjParams &p, int num_sms, cudaStream_t 
     // A CTA takes all registers of its SM, and the projection's have to wait for it: the
     // fewer have work the better. Chunks of 64 and of 256 rows, 16 adapters of rank 64 at
     // N = 4096, then 32 of rank 64 and 32 of rank 16 at N = 6144:
-    //   128 rows   17.5  17.3   27.4  25.9   20.4  19.7 us
-    //   256 rows   22.7  21.1   36.0  33.4   25.7  25.9
-    //   512 rows   33.0  29.7   51.5  46.2   34.4  32.3
+    //   128 rows   18.5  18.3   30.3  28.6   22.2  21.5 us
+    //   256 rows   25.3  23.1   40.8  37.6   27.5  27.3
+    //   512 rows   36.3  32.2   62.0  55.6   37.5  35.3
     const int chunk = p.M > SH_ROWS ? 256 : SH_ROWS;
     const int takes = std::min((p.M + SH_ROWS - 1) / SH_ROWS, chunk / SH_ROWS);
     return launch_behind(chunk == 256 ? mx4_shrink_kernel<256> : mx4_shrink_kernel<SH_ROWS>,
@@ -783,8 +784,9 @@ __device__ __forceinline__ void widen_pair(uint32_t a, uint32_t b, uint32_t fa, 
 // the row and the block so that the eight lanes of a load phase meet different
 // bank groups. Which k a fragment's slots mean is free as long as
 // both operands agree: thread t of four supplies the block t of 128 k.
-// What bounds it is the widening, 17 instructions for 8 codes: 1x4096x32000 takes
-// 30 us (2.3 TB/s of codes), 1x4096x4096 8.1 with its shrink.
+// 1x4096x32000 takes 30 us (2.3 TB/s of codes), 1x4096x4096 8.7 with its shrink. Issue
+// and waits bound it: 62 % of the issue slots are used, and half of the 17.7 million
+// instructions of a warp of the former call widen, 17 for 8 codes.
 __global__ void __launch_bounds__(RW_THREADS, 1)
     mx4_rows_kernel(const __grid_constant__ CUtensorMap codes, const __grid_constant__ Mx4ProjParams p, RowsShape shape)
 {

@@ -9,9 +9,11 @@
 // shared memory is left to x); x comes by TMA, and one thread issues the products.
 // The weight is widened once for all rows of the tile. With tiles of 256 rows
 // the tensor cores and what a tile takes before and after them bound it
-// (8192x4096x14336: 586 us, 550 without adapters, 1.75 PFLOP/s; a stage of 64 k
+// (8192x4096x14336: 598 us, 550 without adapters, 1.75 PFLOP/s; a stage of 64 k
 // takes 515 to 555 cycles, its products 512); with fewer rows it is the widening and what a
-// call takes in any case, shrink, set-up and epilogue (64x4096x4096: 14.5 us).
+// call takes in any case, shrink, set-up and epilogue (64x4096x4096: 15.7 us, 10.1
+// without adapters). Many adapters in a tile are as much work as the base: each of
+// them is multiplied with all rows (512x4096x6144 with 32 of rank 64: 55 us, 28 without).
 //
 // The adapters are more K: s h of the tile's rows (as two bf16, whose sum is good to
 // 2^-17; the sums stay fp32) against the B rows of each slot in the tile,
@@ -50,8 +52,8 @@ constexpr int SEGS = 2;
 //
 // 64 k take 2 tn cycles of the tensor cores. Up to about 128 rows that is less
 // than a stage's waits and commits, so a stage has two sub-tiles there
-// (64x4096x14336: 25.4 us, 6 % longer with one); above, two would leave two stages
-// only (256x4096x14336: 37.8 us with one, 19 % longer with two).
+// (64x4096x14336: 6 % longer with one); above, two would leave two stages
+// only (256x4096x14336: 19 % longer with two).
 //
 // Up to 128 rows the widened weights lie behind both accumulators; above it
 // they take the columns of the adapters' accumulator (ALIAS), which is not written
@@ -705,13 +707,14 @@ __global__ void __launch_bounds__(RINGS::THREADS, 1)
 #pragma unroll 8
                         for (int tok = c * 16; tok < min(c * 16 + 16, rows); ++tok)
                             p.y[(int64_t)(t0 + tok) * p.y_stride + f0 + f] = (uint16_t)lds_2(base + (uint32_t)tok * Y_ROW + (uint32_t)f * 2);
-            } else
-            for (int i = tid & 127; i < tn / GROUPS * 16 + 256; i += 128) {
-                const int tok = ((i >> 8) * GROUPS + group) * 16 + (i >> 4 & 15), f = (i & 15) * 8, feature = f0 + f;
-                if (tok >= rows)
-                    break;
-                const uint4 o = lds_16(base + (uint32_t)tok * Y_ROW + (uint32_t)f * 2);
-                store_8(p.y + (int64_t)(t0 + tok) * p.y_stride + feature, o, p.N - feature, vec);
+            } else {
+                for (int i = tid & 127; i < tn / GROUPS * 16 + 256; i += 128) {
+                    const int tok = ((i >> 8) * GROUPS + group) * 16 + (i >> 4 & 15), f = (i & 15) * 8, feature = f0 + f;
+                    if (tok >= rows)
+                        break;
+                    const uint4 o = lds_16(base + (uint32_t)tok * Y_ROW + (uint32_t)f * 2);
+                    store_8(p.y + (int64_t)(t0 + tok) * p.y_stride + feature, o, p.N - feature, vec);
+                }
             }
         }
         tc_fence_before();
