@@ -1241,15 +1241,20 @@ template <typename T> cudaError_t launch_lp(const LogprobParams &p, int num_sms,
     //   8170 x 20000 bf16  73.9 96.3  110  126   61.0 72.9 96.6  183
     //   2000 x  8000 f32   13.5 20.3 23.9 25.5   15.2 17.2 20.1 33.9
     //   8170 x  8000 f32   42.3 66.0 80.6 79.7   45.1 55.2 68.1  120
-    // The cut is at 16 KB, below which warps take down to a third of the time (and up to
-    // 1.7 us longer in calls of 500 rows). Between that and 40 KB thousands of rows with few
-    // alternatives would be up to 37 % shorter by warps, hundreds of rows or twenty
-    // alternatives up to half as long again.
-    if (parts == 1 && nvec <= SHORT_VECS && p.M > ROW_CTAS * num_sms)
+    //    700 x  8000 bf16   6.3  9.6 10.6 11.9    6.5  7.8  8.4 12.5
+    //    700 x  4000 f32    5.2  7.8  8.9  9.6    5.5  6.9  7.5 11.5
+    // The cut is at 16 KB, below which warps take down to a third of the time; but rows of
+    // more than 12 KB, of which no CTA has more than two, are left to CTAs without
+    // alternatives and with more than 16 (the best nine of 700: 11.5 and 9.6 us, 9.3 and
+    // 8.7). Between 16 and 40 KB thousands of rows with few alternatives would be up to 37 %
+    // shorter by warps, hundreds of rows or twenty alternatives up to half as long again.
+    const int at_once = ROW_CTAS * num_sms;
+    const bool two = nvec > SHORT_VECS * 3 / 4 && p.M <= 2 * at_once && (p.top_k == 0 || p.top_k > 2 * FEW);
+    if (parts == 1 && nvec <= SHORT_VECS && p.M > at_once && !two)
         return launch_behind(p.top_k > 0 ? logprob_short_kernel<T, true> : logprob_short_kernel<T, false>,
                              dim3((unsigned)(((int64_t)p.M + LP_WARPS - 1) / LP_WARPS)), LP_THREADS, 0, 1, st, p);
     if (parts == 1) { // as many CTAs as stay resident, each with rows one after another
-        const dim3 grid((unsigned)(p.M < ROW_CTAS * num_sms ? p.M : ROW_CTAS * num_sms));
+        const dim3 grid((unsigned)(p.M < at_once ? p.M : at_once));
         return launch_behind(p.top_k > FEW  ? logprob_rows_kernel<T, true, 2>
                              : p.top_k > 0 ? logprob_rows_kernel<T, true, 1>
                                            : logprob_rows_kernel<T, false, 1>,
