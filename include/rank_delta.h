@@ -681,7 +681,7 @@ lora_status lora_logprobs_grad(const void *logits, int dtype, int64_t stride, in
 /* Largest vocabulary of lora_sample and lora_distill. */
 #define LORA_MAX_VOCAB 400000
 
-/* Workspace of lora_sample: the status words. */
+/* Workspace of lora_sample: the status words, and counts of the call behind them. */
 size_t lora_sample_workspace_bytes(int M, int V);
 
 /*
@@ -708,7 +708,8 @@ size_t lora_sample_workspace_bytes(int M, int V);
  *   tokens   device [M] int32
  *   logprob, kept   device [M] f32 and int32, each or NULL
  *   ws       device workspace of lora_sample_workspace_bytes bytes, for the
- *            status word
+ *            status word and the call's counts: of any contents, for one call at a
+ *            time
  * inv_temperature has to be at least 2^-64; above 2^64, +infinity included, the row's
  * token is the first of the order (temperature 0). A row with an inv_temperature
  * below, a uniform outside [0, 1] or a NaN among its settings gets token -1, logprob

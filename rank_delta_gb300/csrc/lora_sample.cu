@@ -2595,6 +2595,7 @@ __global__ void __launch_bounds__(256, 3) open_rows_kernel(SampleParams p, int p
             if (last && mine <= CallCounts::LISTED) {
                 const int at = team + turn * teams;
                 row = at < mine ? counts.listed(at) : p.M;
+                row = (uint32_t)row < (uint32_t)p.M ? row : p.M; // whatever else was written there
             } else {
                 while (open == 0u) {
                     int c = 0;
@@ -2683,10 +2684,11 @@ template <typename T> cudaError_t launch_typed(const SampleParams &p, int num_sm
             e = launch_behind(t.parts > 1 ? open_rows_kernel<T, true> : open_rows_kernel<T, false>, dim3((unsigned)(t.teams * t.parts)), 256, t.smem,
                               (unsigned)t.parts, st, p, t.parts, some(t.teams), most, 0);
             if (e != cudaSuccess)
-                return e;
+                return CallCounts::give_up(e, p.status, st);
         }
-        return launch_behind(open_rows_kernel<T, true>, dim3((unsigned)(wide * MAX_PARTS)), 256, smem, (unsigned)MAX_PARTS, st, p, MAX_PARTS,
-                             some(wide), most, 1);
+        e = launch_behind(open_rows_kernel<T, true>, dim3((unsigned)(wide * MAX_PARTS)), 256, smem, (unsigned)MAX_PARTS, st, p, MAX_PARTS,
+                          some(wide), most, 1);
+        return e == cudaSuccess ? e : CallCounts::give_up(e, p.status, st);
     }
     // Two warps a short row (8192 x 1000 bf16 of which nothing is cut 62 us, of top-p 51 us; eight warps 110 and 113 us),
     // four where top-k has to guess a bound from the threads' maxima, of which 64 are too few (top 50: 90 us, with two

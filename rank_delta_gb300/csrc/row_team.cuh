@@ -22,7 +22,10 @@ constexpr float LEAST = -3.402823466e38f; // the lowest finite value
 // with the call's tag above it, that count from 0 wherever they hold another tag;
 // and from there on rows that were counted. Every CTA of the call's first kernel
 // opens them before it uses them; the epoch that the tag is made of moves on when
-// the last CTA of its last kernel has been counted, after all have read it.
+// the last CTA of its last kernel has been counted, after all have read it. That CTA
+// clears them first: the epoch lies in the workspace too, and where it goes back (memory
+// handed out again, a caller that clears the front), counts that stood under a tag
+// would pass for the next call's own.
 struct CallCounts {
     static constexpr int LISTED = 50; // 64 words
     enum { ENDED = 4, NEXT = 6, OPENED = 8, AGAIN = 10, NEXT_AGAIN = 12, ROWS = 14 };
@@ -65,8 +68,22 @@ struct CallCounts {
         if (flags != 0u)
             flag(flags);
         const uint32_t was = (uint32_t)atomicAdd(w, 1ull);
-        if ((was & 0xFFFFFFu) + 1u == ctas)
+        if ((was & 0xFFFFFFu) + 1u == ctas) {
+            clear();
             status_begin(st, was >> 24);
+        }
+    }
+    __device__ __forceinline__ void clear() const
+    {
+#pragma unroll
+        for (int word = ENDED; word < ROWS; word += 2)
+            *reinterpret_cast<volatile u64 *>(st + word) = 0ull;
+    }
+    // A call whose kernels could not all be launched: what the first has counted ends here, since nothing moves its epoch on.
+    static cudaError_t give_up(cudaError_t e, uint32_t *status, cudaStream_t stream)
+    {
+        cudaMemsetAsync(status + ENDED, 0, (ROWS - ENDED) * sizeof(uint32_t), stream);
+        return e;
     }
 };
 
