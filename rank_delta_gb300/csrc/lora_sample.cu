@@ -203,7 +203,9 @@ template <int W> __device__ __forceinline__ void team_sync(int parts)
     }
 }
 
-// The sum of a value over all threads of the team.
+// The sum of a value over all threads of the team, by way of place AT. The others' CTAs
+// read this one's after the team has met: a place is written again only behind another
+// meeting of the team (a sum at another place, say), not behind barriers of a CTA alone.
 template <int AT, int W> __device__ __forceinline__ u64 team_sum(Shared<W> &sm, u64 v, int parts)
 {
     const int lane = threadIdx.x & 31;
@@ -792,7 +794,8 @@ __device__ __noinline__ void exact_row(Shared<W> &sm, const Row<T, W> r, const S
         sm.warp_mass[r.warp] = own;
         sm.warp_ties[r.warp] = ties;
     }
-    above = (int)team_sum<2>(sm, (u64)above, parts); // and a barrier
+    // and a barrier; not by place 2, which others may still read where nothing was cut by rank or sum since
+    above = (int)team_sum<5>(sm, (u64)above, parts);
     u64 before = 0ull, total = 0ull;
     int ties_before = 0, ties_all = 0;
     for (int w = 0; w < W; ++w) {
