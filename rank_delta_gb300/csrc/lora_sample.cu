@@ -1300,6 +1300,20 @@ __device__ __noinline__ bool fine_row(Shared<W> &sm, const Row<T, W> r, const Sa
 // Where it is needed once a row: code that has to be fetched costs more than the call.
 __device__ __noinline__ u64 weight_once(const Scale s, float x, int bits, const u64 *powers) { return weight(s, x, bits, powers); }
 
+// min_p in the unit 2^-scale of listed weights, upwards; and whether a weight w in that unit is so near it that
+// its rounding may decide: half a unit and 2^-43 of w it is off by, up to a unit is `least`. Such a row is left open,
+// for the ways that compare values instead.
+__device__ __forceinline__ u64 min_p_units(float min_p, int scale)
+{
+    const float mp = min_p * __uint_as_float((uint32_t)(127 + scale) << 23);
+    return min_p > 0.0f ? (u64)mp + ((float)(u64)mp < mp ? 1ull : 0ull) : 0ull;
+}
+__device__ __forceinline__ bool at_border(u64 w, u64 least)
+{
+    const u64 off = 2ull + (w >> 40);
+    return w + off >= least && w <= least + off;
+}
+
 // A bound for what is kept, from the threads' own maxima: at least `need` of them
 // (or of their weight, in 2^-20) lie above it. -infinity where they do not suffice.
 __device__ __forceinline__ float guide_bound(uint32_t first_bin, uint32_t second_bin, uint32_t need, float m, float lowest, float per_bin, int lane)
@@ -1427,9 +1441,7 @@ __device__ __noinline__ bool finish_warp(const u64 *powers, Entry *list, const S
             keep[r] = keep[r] && in;
         }
     }
-    // w >= min_p: min_p in the weights' unit, upwards
-    const float mp = min_p * __uint_as_float((uint32_t)(127 + scale) << 23);
-    const u64 least = min_p > 0.0f ? (u64)mp + ((float)(u64)mp < mp ? 1ull : 0ull) : 0ull;
+    const u64 least = min_p_units(min_p, scale);
     const bool zero = u < 0x1p-40f;
     const float floor0 = fmaxf(s.m - 1000.0f / s.c, LEAST);
     int kept = 0;
@@ -1437,9 +1449,10 @@ __device__ __noinline__ bool finish_warp(const u64 *powers, Entry *list, const S
 #pragma unroll
     for (int r = 0; r < PER; ++r) {
         const int at = r * 32 + lane;
+        const float x = order_value((uint32_t)(key[r] >> 32));
+        open |= keep[r] && x != s.m && min_p > 0.0f && at_border(w[r], least); // w = 1 of the best and its equals is exact
         keep[r] = keep[r] && (w[r] >= least || (ordered && at == 0));
         kept += keep[r];
-        const float x = order_value((uint32_t)(key[r] >> 32));
         by_index[r] = keep[r] && !(zero && x < floor0) ? (0xFFFFFFFFu - (uint32_t)key[r]) << 7 | at : 0xFFFFFFFFu;
     }
     if (__any_sync(0xffffffffu, open))
@@ -1586,13 +1599,12 @@ __device__ __noinline__ bool finish_list(S &sm, Entry *list, const SampleParams 
             keep[o] = keep[o] && in;
         }
     }
-    // w >= min_p: min_p in the weights' unit, upwards
-    const float mp = a.least * __uint_as_float((uint32_t)(127 + scale) << 23);
-    const u64 least = a.least > 0.0f ? (u64)mp + ((float)(u64)mp < mp ? 1ull : 0ull) : 0ull;
+    const u64 least = min_p_units(a.least, scale);
     sum = 0ull;
     int kept = 0;
 #pragma unroll
     for (int o = 0; o < OWN; ++o) {
+        open |= keep[o] && x[o] != s.m && a.least > 0.0f && at_border(w[o], least); // w = 1 of the best and its equals is exact
         keep[o] = keep[o] && (w[o] >= least || (ordered && ahead[o] == 0));
         sum += keep[o] ? w[o] : 0ull;
         kept += keep[o];

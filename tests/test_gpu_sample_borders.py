@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from tests.test_gpu_sample import lib, place, sample  # noqa: F401
-from tests.test_gpu_sample_rows import BF16
+from tests.test_gpu_sample_rows import BF16, F32, compare
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +33,65 @@ def test_exact_sums_by_clusters(M, V, how):
         tok, got_lp, got_kept, flags = sample(x, [0.0] * M, None, None, None, q)
         assert flags == 0 and (tok == 0).all() and (got_kept == kept).all()
         assert np.abs(got_lp - lp).max() <= 6e-6 + 2.0 ** -21 * np.abs(lp).max()
+
+
+def around(q, t, m):
+    """The f32 that lies nearest to m + log(q) / t, and the three on either side."""
+    x = np.float32(m + np.log(q) / t)
+    out = [x]
+    for way in (-np.inf, np.inf):
+        y = x
+        for _ in range(3):
+            y = np.nextafter(y, np.float32(way))
+            out.append(y)
+    return [float(a) for a in out]
+
+
+# short rows, a CTA a row, clusters, and many rows
+PATHS = [(9, 2, 0), (12, 100, 5), (470, 700, 5), (12, 5001, 5), (6, 70000, 5), (630, 2100, 5)]
+
+
+@pytest.mark.parametrize("m", [0.0, -6.5, 1000.0])
+@pytest.mark.parametrize("M,V,others", PATHS)
+def test_elements_a_few_steps_from_the_border(M, V, others, m):
+    """min-p of 2^-5 to 2^-39, elements of f32 up to three steps on either side of its border: 1e-6 of their weight and
+    less, where a unit of 2^-53 is up to 2^-14 of it."""
+    gen = torch.Generator().manual_seed(V)
+    x = torch.full((M, V), m - 200.0)
+    qs, ts, us = [], [], torch.rand(M, generator=gen).tolist()
+    for i in range(M):
+        q, t = 2.0 ** -[39, 25, 15, 5][i % 4], float(np.float32([1.0, 0.75, 1.3][i % 3]))
+        at = torch.randperm(V, generator=gen)[:2 + others].tolist()
+        near = around(q, t, m)
+        x[i, at[0]] = m
+        for j, v in enumerate(at[1:]):
+            x[i, v] = near[(i + j) % len(near)]
+        qs.append(q)
+        ts.append(t)
+    assert compare(place(x, F32, 1, 1), us, ts, None, None, qs) == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M,V,others", PATHS)
+def test_a_setting_a_step_from_an_element(M, V, others, dtype):
+    """min_p is the weight of an element as fp32 has it, or one of the two numbers beside: 2^-24 of it apart."""
+    gen = torch.Generator().manual_seed(V + 1)
+    x = torch.full((M, V), -300.0)
+    qs, us = [], torch.rand(M, generator=gen).tolist()
+    for i in range(M):
+        at = torch.randperm(V, generator=gen)[:2 + others].tolist()
+        d = float(torch.tensor([-3.7, -9.3, -14.6, -26.9][i % 4]).to(dtype))
+        x[i, at[0]] = 0.0
+        x[i, at[1:]] = d
+        q = np.float32(np.exp(d))
+        qs.append(float([np.nextafter(q, np.float32(0)), q, np.nextafter(q, np.float32(1))][i % 3]))
+    assert compare(place(x, dtype, 1, 1), us, None, None, None, qs) == 0
+
+
+@pytest.mark.parametrize("M,V", [(3, 100), (6, 70000), (630, 2100)])
+def test_min_p_of_1_keeps_the_equals_of_the_best_alone(M, V):
+    """Elements a step below the best, at temperatures that bring their weights within 2^-60 of 1."""
+    x = torch.full((M, V), 8.0)
+    x[:, 1::2] = float(np.nextafter(np.float32(8.0), np.float32(0)))
+    ts = [[1.0, 2.0 ** -10, 2.0 ** -40][i % 3] for i in range(M)]
+    assert compare(place(x, F32, 0, 1), [0.7] * M, ts, None, None, [1.0] * M) == 0
