@@ -344,6 +344,18 @@ __device__ __forceinline__ void each_between(const Row<T, W> &r, float *queue, f
     __syncwarp();
 }
 
+// The lowest value that min-p keeps, min_p at most 1: the first of m + log(min_p) / t upwards. That sum may be
+// rounded past a neighbour; the difference of a value and m is exact, or so long that its last digits say nothing.
+__device__ __noinline__ float least_kept(float m, float t, float min_p)
+{
+    const double d = log((double)min_p) / (double)t, v = (double)m + d;
+    float x = v < (double)LEAST ? LEAST : __double2float_ru(v);
+    if (x < m && (double)x - (double)m < d)
+        x = nextafterf(x, m);
+    const float below = nextafterf(x, neg_inf());
+    return x > LEAST && (double)below - (double)m >= d ? below : x;
+}
+
 // What is kept: elements above `x`, and the first `ties` of those equal to it.
 struct Cut {
     float x;
@@ -645,10 +657,8 @@ __device__ __noinline__ void exact_row(Shared<W> &sm, const Row<T, W> r, const S
     team_sync<W>(parts);
     if (parts > 1)
         m = warp_top(lane < parts ? cl.map_shared_rank(&sm, lane)->cta_top : neg_inf());
-    if (a.least > 0.0f && tid == 0) { // the lowest value that min-p keeps: m + log(min_p) / t, upwards
-        const double v = (double)m + log((double)a.least) / (double)a.t;
-        sm.least = v < (double)LEAST ? LEAST : __double2float_ru(v);
-    }
+    if (a.least > 0.0f && tid == 0)
+        sm.least = least_kept(m, a.t, a.least);
     const Scale s = scale_of(m, a.t);
     // An exact weight w is the integer w 2^bits, in 2^62 the sum of all: a unit, by which each may be off in half, is
     // then below 2^-42 of the mean weight, whether a few elements have it all or all have as much.
@@ -938,10 +948,8 @@ __device__ __noinline__ bool fine_row(Shared<W> &sm, const Row<T, W> r, const Sa
     team_sync<W>(parts);
     if (parts > 1)
         m = warp_top(lane < parts ? cl.map_shared_rank(&sm, lane)->cta_top : neg_inf());
-    if (a.least > 0.0f && tid == 0) { // the lowest value that min-p keeps: m + log(min_p) / t, upwards
-        const double v = (double)m + log((double)a.least) / (double)a.t;
-        sm.least = v < (double)LEAST ? LEAST : __double2float_ru(v);
-    }
+    if (a.least > 0.0f && tid == 0)
+        sm.least = least_kept(m, a.t, a.least);
     const Scale s = scale_of(m, a.t);
     Cut cut{LEAST, 0x7fffffff}; // all
     float tie_weight = 0.0f;

@@ -95,3 +95,17 @@ def test_min_p_of_1_keeps_the_equals_of_the_best_alone(M, V):
     x[:, 1::2] = float(np.nextafter(np.float32(8.0), np.float32(0)))
     ts = [[1.0, 2.0 ** -10, 2.0 ** -40][i % 3] for i in range(M)]
     assert compare(place(x, F32, 0, 1), [0.7] * M, ts, None, None, [1.0] * M) == 0
+
+
+@pytest.mark.parametrize("M,V", [(4, 100), (4, 70000), (630, 2100)])
+def test_the_border_of_huge_logits(M, V):
+    """m = 2^30, elements 64 apart, min_p as near e^-64 as fp32 numbers come: m + log min_p has no such digits in 64 bits
+    (they end at 2^-22), the difference of an element and m has."""
+    m = 2.0 ** 30
+    q = np.float32(np.exp(-64.0))
+    near = [np.nextafter(q, np.float32(0)), q, np.nextafter(q, np.float32(1))]
+    x = torch.full((M, V), m - 640.0)
+    x[:, V // 2] = m
+    x[:, V // 3] = m - 64.0
+    want = lambda row, u, t, k, p, q: (V // 2, 0.0, 1 + int(-64.0 >= np.log(q)))  # noqa: E731
+    assert compare(place(x, F32), [0.5] * M, None, None, None, [float(near[i % 3]) for i in range(M)], want_of=want) == 0
