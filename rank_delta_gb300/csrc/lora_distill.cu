@@ -80,8 +80,8 @@ struct Numbers {
         rest_max = warp_top(a);
         m = max_nan(rest_max, warp_top(b));
         none = spoilt || !(m < -neg_inf());
-        empty = m == neg_inf();
-        no_rest = rest_max == neg_inf();
+        empty = !none && m == neg_inf();
+        no_rest = !none && rest_max == neg_inf();
     }
     template <int W> __device__ __forceinline__ void sums(const Found<W> &f, const Entries &en, const DistillParams &p, int parts, int lane)
     {
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(W * 32 + 32, W == 8 ? 3 : W == 4 ? 4 : 8) dist
                             : tg * (a.total * expf(a.below) / (1.0f + a.others) - a.q_rest / (a.rest_equal + a.rest_sum));
         const float shift = s.m;
         T *dx = static_cast<T *>(p.dlogits) + (int64_t)row * p.d_stride;
-        const bool zero = a.empty || (a.no_rest && !a.none);
+        const bool zero = a.empty || a.no_rest;
         const f2 nm = make_f2(-shift, -shift), c2 = make_f2(s.c, s.c), k2 = make_f2(slope, slope);
         const bool same = row_lead(dx) == row_lead(logits + (int64_t)row * p.stride);
         if (zero) {
