@@ -468,8 +468,53 @@ __global__ void __launch_bounds__(W * 32 + 32, W == 8 ? 3 : W == 4 ? 4 : 8) dist
 }
 
 namespace {
+
 constexpr int DG_THREADS = 256, DG_UNROLL = 4;
+
+// Statistics have log p_r to 2^-24 of itself, which is what p_v / p_r is off by (6e-5 at -256, all of it at -1e9, where
+// the others are masked by a finite value). Below this, a row whose rest has a share finds its rest's softmax again.
+constexpr float FAR_REST = -256.0f;
+
+// The whole row of dx, by one CTA: -k times the softmax of the others, `own` for the thread's named element (`id`,
+// or -1). dx may be x.
+template <typename T> __device__ __noinline__ void far_rest(const T *x, T *dx, int V, int id, float own, float t, float k)
+{
+    __shared__ float tops[DG_THREADS / 32];
+    __shared__ u64 sums[DG_THREADS / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (dx != x)
+        for (int i = tid; i < V; i += DG_THREADS)
+            dx[i] = x[i];
+    __syncthreads();
+    if (id >= 0)
+        dx[id] = Vec<T>::narrow(neg_inf());
+    __syncthreads();
+    float top = neg_inf();
+    for (int i = tid; i < V; i += DG_THREADS)
+        top = fmaxf(top, Vec<T>::widen(dx[i]));
+    top = warp_top(top);
+    if (lane == 0)
+        tops[warp] = top;
+    __syncthreads();
+    top = warp_top(tops[lane % (DG_THREADS / 32)]);
+    const float c = t * LOG2E, shift = top > neg_inf() ? top : 0.0f;
+    u64 sum = 0ull;
+    for (int i = tid; i < V; i += DG_THREADS)
+        sum += as_fixed(exp2_fast((Vec<T>::widen(dx[i]) - shift) * c), SUM_SCALE);
+    sum = warp_sum64(sum);
+    if (lane == 0)
+        sums[warp] = sum;
+    __syncthreads();
+    sum = warp_sum64(lane < DG_THREADS / 32 ? sums[lane] : 0ull);
+    const float each = sum != 0ull ? -k / ((float)sum * SUM_UNIT) : 0.0f;
+    for (int i = tid; i < V; i += DG_THREADS)
+        dx[i] = Vec<T>::narrow(exp2_fast((Vec<T>::widen(dx[i]) - shift) * c) * each);
+    __syncthreads();
+    if (id >= 0)
+        dx[id] = Vec<T>::narrow(own);
 }
+
+} // namespace
 
 // A CTA takes DG_UNROLL * DG_THREADS vectors of one row of dlogits; named elements
 // that lie among them are written over what the pass stored there. Bound by HBM and
@@ -508,6 +553,9 @@ template <typename T> __global__ void __launch_bounds__(DG_THREADS, 6) distill_g
     const float *st = p.stats + (int64_t)row * LORA_DISTILL_STATS;
     const float m = st[0], log_s = st[1], log_rest = st[2], q_rest = st[3], total = st[4], norm = st[5];
     const float tg = p.inv_t * p.g[row];
+    const bool far = q_rest > 0.0f && !(log_rest >= FAR_REST);
+    if (far && seg != 0) // the row is its first CTA's
+        return;
     // The named elements of this segment, an entry a thread (n <= DG_THREADS)
     __shared__ int ids[LORA_MAX_TEACHER];
     int id = -1;
@@ -520,7 +568,7 @@ template <typename T> __global__ void __launch_bounds__(DG_THREADS, 6) distill_g
     __syncthreads();
     if (id >= 0) {
         const int64_t at = ((int64_t)id + lead) / E;
-        if (id >= p.V || at < first || at >= first + DG_UNROLL * DG_THREADS)
+        if (id >= p.V || (!far && (at < first || at >= first + DG_UNROLL * DG_THREADS)))
             id = -1;
         for (int j = 0; j < tid && id >= 0; ++j)
             id = ids[j] == id ? -1 : id; // a token's first entry counts
@@ -529,15 +577,27 @@ template <typename T> __global__ void __launch_bounds__(DG_THREADS, 6) distill_g
         if (p.rest)
             val = val > 0.0f && val < -neg_inf() ? 0.0f : val;
     }
-    if (p.dlogits == p.logits)
+    if (far || p.dlogits == p.logits)
         __syncthreads(); // every element is read before any is written
     const bool empty = m == neg_inf(), none = !(m == m), no_rest = log_rest == neg_inf();
+    auto named = [&] {
+        const double log_p = ((double)xn - (double)m) * (double)p.inv_t - (double)log_s;
+        const double log_q = (double)val - (double)norm;
+        const float d = tg * named_slope((float)log_p, (float)log_q, (float)(log_p - log_q), total);
+        return none ? quiet_nan() : xn == neg_inf() ? 0.0f : d;
+    };
+    if (far) {
+        far_rest<T>(x, dx, p.V, id, id >= 0 ? named() : 0.0f, p.inv_t, tg * q_rest);
+        return;
+    }
     const bool zero = empty || (no_rest && !none);
-    const float slope = none ? quiet_nan() : zero ? 0.0f : tg * (total * expf(log_rest) - q_rest);
+    // Where the rest has no share, its slopes are t g Q p_v, and p_r is not taken apart.
+    const float of_rest = q_rest > 0.0f ? log_rest : 0.0f;
+    const float slope = none ? quiet_nan() : zero ? 0.0f : tg * (total * expf(of_rest) - q_rest);
     const float c = p.inv_t * LOG2E;
     // 2^a with a = x c - (m c + (log S + log p_r) log2 e), the latter in two parts; rows of huge values take the
     // difference first
-    const float mc = m * c, ml = fmaf(m, c, -mc), ls = (log_s + log_rest) * LOG2E;
+    const float mc = m * c, ml = fmaf(m, c, -mc), ls = (log_s + of_rest) * LOG2E;
     const float hi = mc + ls, pt = hi - mc, lo = ((mc - (hi - pt)) + (ls - pt)) + ml;
     const bool huge = !(fabsf(mc) <= 65536.0f);
     const f2 c2 = make_f2(c, c), hi2 = make_f2(-hi, -hi), lo2 = make_f2(-lo, -lo), k2 = make_f2(slope, slope);
@@ -572,13 +632,8 @@ template <typename T> __global__ void __launch_bounds__(DG_THREADS, 6) distill_g
         }
     }
     __syncthreads(); // over what was stored there
-    if (id >= 0) {
-        const double log_p = ((double)xn - (double)m) * (double)p.inv_t - (double)log_s;
-        const double log_q = (double)val - (double)norm;
-        float d = tg * named_slope((float)log_p, (float)log_q, (float)(log_p - log_q), total);
-        d = none ? quiet_nan() : xn == neg_inf() ? 0.0f : d;
-        dx[id] = Vec<T>::narrow(d);
-    }
+    if (id >= 0)
+        dx[id] = Vec<T>::narrow(named());
 }
 
 template <typename T, int W, bool GRAD> cudaError_t launch_team(const DistillParams &p, int num_sms, cudaStream_t st)

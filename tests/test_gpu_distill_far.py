@@ -1,10 +1,14 @@
-"""lora_distill and lora_distill_grad where a row has no distribution and nothing is left beside what is named.
+"""lora_distill and lora_distill_grad where a row has no distribution and nothing is left beside what is named, and
+where what no entry names is far below the rest of the row.
 
-Tolerances as in test_gpu_distill.py."""
+Tolerances as in test_gpu_distill.py; lora_distill_grad takes a row's rest apart by itself where its log p is below
+-256, so no digits of p / p_r hang on the statistics there, and the bound is the one-pass gradient's, whatever log p_r
+is."""
+import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_distill import INF, NAN, REST, RENORM, check, distill, lib, place  # noqa: F401
+from tests.test_gpu_distill import INF, NAN, REST, RENORM, check, define, distill, gradient, lib, place, same  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +38,58 @@ def test_no_distribution_and_nothing_beside_what_is_named(dtype, V, mode):
     dx = torch.zeros_like(x)
     loss, _, _ = distill(x, ids, teacher, mode, 1.0, g, dx)
     assert loss.isnan().all() and dx.isnan().all()
+
+
+def far_rows(V, n, dtype, values, gen):
+    """Rows whose named tokens have ordinary values and whose others have one of `values`, or two a step apart."""
+    M = 2 * len(values)
+    x = torch.empty(M, V)
+    ids = torch.stack([torch.randperm(V, generator=gen)[:n] for _ in range(M)]).int()
+    for i, value in enumerate(values):
+        x[2 * i] = value
+        x[2 * i + 1] = value
+        x[2 * i + 1, ::3] = value * 1.5 if abs(value) < 1e38 else value / 2
+        if value > -1e9:
+            x[2 * i + 1] += torch.randn(V, generator=gen)
+    x.scatter_(1, ids.long(), torch.randn(M, n, generator=gen) * 2)
+    teacher = torch.log_softmax(torch.randn(M, n + 1, generator=gen), -1)[:, :n].contiguous()  # a share is left for the rest
+    return x, ids.cuda(), teacher.cuda()
+
+
+@pytest.mark.parametrize("mode", [RENORM, REST])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V,n,t,lead", [(40, 6, 1.0, 0), (5003, 20, 0.75, 3), (40000, 256, 1.25, 1), (131072, 20, 2.0, 0)])
+def test_the_rest_far_below(dtype, V, n, t, lead, mode):
+    gen = torch.Generator().manual_seed(V)
+    low = torch.finfo(dtype).min
+    x, ids, teacher = far_rows(V, n, dtype, [-100.0, -300.0, -1e4, -1e6, -1e9, -1e20, low / 4, low], gen)
+    x = place(x, dtype, lead, 1)
+    M = x.shape[0]
+    want = define(x.double().cpu().numpy(), ids.cpu().numpy(), teacher.double().cpu().numpy(), mode, t)
+    rows = x.double().cpu().numpy()
+    for i in range(M):  # p / p_r from the rest alone: log p_r of -1e20 leaves no digits of log p - log p_r, in 64 bits either
+        rest = rows[i].copy()
+        rest[ids[i].cpu().numpy()] = -INF
+        share = np.exp((rest - rest.max()) * t)
+        share /= share.sum()
+        log_rest, qr, Q = want["stats"][i, 2:5]
+        other = rest > -INF
+        want["dx"][i, other] = t * (Q * np.exp(log_rest) - qr) * share[other]
+        want["terms"][i, other] = t * (Q * np.exp(log_rest) + qr) * share[other]
+    g = torch.linspace(-1.0, 2.0, M, device="cuda")
+    f64 = lambda a: a.double().cpu().numpy()  # noqa: E731
+    dx = place(torch.full((M, V), 5.0), dtype, lead, 1)
+    loss, stats, _ = distill(x, ids, teacher, mode, t, g, dx)
+    big = (want["stats"][:, 2] < -3.4029e38) & (mode == REST)  # a log probability beyond fp32, whose largest is 3.40283e38
+    assert same(f64(loss), want["loss"], want["slack"])[~big].all() and (f64(loss)[big] == INF).all()
+    by = f64(g)[:, None] * want["dx"]
+    tol = 2e-5 * np.abs(f64(g))[:, None] * want["terms"] + torch.finfo(dtype).eps / 2 * 1.01 * np.abs(by) + 1e-37
+    logs = np.abs(want["stats"][:, 2]) + want["stats"][:, 1]
+    near = np.where(logs < 300, logs, 0.0)[:, None]  # only there the statistics' digits
+    from_stats = 2.0 ** -22 * near * np.abs(f64(g))[:, None] * want["terms"]
+    for what, have, slack in (("step", dx, 0.0), ("grad", gradient(x, ids, teacher, mode, stats, g, torch.full_like(dx, 5.0), t), from_stats),
+                              ("elsewhere in a vector", gradient(x, ids, teacher, mode, stats, g, place(torch.zeros(M, V), dtype, lead + 1, 3), t),
+                               from_stats),
+                              ("over the logits", (lambda c: gradient(c, ids, teacher, mode, stats, g, c, t))(place(x, dtype, lead, 1)), from_stats)):
+        ok = same(f64(have), by, tol + slack)
+        assert ok.all(), (what, np.argwhere(~ok)[:5].tolist(), f64(have)[~ok][:5], by[~ok][:5], tol[~ok][:5])
