@@ -472,7 +472,7 @@ namespace {
 constexpr int DG_THREADS = 256, DG_UNROLL = 4;
 
 // Statistics have log p_r to 2^-24 of itself, which is what p_v / p_r is off by (6e-5 at -256, all of it at -1e9, where
-// the others are masked by a finite value). Below this, a row whose rest has a share finds its rest's softmax again.
+// the others are masked by a finite value). Below this, a row whose rest has a share finds its rest's softmax again, by its first CTA.
 constexpr float FAR_REST = -256.0f;
 
 // The whole row of dx, by one CTA: -k times the softmax of the others, `own` for the thread's named element (`id`,
@@ -520,7 +520,7 @@ template <typename T> __device__ __noinline__ void far_rest(const T *x, T *dx, i
 // that lie among them are written over what the pass stored there. Bound by HBM and
 // by that order: 8192 x 32000 bf16 178 us, 5.9 TB/s (172 without the named ones; eight
 // vectors a thread 225 us, two 213; 512 threads 216).
-template <typename T> __global__ void __launch_bounds__(DG_THREADS, 6) distill_grad_kernel(DistillParams p, int segs)
+template <typename T, bool REST> __global__ void __launch_bounds__(DG_THREADS, 6) distill_grad_kernel(DistillParams p, int segs)
 {
     constexpr int E = Vec<T>::E;
     begin_behind();
@@ -551,11 +551,8 @@ template <typename T> __global__ void __launch_bounds__(DG_THREADS, 6) distill_g
         }
     }
     const float *st = p.stats + (int64_t)row * LORA_DISTILL_STATS;
-    const float m = st[0], log_s = st[1], log_rest = st[2], q_rest = st[3], total = st[4], norm = st[5];
+    const float m = st[0], log_s = st[1], log_rest = st[2], q_rest = REST ? st[3] : 0.0f, total = st[4], norm = REST ? 0.0f : st[5];
     const float tg = p.inv_t * p.g[row];
-    const bool far = q_rest > 0.0f && !(log_rest >= FAR_REST);
-    if (far && seg != 0) // the row is its first CTA's
-        return;
     // The named elements of this segment, an entry a thread (n <= DG_THREADS)
     __shared__ int ids[LORA_MAX_TEACHER];
     int id = -1;
@@ -566,6 +563,7 @@ template <typename T> __global__ void __launch_bounds__(DG_THREADS, 6) distill_g
         ids[tid] = id;
     }
     __syncthreads();
+    const bool far = REST && q_rest > 0.0f && !(log_rest >= FAR_REST);
     if (id >= 0) {
         const int64_t at = ((int64_t)id + lead) / E;
         if (id >= p.V || (!far && (at < first || at >= first + DG_UNROLL * DG_THREADS)))
@@ -574,7 +572,7 @@ template <typename T> __global__ void __launch_bounds__(DG_THREADS, 6) distill_g
             id = ids[j] == id ? -1 : id; // a token's first entry counts
         if (id >= 0)
             xn = Vec<T>::widen(x[id]);
-        if (p.rest)
+        if (REST)
             val = val > 0.0f && val < -neg_inf() ? 0.0f : val;
     }
     if (far || p.dlogits == p.logits)
@@ -587,7 +585,8 @@ template <typename T> __global__ void __launch_bounds__(DG_THREADS, 6) distill_g
         return none ? quiet_nan() : xn == neg_inf() ? 0.0f : d;
     };
     if (far) {
-        far_rest<T>(x, dx, p.V, id, id >= 0 ? named() : 0.0f, p.inv_t, tg * q_rest);
+        if (seg == 0) // the row is its first CTA's
+            far_rest<T>(x, dx, p.V, id, id >= 0 ? named() : 0.0f, p.inv_t, tg * q_rest);
         return;
     }
     const bool zero = empty || (no_rest && !none);
@@ -662,7 +661,8 @@ template <typename T> cudaError_t launch_grad(const DistillParams &p, cudaStream
     // one vector more than V fills, for rows that start inside one
     const int64_t nvec = ((int64_t)p.V + Vec<T>::E - 1) / Vec<T>::E + 1;
     const int segs = (int)((nvec + DG_UNROLL * DG_THREADS - 1) / (DG_UNROLL * DG_THREADS));
-    return launch_behind(distill_grad_kernel<T>, dim3((unsigned)(p.M * segs)), DG_THREADS, 0, 1, st, p, segs);
+    return launch_behind(p.rest ? distill_grad_kernel<T, true> : distill_grad_kernel<T, false>, dim3((unsigned)(p.M * segs)), DG_THREADS, 0,
+                         1, st, p, segs);
 }
 
 cudaError_t launch_distill_grad(const DistillParams &p, int dtype, cudaStream_t st)
