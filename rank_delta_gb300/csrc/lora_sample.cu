@@ -712,7 +712,7 @@ __device__ __noinline__ void exact_row(Shared<W> &sm, const Row<T, W> r, const S
                 Vec<T>::unpack(raw, x);
 #pragma unroll
                 for (int e = 0; e < E; ++e)
-                    if (x[e] >= low)
+                    if (x[e] >= low && x[e] <= m) // above it only after a copy's wait gave up
                         atomicAdd(&sm.bins.low[(hi - order_bits(x[e])) >> shift], (uint32_t)(exp2_fast((x[e] - m) * s.c) * unit + 0.5f));
             }
             cross_bins<true>(sm, 0, 0ull, (u64)(a.p * whole * unit), parts);

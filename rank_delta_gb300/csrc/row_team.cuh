@@ -358,12 +358,13 @@ template <typename T, int W> __device__ __forceinline__ u64 rest_of(const Row<T,
     equal = 0;
     int held = -1;
     uint4 kept;
-    if (mine == s.m) {
+    if (mine == s.m)
         for (int v = group; v < r.w1; v += 32)
             if (Vec<T>::largest(r.vec[v]) == s.m) {
                 held = v;
                 break;
             }
+    if (held >= 0) { // it is there, but for a copy that comes after its wait gave up
         kept = r.vec[held];
         r.vec[held] = empty_vec<T>();
         sum = as_fixed(vector_rest<T, true>(kept, s, equal), SUM_SCALE);
