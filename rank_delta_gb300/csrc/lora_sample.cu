@@ -1825,6 +1825,8 @@ __global__ void __launch_bounds__(W * 32 + (TEAM ? 0 : 32), W == 8 ? 3 : 8) samp
             }
             for (int i = tid; i < GUIDE; i += W * 32)
                 sm.guide[h ^ 1][i] = 0u;
+            if (tid == 0) // all have read what the row before listed, and list again behind the next barrier
+                sm.listed = 0;
             Settings a;
             a.take(sm.settings[h]);
             if (tid < 5 && next < p.M)
@@ -2030,7 +2032,6 @@ __global__ void __launch_bounds__(W * 32 + (TEAM ? 0 : 32), W == 8 ? 3 : 8) samp
                             q.row = row;
                             q.a = a;
                             q.s = s;
-                            sm.listed = 0;
                         }
                         if (!TEAM) {
                             if (r.warp == 0) {
