@@ -1314,7 +1314,7 @@ __device__ __noinline__ u64 weight_once(const Scale s, float x, int bits, const 
 __device__ __forceinline__ u64 min_p_units(float min_p, int scale)
 {
     const float mp = min_p * __uint_as_float((uint32_t)(127 + scale) << 23);
-    return min_p > 0.0f ? (u64)mp + ((float)(u64)mp < mp ? 1ull : 0ull) : 0ull;
+    return (u64)mp + ((float)(u64)mp < mp ? 1ull : 0ull);
 }
 __device__ __forceinline__ bool at_border(u64 w, u64 least)
 {
@@ -1449,7 +1449,15 @@ __device__ __noinline__ bool finish_warp(const u64 *powers, Entry *list, const S
             keep[r] = keep[r] && in;
         }
     }
-    const u64 least = min_p_units(min_p, scale);
+    if (min_p > 0.0f) { // w >= min_p
+        const u64 least = min_p_units(min_p, scale);
+#pragma unroll
+        for (int r = 0; r < PER; ++r) {
+            const bool best = order_value((uint32_t)(key[r] >> 32)) == s.m; // its w = 1 is exact
+            open |= keep[r] && !best && at_border(w[r], least);
+            keep[r] = keep[r] && (w[r] >= least || (ordered && r * 32 + lane == 0));
+        }
+    }
     const bool zero = u < 0x1p-40f;
     const float floor0 = fmaxf(s.m - 1000.0f / s.c, LEAST);
     int kept = 0;
@@ -1458,8 +1466,6 @@ __device__ __noinline__ bool finish_warp(const u64 *powers, Entry *list, const S
     for (int r = 0; r < PER; ++r) {
         const int at = r * 32 + lane;
         const float x = order_value((uint32_t)(key[r] >> 32));
-        open |= keep[r] && x != s.m && min_p > 0.0f && at_border(w[r], least); // w = 1 of the best and its equals is exact
-        keep[r] = keep[r] && (w[r] >= least || (ordered && at == 0));
         kept += keep[r];
         by_index[r] = keep[r] && !(zero && x < floor0) ? (0xFFFFFFFFu - (uint32_t)key[r]) << 7 | at : 0xFFFFFFFFu;
     }
@@ -1607,12 +1613,13 @@ __device__ __noinline__ bool finish_list(S &sm, Entry *list, const SampleParams 
             keep[o] = keep[o] && in;
         }
     }
-    const u64 least = min_p_units(a.least, scale);
+    const bool bounded = a.least > 0.0f; // w >= min_p
+    const u64 least = bounded ? min_p_units(a.least, scale) : 0ull;
     sum = 0ull;
     int kept = 0;
 #pragma unroll
     for (int o = 0; o < OWN; ++o) {
-        open |= keep[o] && x[o] != s.m && a.least > 0.0f && at_border(w[o], least); // w = 1 of the best and its equals is exact
+        open |= keep[o] && x[o] != s.m && bounded && at_border(w[o], least); // w = 1 of the best and its equals is exact
         keep[o] = keep[o] && (w[o] >= least || (ordered && ahead[o] == 0));
         sum += keep[o] ? w[o] : 0ull;
         kept += keep[o];
