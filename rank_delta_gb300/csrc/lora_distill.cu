@@ -71,14 +71,10 @@ struct Numbers {
 
     template <int W> __device__ __forceinline__ void maxima(const Found<W> &f, int parts, bool spoilt, int lane)
     {
-        const bool first = lane < parts * W, second = W > 4 && lane + 32 < parts * W;
-        float a = first ? f.rest_max[lane] : neg_inf(), b = first ? f.named_max[lane] : neg_inf();
-        if (second) {
-            a = max_nan(a, f.rest_max[lane + 32]);
-            b = max_nan(b, f.named_max[lane + 32]);
-        }
-        rest_max = warp_top(a);
-        m = max_nan(rest_max, warp_top(b));
+        static_assert(MAX_PARTS * W <= 32, "a lane for each");
+        const bool one = lane < parts * W;
+        rest_max = warp_top(one ? f.rest_max[lane] : neg_inf());
+        m = max_nan(rest_max, warp_top(one ? f.named_max[lane] : neg_inf()));
         none = spoilt || !(m < -neg_inf());
         empty = !none && m == neg_inf();
         no_rest = !none && rest_max == neg_inf();
@@ -87,10 +83,10 @@ struct Numbers {
     {
         u64 r = 0ull, n = 0ull;
         int e = 0;
-        for (int i = lane; i < parts * W; i += 32) {
-            r += f.rest[i];
-            n += f.named[i];
-            e += f.equal[i];
+        if (lane < parts * W) {
+            r = f.rest[lane];
+            n = f.named[lane];
+            e = f.equal[lane];
         }
         r = warp_sum64(r);
         n = warp_sum64(n);
@@ -198,8 +194,7 @@ template <int W> __device__ __forceinline__ void finish(const Found<W> &f, const
         if (a.q_rest > 0.0f)
             loss = fmaf(a.q_rest, logf(a.q_rest) - log_rest, loss);
         const float n = quiet_nan();
-        if (p.loss != nullptr)
-            p.loss[row] = a.none ? n : loss;
+        p.loss[row] = a.none ? n : loss;
         if (p.stats != nullptr) {
             float *st = p.stats + (int64_t)row * LORA_DISTILL_STATS;
             st[0] = a.none ? n : a.m;
@@ -230,7 +225,7 @@ __device__ __forceinline__ float named_slope(float log_p, float log_q, float gap
 // Long rows meet twice in a cluster: 1000 x 131072 bf16 with gradient and 128 entries 199 us (217 where a
 // warp went through each 32 entries together).
 template <typename T, int W, bool GRAD>
-__global__ void __launch_bounds__(W * 32 + 32, W == 8 ? 3 : W == 4 ? 4 : 8) distill_kernel(DistillParams p, int parts)
+__global__ void __launch_bounds__(W * 32 + 32, W == 4 ? 4 : 8) distill_kernel(DistillParams p, int parts)
 {
     constexpr int E = Vec<T>::E;
     extern __shared__ uint4 slice[];

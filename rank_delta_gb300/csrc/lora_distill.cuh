@@ -14,7 +14,7 @@ struct DistillParams {
     const float *teacher; // [M][n]
     int n;
     int rest;             // the rest of the vocabulary is one more class
-    float *loss;          // [M], or nullptr
+    float *loss;          // [M]; not the gradient by itself
     float *stats;         // [M][LORA_DISTILL_STATS], or nullptr; read by the gradient by itself
     const float *g;       // [M]
     void *dlogits;        // or nullptr

@@ -1517,87 +1517,65 @@ __device__ __forceinline__ bool finish_any(const u64 *powers, Entry *list, const
                        : finish_warp<LIST / 32>(powers, list, p, q);
 }
 
-// The listed elements: top-k, top-p of what it left, min-p, and the draw, by the
-// CTA's W warps, or by one (THREADS 32). An element is OWN of a thread's, or where it
-// is one, that of up to eight threads side by side, which count what precedes it
-// together. False where the sums leave it open.
-template <int THREADS, int OWN, typename S>
-__device__ __noinline__ bool finish_list(S &sm, Entry *list, const SampleParams &p, const ListTask &q)
+// The listed elements: top-k, top-p of what it left, min-p, and the draw, by the CTA's W
+// warps. An element is that of up to eight threads side by side, which count what
+// precedes it together. False where the sums leave it open. Clusters' lists are worked out so: their rows are
+// few, and what counts is how long one takes. One row of 32000 bf16 with every setting 12.5 us, 13.5 with the
+// sort in one warp; 8 rows 14.2 and 16.3, 64 rows 18.7 and 19.9. Where one more warp
+// works out the lists of many rows beside the others, the sort takes less of the SM.
+template <int W> __device__ __noinline__ bool finish_list(Shared<W> &sm, Entry *list, const SampleParams &p, const ListTask &q)
 {
+    constexpr int THREADS = W * 32;
     const int tid = threadIdx.x % THREADS, n = q.n, row = q.row;
     const Settings a = q.a;
     const Scale s = q.s;
     int ways = 1;
-    if (OWN == 1)
-        while (ways < 8 && 2 * ways * n <= THREADS)
-            ways *= 2;
-    const int id = OWN == 1 ? tid / ways : tid, sub = OWN == 1 ? tid & (ways - 1) : 0;
-    auto sync = [&] {
-        if (THREADS == 32)
-            __syncwarp();
-        else
-            named_bar_sync(BAR_LIST, THREADS);
-    };
+    while (ways < 8 && 2 * ways * n <= THREADS)
+        ways *= 2;
+    const int id = tid / ways, sub = tid & (ways - 1);
+    auto sync = [&] { named_bar_sync(BAR_LIST, THREADS); };
     auto sum_of = [&](u64 v, int at) {
         v = warp_sum64(v);
-        if constexpr (THREADS > 32) {
-            if ((tid & 31) == 0)
-                sm.sums[at][tid >> 5] = v;
-            sync();
-            v = 0ull;
+        if ((tid & 31) == 0)
+            sm.sums[at][tid >> 5] = v;
+        sync();
+        v = 0ull;
 #pragma unroll
-            for (int w = 0; w < THREADS / 32; ++w)
-                v += sm.sums[at][w];
-        }
+        for (int w = 0; w < W; ++w)
+            v += sm.sums[at][w];
         return v;
     };
     const int scale = min(LIST_SCALE, 62 - (32 - __clz((int)((q.rest >> SUM_SCALE) + (u64)q.equal + 1ull))));
-    float x[OWN];
-    int i[OWN], ahead[OWN];
-    u64 w[OWN], before[OWN];
-#pragma unroll
-    for (int o = 0; o < OWN; ++o) {
-        const int at = id + o * THREADS;
-        x[o] = neg_inf();
-        i[o] = 0x7fffffff;
-        w[o] = before[o] = 0ull;
-        ahead[o] = 0;
-        if (at < n) {
-            x[o] = list[at].x;
-            i[o] = list[at].i;
-            w[o] = weight_once(s, x[o], scale, sm.powers);
-            if (sub == 0)
-                list[at].w = w[o];
-        }
+    float x = neg_inf();
+    int i = 0x7fffffff, ahead = 0;
+    u64 w = 0ull, before = 0ull;
+    if (id < n) {
+        x = list[id].x;
+        i = list[id].i;
+        w = weight_once(s, x, scale, sm.powers);
+        if (sub == 0)
+            list[id].w = w;
     }
     sync();
     const bool ordered = q.k > 0 || q.by_p; // else min-p alone, which the best passes (it is at most 1)
-    const bool busy = OWN > 1 || (tid & ~31) < n * ways;
+    const bool busy = (tid & ~31) < n * ways;
     if (busy && ordered) {
 #pragma unroll 4
         for (int j = sub; j < n; j += ways) { // their places in the order
             const Entry e = list[j];
-#pragma unroll
-            for (int o = 0; o < OWN; ++o) {
-                const bool is = e.x > x[o] || (e.x == x[o] && e.i < i[o]);
-                ahead[o] += is;
-                before[o] += is ? e.w : 0ull;
-            }
+            const bool is = e.x > x || (e.x == x && e.i < i);
+            ahead += is;
+            before += is ? e.w : 0ull;
         }
         for (int o = 1; o < ways; o *= 2) {
-            ahead[0] += __shfl_xor_sync(0xffffffffu, ahead[0], o);
-            before[0] += __shfl_xor_sync(0xffffffffu, before[0], o);
+            ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
+            before += __shfl_xor_sync(0xffffffffu, before, o);
         }
     }
-    bool keep[OWN], open = a.least > 0.0f && a.least < 0x1p-40f; // beneath the weights' unit
-    u64 sum = 0ull;
-#pragma unroll
-    for (int o = 0; o < OWN; ++o) {
-        keep[o] = id + o * THREADS < n && sub == 0 && (q.k == 0 || ahead[o] < q.k);
-        sum += keep[o] ? w[o] : 0ull;
-    }
+    bool keep = id < n && sub == 0 && (q.k == 0 || ahead < q.k);
+    bool open = a.least > 0.0f && a.least < 0x1p-40f; // beneath the weights' unit
     if (q.by_p) {
-        const u64 listed = sum_of(sum, 0), f = fraction(a.p);
+        const u64 listed = sum_of(keep ? w : 0ull, 0), f = fraction(a.p);
         u64 z_low = listed, z_high = listed;
         if (q.k == 0) {
             const u64 z = q.rest + ((u64)q.equal << SUM_SCALE), mg = (u64)(q.margin * SUM_UNITS) + 1ull;
@@ -1605,39 +1583,26 @@ __device__ __noinline__ bool finish_list(S &sm, Entry *list, const SampleParams 
             z_high = (z + mg) << (scale - SUM_SCALE);
         }
         const u64 t_low = share_up(f, z_low), t_high = share_up(f, z_high);
+        const bool in = before < t_low || ahead == 0;
         open |= q.k == 0 && listed < t_high && !q.least_bound;
-#pragma unroll
-        for (int o = 0; o < OWN; ++o) {
-            const bool in = before[o] < t_low || ahead[o] == 0;
-            open |= keep[o] && in != (before[o] < t_high || ahead[o] == 0);
-            keep[o] = keep[o] && in;
-        }
+        open |= keep && in != (before < t_high || ahead == 0);
+        keep = keep && in;
     }
-    const bool bounded = a.least > 0.0f; // w >= min_p
-    const u64 least = bounded ? min_p_units(a.least, scale) : 0ull;
-    sum = 0ull;
-    int kept = 0;
-#pragma unroll
-    for (int o = 0; o < OWN; ++o) {
-        open |= keep[o] && x[o] != s.m && bounded && at_border(w[o], least); // w = 1 of the best and its equals is exact
-        keep[o] = keep[o] && (w[o] >= least || (ordered && ahead[o] == 0));
-        sum += keep[o] ? w[o] : 0ull;
-        kept += keep[o];
+    if (a.least > 0.0f) { // w >= min_p
+        const u64 least = min_p_units(a.least, scale);
+        open |= keep && x != s.m && at_border(w, least); // w = 1 of the best and its equals is exact
+        keep = keep && (w >= least || (ordered && ahead == 0));
     }
     // the count, and in the upper half whether any is open
-    kept = __reduce_add_sync(0xffffffffu, kept);
-    open = __any_sync(0xffffffffu, open);
-    kept |= open ? 1 << 20 : 0;
-    if constexpr (THREADS > 32)
-        if ((tid & 31) == 0)
-            sm.firsts[tid >> 5] = kept;
-    const u64 total = sum_of(sum, 1); // and all are through with the list's weights
-    if constexpr (THREADS > 32) {
-        kept = 0;
+    int kept = __reduce_add_sync(0xffffffffu, (int)keep);
+    kept |= __any_sync(0xffffffffu, open) ? 1 << 20 : 0;
+    if ((tid & 31) == 0)
+        sm.firsts[tid >> 5] = kept;
+    const u64 total = sum_of(keep ? w : 0ull, 1); // and all are through with the list's weights
+    kept = 0;
 #pragma unroll
-        for (int v = 0; v < THREADS / 32; ++v)
-            kept += sm.firsts[v];
-    }
+    for (int v = 0; v < W; ++v)
+        kept += sm.firsts[v];
     if (kept >> 20 != 0)
         return false;
     const u64 target = __umul64hi(fraction(a.u), total);
@@ -1645,47 +1610,34 @@ __device__ __noinline__ bool finish_list(S &sm, Entry *list, const SampleParams 
     int first = 0x7fffffff;
     if (zero) { // the first with a weight above e^-693
         const float floor0 = fmaxf(s.m - 1000.0f / s.c, LEAST);
+        first = __reduce_min_sync(0xffffffffu, keep && x >= floor0 ? i : 0x7fffffff);
+        sync();
+        if ((tid & 31) == 0)
+            sm.firsts[tid >> 5] = first;
+        sync();
 #pragma unroll
-        for (int o = 0; o < OWN; ++o)
-            if (keep[o] && x[o] >= floor0)
-                first = min(first, i[o]);
-        first = __reduce_min_sync(0xffffffffu, first);
-        if constexpr (THREADS > 32) {
-            sync();
-            if ((tid & 31) == 0)
-                sm.firsts[tid >> 5] = first;
-            sync();
-#pragma unroll
-            for (int v = 0; v < THREADS / 32; ++v)
-                first = min(first, sm.firsts[v]);
-        }
+        for (int v = 0; v < W; ++v)
+            first = min(first, sm.firsts[v]);
     } else { // the first, in index order, past u of their sum
-#pragma unroll
-        for (int o = 0; o < OWN; ++o) {
-            before[o] = 0ull;
-            if (id + o * THREADS < n && sub == 0)
-                list[id + o * THREADS].w = keep[o] ? w[o] : 0ull;
-        }
+        before = 0ull;
+        if (id < n && sub == 0)
+            list[id].w = keep ? w : 0ull;
         sync();
         if (busy) {
 #pragma unroll 4
             for (int j = sub; j < n; j += ways) {
                 const Entry e = list[j];
-#pragma unroll
-                for (int o = 0; o < OWN; ++o)
-                    before[o] += e.i < i[o] ? e.w : 0ull;
+                before += e.i < i ? e.w : 0ull;
             }
             for (int o = 1; o < ways; o *= 2)
-                before[0] += __shfl_xor_sync(0xffffffffu, before[0], o);
+                before += __shfl_xor_sync(0xffffffffu, before, o);
         }
     }
-#pragma unroll
-    for (int o = 0; o < OWN; ++o)
-        if (keep[o] && (zero ? i[o] == first : target >= before[o] && target - before[o] < w[o])) {
-            p.tokens[row] = i[o];
-            if (p.logprob != nullptr)
-                p.logprob[row] = (x[o] - s.m) * a.t - log1pf((float)(total - (1ull << scale)) / (float)(1ull << scale));
-        }
+    if (keep && (zero ? i == first : target >= before && target - before < w)) {
+        p.tokens[row] = i;
+        if (p.logprob != nullptr)
+            p.logprob[row] = (x - s.m) * a.t - log1pf((float)(total - (1ull << scale)) / (float)(1ull << scale));
+    }
     if (tid == 0 && p.kept != nullptr)
         p.kept[row] = kept;
     return true;
@@ -2048,7 +2000,7 @@ __global__ void __launch_bounds__(W * 32 + (TEAM ? 0 : 32), W == 8 ? 3 : 8) samp
                             given = true;
                         } else {
                             cta_sync<W>(); // the task is there
-                            const bool ok = finish_list<W * 32, 1>(sm, sm.list, p, sm.task);
+                            const bool ok = finish_list(sm, sm.list, p, sm.task);
                             if (!ok && r.warp == 0 && lane < parts)
                                 told->open[h] = turn;
                         }
