@@ -952,6 +952,7 @@ __device__ __noinline__ bool fine_row(Shared<W> &sm, const Row<T, W> r, const Sa
         sm.least = least_kept(m, a.t, a.least);
     const Scale s = scale_of(m, a.t);
     Cut cut{LEAST, 0x7fffffff}; // all
+    bool all = true;            // a cut by rank may lie at the lowest value too
     float tie_weight = 0.0f;
     if (k > 0) { // exactly, by counting; first among those above a bound that most rows' first thousands reach
         Crossing at;
@@ -961,6 +962,7 @@ __device__ __noinline__ bool fine_row(Shared<W> &sm, const Row<T, W> r, const Sa
             at.above_mass = 0ull;
             if (descend<false>(sm, r, s, SUM_SCALE, (u64)k, fmaxf(low, LEAST), m, parts, at)) {
                 cut = Cut{at.x, k - at.above};
+                all = false;
                 break;
             }
             if (!(low > LEAST))
@@ -969,7 +971,6 @@ __device__ __noinline__ bool fine_row(Shared<W> &sm, const Row<T, W> r, const Sa
         }
         tie_weight = (float)weight(s, cut.x, SUM_SCALE, sm.powers) * SUM_UNIT;
     }
-    const bool all = cut.x <= LEAST;
     u64 own = 0ull, exact = 0ull; // this thread's part of what is kept, and what of it was listed
     int above = 0, ties = 0;
     bool sure = true, summed = false;

@@ -109,3 +109,20 @@ def test_the_border_of_huge_logits(M, V):
     x[:, V // 3] = m - 64.0
     want = lambda row, u, t, k, p, q: (V // 2, 0.0, 1 + int(-64.0 >= np.log(q)))  # noqa: E731
     assert compare(place(x, F32), [0.5] * M, None, None, None, [float(near[i % 3]) for i in range(M)], want_of=want) == 0
+
+
+@pytest.mark.parametrize("few", [2, 100, 128, 129, 700])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M,V", [(12, 1500), (12, 5000), (6, 70000), (630, 2100)])
+def test_rows_with_nothing_but_the_lowest_value(M, V, dtype, few):
+    """All that is not masked by -infinity has the type's lowest value: equal weights, of which top-k keeps the first, and
+    top-p and min-p of those."""
+    gen = torch.Generator().manual_seed(V + few)
+    x = torch.full((M, V), -np.inf)
+    for i in range(M):
+        x[i, torch.randperm(V, generator=gen)[:few]] = torch.finfo(dtype).min
+    r = torch.rand(3, M, generator=gen).tolist()
+    k = [[5, 0, 64, 1000][i % 4] for i in range(M)]
+    p = [[0.5, 0.9, 1.0][i % 3] for i in range(M)]
+    q = [[0.0, 0.3][i % 2] for i in range(M)]
+    assert compare(place(x, dtype, 1, 1), r[0], [0.5 + a for a in r[1]], k, p, q) == 0
