@@ -207,12 +207,13 @@ template <int W> __device__ __forceinline__ void finish(const Found<W> &f, const
     }
 }
 
-// dx of a named element over t g: Q p - q from their logarithms, good where they are near.
+// dx of a named element over t g: Q p - q from their logarithms, good where they are near; `gap` is log p - log q. Q is
+// far from 1 where the teacher gives little, or more than 1, to tokens beside which nothing is left.
 __device__ __forceinline__ float named_slope(float log_p, float log_q, float gap, float total)
 {
-    const float p = expf(log_p);
-    const float d = gap > 0.0f ? -p * expm1f(-gap) : expf(log_q) * expm1f(gap); // p - q, gap = log p - log q
-    return fmaf(total - 1.0f, p, d);
+    const float near = gap + logf(total);
+    const float d = near > 0.0f ? -total * expf(log_p) * expm1f(-near) : expf(log_q) * expm1f(near);
+    return total == 0.0f ? 0.0f : d;
 }
 
 } // namespace

@@ -93,3 +93,34 @@ def test_the_rest_far_below(dtype, V, n, t, lead, mode):
                               ("over the logits", (lambda c: gradient(c, ids, teacher, mode, stats, g, c, t))(place(x, dtype, lead, 1)), from_stats)):
         ok = same(f64(have), by, tol + slack)
         assert ok.all(), (what, np.argwhere(~ok)[:5].tolist(), f64(have)[~ok][:5], by[~ok][:5], tol[~ok][:5])
+
+
+@pytest.mark.parametrize("mode", [RENORM, REST])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V,n", [(1, 3), (50, 50), (5003, 20), (40000, 100)])
+def test_tokens_beside_which_nothing_is_left_with_little_of_the_teacher(dtype, V, n, mode):
+    """Q, the teacher's sum over them, is e^-1 to e^-25 and up to e^3, and a slope is Q p - q: of Q's size, not of p's."""
+    gen = torch.Generator().manual_seed(V + n)
+    sums = torch.tensor([3.0, 0.1, 0.0, -1e-6, -1.0, -5.0, -10.0, -17.0, -25.0])
+    M = len(sums)
+    x = torch.full((M, V), -INF)
+    ids = torch.stack([torch.randperm(V, generator=gen)[:min(n, V)] for _ in range(M)])
+    own = torch.randn(M, ids.shape[1], generator=gen) * 2
+    x.scatter_(1, ids, own)
+    teacher = torch.log_softmax(own + 0.01 * torch.randn(own.shape, generator=gen), 1) + sums[:, None]
+    x, ids, teacher = place(x, dtype, 1, 1), ids.int().cuda(), teacher.cuda()
+    f64 = lambda a: a.double().cpu().numpy()  # noqa: E731
+    want = define(f64(x), ids.cpu().numpy(), f64(teacher), mode, 1.0)
+    g = torch.linspace(-1.0, 2.0, M, device="cuda")
+    dx = torch.zeros_like(x)
+    loss, stats, _ = distill(x, ids, teacher, mode, 1.0, g, dx)
+    assert same(f64(loss), want["loss"], want["slack"]).all()
+    # a share is an integer of 2^-53, off by half of one, and Q the sum of n of them
+    units = ids.shape[1] * 2.0 ** -54
+    Q = want["stats"][:, 4]
+    assert (np.abs(f64(stats[:, 4]) - Q) <= 2.0 ** -23 * Q + units).all()
+    by = f64(g)[:, None] * want["dx"]
+    tol = np.abs(f64(g))[:, None] * (2e-5 * want["terms"] + units) + torch.finfo(dtype).eps / 2 * 1.01 * np.abs(by) + 1e-37
+    for what, have in (("step", dx), ("grad", gradient(x, ids, teacher, mode, stats, g, torch.full_like(dx, 5.0)))):
+        ok = same(f64(have), by, tol)
+        assert ok.all(), (what, np.argwhere(~ok)[:5].tolist(), f64(have)[~ok][:5], by[~ok][:5], tol[~ok][:5])
