@@ -769,14 +769,18 @@ size_t lora_distill_workspace_bytes(int M, int V, int n);
  *   ws       device workspace of lora_distill_workspace_bytes bytes, for the
  *            status word
  * A named token of share 0 adds nothing; one of another share that is masked
- * (-infinity) makes the loss +infinity. Where no token is left in the rest, or all
- * of it is masked, the rest has no share. A row without entries, or whose values
- * are all -infinity, has loss 0, and for LORA_DISTILL_RENORM gradient 0 (for
- * LORA_DISTILL_REST its rest is all tokens, so the gradient is 0 as well). A row
- * with nothing but -infinity has gradient 0 and a loss of +infinity (0 without
- * entries), a masked element gradient 0. A row that holds a NaN or +infinity, or
- * an entry with such a value, gets NaN everywhere. Values above 0 count as 0 for
+ * (-infinity), or whose log probability fp32 does not hold, makes the loss
+ * +infinity, and so does a rest of such a log probability that has a share. Where
+ * no token is left in the rest, or all of it is masked, the rest has no share. A row
+ * without entries has loss and gradient 0 (for LORA_DISTILL_REST its rest is all
+ * tokens). Entries whose values are all -infinity give loss and gradient 0 for
+ * LORA_DISTILL_RENORM; for LORA_DISTILL_REST they still name their tokens, so the rest
+ * has it all: the loss is -log p_r, and the gradient the formula's. A row with nothing
+ * but -infinity has gradient 0 and a loss of +infinity (0 where no entry has a
+ * share), a masked element gradient 0. A row that holds a NaN or +infinity, or an entry with
+ * such a value, gets NaN everywhere. Values above 0 count as 0 for
  * LORA_DISTILL_REST.
+ * The shares are summed in units of 2^-53.
  * Sums are fp32 or more, the gradient is rounded once. Results are the same on
  * every run. M = 0 is a no-op. Enqueued on `stream` only (no allocation, no
  * synchronisation; graph-safe).
@@ -794,7 +798,9 @@ lora_status lora_distill(const void *logits, int dtype, int64_t stride, int M, i
 /*
  * The gradient of sum_i grad_loss[i] * loss[i] with respect to the logits, as
  * above, from the stats of lora_distill on the same logits, entries, mode and
- * inv_temperature. An id >= V counts as negative.
+ * inv_temperature. An id >= V counts as negative. Where the rest has a share,
+ * p_v / p_r is as good as the stats' log p_r (2^-24 of it), below -256 as good as the
+ * logits.
  * Errors: as lora_distill; NULL stats, grad_loss or dlogits.
  */
 lora_status lora_distill_grad(const void *logits, int dtype, int64_t stride, int M, int V, float inv_temperature,

@@ -219,12 +219,13 @@ __device__ __forceinline__ float named_slope(float log_p, float log_q, float gap
 } // namespace
 
 // W warps go through the row; one more prepares the next row's entries and writes
-// the last one's loss meanwhile. Four warps, three of whose CTAs' rows of 64 KB an SM holds
-// (8192 x 32000 bf16: the loss 120 us, eight warps 131; with the gradient 224 us), two for
-// short rows. The sum of powers takes as long as the copy, 4.3 TB/s; with the gradient
-// reading and writing come to 4.7 TB/s. A row of few vectors is latency: 64 x 32003 f32 9.3 us.
-// Long rows meet twice in a cluster: 1000 x 131072 bf16 with gradient and 128 entries 199 us (217 where a
-// warp went through each 32 entries together).
+// the last one's loss meanwhile. Four warps, three of whose CTAs' rows of 64 KB an SM holds,
+// two for short rows. 8192 x 32000 bf16: the loss 117 us, 4.5 TB/s; with the gradient, reading
+// and writing, 217 us, 4.8 TB/s. Neither memory nor issue bounds these (half of DRAM's rate, 54 and 53 % of the
+// issue slots, 26 and 28 % of the exponentials' unit): a CTA waits for its own row's copy,
+// maxima and sums in turn, and three of them an SM do not hide that. Only the gradient needs the
+// row to stay. A row of few vectors is latency: 64 x 32003 f32 9.3 us.
+// Long rows meet twice in a cluster: 1000 x 131072 bf16 with gradient and 128 entries 201 us.
 template <typename T, int W, bool GRAD>
 __global__ void __launch_bounds__(W * 32 + 32, W == 4 ? 4 : 8) distill_kernel(DistillParams p, int parts)
 {
@@ -513,9 +514,11 @@ template <typename T> __device__ __noinline__ void far_rest(const T *x, T *dx, i
 } // namespace
 
 // A CTA takes DG_UNROLL * DG_THREADS vectors of one row of dlogits; named elements
-// that lie among them are written over what the pass stored there. Bound by HBM and
-// by that order: 8192 x 32000 bf16 178 us, 5.9 TB/s (172 without the named ones; eight
-// vectors a thread 225 us, two 213; 512 threads 216).
+// that lie among them are written over what the pass stored there. 8192 x 32000 bf16 179 us,
+// 5.9 TB/s: 68 % of DRAM's rate and 61 % of the issue slots. The gradient of the log probabilities,
+// which names one token a row, is at 7.0 TB/s; without the named elements this one was 3 % faster, so most of the
+// difference is elsewhere and not explained. Other shapes were slower: eight vectors a thread 225 us,
+// two 213, 512 threads 216.
 template <typename T, bool REST> __global__ void __launch_bounds__(DG_THREADS, 6) distill_grad_kernel(DistillParams p, int segs)
 {
     constexpr int E = Vec<T>::E;

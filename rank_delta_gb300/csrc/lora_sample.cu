@@ -17,12 +17,19 @@
 // A row lies in shared memory, spread over a cluster where it is long or rows
 // are few (row_team.cuh). Of the threads' own maxima, which cost nothing, those that
 // top-k or top-p need give a bound that every kept element reaches; the few
-// elements that do are listed, and one warp finds each its place by counting, while
-// the others are at the next row. A row of which more may be kept than the list
-// holds, or that the list leaves open, is cut by counting in bins of the values'
-// order-preserving bits instead, as often as it takes to reach one value. Rows are
-// taken as teams get through, since those take several times as long. Hundreds of
-// rows are read through registers instead, by warps that do nothing else.
+// elements that do are listed, and one warp sorts them while the others are at the
+// next row (in a cluster, the leading CTA counts each its place). A row of which
+// more may be kept than the list holds, or that the list leaves open, is gone through
+// by fine_row: top-k by counting in bins of the values' order-preserving bits, top-p
+// in bins of the exponent, whose one bin that the border lies in is listed, sums in
+// fp32 with the exponent's rounding put right. What that leaves open exact_row
+// decides, by exact sums in bins of the values' bits, as often as it takes to reach
+// one value. Rows are taken as teams get through, since those take several times
+// as long. Hundreds of rows are read through registers instead, by warps that do
+// nothing else.
+//
+// Times below are of calls one after another on a GB300, on rows as perf/more_operators.py
+// makes them for the sizes and settings named (seed 1), unless they say otherwise.
 #include <cooperative_groups.h>
 
 #include "behind.cuh"
@@ -1650,8 +1657,10 @@ template <int W> __device__ __noinline__ bool finish_list(Shared<W> &sm, Entry *
 // all its warps. Else one more warp does, while the others are at the next row, and
 // a row that it leaves open is gone through again when that is known. Latency bounds
 // it: one row of 32000 takes 12 us (top 50, top-p and min-p, a cluster of eight), of which
-// its copy takes 3; 64 rows of 32003 f32 with settings of their own 28 us, 590 x 32000 bf16
-// of top 50 34 us.
+// its copy takes 3; 590 x 32000 bf16 of top 50 32 us. 64 rows of 32003 f32 with settings of
+// every kind take 18 to 39 us, as rows that the list leaves open, or their exact sums, come
+// up or not. The registers that the CTAs an SM may have do not hold it all: 250 to 450 bytes a
+// thread are stored to local memory and 340 to 940 loaded (-Xptxas -v), most with four warps.
 template <typename T, int W, bool TEAM>
 __global__ void __launch_bounds__(W * 32 + (TEAM ? 0 : 32), W == 8 ? 3 : 8) sample_kernel(SampleParams p, int parts_)
 {
@@ -2074,10 +2083,9 @@ namespace {
 // maximum reaches the bound are few, and their shares are read again from L2; a draw
 // from the whole vocabulary reads the run that it falls into. Nothing the finishing
 // warps do stops the loads. What they leave open is marked in `tokens`, for the
-// kernels behind. 8192 x 32000 bf16 (77 us by its bytes): 125 us of min-p, 4.2 TB/s, where
-// the maxima bound it; 124 with the sum of nothing cut; 160 of top-p at temperature 0.5, 215 of
-// top 50, where the finishing warps do (fewer of them: 244 us; three such CTAs on an SM
-// have too few registers to read ahead).
+// kernels behind. 8192 x 32000 bf16 (77 us by its bytes), whole calls: 137 us of min-p, where
+// the maxima bound it; 180 where nothing is cut, with some 70 rows for the kernels behind;
+// 185 of top-p at temperature 0.5, 241 of top 50, where the finishing warps do.
 constexpr int READERS = 256, READ_WARPS = READERS / 32, FINISHERS = 4, AHEAD = 4;
 constexpr int READ_THREADS = READERS + 32 * FINISHERS;
 constexpr int GROUP = AHEAD * READERS;                                 // vectors that a CTA reads at once,
@@ -2542,10 +2550,9 @@ template <typename T> __global__ void __launch_bounds__(READ_THREADS, 2) read_ro
 // in front of it, by teams as large as they have to be, and the last one has those that
 // fine sums leave open too. A few are in the workspace's list, others have to be
 // looked for among `some` rows at a time. The last kernel writes the call's status.
-// Of 8192 x 32000 bf16, top-p 0.95 at temperature 1, 2440 rows come here and take 320 us by
-// three CTAs an SM: 76000 cycles each, 22000 of them in the fine sums and 14000 in the bins, in
-// shared memory; 24 warps do not hide the barriers between. The last kernel alone
-// takes 7 us where it finds nothing.
+// Of 8192 x 32000 bf16, top-p 0.95 at temperature 1 (571 us a call), some 2400 rows come here
+// and take more than half of it by three CTAs an SM: maximum, rough sum, bins, fine sums and
+// draw one after another in shared memory, whose barriers 24 warps do not hide.
 template <typename T, bool TEAM>
 __global__ void __launch_bounds__(256, 3) open_rows_kernel(SampleParams p, int parts_, int some, int most, int last)
 {
@@ -2635,10 +2642,12 @@ template <typename T, int W, bool TEAM> cudaError_t launch_as(const SampleParams
 template <typename T> cudaError_t launch_typed(const SampleParams &p, int num_sms, cudaStream_t st)
 {
     // Read through registers, rows get along without a cluster's barriers, but wait for the other kernels of the call.
-    // 600 rows: (512 and 590) x 32000 bf16 of top 50 take 36 and 38 us there and 32 and 34 here, of top-p at temperature
-    // 0.5 49 and 53 us against 56 and 64, x 9000 24 and 21 us against 21 and 22. A row that nothing cuts is summed
-    // there in runs, few of which have to be looked into: 64 and 152 x 32000 24 and 32 us against 25 and 51, x 131072 64
-    // and 89 us against 84 and 129, but 152 x 4000 12 against 11.
+    // 600 rows: (512 and 590) x 32000 bf16 of top 50 take 37.5 and 37.6 us there and 30.5 and 32.2 here, x 9000 30.1
+    // and 30.2 against 23.6 and 24.6, and of top-p at temperature 0.5 23.6 and 23.8 against 20.4 and 21.2, but x 32000
+    // 37 and 62 us against 51 and 67. A row that nothing cuts is summed there in runs, few of which have to be looked
+    // into: 152 x 131072 86 us against 121, 64 x 32000 45 against 47, but 152 x 32000 31 against 29, 64 x 131072 40
+    // against 33, and 152 x 4000 16 against 11. Which settings rows have is not known here, only which arrays there are:
+    // 256 and 512 x 131072 of mixed settings take 277 and 358 us, and would take 199 and 237 there.
     const bool plain = p.top_k == nullptr && p.top_p == nullptr && p.min_p == nullptr;
     const int many_rows = plain && p.V >= 16384 ? 64 : 600;
 
@@ -2653,9 +2662,8 @@ template <typename T> cudaError_t launch_typed(const SampleParams &p, int num_sm
         if (e != cudaSuccess)
             return e;
         // One open row a cluster of eight: it takes a row a fifth of the time that a CTA does, but three times the SMs' time.
-        // (8192 x 32000 bf16 of which nothing is cut, some 70 open: 187 us, with up to six rows a cluster 202, without
-        // clusters 229. 1000 x 32000 of top-p at temperature 1, 300 open: 145 us, with up to six 266.) The few that fine
-        // sums leave open again are theirs in any case: 140 us a row by a CTA, 40 by a cluster.
+        // (8192 x 32000 bf16 of which nothing is cut: 180 us, with up to six rows a cluster 194. 1000 x 32000 of top-p at
+        // temperature 1: 168 us, with up to six 270.) The few that fine sums leave open again are theirs in any case.
         const int64_t nvec = ((int64_t)p.V + Vec<T>::E - 1) / Vec<T>::E + 1;
         const int wide = num_sms * 3 / MAX_PARTS, most = wide;
         const size_t smem = (size_t)((nvec + MAX_PARTS - 1) / MAX_PARTS) * 16;
@@ -2674,9 +2682,9 @@ template <typename T> cudaError_t launch_typed(const SampleParams &p, int num_sm
                           some(wide), most, 1);
         return e == cudaSuccess ? e : CallCounts::give_up(e, p.status, st);
     }
-    // Two warps a short row (8192 x 1000 bf16 of which nothing is cut 62 us, of top-p 51 us; eight warps 110 and 113 us),
-    // four where top-k has to guess a bound from the threads' maxima, of which 64 are too few (top 50: 90 us, with two
-    // warps 146), but not of the shortest rows (500 elements: 165 us, with two 130).
+    // Two warps a short row (8192 x 1000 bf16 of which nothing is cut 66 us, of top-p 65; four 78 and 81, eight 112 and
+    // 128), four where top-k has to guess a bound from the threads' maxima, of which 64 are too few (top 50: 86 us, with
+    // two warps 145, with eight 144), but not of the shortest rows (500 elements: 172 us, with two 137).
     if (short_rows<T>(p.M, p.V, num_sms)) {
         if (p.top_k != nullptr && p.V >= 96 * Vec<T>::E)
             return launch_as<T, 4, false>(p, plan_teams<T, 4>(p.M, p.V, num_sms, sizeof(Shared<4>)), st);
