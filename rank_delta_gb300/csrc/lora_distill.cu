@@ -67,6 +67,7 @@ struct Numbers {
     float m, rest_max;
     bool none, empty, no_rest;
     float rest_sum, rest_equal, below, others; // the rest's over its maximum; log of that over the row's; S - 1
+    float named;                               // what S has of the named ones
     float q_rest, total;
 
     template <int W> __device__ __forceinline__ void maxima(const Found<W> &f, int parts, bool spoilt, int lane)
@@ -97,6 +98,7 @@ struct Numbers {
         const int of_rest = rest_max == m; // one of the maxima is left out, of the rest where it has one
         const float at_rest = no_rest ? 0.0f : expf(below) * ((rest_equal - (float)of_rest) + rest_sum);
         others = fmaxf(at_rest + (float)((e >> 20) - (1 - of_rest)) + (float)n * 0x1p-53f, 0.0f);
+        named = (float)(e >> 20) + (float)n * 0x1p-53f;
         q_rest = 0.0f;
         if (p.rest) {
             const u64 one = 1ull << SHARE_SCALE;
@@ -108,6 +110,16 @@ struct Numbers {
         }
     }
     __device__ __forceinline__ float log_s() const { return none || empty ? 0.0f : log1pf(others); }
+    // log p_r by the ratio of the named ones to the rest, whose digits it keeps where p_r is near 1: the difference of two
+    // logarithms of 4 has 2^-22 of them at best. Where the rest is far below, by that.
+    __device__ __forceinline__ float log_rest(float log_s) const
+    {
+        if (no_rest)
+            return neg_inf();
+        if (below > -64.0f)
+            return -log1pf(named / (expf(below) * (rest_equal + rest_sum)));
+        return below + (log1pf((rest_equal - 1.0f) + rest_sum) - log_s);
+    }
 };
 
 // log q - log p of an entry, as good as its parts: the products and differences as two numbers each.
@@ -182,7 +194,7 @@ template <int W> __device__ __forceinline__ void finish(const Found<W> &f, const
     a.maxima(f, parts, en.spoilt != 0, lane);
     a.sums(f, en, p, parts, lane);
     const float log_s = a.log_s();
-    const float log_rest = a.no_rest ? neg_inf() : a.below + (log1pf((a.rest_equal - 1.0f) + a.rest_sum) - log_s);
+    const float log_rest = a.log_rest(log_s);
     float loss = 0.0f;
     for (int c = 0; c < p.n; c += 32) {
         const float val = en.val[c + lane], q = expf(val - en.norm);
@@ -191,8 +203,10 @@ template <int W> __device__ __forceinline__ void finish(const Found<W> &f, const
     }
     loss = warp_sum(loss);
     if (lane == 0) {
-        if (a.q_rest > 0.0f)
-            loss = fmaf(a.q_rest, logf(a.q_rest) - log_rest, loss);
+        if (a.q_rest > 0.0f) { // near 1, as p_r may be: by what it lacks of 1
+            const float others = (float)en.shares * 0x1p-53f;
+            loss = fmaf(a.q_rest, (others < 0.5f ? log1pf(-others) : logf(a.q_rest)) - log_rest, loss);
+        }
         const float n = quiet_nan();
         p.loss[row] = a.none ? n : loss;
         if (p.stats != nullptr) {

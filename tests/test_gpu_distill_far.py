@@ -124,3 +124,25 @@ def test_tokens_beside_which_nothing_is_left_with_little_of_the_teacher(dtype, V
     for what, have in (("step", dx), ("grad", gradient(x, ids, teacher, mode, stats, g, torch.full_like(dx, 5.0)))):
         ok = same(f64(have), by, tol)
         assert ok.all(), (what, np.argwhere(~ok)[:5].tolist(), f64(have)[~ok][:5], by[~ok][:5], tol[~ok][:5])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,V,n", [(40, 3000, 2), (12, 32003, 8), (4, 131072, 20), (700, 5000, 3)])
+def test_a_near_teacher_that_names_little_of_a_flat_row(dtype, M, V, n):
+    """The rest has nearly all on both sides, so the loss is a small difference: log q_r and log p_r go by what they lack
+    of 1. A row's sum is good to 4e-6 of itself, which is 4e-6 (1 - p_r) in log p_r; a named term to 4e-6 of its share
+    (its logarithms of up to 16 have 2^-21 of them, 8e-6 of the share); the two logarithms of the rest to 2^-22 each."""
+    gen = torch.Generator().manual_seed(V)
+    x = place(torch.randn(M, V, generator=gen) * 0.5, dtype, 1, 1)
+    ids = torch.stack([torch.randperm(V, generator=gen)[:n] for _ in range(M)])
+    near = x.double().cpu() + 0.1 * torch.randn(M, V, generator=gen)
+    teacher = torch.gather(torch.log_softmax(near, 1), 1, ids).float()
+    f64 = lambda a: a.double().cpu().numpy()  # noqa: E731
+    want = define(f64(x), ids.numpy(), f64(teacher), REST, 1.0)
+    loss, stats, _ = distill(x, ids.int().cuda(), teacher.cuda(), REST)
+    log_rest, qr, Q = want["stats"][:, 2], want["stats"][:, 3], want["stats"][:, 4]
+    tol = 4e-6 * -np.expm1(log_rest) + 2.0 ** -22 * np.abs(log_rest)
+    assert (np.abs(f64(stats[:, 2]) - log_rest) <= tol).all()
+    off = np.abs(f64(loss) - want["loss"])
+    tol += 1.2e-5 * (Q - qr) + 2.0 ** -22 * np.abs(np.log(qr)) + 2.0 ** -50
+    assert (off <= tol).all(), (off.max(), tol[off.argmax()], want["loss"][off.argmax()])
