@@ -798,9 +798,9 @@ lora_status lora_distill(const void *logits, int dtype, int64_t stride, int M, i
 /*
  * The gradient of sum_i grad_loss[i] * loss[i] with respect to the logits, as
  * above, from the stats of lora_distill on the same logits, entries, mode and
- * inv_temperature. An id >= V counts as negative. Where the rest has a share,
- * p_v / p_r is as good as the stats' log p_r (2^-24 of it), below -256 as good as the
- * logits.
+ * inv_temperature. An id >= V counts as negative. The shares are as good as the
+ * stats' log of their sum (2^-24 of it), and where the rest has a share, p_v / p_r is
+ * as good as their log p_r, below -256 as good as the logits.
  * Errors: as lora_distill; NULL stats, grad_loss or dlogits.
  */
 lora_status lora_distill_grad(const void *logits, int dtype, int64_t stride, int M, int V, float inv_temperature,

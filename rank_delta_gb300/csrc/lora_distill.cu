@@ -33,7 +33,7 @@ struct __align__(16) Entries {
     int id[LORA_MAX_TEACHER];
     float val[LORA_MAX_TEACHER];
     u64 shares; // the sum of e^val 2^53, over e^best where they are to sum to 1
-    float norm; // log q = val - norm
+    float norm, norm_low; // log q = val - norm - norm_low: a teacher's plain logits may lie far from 0
     int spoilt;
 };
 
@@ -137,7 +137,7 @@ __device__ __forceinline__ float log_ratio(const Numbers &a, const Entries &en, 
     const float q = val - en.norm, w = q - val, q_low = (val - (q - w)) - (en.norm + w);
     const float g = q - z, y = g - q, g_low = (q - (g - y)) - (z + y);
     const float h = g + log_s, u = h - g, h_low = (g - (h - u)) + (log_s - u);
-    return h + ((g_low + h_low) + (q_low - z_low));
+    return h + ((g_low + h_low) + ((q_low - en.norm_low) - z_low));
 }
 
 // The entries of a row, by one warp.
@@ -181,7 +181,11 @@ __device__ __forceinline__ bool prepare(Entries &en, const DistillParams &p, int
     spoilt = __any_sync(0xffffffffu, spoilt);
     if (lane == 0) {
         en.shares = shares;
-        en.norm = p.rest || shares == 0ull || spoilt ? 0.0f : high + log_fixed(shares, SHARE_SCALE);
+        const bool plain = p.rest || shares == 0ull || spoilt;
+        const float from = plain ? 0.0f : high, sum = plain ? 0.0f : log_fixed(shares, SHARE_SCALE);
+        const float norm = from + sum, v = norm - from;
+        en.norm = norm;
+        en.norm_low = (from - (norm - v)) + (sum - v);
         en.spoilt = spoilt;
     }
     return past;
@@ -197,7 +201,7 @@ template <int W> __device__ __forceinline__ void finish(const Found<W> &f, const
     const float log_rest = a.log_rest(log_s);
     float loss = 0.0f;
     for (int c = 0; c < p.n; c += 32) {
-        const float val = en.val[c + lane], q = expf(val - en.norm);
+        const float val = en.val[c + lane], q = expf((val - en.norm) - en.norm_low);
         if (q > 0.0f && val > neg_inf())
             loss = fmaf(q, a.empty ? -neg_inf() : log_ratio(a, en, log_s, p.inv_t, x[c + lane], val), loss);
     }
@@ -467,7 +471,7 @@ __global__ void __launch_bounds__(W * 32 + 32, W == 4 ? 4 : 8) distill_kernel(Di
                 const int j = (__ffs(left) - 1) * 32 + lane;
                 const float x = taken[j], val = en.val[j];
                 const float gap = -log_ratio(a, en, log_s, p.inv_t, x, val);
-                float d = tg * named_slope((x - a.m) * p.inv_t - log_s, val - en.norm, gap, a.total);
+                float d = tg * named_slope((x - a.m) * p.inv_t - log_s, (val - en.norm) - en.norm_low, gap, a.total);
                 d = a.none ? quiet_nan() : a.empty || x == neg_inf() ? 0.0f : d;
                 dx[en.id[j]] = Vec<T>::narrow(d);
             }

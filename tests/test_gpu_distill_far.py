@@ -146,3 +146,28 @@ def test_a_near_teacher_that_names_little_of_a_flat_row(dtype, M, V, n):
     off = np.abs(f64(loss) - want["loss"])
     tol += 1.2e-5 * (Q - qr) + 2.0 ** -22 * np.abs(np.log(qr)) + 2.0 ** -50
     assert (off <= tol).all(), (off.max(), tol[off.argmax()], want["loss"][off.argmax()])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("offset", [0.0, 64.0, -1024.0, 2.0 ** 13])
+def test_a_teacher_of_plain_logits_far_from_0(dtype, offset):
+    """LORA_DISTILL_RENORM takes values up to a constant. Those of this test are multiples of 2^-9, so that they are exact with
+    each offset, and so is what the call makes of them: the share's logarithm is (val - best) - log of a sum, each
+    within 2^-21 of up to 16, and so is log p; a share is off by 2^-21 of itself more, and times |log q - log p|. The
+    loss is a sum of such terms."""
+    gen = torch.Generator().manual_seed(6)
+    M, V, n = 64, 3000, 30
+    ids = torch.stack([torch.randperm(V, generator=gen)[:n] for _ in range(M)])
+    teacher = (torch.randn(M, n, generator=gen) * 512).round() / 512
+    x = torch.randn(M, V, generator=gen) - 12.0
+    x.scatter_(1, ids, teacher + 0.05 * torch.randn(M, n, generator=gen))  # a near student
+    x = place(x, dtype, 1, 1)
+    f64 = lambda a: a.double().cpu().numpy()  # noqa: E731
+    want = define(f64(x), ids.numpy(), f64(teacher), RENORM, 1.0)
+    g = torch.ones(M, device="cuda")
+    dx = torch.zeros_like(x)
+    loss, _, _ = distill(x, ids.int().cuda(), (teacher + offset).cuda(), RENORM, 1.0, g, dx)
+    off = np.abs(f64(loss) - want["loss"])
+    assert off.max() <= 4e-6, (off.max(), want["loss"][off.argmax()])
+    tol = 2e-5 * want["terms"] + torch.finfo(dtype).eps / 2 * 1.01 * np.abs(want["dx"]) + 1e-37
+    assert same(f64(dx), want["dx"], tol).all()
